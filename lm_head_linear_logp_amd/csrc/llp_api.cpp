@@ -10,6 +10,7 @@
 #include <mutex>
 
 #include "llp.h"
+#include "llp_host.h"
 #include "llp_internal.h"
 
 using namespace llp;
@@ -18,33 +19,21 @@ namespace {
 
 thread_local char g_err[512] = "";
 
+constexpr int kMaxDevices = 64;
+std::mutex g_mu;
+int g_opened[kMaxDevices] = {0};
+int g_num_cus[kMaxDevices] = {0};
+
+}  // namespace
+
+namespace llp {
+
 llp_status fail(llp_status st, const char* fmt, ...) {
   va_list ap;
   va_start(ap, fmt);
   vsnprintf(g_err, sizeof(g_err), fmt, ap);
   va_end(ap);
   return st;
-}
-
-#define LLP_CHECK(cond, st, ...) \
-  do {                           \
-    if (!(cond)) return fail(st, __VA_ARGS__); \
-  } while (0)
-
-constexpr int kMaxDevices = 64;
-std::mutex g_mu;
-int g_opened[kMaxDevices] = {0};
-int g_num_cus[kMaxDevices] = {0};
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
-
-int64_t local_real(const llp_vocab_partition& v) {
-  int64_t n = v.real_vocab - v.offset;
-  if (n < 0) n = 0;
-  if (n > v.local_size) n = v.local_size;
-  return n;
 }
 
 llp_status check_partition(const llp_vocab_partition& v) {
@@ -67,6 +56,10 @@ llp_status check_partition(const llp_vocab_partition& v) {
             "padded_vocab %lld exceeds int32 indexing", (long long)v.padded_vocab);
   return LLP_OK;
 }
+
+}  // namespace llp
+
+namespace {
 
 llp_status check_request(const llp_request* req) {
   LLP_CHECK(req != nullptr, LLP_ERR_INVALID_ARGUMENT, "request is NULL");
@@ -122,28 +115,19 @@ llp_status check_request(const llp_request* req) {
   return LLP_OK;
 }
 
-// Workspace regions (byte offsets, each 256-byte aligned).
-struct Ws {
-  size_t count, qctr, scored, pos, tloc, tz, pm, ps, pq, G, hgT, P, dbp, total;
-  int64_t T_cap, nvt, ldg;
-  int64_t slab_tiles, nslab;   // vocabulary tiles per slab of G and slabs per backward call
-};
+}  // namespace
 
-// `slabs` (backward only): G is held one vocabulary slab of G_SLAB_TILES tiles at a time, so
-// its region (and the bias-gradient partials) take one slab's columns, ldg = the slab width.
-Ws ws_layout(int64_t T, int64_t n_real, int64_t H, int op, bool slabs = false) {
+namespace llp {
+
+Ws ws_layout(int64_t T, int64_t n_real, int64_t H, int op, bool slabs) {
   Ws w{};
   w.T_cap = round_up(T > 0 ? T : 1, TILE);
   w.nvt = (n_real + TILE - 1) / TILE;
   w.slab_tiles = slabs && w.nvt > G_SLAB_TILES ? G_SLAB_TILES : (w.nvt > 0 ? w.nvt : 1);
   w.nslab = w.nvt > 0 ? (w.nvt + w.slab_tiles - 1) / w.slab_tiles : 0;
   w.ldg = w.slab_tiles * TILE;
-  size_t off = 0;
-  auto take = [&](size_t bytes) {
-    const size_t o = off;
-    off += (size_t)round_up((int64_t)(bytes > 0 ? bytes : 1), 256);
-    return o;
-  };
+  Regions r;
+  auto take = [&](size_t bytes) { return r.take(bytes); };
   w.count = take((size_t)(1 + layout_blocks(T)) * 4);   // 256 bytes up to 63 layout blocks
   // Tile-queue counters: QCTR_INTS per GEMM kernel launch of the call (3 per slab backward).
   w.qctr = take((size_t)(w.nslab > 1 ? 3 * w.nslab : 4) * QCTR_INTS * 4);
@@ -161,12 +145,11 @@ Ws ws_layout(int64_t T, int64_t n_real, int64_t H, int op, bool slabs = false) {
     w.P = take((size_t)DH_SPLITS * (size_t)w.T_cap * (size_t)H * 4);
     w.dbp = take((size_t)(w.T_cap / TILE) * (size_t)w.ldg * 4);   // bias-gradient partials
   }
-  w.total = off;
+  w.total = r.off;
   return w;
 }
 
-// The current device must have been opened; `num_cus` (optional) receives its compute units.
-llp_status check_device(int* num_cus = nullptr) {
+llp_status check_device(int* num_cus) {
   int dev = -1;
   if (hipGetDevice(&dev) != hipSuccess) return fail(LLP_ERR_HIP, "hipGetDevice failed");
   std::lock_guard<std::mutex> lk(g_mu);
@@ -181,18 +164,23 @@ llp_status hip_status(hipError_t e, const char* what) {
   return fail(LLP_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
 }
 
-#define LLP_HIP(expr, what)                         \
-  do {                                              \
-    llp_status s_ = hip_status((expr), (what));     \
-    if (s_ != LLP_OK) return s_;                    \
-  } while (0)
-
-template <class T>
-T* at(void* ws, size_t off) {
-  return reinterpret_cast<T*>(static_cast<char*>(ws) + off);
+llp_status check_forward_out(int64_t T, bool want_ent, const llp_partials* out, const Ws& w,
+                             const void* workspace, size_t workspace_bytes) {
+  LLP_CHECK(out != nullptr, LLP_ERR_INVALID_ARGUMENT, "out is NULL");
+  if (T > 0) {
+    LLP_CHECK(out->target_logit && out->in_range && out->lse, LLP_ERR_INVALID_ARGUMENT,
+              "out.target_logit, out.in_range and out.lse are required");
+  }
+  LLP_CHECK(T == 0 || !want_ent || out->entropy != nullptr, LLP_ERR_INVALID_ARGUMENT,
+            "LLP_FLAG_WANT_ENTROPY needs out.entropy");
+  LLP_CHECK(workspace_bytes >= w.total, LLP_ERR_INVALID_ARGUMENT,
+            "workspace of %zu bytes is smaller than the %zu required", workspace_bytes, w.total);
+  LLP_CHECK(workspace != nullptr && aligned(workspace, 256), LLP_ERR_INVALID_ARGUMENT,
+            "workspace must be non-NULL and 256-byte aligned");
+  return LLP_OK;
 }
 
-}  // namespace
+}  // namespace llp
 
 extern "C" {
 
@@ -382,94 +370,28 @@ llp_status forward_impl(const llp_request* req, const llp_partials* out, void* w
                         size_t workspace_bytes, void* stream) {
   llp_status st = check_request(req);
   if (st != LLP_OK) return st;
-  LLP_CHECK(out != nullptr, LLP_ERR_INVALID_ARGUMENT, "out is NULL");
   const int64_t T = req->layout.num_tokens;
   const bool want_ent = (req->flags & LLP_FLAG_WANT_ENTROPY) != 0;
-  if (T > 0) {
-    LLP_CHECK(out->target_logit && out->in_range && out->lse, LLP_ERR_INVALID_ARGUMENT,
-              "out.target_logit, out.in_range and out.lse are required");
-  }
-  LLP_CHECK(T == 0 || !want_ent || out->entropy != nullptr, LLP_ERR_INVALID_ARGUMENT,
-            "LLP_FLAG_WANT_ENTROPY needs out.entropy");
-  const int64_t n_real = local_real(req->vocab);
   const int64_t H = req->proj.hidden_size;
-  const Ws w = ws_layout(T, n_real, H, LLP_OP_FORWARD);
-  LLP_CHECK(workspace_bytes >= w.total, LLP_ERR_INVALID_ARGUMENT,
-            "workspace of %zu bytes is smaller than the %zu required", workspace_bytes, w.total);
-  LLP_CHECK(workspace != nullptr && aligned(workspace, 256), LLP_ERR_INVALID_ARGUMENT,
-            "workspace must be non-NULL and 256-byte aligned");
+  const Ws w = ws_layout(T, local_real(req->vocab), H, LLP_OP_FORWARD);
+  st = check_forward_out(T, want_ent, out, w, workspace, workspace_bytes);
+  if (st != LLP_OK) return st;
   int num_cus = 0;
   st = check_device(&num_cus);
   if (st != LLP_OK) return st;
   if (T == 0) return LLP_OK;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  float* ent = want_ent ? out->entropy : nullptr;
-
-  LayoutArgs la{};
-  la.T = T;
-  la.mask = req->layout.loss_mask;
-  la.cu_seqlens = req->layout.cu_seqlens;
-  la.num_seqs = req->layout.num_seqs;
-  la.world = req->vocab.world;
-  la.targets = req->target_ids;
-  la.offset = req->vocab.offset;
-  la.n_real = n_real;
-  la.real_vocab = req->vocab.real_vocab;
-  la.count = at<int32_t>(workspace, w.count);
-  la.scored = at<int32_t>(workspace, w.scored);
-  la.pos = at<int32_t>(workspace, w.pos);
-  la.tloc = at<int32_t>(workspace, w.tloc);
-  la.out_t = out->target_logit;
-  la.out_f = out->in_range;
-  la.out_l = out->lse;
-  la.out_e = ent;
-  la.out_p = out->logp;
-  la.status = req->status_word;
-  la.qctr = at<int32_t>(workspace, w.qctr);   // the forward kernel's tile-queue counters
-  la.nqctr = QCTR_INTS;
-  LLP_HIP(launch_layout(la, s), "layout kernel launch");
-
-  FwdArgs fa{};
-  fa.W = static_cast<const uint16_t*>(req->proj.weight);
-  fa.ldw = req->proj.weight_stride;
-  fa.h = static_cast<const uint16_t*>(req->proj.hidden);
-  fa.ldh = req->proj.hidden_stride;
-  fa.bias = req->proj.bias;
-  fa.bias_f32 = req->proj.bias_dtype == LLP_DTYPE_F32;
-  fa.H = (int32_t)H;
-  fa.n_real = n_real;
-  fa.nvt = (int32_t)w.nvt;
-  fa.ntb = (int32_t)(w.T_cap / TILE);
-  fa.c1 = (float)(1.0 / (double)req->temperature);
-  fa.count = la.count;
-  fa.scored = la.scored;
-  fa.tloc = la.tloc;
-  fa.pm = at<float>(workspace, w.pm);
-  fa.ps = at<float>(workspace, w.ps);
-  fa.pq = at<float>(workspace, w.pq);
-  fa.tz = at<float>(workspace, w.tz);
-  fa.pstride = w.T_cap;
-  fa.qctr = la.qctr;
-  fa.workers = num_cus;
-  LLP_HIP(launch_fwd(fa, s), "forward kernel launch");
-
-  CombineArgs ca{};
-  ca.nvt = (int32_t)w.nvt;
-  ca.pstride = w.T_cap;
-  ca.count = la.count;
-  ca.scored = la.scored;
-  ca.tloc = la.tloc;
-  ca.pm = fa.pm;
-  ca.ps = fa.ps;
-  ca.pq = fa.pq;
-  ca.tz = fa.tz;
-  ca.out_t = out->target_logit;
-  ca.out_f = out->in_range;
-  ca.out_l = out->lse;
-  ca.out_e = ent;
-  ca.out_p = out->logp;
-  LLP_HIP(launch_combine(ca, w.T_cap, s), "combine kernel launch");
-  return LLP_OK;
+  return run_forward(req->vocab, req->layout, req->target_ids, req->temperature, want_ent,
+                     req->status_word, w, out, workspace, num_cus, s, [&](FwdArgs& fa) {
+    fa.W = static_cast<const uint16_t*>(req->proj.weight);
+    fa.ldw = req->proj.weight_stride;
+    fa.h = static_cast<const uint16_t*>(req->proj.hidden);
+    fa.ldh = req->proj.hidden_stride;
+    fa.bias = req->proj.bias;
+    fa.bias_f32 = req->proj.bias_dtype == LLP_DTYPE_F32;
+    fa.H = (int32_t)H;
+    return launch_fwd(fa, s);
+  });
 }
 
 }  // namespace

@@ -1,5 +1,5 @@
-// llp_tile.hpp -- the bf16 MFMA GEMM tile for gfx950 shared by the fused forward, the
-// gradient recompute and the two backward products.
+// llp_tile.hpp -- the MFMA GEMM tile for gfx950 shared by the fused forward, the gradient
+// recompute, the two backward products (bf16) and the fused forward on 8-bit integers.
 //
 // Workgroup tile: BM x BN = 256 x 256 outputs. With 4 wave64s (2 x 2, one per SIMD) each wave
 // owns a 128 x 128 sub-tile as 4 x 4 blocks of v_mfma_f32_32x32x16_bf16 (256 fp32 accumulators
@@ -12,6 +12,13 @@
 // MFMA 32x32x16 bf16 lane layout (CDNA4 ISA): lane l supplies A[i][k] and B[k][j] for
 // i, j = l % 32 and k = 8 * (l / 32) + 0..7; accumulator register r of lane l holds D[i][j]
 // with j = l % 32 and i = 8 * (r / 4) + 4 * (l / 32) + r % 4.
+//
+// 8-bit integers run through the same tile: v_mfma_i32_32x32x32_i8 takes 16 bytes per lane and
+// operand, as the bf16 MFMA does, k = 16 * (l / 32) + 0..15, and its int32 accumulators have the
+// same layout. The stages, the DMA and the fragment reads move bytes, so an int8 operand of K
+// columns is handed to them as one of K / 2 16-bit elements (a K step is 128 columns); only the
+// accumulators' type tells the two apart. Which k a byte of a lane stands for does not matter,
+// since both operands are read alike and integer sums are exact in any order.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -21,6 +28,8 @@ namespace llp {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef int i32x16 __attribute__((ext_vector_type(16)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int BM = 256;
@@ -145,14 +154,14 @@ __device__ __forceinline__ float acc_read(float x) {
   return r;
 }
 
-template <int NFB>
-__device__ __forceinline__ void zero_acc(f32x16 (&acc)[4][NFB]) {
+template <int NFB, class ACC>
+__device__ __forceinline__ void zero_acc(ACC (&acc)[4][NFB]) {
 #pragma unroll
   for (int mi = 0; mi < 4; ++mi)
 #pragma unroll
     for (int ni = 0; ni < NFB; ++ni)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) acc[mi][ni][r] = 0.f;
+      for (int r = 0; r < 16; ++r) acc[mi][ni][r] = 0;
 }
 
 // ------------------------------------------------------------------------------------
@@ -369,14 +378,22 @@ __device__ __forceinline__ void load_frag(const uint16_t* As, const uint16_t* Bs
   }
 }
 
+// One MFMA on 16-byte fragments: bf16 products into fp32 accumulators, or int8 products into
+// int32 ones.
+__device__ __forceinline__ void mfma1(const bf16x8& a, const bf16x8& b, f32x16& c) {
+  c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ void mfma1(const bf16x8& a, const bf16x8& b, i32x16& c) {
+  c = __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4, a),
+                                            __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
+}
+
 // MFMAs number lo..hi-1 of one 16-deep substep, in (mi, ni) row-major order.
-template <int LO, int HI, int NFB>
+template <int LO, int HI, int NFB, class ACC>
 __device__ __forceinline__ void mfmas(const bf16x8 (&a)[4], const bf16x8 (&b)[NFB],
-                                      f32x16 (&acc)[4][NFB]) {
+                                      ACC (&acc)[4][NFB]) {
 #pragma unroll
-  for (int k = LO; k < HI; ++k)
-    acc[k / NFB][k % NFB] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[k / NFB], b[k % NFB],
-                                                                   acc[k / NFB][k % NFB], 0, 0, 0);
+  for (int k = LO; k < HI; ++k) mfma1(a[k / NFB], b[k % NFB], acc[k / NFB][k % NFB]);
 }
 
 // Wait until at most n of this wave's vector-memory instructions are outstanding
@@ -470,12 +487,12 @@ __device__ __forceinline__ void region_mem(const LA& la, const LB& lb, const uin
 
 // One region: 4 x NFB MFMAs on (a, b); fragment reads of substep kk from stage `st` into
 // (na, nb); DMA instructions QB .. QB+D-1 of step `kstep` into stage `dst`.
-template <int D, int QB, bool AK, bool BK, int NFB, class LA, class LB>
+template <int D, int QB, bool AK, bool BK, int NFB, class LA, class LB, class ACC>
 __device__ __forceinline__ void region(const LA& la, const LB& lb, const bf16x8 (&a)[4],
                                        const bf16x8 (&b)[NFB], const uint16_t* st,
                                        const Frag<AK, BK, NFB>& f, int kk, bf16x8 (&na)[4],
                                        bf16x8 (&nb)[NFB], uint16_t* dst, int kstep,
-                                       f32x16 (&acc)[4][NFB]) {
+                                       ACC (&acc)[4][NFB]) {
   using P = ReadPlan<AK, BK, NFB>;
   v4i16 tmp[4];
   mfmas<0, P::NM, NFB>(a, b, acc);
@@ -498,9 +515,9 @@ __device__ __forceinline__ void region(const LA& la, const LB& lb, const bf16x8 
 // steps past the end are clamped to the last step (an in-bounds reload into a stage that is
 // never read again), which keeps every iteration the same shape. All DMA is drained before
 // returning.
-template <class LA, class LB, int NFB = 4>
+template <class LA, class LB, int NFB, class ACC>
 __device__ __forceinline__ void mainloop(const LA& la, const LB& lb, int ks0, int ks1,
-                                         uint16_t* smem, f32x16 (&acc)[4][NFB]) {
+                                         uint16_t* smem, ACC (&acc)[4][NFB]) {
   constexpr bool AK = LA::KMAJOR, BK = LB::KMAJOR;
   static_assert(LA::NIW == LB::NIW, "both operands take the same loads per wave");
   constexpr int NIW = LA::NIW;
@@ -535,12 +552,12 @@ __device__ __forceinline__ void mainloop(const LA& la, const LB& lb, int ks0, in
 
 // One K step of mainloop with its loaders made explicit: the DMA slots for step s+1 (regions
 // 1-3) take (ln, lbn) at K step kn, those for step s+2 (region 4) take (ld, lbd) at kd.
-template <class LA, class LB, int NFB, bool AK, bool BK>
+template <class LA, class LB, int NFB, bool AK, bool BK, class ACC>
 __device__ __forceinline__ void chain_step(const LA& ln, const LB& lbn, int kn, const LA& ld,
                                            const LB& lbd, int kd, uint16_t* cur, uint16_t* nx,
                                            const Frag<AK, BK, NFB>& f, bf16x8 (&a0)[4],
                                            bf16x8 (&b0)[NFB], bf16x8 (&a1)[4], bf16x8 (&b1)[NFB],
-                                           f32x16 (&acc)[4][NFB]) {
+                                           ACC (&acc)[4][NFB]) {
   constexpr int NIW = LA::NIW;
   constexpr int NQ = 2 * NIW, Q4 = NIW, Q1 = NIW;
   region<Q1, Q4>(ln, lbn, a0, b0, cur, f, 1, a1, b1, nx, kn, acc);
@@ -561,10 +578,10 @@ __device__ __forceinline__ void chain_step(const LA& ln, const LB& lbn, int kn, 
 //    `more` false: the slots reload the last step (as in mainloop) and all DMA is drained
 //    before returning.
 // The epilogue must not use the two stages (the next tile's loads land there).
-template <class LA, class LB, int NFB>
+template <class LA, class LB, int NFB, class ACC>
 __device__ __forceinline__ void mainloop_chain(const LA& la, const LB& lb, const LA& la2,
                                                const LB& lb2, bool primed, bool more, int n,
-                                               uint16_t* smem, f32x16 (&acc)[4][NFB]) {
+                                               uint16_t* smem, ACC (&acc)[4][NFB]) {
   constexpr bool AK = LA::KMAJOR, BK = LB::KMAJOR;
   static_assert(LA::NIW == LB::NIW, "both operands take the same loads per wave");
   constexpr int NQ = 2 * LA::NIW, Q4 = LA::NIW;
