@@ -20,7 +20,7 @@
  *   - Tensor pointers are DEVICE pointers unless stated otherwise; the caller owns all memory
  *     and keeps it valid until the work enqueued on `stream` completes.
  *   - `stream` is a hipStream_t passed as void* (NULL = the null stream).
- *   - Execution calls (forward, merge, backward, top_p_replay) never allocate, never
+ *   - Execution calls (every call but llp_open and the workspace sizes) never allocate, never
  *     synchronize and never read device memory on the host, so they can be captured into a
  *     HIP graph. Every row's result is a function of that row's inputs and the fixed kernel
  *     configuration only: results are bitwise reproducible run to run and do not depend on
@@ -31,7 +31,8 @@
  *     return LLP_ERR_INVALID_ARGUMENT before anything is enqueued. Data-dependent problems
  *     found on the device (a bad target or replay id, a malformed cu_seqlens) are OR-ed into
  *     the optional device `status_word` (LLP_STATUS_* bits) and the affected rows get -inf
- *     log-probabilities; nothing becomes NaN.
+ *     log-probabilities; nothing becomes NaN. (What the losses and the embedding do with such
+ *     rows stands at their requests.)
  */
 #ifndef LLP_H
 #define LLP_H
@@ -70,7 +71,9 @@ enum {
   LLP_STATUS_TARGET_OUT_OF_RANGE = 1, /* a scored row's target is outside [0, real_vocab) */
   LLP_STATUS_TARGET_NOT_FOUND = 2,    /* no shard (or no replay candidate) holds the target */
   LLP_STATUS_REPLAY_ID_INVALID = 4,   /* a replay id outside [-1, real_vocab) (slot ignored) */
-  LLP_STATUS_LAYOUT_INVALID = 8       /* cu_seqlens not 0 = c0 <= c1 <= ... <= cS = T */
+  LLP_STATUS_LAYOUT_INVALID = 8,      /* cu_seqlens not 0 = c0 <= c1 <= ... <= cS = T */
+  LLP_STATUS_TOKEN_OUT_OF_RANGE = 16, /* an embedded token id outside [0, real_vocab) */
+  LLP_STATUS_VALUE_NOT_FINITE = 32    /* a scored row of a loss holds an infinity or NaN */
 };
 
 enum { LLP_DTYPE_BF16 = 1, LLP_DTYPE_F32 = 2 };
@@ -317,6 +320,199 @@ typedef struct {
   int32_t* status_word;
 } llp_keep_mask_request;
 
+/* ---- Scoring with a head in 8-bit integers -------------------------------------------------
+ * A frozen policy (the reference of a KL term or of a preference loss) needs log-probabilities
+ * and no gradient. Its head may then be held as int8 rows with one fp32 scale per vocabulary
+ * column, and the hidden states be quantised per token: half the bytes and twice the MFMA rate
+ * of bf16. */
+#define LLP_INT8_COLUMNS 128 /* int8 rows hold a multiple of this many columns */
+
+/* Symmetric 8-bit quantisation of rows.
+ *   x      [rows, cols] bf16 or fp32 (x_dtype), row stride x_stride elements (>= cols), any
+ *          alignment of its element type.
+ *   q      int8 [rows, cols_padded], cols_padded = cols rounded up to LLP_INT8_COLUMNS; row
+ *          stride q_stride bytes (>= cols_padded, multiple of 16), 16-byte aligned base.
+ *          Columns cols .. cols_padded - 1 are written as 0.
+ *   scale  fp32 [rows].
+ * With a = max_k |x[r][k]|: scale[r] = max(a, 1e-30) / 127 and q[r][k] = x[r][k] / scale[r]
+ * rounded to the nearest integer, ties to even (both divisions in fp32, correctly rounded). A
+ * row of zeros gives q = 0. A row holding an infinity or NaN gives q = 0 and scale = NaN. */
+typedef struct {
+  const void* x;
+  int32_t x_dtype;
+  int32_t reserved;
+  int64_t x_stride;
+  int64_t rows; /* 0 <= rows < 2^31 */
+  int64_t cols; /* 1 <= cols <= 2^20 */
+  int8_t* q;
+  int64_t q_stride;
+  float* scale;
+} llp_quant_request;
+
+/* llp_request with the projection in 8-bit integers: z = (sum_k hidden[t][k] weight[v][k] *
+ * hidden_scale[t] * weight_scale[v] + bias[v]) * fl32(1/temperature), the sum exact in int32.
+ *   hidden        int8 [T, hidden_size], row stride hidden_stride bytes; weight int8
+ *                 [local_size, hidden_size], row stride weight_stride bytes: strides >=
+ *                 hidden_size and multiples of 16, 16-byte aligned bases. As
+ *                 llp_quantize_rows writes them (values in [-127, 127]; -128 is read as such).
+ *   hidden_scale  fp32 [T]; weight_scale fp32 [local_size] (16-byte aligned base).
+ *   hidden_size   the padded width: a positive multiple of LLP_INT8_COLUMNS, at most 2^17 - 128
+ *                 (the int32 sums cannot overflow; else LLP_ERR_UNSUPPORTED).
+ *   hidden_stride and weight_stride < 2^24, T * hidden_stride < 2^31 and the row limits of
+ *   llp_projection (else LLP_ERR_UNSUPPORTED).
+ * The other fields are those of llp_request (flags: LLP_FLAG_WANT_ENTROPY). Values that are not
+ * finite (scales of rows that were not) spread as they do in llp_forward. */
+typedef struct {
+  const int8_t* hidden;
+  int64_t hidden_stride;
+  const float* hidden_scale;
+  const int8_t* weight;
+  int64_t weight_stride;
+  const float* weight_scale;
+  const void* bias;
+  int32_t bias_dtype;
+  uint32_t flags;
+  int64_t hidden_size;
+  llp_vocab_partition vocab;
+  llp_token_layout layout;
+  const int64_t* target_ids;
+  float temperature;
+  int32_t reserved;
+  int32_t* status_word;
+} llp_int8_request;
+
+/* ---- Losses on the scored log-probabilities ------------------------------------------------
+ * Both read what llp_forward / llp_merge write (logp, entropy) and write what llp_backward takes
+ * (dlogp, dentropy). Rows whose loss_mask is 0 are never read into a result (they may hold
+ * anything) and get gradient 0. */
+enum { LLP_KL_K1 = 1, LLP_KL_K2 = 2, LLP_KL_K3 = 3 };
+enum { LLP_REDUCE_TOKEN_MEAN = 1, LLP_REDUCE_SEQ_MEAN = 2, LLP_REDUCE_SUM = 3 };
+/* Log ratios are clamped to [-20, 20] before their exponential; outside, it passes no gradient. */
+#define LLP_LOG_RATIO_MAX 20
+#define LLP_POLICY_STATS 8
+
+/* Clipped policy loss with a KL term and an entropy bonus. For a scored row with
+ * d = logp - old_logp, r = exp(clamp(d)), A = advantages:
+ *   policy  = -min(A r, A clip(r, 1 - clip_low, 1 + clip_high)); with dual_clip = c > 0 and A < 0
+ *             at most -A c. Where the clip holds (r > 1 + clip_high for A > 0; r < 1 - clip_low
+ *             or r > c for A < 0) it passes no gradient, else d policy / d logp = -A r. The
+ *             borders, the clamps' too, are compared in 64 bits: d > log(1 + clip_high) and so on.
+ *   kl      = with x = ref_logp - logp: k1 = -x, k2 = x^2 / 2, k3 = exp(clamp(x)) - clamp(x) - 1.
+ *   loss    = sum_t w_t (policy + kl_coef kl - entropy_coef entropy)
+ * and w_t by `reduction`: TOKEN_MEAN 1 / (scored rows); SEQ_MEAN 1 / (scored rows of t's
+ * sequence * sequences that have any); SUM 1. `denominator` (a device float, or NULL) takes the
+ * place of the number of rows (TOKEN_MEAN) or sequences (SEQ_MEAN), for a batch spread over
+ * several processes; a value that is not finite and > 0 gives w = 0, as a batch without scored
+ * rows does.
+ *   logp, old_logp, advantages   fp32 [T]
+ *   ref_logp   fp32 [T], or NULL (then no KL term; kl_coef must be 0)
+ *   entropy    fp32 [T], or NULL (then no bonus; entropy_coef must be 0)
+ *   layout     T < 2^31; cu_seqlens is required for SEQ_MEAN. A malformed cu_seqlens sets
+ *              LLP_STATUS_LAYOUT_INVALID, and with SEQ_MEAN every output is 0 then.
+ *   0 <= clip_low <= 1, clip_high >= 0, dual_clip 0 (none) or > 1, all coefficients finite.
+ * A scored row holding a value that is not finite (of the arrays that are used) sets
+ * LLP_STATUS_VALUE_NOT_FINITE, adds nothing and gets gradient 0; it still counts as scored. */
+typedef struct {
+  const float* logp;
+  const float* old_logp;
+  const float* advantages;
+  const float* ref_logp;
+  const float* entropy;
+  llp_token_layout layout;
+  double clip_low;
+  double clip_high;
+  double dual_clip;
+  double kl_coef;
+  double entropy_coef;
+  int32_t kl_kind;
+  int32_t reduction;
+  const float* denominator;
+  int32_t* status_word;
+} llp_policy_request;
+
+/*   loss      fp32 [1]
+ *   stats     fp32 [LLP_POLICY_STATS], or NULL: loss, then the w-weighted sums of policy, kl,
+ *             entropy, clipped (0/1), r and -d, then the number of scored rows
+ *   dloss     fp32 [1] upstream gradient of the loss (device), or NULL for 1
+ *   dlogp     fp32 [T] d loss / d logp * dloss, or NULL
+ *   dentropy  fp32 [T], or NULL (needs entropy when given) */
+typedef struct {
+  float* loss;
+  float* stats;
+  const float* dloss;
+  float* dlogp;
+  float* dentropy;
+} llp_policy_out;
+
+enum { LLP_PREF_SIGMOID = 1, LLP_PREF_HINGE = 2, LLP_PREF_IPO = 3 };
+
+/* Preference loss of P pairs of packed sequences: sequence 2i is pair i's chosen response, 2i + 1
+ * the rejected one (layout.num_seqs = 2 P, cu_seqlens required). For each sequence R = the sum,
+ * or with `average` the mean, of logp - ref_logp over its scored rows (0 when it has none), and
+ * h = R_chosen - R_rejected:
+ *   SIGMOID  (1 - e) softplus(-m) + e softplus(m), m = beta h - gamma, e = label_smoothing
+ *   HINGE    max(0, 1 - m)
+ *   IPO      (h - 1 / (2 beta))^2
+ * loss = sum_i pair_weight_i l_i / P, or without the 1 / P for LLP_REDUCE_SUM.
+ *   logp         fp32 [T];  ref_logp fp32 [T] or NULL
+ *   pair_weight  fp32 [P] or NULL (1). A pair of weight 0 adds nothing whatever its rows hold.
+ *   beta > 0, 0 <= label_smoothing < 1 (0 unless SIGMOID), gamma finite (0 for IPO)
+ *   reduction    LLP_REDUCE_SUM, or LLP_REDUCE_TOKEN_MEAN for the mean over pairs
+ * A pair with a scored row (or a weight) that is not finite sets LLP_STATUS_VALUE_NOT_FINITE,
+ * adds nothing, and its outputs and gradients are 0. A malformed cu_seqlens sets
+ * LLP_STATUS_LAYOUT_INVALID and every output is 0. */
+typedef struct {
+  const float* logp;
+  const float* ref_logp;
+  const float* pair_weight;
+  llp_token_layout layout;
+  double beta;
+  double gamma;
+  double label_smoothing;
+  int32_t kind;
+  int32_t average;
+  int32_t reduction;
+  int32_t reserved;
+  int32_t* status_word;
+} llp_pref_request;
+
+/*   loss                       fp32 [1]
+ *   pair_loss                  fp32 [P] (l_i), or NULL
+ *   chosen, rejected           fp32 [P] (beta R), or NULL
+ *   dloss, dlogp               as in llp_policy_out */
+typedef struct {
+  float* loss;
+  float* pair_loss;
+  float* chosen;
+  float* rejected;
+  const float* dloss;
+  float* dlogp;
+} llp_pref_out;
+
+/* ---- Token embedding -----------------------------------------------------------------------
+ * The input side of a vocabulary-partitioned table (the LM head's own weight in a model that
+ * ties the two): out[t] = scale * weight[id_t - offset], and its gradient, which adds into the
+ * same fp32 dweight that llp_backward writes.
+ *   token_ids    int64 [T]; a row whose token_mask (uint8 [T], or NULL) is 0, or whose id is
+ *                another shard's, gives a row of zeros and no gradient (the caller sums the
+ *                shards); so does an id outside [0, real_vocab), with
+ *                LLP_STATUS_TOKEN_OUT_OF_RANGE.
+ *   weight       [local_size, hidden_size] of weight_dtype (bf16 or fp32); llp_embedding only
+ *   hidden_size  a positive multiple of 8, at most 2^20. Every row operand has a stride in
+ *                elements >= hidden_size that is a multiple of 8, and a 16-byte aligned base.
+ *   num_tokens   0 <= T <= 2^23 - 256; local_size <= 2^23 - 256 (else LLP_ERR_UNSUPPORTED)
+ *   scale        finite */
+typedef struct {
+  const int64_t* token_ids;
+  const uint8_t* token_mask;
+  int64_t num_tokens;
+  llp_vocab_partition vocab;
+  int64_t hidden_size;
+  float scale;
+  uint32_t flags; /* llp_embedding_backward: LLP_FLAG_OVERWRITE_GRADS */
+  int32_t* status_word;
+} llp_embedding_request;
+
 /* Loading phase: checks that `device` is a gfx950 GPU and loads the kernels on it; fills
  * `info` (may be NULL). Returns LLP_ERR_UNAVAILABLE when there is no such device. Must
  * succeed on the current device before any execution call. Idempotent. */
@@ -386,6 +582,40 @@ LLP_API llp_status llp_forward_logits(const llp_logits_request* req, const llp_p
  * ids the results are bitwise those of llp_top_p_replay given the same ids. */
 LLP_API llp_status llp_keep_mask_replay(const llp_keep_mask_request* req,
                                         const llp_partials* out, void* stream);
+
+/* 8-bit quantisation of rows (see llp_quant_request). Needs no workspace. */
+LLP_API llp_status llp_quantize_rows(const llp_quant_request* req, void* stream);
+
+/* llp_forward with the projection in 8-bit integers (see llp_int8_request): the same partials,
+ * checks and guarantees; the workspace size comes from llp_int8_workspace_bytes. */
+LLP_API llp_status llp_int8_workspace_bytes(const llp_int8_request* req, size_t* bytes);
+LLP_API llp_status llp_forward_int8(const llp_int8_request* req, const llp_partials* out,
+                                    void* workspace, size_t workspace_bytes, void* stream);
+
+/* The losses (see llp_policy_request and llp_pref_request): the loss and, where out->dlogp (and
+ * out->dentropy) is given, its gradient. Workspace: device memory, 256-byte aligned. */
+LLP_API llp_status llp_policy_workspace_bytes(const llp_policy_request* req, size_t* bytes);
+LLP_API llp_status llp_policy_loss(const llp_policy_request* req, const llp_policy_out* out,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+LLP_API llp_status llp_preference_workspace_bytes(const llp_pref_request* req, size_t* bytes);
+LLP_API llp_status llp_preference_loss(const llp_pref_request* req, const llp_pref_out* out,
+                                       void* workspace, size_t workspace_bytes, void* stream);
+
+/* Token embedding (see llp_embedding_request): `weight` and `out` share weight_dtype; out is
+ * [T, hidden_size], every row written. Needs no workspace. */
+LLP_API llp_status llp_embedding(const llp_embedding_request* req, const void* weight,
+                                 int32_t weight_dtype, int64_t weight_stride, void* out,
+                                 int64_t out_stride, void* stream);
+
+/* Its gradient: dweight[v] += scale * sum of dout[t] over the rows with token v, in ascending t
+ * within fixed groups of rows (reproducible for a fixed batch). dout [T, hidden_size] of dout_dtype (bf16 or
+ * fp32). dweight fp32 [local_size, hidden_size]: ACCUMULATED, rows no token names untouched;
+ * with LLP_FLAG_OVERWRITE_GRADS every row is written, those rows as 0. */
+LLP_API llp_status llp_embedding_workspace_bytes(const llp_embedding_request* req, size_t* bytes);
+LLP_API llp_status llp_embedding_backward(const llp_embedding_request* req, const void* dout,
+                                          int32_t dout_dtype, int64_t dout_stride, float* dweight,
+                                          int64_t dweight_stride, void* workspace,
+                                          size_t workspace_bytes, void* stream);
 
 /* Message for the calling thread's last non-OK status ("" if none). */
 LLP_API const char* llp_last_error(void);

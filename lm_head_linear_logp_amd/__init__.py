@@ -7,6 +7,11 @@ CPU fallback: if the library is missing or the device is not a gfx950 GPU, calls
 Functions mirror the ABI: ``open``, ``workspace_bytes``, ``forward``, ``merge``, ``backward``,
 ``top_p_replay``, ``last_error``. ``linear_logp`` composes ``forward`` and ``backward`` into
 one autograd node for a full-vocabulary shard.
+
+Around it (ops.py): scoring with a head in 8-bit integers (``quantize_rows``,
+``forward_int8``), the losses on the scored log-probabilities (``policy_grads``,
+``preference_grads``, as autograd nodes ``policy_loss``, ``preference_loss``) and the token
+embedding (``embedding_forward``, ``embedding_backward``, as an autograd node ``embedding``).
 """
 from __future__ import annotations
 
@@ -19,7 +24,9 @@ from . import _capi as A
 
 __all__ = ["LLPError", "open", "workspace_bytes", "forward", "forward_noalloc", "merge",
            "backward", "top_p_replay", "last_error", "STATUS_BITS", "forward_logits",
-           "keep_mask_replay", "SCRATCH_BYTES", "linear_logp"]
+           "keep_mask_replay", "SCRATCH_BYTES", "linear_logp", "quantize_rows", "forward_int8",
+           "policy_grads", "policy_loss", "preference_grads", "preference_loss",
+           "embedding_forward", "embedding_backward", "embedding"]
 
 # Size of the static device scratch llp_forward_noalloc works in (include/llp.h).
 SCRATCH_BYTES = 32 << 20
@@ -27,7 +34,9 @@ SCRATCH_BYTES = 32 << 20
 STATUS_BITS = {"TARGET_OUT_OF_RANGE": A.LLP_STATUS_TARGET_OUT_OF_RANGE,
                "TARGET_NOT_FOUND": A.LLP_STATUS_TARGET_NOT_FOUND,
                "REPLAY_ID_INVALID": A.LLP_STATUS_REPLAY_ID_INVALID,
-               "LAYOUT_INVALID": A.LLP_STATUS_LAYOUT_INVALID}
+               "LAYOUT_INVALID": A.LLP_STATUS_LAYOUT_INVALID,
+               "TOKEN_OUT_OF_RANGE": A.LLP_STATUS_TOKEN_OUT_OF_RANGE,
+               "VALUE_NOT_FINITE": A.LLP_STATUS_VALUE_NOT_FINITE}
 
 
 class LLPError(RuntimeError):
@@ -570,3 +579,7 @@ def linear_logp(hidden: torch.Tensor, weight: torch.Tensor, target_ids: torch.Te
         loss_mask = loss_mask.to(torch.uint8)
     return _LinearLogp.apply(hidden, weight, bias, target_ids, loss_mask, temperature,
                              real_vocab, padded_vocab, want_entropy, g_slabs)
+
+
+from .ops import (embedding, embedding_backward, embedding_forward, forward_int8,  # noqa: E402
+                  policy_grads, policy_loss, preference_grads, preference_loss, quantize_rows)

@@ -17,6 +17,8 @@ LLP_STATUS_TARGET_OUT_OF_RANGE = 1
 LLP_STATUS_TARGET_NOT_FOUND = 2
 LLP_STATUS_REPLAY_ID_INVALID = 4
 LLP_STATUS_LAYOUT_INVALID = 8
+LLP_STATUS_TOKEN_OUT_OF_RANGE = 16
+LLP_STATUS_VALUE_NOT_FINITE = 32
 
 LLP_DTYPE_BF16 = 1
 LLP_DTYPE_F32 = 2
@@ -28,6 +30,12 @@ LLP_FLAG_G_SLABS = 4
 LLP_G_SLAB_COLUMNS = 32768
 LLP_MAX_REPLAY_IDS = 64
 LLP_MAX_WORLD = 64
+LLP_INT8_COLUMNS = 128
+LLP_KL_K1, LLP_KL_K2, LLP_KL_K3 = 1, 2, 3
+LLP_REDUCE_TOKEN_MEAN, LLP_REDUCE_SEQ_MEAN, LLP_REDUCE_SUM = 1, 2, 3
+LLP_LOG_RATIO_MAX = 20
+LLP_POLICY_STATS = 8
+LLP_PREF_SIGMOID, LLP_PREF_HINGE, LLP_PREF_IPO = 1, 2, 3
 
 vp = C.c_void_p
 
@@ -101,6 +109,51 @@ class llp_keep_mask_request(C.Structure):
                 ("status_word", vp)]
 
 
+class llp_quant_request(C.Structure):
+    _fields_ = [("x", vp), ("x_dtype", C.c_int32), ("reserved", C.c_int32),
+                ("x_stride", C.c_int64), ("rows", C.c_int64), ("cols", C.c_int64), ("q", vp),
+                ("q_stride", C.c_int64), ("scale", vp)]
+
+
+class llp_int8_request(C.Structure):
+    _fields_ = [("hidden", vp), ("hidden_stride", C.c_int64), ("hidden_scale", vp),
+                ("weight", vp), ("weight_stride", C.c_int64), ("weight_scale", vp),
+                ("bias", vp), ("bias_dtype", C.c_int32), ("flags", C.c_uint32),
+                ("hidden_size", C.c_int64), ("vocab", llp_vocab_partition),
+                ("layout", llp_token_layout), ("target_ids", vp), ("temperature", C.c_float),
+                ("reserved", C.c_int32), ("status_word", vp)]
+
+
+class llp_policy_request(C.Structure):
+    _fields_ = [("logp", vp), ("old_logp", vp), ("advantages", vp), ("ref_logp", vp),
+                ("entropy", vp), ("layout", llp_token_layout), ("clip_low", C.c_double),
+                ("clip_high", C.c_double), ("dual_clip", C.c_double), ("kl_coef", C.c_double),
+                ("entropy_coef", C.c_double), ("kl_kind", C.c_int32), ("reduction", C.c_int32),
+                ("denominator", vp), ("status_word", vp)]
+
+
+class llp_policy_out(C.Structure):
+    _fields_ = [("loss", vp), ("stats", vp), ("dloss", vp), ("dlogp", vp), ("dentropy", vp)]
+
+
+class llp_pref_request(C.Structure):
+    _fields_ = [("logp", vp), ("ref_logp", vp), ("pair_weight", vp),
+                ("layout", llp_token_layout), ("beta", C.c_double), ("gamma", C.c_double),
+                ("label_smoothing", C.c_double), ("kind", C.c_int32), ("average", C.c_int32),
+                ("reduction", C.c_int32), ("reserved", C.c_int32), ("status_word", vp)]
+
+
+class llp_pref_out(C.Structure):
+    _fields_ = [("loss", vp), ("pair_loss", vp), ("chosen", vp), ("rejected", vp),
+                ("dloss", vp), ("dlogp", vp)]
+
+
+class llp_embedding_request(C.Structure):
+    _fields_ = [("token_ids", vp), ("token_mask", vp), ("num_tokens", C.c_int64),
+                ("vocab", llp_vocab_partition), ("hidden_size", C.c_int64),
+                ("scale", C.c_float), ("flags", C.c_uint32), ("status_word", vp)]
+
+
 SIGNATURES = {
     "llp_open": (C.c_int, [C.c_int32, C.POINTER(llp_info)]),
     "llp_workspace_bytes": (C.c_int, [C.POINTER(llp_request), C.c_int32, C.POINTER(C.c_size_t)]),
@@ -114,6 +167,24 @@ SIGNATURES = {
     "llp_forward_logits": (C.c_int, [C.POINTER(llp_logits_request), C.POINTER(llp_partials), vp]),
     "llp_keep_mask_replay": (C.c_int, [C.POINTER(llp_keep_mask_request), C.POINTER(llp_partials),
                                        vp]),
+    "llp_quantize_rows": (C.c_int, [C.POINTER(llp_quant_request), vp]),
+    "llp_int8_workspace_bytes": (C.c_int, [C.POINTER(llp_int8_request), C.POINTER(C.c_size_t)]),
+    "llp_forward_int8": (C.c_int, [C.POINTER(llp_int8_request), C.POINTER(llp_partials), vp,
+                                   C.c_size_t, vp]),
+    "llp_policy_workspace_bytes": (C.c_int, [C.POINTER(llp_policy_request),
+                                             C.POINTER(C.c_size_t)]),
+    "llp_policy_loss": (C.c_int, [C.POINTER(llp_policy_request), C.POINTER(llp_policy_out), vp,
+                                  C.c_size_t, vp]),
+    "llp_preference_workspace_bytes": (C.c_int, [C.POINTER(llp_pref_request),
+                                                 C.POINTER(C.c_size_t)]),
+    "llp_preference_loss": (C.c_int, [C.POINTER(llp_pref_request), C.POINTER(llp_pref_out), vp,
+                                      C.c_size_t, vp]),
+    "llp_embedding": (C.c_int, [C.POINTER(llp_embedding_request), vp, C.c_int32, C.c_int64, vp,
+                                C.c_int64, vp]),
+    "llp_embedding_workspace_bytes": (C.c_int, [C.POINTER(llp_embedding_request),
+                                                C.POINTER(C.c_size_t)]),
+    "llp_embedding_backward": (C.c_int, [C.POINTER(llp_embedding_request), vp, C.c_int32,
+                                         C.c_int64, vp, C.c_int64, vp, C.c_size_t, vp]),
     "llp_last_error": (C.c_char_p, []),
 }
 

@@ -15,7 +15,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libllp.so")
-SOURCES = ["llp_api.cpp", "llp_kernels.hip"]
+SOURCES = ["llp_api.cpp", "llp_api_ops.cpp", "llp_kernels.hip", "llp_int8.hip", "llp_losses.hip",
+           "llp_embedding.hip"]
 ARCH = "gfx950"
 
 

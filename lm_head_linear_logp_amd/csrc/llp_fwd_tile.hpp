@@ -1,5 +1,6 @@
 // llp_fwd_tile.hpp -- what the fused forward's kernels share: the operands' loaders, the bias
-// as starting accumulators, and the tile epilogue (max, sum-exp, entropy sum, target logit).
+// as starting accumulators, the tile epilogue (max, sum-exp, entropy sum, target logit), and the
+// two ways a launch walks its tiles.
 #pragma once
 
 #include "llp_internal.h"
@@ -243,6 +244,97 @@ __device__ __forceinline__ void fwd_tile_epilogue(const f32x16 (&acc)[4][NFB], c
   const int v0 = vt * BM, j0 = tb * BN;
   if (v0 + BM > a.n_real) fwd_epilogue<true, NFB>(acc, a, vt, v0, j0, Ts, red);
   else fwd_epilogue<false, NFB>(acc, a, vt, v0, j0, Ts, red);
+}
+
+// The forward GEMM as persistent workers (the host launches one per compute unit, a multiple
+// of NUM_XCD, when the K steps are even). XCD x owns a contiguous share of the logical tiles
+// (its queue, as for the backward kernels). Worker wi of the XCD runs positions wi, wi + nwx,
+// ... of the queue's static first three quarters, in the order one workgroup per tile would
+// start them, then claims tiles of the dynamic last quarter one at a time (own XCD first, then
+// the others'), so that workers of a faster XCD take over the tail of a slower one. Against
+// one workgroup per tile this saves each tile's launch, address setup and first DMA round
+// trip: the last two K steps of a tile load the first two of the worker's next tile, which
+// land during the epilogue. Tiles past the scored rows are skipped. A tile's arithmetic is
+// that of fwd_one_tile, whoever runs it: results are bitwise the same.
+// `init` sets the starting accumulators of tile (vt, tb), `epilogue` takes the finished ones;
+// their type (f32x16 or i32x16) picks bf16 or int8 products.
+template <int NW, class ACC, class Init, class Epilogue>
+__device__ __forceinline__ void fwd_persistent(const FwdArgs& a, uint16_t* smem, Init init,
+                                               Epilogue epilogue) {
+  constexpr int NFB = 16 / NW;
+  float* const red = reinterpret_cast<float*>(smem + dma::LDS_BYTES / 2);
+  int* const slot = reinterpret_cast<int*>(red + 6 * 256);
+  const int Ts = *a.count;
+  const int ntiles = a.nvt * a.ntb;
+  const int x = blockIdx.x % NUM_XCD, nwx = gridDim.x / NUM_XCD;
+  const int qf = queue_first(ntiles, x), s0 = queue_static(queue_size(ntiles, x));
+  int pos = blockIdx.x / NUM_XCD;   // the worker's next static position
+  // The worker's next tile with scored rows: false when there is none.
+  auto next_tile = [&](int& vt, int& tb) -> bool {
+    for (;;) {
+      int t;
+      if (pos < s0) {
+        t = qf + pos;
+        pos += nwx;
+      } else {
+        if (threadIdx.x == 0) *slot = claim_dynamic(a.qctr, ntiles, x);
+        dma::lds_barrier();
+        t = *slot;
+        dma::lds_barrier();   // every wave has read the slot before the next claim writes it
+        if (t < 0) return false;
+      }
+      vocab_token_tile(t, a.nvt, a.ntb, vt, tb);
+      if (tb * BN < Ts) return true;
+    }
+  };
+  int vt = 0, tb = 0;
+  if (!next_tile(vt, tb)) return;
+  const int n = a.H / dma::BKD;
+  dma::LoaderT<NW> la, lb, la2, lb2;
+  weight_hidden_loaders<NW>(a.W, a.ldw, a.n_real, vt * BM, a.h, a.ldh, a.scored, tb * BN, Ts,
+                            a.H, la, lb);
+  bool primed = false;
+  for (;;) {
+    int vt2 = 0, tb2 = 0;
+    const bool more = next_tile(vt2, tb2);
+    if (more) {
+      weight_hidden_loaders<NW>(a.W, a.ldw, a.n_real, vt2 * BM, a.h, a.ldh, a.scored, tb2 * BN,
+                                Ts, a.H, la2, lb2);
+    } else {
+      la2 = la;
+      lb2 = lb;
+    }
+    ACC acc[4][NFB];
+    init(acc, vt, tb, Ts);
+    dma::mainloop_chain(la, lb, la2, lb2, primed, more, n, smem, acc);
+    epilogue(acc, vt, tb, Ts, red);
+    if (!more) break;
+    vt = vt2;
+    tb = tb2;
+    la = la2;
+    lb = lb2;
+    primed = true;
+  }
+}
+
+// One workgroup per tile in the static XCD order: the forward for an odd number of K steps,
+// where the persistent workers' stage parity does not carry from one tile to the next.
+template <int NW, class ACC, class Init, class Epilogue>
+__device__ __forceinline__ void fwd_one_tile(const FwdArgs& a, uint16_t* smem, Init init,
+                                             Epilogue epilogue) {
+  constexpr int NFB = 16 / NW;
+  float* const red = reinterpret_cast<float*>(smem + dma::LDS_BYTES / 2);
+  int vt, tb;
+  vocab_token_tile(xcd_remap(blockIdx.x, gridDim.x), a.nvt, a.ntb, vt, tb);
+  const int Ts = *a.count;
+  if (tb * BN >= Ts) return;
+  dma::LoaderT<NW> la, lb;
+  weight_hidden_loaders<NW>(a.W, a.ldw, a.n_real, vt * BM, a.h, a.ldh, a.scored, tb * BN, Ts,
+                            a.H, la, lb);
+  ACC acc[4][NFB];
+  init(acc, vt, tb, Ts);
+  dma::mainloop(la, lb, 0, a.H / dma::BKD, smem, acc);
+  epilogue(acc, vt, tb, Ts, red);
 }
 
 }  // namespace llp

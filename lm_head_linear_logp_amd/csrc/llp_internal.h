@@ -255,6 +255,120 @@ struct DbArgs {
   int32_t overwrite;  // 1: db = the sum; 0: db += the sum
 };
 
+struct QuantArgs {
+  const void* x;
+  int32_t bf16;
+  int64_t ldx;
+  int64_t rows;
+  int32_t cols, colsp;  // columns, and rounded up to LLP_INT8_COLUMNS
+  int8_t* q;
+  int64_t ldq;
+  float* scale;
+};
+
+// The fused forward on int8 operands: `f` holds the rows as 16-bit elements (W, ldw, h, ldh and H
+// count pairs of columns).
+struct Fwd8Args {
+  FwdArgs f;
+  const float* hs;  // [T] scale of each hidden row
+  const float* ws;  // [local vocabulary] scale of each weight row
+};
+
+struct EmbArgs {
+  const int64_t* ids;
+  const uint8_t* mask;
+  int64_t T;
+  int64_t offset, n_real, real_vocab;
+  int32_t H;
+  float scale;
+  const void* W;
+  int32_t bf16;
+  int64_t ldw;
+  void* out;
+  int64_t ldo;
+  int32_t* status;
+};
+
+// Embedding gradient: rows are sorted by token in groups of EMB_ROWS_MAX local ids at most, and
+// summed in units of EMB_UNIT consecutive sorted rows.
+constexpr int EMB_ROWS_MAX = 2048;
+constexpr int EMB_UNIT = 32;
+struct EmbBwdArgs {
+  const int64_t* ids;
+  const uint8_t* mask;
+  int64_t T;
+  int64_t offset, n_real, real_vocab, local_size;
+  int32_t H;
+  int32_t rows_per_group;
+  float scale;
+  int32_t overwrite;
+  const void* dout;
+  int32_t bf16;
+  int64_t ldo;
+  float* dW;
+  int64_t ldw;
+  int32_t* start;   // [n_real + 1] first sorted position of each local row
+  int32_t* order;   // [T] sorted position -> row of dout
+  int32_t* row;     // [T] sorted position -> local row
+  float* part;      // [units][2][H] sums of a unit's first and last segment (rows shared by units)
+  int32_t* status;
+};
+
+struct PolicyArgs {
+  int64_t T;
+  const float* logp;
+  const float* old;
+  const float* adv;
+  const float* ref;
+  const float* ent;
+  const uint8_t* mask;
+  const int32_t* cu;
+  int32_t S;
+  double log_lo, log_hi, log_dual;     // borders of d = logp - old_logp
+  float lo, hi, dual;                  // the clipped ratios
+  float klc, entc;
+  int32_t kl_kind, reduction;
+  const float* denom;
+  int32_t nblocks;                     // blocks of the loss kernel
+  int32_t ncount;                      // blocks of the count kernel (0: nothing to count)
+  int32_t* count;                      // [ncount] scored rows, or [S] for SEQ_MEAN
+  int32_t* meta;                       // [2] sequences with scored rows, malformed cu_seqlens
+  double* part;                        // [nblocks][LLP_POLICY_STATS]
+  float* loss;
+  float* stats;
+  const float* dloss;
+  float* dlogp;
+  float* dent;
+  double klc64, entc64;
+  int32_t* status;
+};
+
+// Workgroups that share one sequence's sum of a preference loss (fixed: the sum's order depends on
+// the sequence alone).
+constexpr int PREF_SPLIT = 4;
+constexpr int PREF_CHUNK = 4096;
+struct PrefArgs {
+  int64_t T;
+  const float* logp;
+  const float* ref;
+  const float* weight;
+  const uint8_t* mask;
+  const int32_t* cu;
+  int32_t P;
+  double beta, gamma, smooth;
+  int32_t kind, average, mean;
+  double* sum;       // [2 P][PREF_SPLIT]
+  int32_t* cnt;      // [2 P][PREF_SPLIT], scored rows; -1 when one of them is not finite
+  float* coef;       // [2 P] d loss / d logp of a scored row of the sequence
+  float* loss;
+  float* pair_loss;
+  float* chosen;
+  float* rejected;
+  const float* dloss;
+  float* dlogp;
+  int32_t* status;
+};
+
 hipError_t launch_layout(const LayoutArgs& a, hipStream_t s);
 hipError_t launch_fwd(const FwdArgs& a, hipStream_t s);
 hipError_t launch_combine(const CombineArgs& a, int64_t T_cap, hipStream_t s);
@@ -269,6 +383,13 @@ hipError_t launch_dbias(const DbArgs& a, hipStream_t s);
 hipError_t launch_zero_rows(const ZeroArgs& a, hipStream_t s);
 hipError_t launch_logits(const LogitsArgs& a, hipStream_t s);
 hipError_t launch_keep(const KeepArgs& a, hipStream_t s);
+hipError_t launch_quant(const QuantArgs& a, hipStream_t s);
+hipError_t launch_fwd8(const Fwd8Args& a, hipStream_t s);
+hipError_t launch_embedding(const EmbArgs& a, hipStream_t s);
+hipError_t launch_embedding_sort(const EmbBwdArgs& a, hipStream_t s);
+hipError_t launch_embedding_sum(const EmbBwdArgs& a, hipStream_t s);
+hipError_t launch_policy(const PolicyArgs& a, hipStream_t s);
+hipError_t launch_preference(const PrefArgs& a, hipStream_t s);
 hipError_t probe_kernels();
 // Looks up this device's copy of the static scratch (the current device must be `device`);
 // idempotent. Called under the library's open lock.
