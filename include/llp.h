@@ -334,9 +334,9 @@ typedef struct {
  *          stride q_stride bytes (>= cols_padded, multiple of 16), 16-byte aligned base.
  *          Columns cols .. cols_padded - 1 are written as 0.
  *   scale  fp32 [rows].
- * With a = max_k |x[r][k]|: scale[r] = max(a, 1e-30) / 127 and q[r][k] = x[r][k] / scale[r]
- * rounded to the nearest integer, ties to even (both divisions in fp32, correctly rounded). A
- * row of zeros gives q = 0. A row holding an infinity or NaN gives q = 0 and scale = NaN. */
+ * With a = max_k |x[r][k]|: scale[r] = max(a, 1e-30) * fl32(1/127) and q[r][k] = x[r][k] /
+ * scale[r] (fp32, correctly rounded) to the nearest integer, ties to even. A row of zeros
+ * gives q = 0. A row holding an infinity or NaN gives q = 0 and scale = NaN. */
 typedef struct {
   const void* x;
   int32_t x_dtype;

@@ -224,16 +224,18 @@ llp_status check_rows(const char* name, const void* p, int32_t dtype, int64_t st
 }
 
 struct EmbWs {
-  size_t start, order, row, part, total;
+  size_t loc, start, order, row, span, part, total;
 };
 
 EmbWs embedding_ws(const llp_embedding_request& r) {
   EmbWs w{};
   Regions g;
   const int64_t T = r.num_tokens, units = (T + EMB_UNIT - 1) / EMB_UNIT;
+  w.loc = g.take((size_t)T * 4);
   w.start = g.take((size_t)(local_real(r.vocab) + 1) * 4);
   w.order = g.take((size_t)T * 4);
   w.row = g.take((size_t)T * 4);
+  w.span = g.take((size_t)units * 4);
   w.part = g.take((size_t)units * 2 * (size_t)r.hidden_size * 4);
   w.total = g.off;
   return w;
@@ -316,6 +318,7 @@ LLP_API llp_status llp_forward_int8(const llp_int8_request* req, const llp_parti
     a.f = fa;
     a.hs = req->hidden_scale;
     a.ws = req->weight_scale;
+    a.rows = T;
     return launch_fwd8(a, s);
   });
 }
@@ -499,9 +502,11 @@ LLP_API llp_status llp_embedding_backward(const llp_embedding_request* req, cons
   a.ldo = dout_stride;
   a.dW = dweight;
   a.ldw = dweight_stride;
+  a.loc = at<int32_t>(workspace, w.loc);
   a.start = at<int32_t>(workspace, w.start);
   a.order = at<int32_t>(workspace, w.order);
   a.row = at<int32_t>(workspace, w.row);
+  a.span = at<int32_t>(workspace, w.span);
   a.part = at<float>(workspace, w.part);
   a.status = req->status_word;
   hipStream_t s = static_cast<hipStream_t>(stream);

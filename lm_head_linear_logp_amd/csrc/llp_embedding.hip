@@ -86,58 +86,103 @@ hipError_t launch_embedding(const EmbArgs& a, hipStream_t s) {
 }
 
 // ------------------------------------------------------------------------------------
-// Gradient, first launch: a stable counting sort of the rows by token. Workgroup g owns the local
-// rows [g R, (g + 1) R), at most EMB_ROWS_MAX of them, and reads every token id twice: each of
-// its 16 waves counts its own contiguous part of the tokens into LDS counters of its own, a
-// scan over (row, wave) turns them into positions, and the second pass hands out the positions
-// in token order (lanes with the same row are ranked by ballot). The tokens of lower rows,
-// counted in the first pass, give the group's first position, so no group waits for another.
-// No atomic decides an order: the counters only count. Reading the ids once per group costs
-// 2 x 9 bytes x groups per token from L2, against 2 H bytes of its gradient row from memory.
+// Gradient. Launches: k_embed_ids (ids to int32 local rows), k_embed_sort (a stable counting sort
+// of the rows by token), k_embed_sum (the sums, and the rows without a token), k_embed_fix (the
+// sums of tokens that several units share).
+//
+// The sort: workgroup g owns the local rows [g R, (g + 1) R), at most EMB_ROWS_MAX of them, and
+// reads every token's local row. Each of its 16 waves counts its own contiguous part of the
+// tokens into LDS counters of its own and keeps the ones it found in an LDS list; a scan over
+// (row, wave) turns the counters into positions; then the list (and, past its end, the tokens
+// again) is walked in order to hand them out, lanes with the same row ranked by ballot. The
+// tokens of lower rows, counted on the way, give the group's first position, so no group waits
+// for another. No atomic decides an order: the counters only count. Every group reads 4 bytes
+// per token from L2, a kilobyte per token in all, against 2 H bytes of its gradient row from
+// memory; read as the caller's int64 ids, twice, it was bound by the vector ALUs (64.6 us at
+// 56583 tokens).
 // ------------------------------------------------------------------------------------
-constexpr int SORT_WAVES = 16, SORT_UNROLL = 8;
+__global__ __launch_bounds__(256) void k_embed_ids(EmbBwdArgs a) {
+  const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (t >= a.T) return;
+  int status = 0;
+  a.loc[t] = emb_local(a, t, status);
+  if (status && a.status) atomicOr(a.status, status);
+}
+
+constexpr int SORT_WAVES = 16, SORT_UNROLL = 8, SORT_LIST = 256;
+
+// Hands out positions, in lane order, to the lanes with `in` (local row r of the group, token t).
+__device__ __forceinline__ void sort_place(const EmbBwdArgs& a, volatile int* next, int lo, bool in,
+                                           int r, int t, int lane) {
+  uint64_t left = __builtin_amdgcn_ballot_w64(in);
+  while (left != 0) {
+    const int leader = __builtin_ctzll(left);
+    const int rr = __builtin_amdgcn_readlane(r, leader);
+    const uint64_t same = __builtin_amdgcn_ballot_w64(in && r == rr);
+    const int first = next[rr];
+    if (in && r == rr) {
+      const int pos = first + __popcll(same & ((1ull << lane) - 1));
+      a.order[pos] = t;
+      a.row[pos] = lo + rr;
+    }
+    __builtin_amdgcn_wave_barrier();
+    if (lane == leader) next[rr] = first + __popcll(same);
+    __builtin_amdgcn_wave_barrier();
+    left &= ~same;
+  }
+}
 
 __global__ __launch_bounds__(64 * SORT_WAVES) void k_embed_sort(EmbBwdArgs a) {
   __shared__ int cnt[SORT_WAVES * EMB_ROWS_MAX];   // [wave][row]
+  __shared__ int2 list[SORT_WAVES][SORT_LIST];     // token, row
   __shared__ int wtot[SORT_WAVES], wbelow[SORT_WAVES];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int R = a.rows_per_group;
-  const int64_t lo64 = (int64_t)blockIdx.x * R;
-  const int lo = (int)lo64;
-  const int nr = (int)(a.n_real - lo64 < R ? a.n_real - lo64 : R);
-  const int64_t part = (((a.T + SORT_WAVES - 1) / SORT_WAVES) + 63) / 64 * 64;
-  const int64_t tb = w * part, te = tb + part < a.T ? tb + part : a.T;
+  const int R = a.rows_per_group, T = (int)a.T;
+  const int lo = (int)(blockIdx.x * (int64_t)R);
+  const int nr = (int)(a.n_real - lo < R ? a.n_real - lo : R);
+  const int part = ((T + SORT_WAVES - 1) / SORT_WAVES + 63) / 64 * 64;
+  const int tb = w * part < T ? w * part : T, te = tb + part < T ? tb + part : T;
   int* const mine = cnt + w * R;
   for (int i = lane; i < nr; i += 64) mine[i] = 0;
   __builtin_amdgcn_wave_barrier();
-  int below = 0, status = 0;
-  for (int64_t t0 = tb; t0 < te; t0 += 64 * SORT_UNROLL) {
+  int below = 0, found = 0, resume = te;   // resume: the tokens from here on are not in the list
+  for (int t0 = tb; t0 < te; t0 += 64 * SORT_UNROLL) {
     int loc[SORT_UNROLL];
 #pragma unroll
     for (int u = 0; u < SORT_UNROLL; ++u) {
-      const int64_t t = t0 + u * 64 + lane;
-      loc[u] = t < te ? emb_local(a, t, status) : -1;
+      const int t = t0 + u * 64 + lane;
+      loc[u] = t < te ? a.loc[t] : -1;
     }
 #pragma unroll
     for (int u = 0; u < SORT_UNROLL; ++u) {
-      const int r = loc[u] - lo;
-      below += loc[u] >= 0 && r < 0 ? 1 : 0;
-      if (loc[u] >= 0 && r >= 0 && r < nr) atomicAdd(mine + r, 1);
+      // Unsigned, -1 is past every row.
+      below += (uint32_t)loc[u] < (uint32_t)lo ? 1 : 0;
+      const uint32_t r = (uint32_t)loc[u] - (uint32_t)lo;
+      const bool in = loc[u] >= 0 && r < (uint32_t)nr;
+      const uint64_t hits = __builtin_amdgcn_ballot_w64(in);
+      if (hits != 0) {
+        if (in) atomicAdd(mine + r, 1);
+        const int n = __popcll(hits);
+        if (resume == te && found + n <= SORT_LIST) {
+          if (in) list[w][found + __popcll(hits & ((1ull << lane) - 1))] = make_int2(t0 + u * 64 + lane, (int)r);
+          found += n;
+        } else if (resume == te) {
+          resume = t0 + u * 64;
+        }
+      }
     }
   }
-  if (blockIdx.x == 0 && status && a.status) atomicOr(a.status, status);
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) below += __shfl_xor(below, off);
   if (lane == 0) wbelow[w] = below;
   __syncthreads();
-  // Exclusive scan of the rows' totals; thread i takes rows 2i and 2i + 1.
-  const int r0 = 2 * threadIdx.x;
-  int tot[2] = {0, 0};
-#pragma unroll
-  for (int k = 0; k < 2; ++k)
-    if (r0 + k < nr)
-      for (int v = 0; v < SORT_WAVES; ++v) tot[k] += cnt[v * R + r0 + k];
-  int incl = tot[0] + tot[1];
+  // Exclusive scan of the rows' totals, one row per thread.
+  static_assert(EMB_ROWS_MAX <= 64 * SORT_WAVES, "one row per thread");
+  const int r = threadIdx.x;
+  int tot = 0;
+  if (r < nr)
+    for (int v = 0; v < SORT_WAVES; ++v) tot += cnt[v * R + r];
+  int incl = tot;
 #pragma unroll
   for (int off = 1; off < 64; off <<= 1) {
     const int o = __shfl_up(incl, off);
@@ -145,71 +190,53 @@ __global__ __launch_bounds__(64 * SORT_WAVES) void k_embed_sort(EmbBwdArgs a) {
   }
   if (lane == 63) wtot[w] = incl;
   __syncthreads();
-  int run = incl - tot[0] - tot[1];
+  int run = incl - tot;
   for (int v = 0; v < SORT_WAVES; ++v) {
     run += wbelow[v];
     if (v < w) run += wtot[v];
   }
-#pragma unroll
-  for (int k = 0; k < 2; ++k)
-    if (r0 + k < nr) {
-      a.start[lo + r0 + k] = run;
-      for (int v = 0; v < SORT_WAVES; ++v) {
-        const int c = cnt[v * R + r0 + k];
-        cnt[v * R + r0 + k] = run;
-        run += c;
-      }
-      if (lo + r0 + k == a.n_real - 1) a.start[a.n_real] = run;
+  if (r < nr) {
+    a.start[lo + r] = run;
+    for (int v = 0; v < SORT_WAVES; ++v) {
+      const int c = cnt[v * R + r];
+      cnt[v * R + r] = run;
+      run += c;
     }
+    if (lo + r == a.n_real - 1) a.start[a.n_real] = run;
+  }
   __syncthreads();
-  volatile int* const next = mine;
-  for (int64_t t0 = tb; t0 < te; t0 += 64 * SORT_UNROLL) {
-    int loc[SORT_UNROLL];
-#pragma unroll
-    for (int u = 0; u < SORT_UNROLL; ++u) {
-      const int64_t t = t0 + u * 64 + lane;
-      loc[u] = t < te ? emb_local(a, t, status) : -1;
-    }
-#pragma unroll
-    for (int u = 0; u < SORT_UNROLL; ++u) {
-      const int r = loc[u] >= 0 ? loc[u] - lo : -1;
-      const bool in = r >= 0 && r < nr;
-      uint64_t left = __builtin_amdgcn_ballot_w64(in);
-      while (left != 0) {
-        const int leader = __builtin_ctzll(left);
-        const int rr = __builtin_amdgcn_readlane(r, leader);
-        const uint64_t same = __builtin_amdgcn_ballot_w64(in && r == rr);
-        const int first = next[rr];
-        if (in && r == rr) {
-          const int pos = first + __popcll(same & ((1ull << lane) - 1));
-          a.order[pos] = (int)(t0 + u * 64 + lane);
-          a.row[pos] = lo + rr;
-        }
-        __builtin_amdgcn_wave_barrier();
-        if (lane == leader) next[rr] = first + __popcll(same);
-        __builtin_amdgcn_wave_barrier();
-        left &= ~same;
-      }
-    }
+  for (int i = 0; i < found; i += 64) {
+    const bool in = i + lane < found;
+    const int2 e = in ? list[w][i + lane] : make_int2(0, 0);
+    sort_place(a, mine, lo, in, e.y, e.x, lane);
+  }
+  for (int t0 = resume; t0 < te; t0 += 64) {
+    const int t = t0 + lane;
+    const int loc = t < te ? a.loc[t] : -1;
+    const uint32_t q = (uint32_t)loc - (uint32_t)lo;
+    sort_place(a, mine, lo, loc >= 0 && q < (uint32_t)nr, (int)q, t, lane);
   }
 }
 
 hipError_t launch_embedding_sort(const EmbBwdArgs& a, hipStream_t s) {
-  // A shard without real rows still reports ids out of range (one group with no rows).
-  const int64_t groups = a.n_real > 0 ? (a.n_real + a.rows_per_group - 1) / a.rows_per_group : 1;
-  if (a.T > 0)
-    hipLaunchKernelGGL(k_embed_sort, dim3((unsigned)groups), dim3(64 * SORT_WAVES), 0, s, a);
+  if (a.T <= 0) return hipGetLastError();
+  hipLaunchKernelGGL(k_embed_ids, dim3((unsigned)((a.T + 255) / 256)), dim3(256), 0, s, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.n_real <= 0) return e;
+  const int64_t groups = (a.n_real + a.rows_per_group - 1) / a.rows_per_group;
+  hipLaunchKernelGGL(k_embed_sort, dim3((unsigned)groups), dim3(64 * SORT_WAVES), 0, s, a);
   return hipGetLastError();
 }
 
 // ------------------------------------------------------------------------------------
-// Second launch: the sorted rows are cut into units of EMB_UNIT, whatever tokens they hold, so a
-// token that fills half the batch costs no more than any other. A unit adds up its rows in
-// order, 8 columns per thread in fp32, and writes each token's sum when the token changes; the
-// sums of a token whose rows reach into another unit go to `part` (slot 0: it began in an earlier
-// unit; slot 1: it begins here) and the third launch adds those up in unit order. Behind the
-// units, when the gradient is overwritten, workgroups write the rows that no token names as 0.
-// Bound by memory: one read of dout, one write (or read and write) of the touched rows.
+// The sums: the sorted rows are cut into units of EMB_UNIT, whatever tokens they hold, so a token
+// that fills half the batch costs no more than any other. A unit adds up its rows in order, 8
+// columns per thread in fp32, and writes each token's sum when the token changes; the sums of a
+// token whose rows reach into another unit go to `part` (slot 0: it began in an earlier unit;
+// slot 1: it begins here), and the unit where such a token begins notes in `span` how many units
+// follow. Behind the units, when the gradient is overwritten, workgroups write the rows that no
+// token names as 0. Bound by memory: one read of dout, one write (or read and write) of the
+// touched rows.
 // ------------------------------------------------------------------------------------
 constexpr int EMB_ZERO_ROWS = 16;
 
@@ -249,26 +276,44 @@ __device__ __forceinline__ void emb_finish(const EmbBwdArgs& a, int row, int c, 
   emb_store8(p, v);
 }
 
+// Rows v0 .. v0 + EMB_ZERO_ROWS - 1 without a token become 0: whole cache lines per wave and store.
+// (The workgroups of one v0 share the columns.)
+__device__ __forceinline__ void emb_zero(const EmbBwdArgs& a, int64_t v0) {
+  const int lane = threadIdx.x & 63;
+  const int64_t mine = v0 + lane;
+  bool empty = lane < EMB_ZERO_ROWS && mine < a.local_size;
+  if (empty && mine < a.n_real && a.T > 0) empty = a.start[mine + 1] == a.start[mine];
+  uint64_t rows = __builtin_amdgcn_ballot_w64(empty);
+  while (rows != 0) {
+    const int i = __builtin_ctzll(rows);
+    rows &= rows - 1;
+    float* p = a.dW + (v0 + i) * a.ldw;
+    for (int c = (blockIdx.y * blockDim.x + threadIdx.x) * 4; c < a.H; c += gridDim.y * blockDim.x * 4)
+      *reinterpret_cast<float4*>(p + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+}
+
 template <bool BF16>
 __global__ __launch_bounds__(256) void k_embed_sum(EmbBwdArgs a, int units) {
-  const int c = ((int)blockIdx.y * (int)blockDim.x + (int)threadIdx.x) * 8;
   if ((int)blockIdx.x >= units) {
-    // Rows without a token (and padding rows) become 0.
-    if (c >= a.H) return;
-    const int64_t v0 = ((int64_t)blockIdx.x - units) * EMB_ZERO_ROWS;
-    for (int64_t v = v0; v < v0 + EMB_ZERO_ROWS && v < a.local_size; ++v) {
-      if (v < a.n_real && a.T > 0 && a.start[v + 1] != a.start[v]) continue;
-      const float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      emb_store8(a.dW + v * a.ldw + c, z);
-    }
+    emb_zero(a, ((int64_t)blockIdx.x - units) * EMB_ZERO_ROWS);
     return;
   }
+  const int c = ((int)blockIdx.y * (int)blockDim.x + (int)threadIdx.x) * 8;
   const int N = a.start[a.n_real];
   const int u = blockIdx.x, s0 = u * EMB_UNIT;
-  if (s0 >= N || c >= a.H) return;
   const int s1 = s0 + EMB_UNIT < N ? s0 + EMB_UNIT : N;
-  const bool began = s0 > 0 && a.row[s0 - 1] == a.row[s0];
-  const bool goes_on = s1 < N && a.row[s1 - 1] == a.row[s1];
+  const bool began = s0 < N && s0 > 0 && a.row[s0 - 1] == a.row[s0];
+  const bool goes_on = s0 < N && s1 < N && a.row[s1 - 1] == a.row[s1];
+  if (blockIdx.y == 0 && threadIdx.x == 0) {
+    int n = 0;
+    if (goes_on) {
+      const int r = a.row[s1];
+      if (a.start[r] >= s0) n = (a.start[r + 1] - 1) / EMB_UNIT - u;
+    }
+    a.span[u] = n;
+  }
+  if (s0 >= N || c >= a.H) return;
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   bool first = true;
   constexpr int B = BF16 ? 8 : 4;   // rows in flight
@@ -298,41 +343,45 @@ __global__ __launch_bounds__(256) void k_embed_sum(EmbBwdArgs a, int units) {
   }
 }
 
-// Third launch: the workgroup of the unit where a token shared by several units begins adds its
-// partial sums: 8 waves take consecutive eighths of the units, then their sums are added in order.
-constexpr int FIX_WAVES = 8;
+// Tokens shared by several units: a workgroup looks through FIX_UNITS units and, where such a
+// token begins, adds its partial sums: 8 waves take consecutive eighths of the units, then their
+// sums are added in order.
+constexpr int FIX_WAVES = 8, FIX_UNITS = 4;
 
-__global__ __launch_bounds__(64 * FIX_WAVES) void k_embed_fix(EmbBwdArgs a) {
+__global__ __launch_bounds__(64 * FIX_WAVES) void k_embed_fix(EmbBwdArgs a, int units) {
   __shared__ float sh[FIX_WAVES][64][8];
-  const int N = a.start[a.n_real];
-  const int u = blockIdx.x, s0 = u * EMB_UNIT, s1 = s0 + EMB_UNIT;
-  if (s1 >= N) return;
-  const int r = a.row[s1];
-  if (a.row[s1 - 1] != r || a.start[r] < s0) return;
-  const int last = (a.start[r + 1] - 1) / EMB_UNIT;
-  const int n = last - u;   // units after this one
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int c = (blockIdx.y * 64 + lane) * 8;
-  const int b = u + 1 + (int)((int64_t)n * w / FIX_WAVES), e = u + 1 + (int)((int64_t)n * (w + 1) / FIX_WAVES);
-  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (c < a.H) {
-    if (w == 0) emb_load8<false>(a.part, ((int64_t)u * 2 + 1) * a.H + c, acc);
+  const int u0 = blockIdx.x * FIX_UNITS;
+  const int span = lane < FIX_UNITS && u0 + lane < units ? a.span[u0 + lane] : 0;
+  uint64_t begins = __builtin_amdgcn_ballot_w64(span > 0);
+  while (begins != 0) {
+    const int i = __builtin_ctzll(begins);
+    begins &= begins - 1;
+    const int u = u0 + i, n = __builtin_amdgcn_readlane(span, i);   // n units after this one
+    const int b = u + 1 + (int)((int64_t)n * w / FIX_WAVES), e = u + 1 + (int)((int64_t)n * (w + 1) / FIX_WAVES);
+    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (c < a.H) {
+      if (w == 0) emb_load8<false>(a.part, ((int64_t)u * 2 + 1) * a.H + c, acc);
 #pragma unroll 4
-    for (int k = b; k < e; ++k) {
-      float v[8];
-      emb_load8<false>(a.part, (int64_t)k * 2 * a.H + c, v);
+      for (int k = b; k < e; ++k) {
+        float v[8];
+        emb_load8<false>(a.part, (int64_t)k * 2 * a.H + c, v);
 #pragma unroll
-      for (int x = 0; x < 8; ++x) acc[x] += v[x];
+        for (int x = 0; x < 8; ++x) acc[x] += v[x];
+      }
     }
+#pragma unroll
+    for (int x = 0; x < 8; ++x) sh[w][lane][x] = acc[x];
+    __syncthreads();
+    if (w == 0 && c < a.H) {
+      for (int k = 1; k < FIX_WAVES; ++k)
+#pragma unroll
+        for (int x = 0; x < 8; ++x) acc[x] += sh[k][lane][x];
+      emb_finish(a, a.row[u * EMB_UNIT + EMB_UNIT], c, acc);
+    }
+    __syncthreads();
   }
-#pragma unroll
-  for (int x = 0; x < 8; ++x) sh[w][lane][x] = acc[x];
-  __syncthreads();
-  if (w != 0 || c >= a.H) return;
-  for (int k = 1; k < FIX_WAVES; ++k)
-#pragma unroll
-    for (int x = 0; x < 8; ++x) acc[x] += sh[k][lane][x];
-  emb_finish(a, r, c, acc);
 }
 
 hipError_t launch_embedding_sum(const EmbBwdArgs& a, hipStream_t s) {
@@ -345,8 +394,8 @@ hipError_t launch_embedding_sum(const EmbBwdArgs& a, hipStream_t s) {
   else hipLaunchKernelGGL(k_embed_sum<false>, grid, dim3(threads), 0, s, a, units);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || units <= 1) return e;
-  hipLaunchKernelGGL(k_embed_fix, dim3((unsigned)units - 1, (unsigned)((a.H / 8 + 63) / 64)),
-                     dim3(64 * FIX_WAVES), 0, s, a);
+  hipLaunchKernelGGL(k_embed_fix, dim3((unsigned)((units + FIX_UNITS - 1) / FIX_UNITS), (unsigned)((a.H / 8 + 63) / 64)),
+                     dim3(64 * FIX_WAVES), 0, s, a, units);
   return hipGetLastError();
 }
 

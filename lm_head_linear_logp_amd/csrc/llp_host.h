@@ -122,6 +122,7 @@ llp_status run_forward(const llp_vocab_partition& vocab, const llp_token_layout&
 
   CombineArgs ca{};
   ca.nvt = (int32_t)w.nvt;
+  ca.rows = layout.num_tokens;
   ca.pstride = w.T_cap;
   ca.count = la.count;
   ca.scored = la.scored;

@@ -9,12 +9,12 @@
 namespace llp {
 
 // ------------------------------------------------------------------------------------
-// Row quantisation: scale = max(max |x|, 1e-30) / 127, q = x / scale to the nearest integer,
-// ties to even. A wave takes a row and holds 8 columns per lane and pass in registers; rows of up to
+// Row quantisation: scale = max(max |x|, 1e-30) * fl32(1/127), q = x / scale to the nearest
+// integer, ties to even. A wave takes a row and holds 8 columns per lane and pass in registers; rows of up to
 // QUANT_PASSES * 512 columns are read once, wider ones twice (the second time from L2).
 // Bound by memory: one read, half of it (bf16) written.
 // ------------------------------------------------------------------------------------
-constexpr int QUANT_PASSES = 8;
+constexpr int QUANT_PASSES = 2;
 constexpr int QUANT_WAVES = 4;
 
 // Columns c .. c + 7 of a row (0 past `cols`). VEC: rows are 16-byte aligned.
@@ -45,64 +45,69 @@ __device__ __forceinline__ void quant_load(const void* row, int c, int cols, flo
   }
 }
 
-// x / scale rounded to an integer (ties to even) as the correctly rounded fp32 quotient gives it.
-// With inv = fl(1 / scale), x * inv is off from x / scale by at most 2^-23 of it, 1.6e-5 at
-// 127; only where that leaves the rounding open is the division carried out.
-__device__ __forceinline__ float quant_round(float x, float scale, float inv) {
-  const float p = x * inv;
-  const float r = rintf(p);
-  if (__builtin_expect(fabsf(fabsf(p - r) - 0.5f) < 1e-4f, 0)) return rintf(x / scale);
-  return r;
-}
-
+// Eight values as bytes: x / scale rounded to an integer (ties to even) as the correctly rounded
+// fp32 quotient gives it. With inv = fl(1 / scale), x * inv is off from x / scale by at most
+// 2^-23 of it, 1.6e-5 at 127; only where that leaves a lane's rounding open are the wave's
+// divisions carried out (2e-4 of the values).
 __device__ __forceinline__ uint2 quant_pack(const float (&v)[8], float scale, float inv) {
-  uint32_t w[2];
+  float r[8];
+  bool open = false;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    w[h] = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      w[h] |= ((uint32_t)(int)quant_round(v[4 * h + i], scale, inv) & 0xFFu) << (8 * i);
+  for (int i = 0; i < 8; ++i) {
+    const float p = v[i] * inv;
+    r[i] = rintf(p);
+    open |= fabsf(p - r[i]) > 0.4999f;
   }
+  if (__builtin_amdgcn_ballot_w64(open) != 0) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = rintf(v[i] / scale);
+  }
+  uint32_t w[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i / 4] |= ((uint32_t)(int)r[i] & 0xFFu) << (8 * (i & 3));
   return make_uint2(w[0], w[1]);
 }
 
-template <bool BF16, bool VEC>
+// WPR waves share a row: 1, or the whole workgroup.
+template <bool BF16, bool VEC, int WPR>
 __global__ __launch_bounds__(64 * QUANT_WAVES) void k_quant(QuantArgs a) {
-  const int lane = threadIdx.x & 63;
-  const int64_t r = (int64_t)blockIdx.x * QUANT_WAVES + (threadIdx.x >> 6);
+  __shared__ float tops[QUANT_WAVES];
+  constexpr int STEP = 64 * WPR * 8;   // columns per pass
+  const int lane = threadIdx.x % (64 * WPR);
+  const int64_t r = (int64_t)blockIdx.x * (QUANT_WAVES / WPR) + threadIdx.x / (64 * WPR);
   if (r >= a.rows) return;
   const void* row = static_cast<const char*>(a.x) + r * a.ldx * (BF16 ? 2 : 4);
   float v[QUANT_PASSES][8];
-  float top = 0.f;
-  bool bad = false;
-  for (int c0 = 0; c0 < a.cols; c0 += QUANT_PASSES * 512) {
+  float top = 0.f;   // becomes infinite with an infinity or NaN in the row
+  for (int c0 = 0; c0 < a.cols; c0 += QUANT_PASSES * STEP) {
 #pragma unroll
-    for (int p = 0; p < QUANT_PASSES; ++p) {
-      const int c = c0 + p * 512 + lane * 8;
-      quant_load<BF16, VEC>(row, c, a.cols, v[p]);
-    }
+    for (int p = 0; p < QUANT_PASSES; ++p) quant_load<BF16, VEC>(row, c0 + p * STEP + lane * 8, a.cols, v[p]);
 #pragma unroll
     for (int p = 0; p < QUANT_PASSES; ++p)
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float m = fabsf(v[p][i]);
-        bad |= !(m < INFINITY);
-        top = fmaxf(top, m);
+        top = m <= top ? top : m < INFINITY ? m : INFINITY;
       }
   }
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off));
-  bad = __builtin_amdgcn_ballot_w64(bad) != 0;
-  const float scale = fmaxf(top, 1e-30f) / 127.f;
+  if constexpr (WPR > 1) {
+    if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < WPR; ++w) top = fmaxf(top, tops[w]);
+  }
+  const bool bad = !(top < INFINITY);
+  const float scale = fmaxf(top, 1e-30f) * (1.f / 127.f);
   const float inv = 1.f / scale;
   if (lane == 0) a.scale[r] = bad ? __builtin_nanf("") : scale;
   int8_t* q = a.q + r * a.ldq;
-  const bool held = a.cols <= QUANT_PASSES * 512;
-  for (int c0 = 0; c0 < a.colsp; c0 += QUANT_PASSES * 512) {
+  const bool held = a.cols <= QUANT_PASSES * STEP;
+  for (int c0 = 0; c0 < a.colsp; c0 += QUANT_PASSES * STEP) {
 #pragma unroll
     for (int p = 0; p < QUANT_PASSES; ++p) {
-      const int c = c0 + p * 512 + lane * 8;
+      const int c = c0 + p * STEP + lane * 8;
       if (c >= a.colsp) continue;
       if (!held) quant_load<BF16, VEC>(row, c, a.cols, v[p]);
       uint2 w = quant_pack(v[p], scale, inv);
@@ -112,14 +117,21 @@ __global__ __launch_bounds__(64 * QUANT_WAVES) void k_quant(QuantArgs a) {
   }
 }
 
+template <bool BF16, bool VEC>
+static void launch_quant_as(const QuantArgs& a, hipStream_t s) {
+  // Rows wider than one wave's registers go to the whole workgroup.
+  if (a.cols > QUANT_PASSES * 512)
+    hipLaunchKernelGGL((k_quant<BF16, VEC, QUANT_WAVES>), dim3((unsigned)a.rows), dim3(64 * QUANT_WAVES), 0, s, a);
+  else
+    hipLaunchKernelGGL((k_quant<BF16, VEC, 1>), dim3((unsigned)((a.rows + QUANT_WAVES - 1) / QUANT_WAVES)),
+                       dim3(64 * QUANT_WAVES), 0, s, a);
+}
+
 hipError_t launch_quant(const QuantArgs& a, hipStream_t s) {
   if (a.rows <= 0) return hipSuccess;
-  const dim3 grid((unsigned)((a.rows + QUANT_WAVES - 1) / QUANT_WAVES)), block(64 * QUANT_WAVES);
   const bool vec = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && a.ldx * (a.bf16 ? 2 : 4) % 16 == 0;
-  if (a.bf16 && vec) hipLaunchKernelGGL((k_quant<true, true>), grid, block, 0, s, a);
-  else if (a.bf16) hipLaunchKernelGGL((k_quant<true, false>), grid, block, 0, s, a);
-  else if (vec) hipLaunchKernelGGL((k_quant<false, true>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((k_quant<false, false>), grid, block, 0, s, a);
+  if (a.bf16) vec ? launch_quant_as<true, true>(a, s) : launch_quant_as<true, false>(a, s);
+  else vec ? launch_quant_as<false, true>(a, s) : launch_quant_as<false, false>(a, s);
   return hipGetLastError();
 }
 
@@ -216,8 +228,180 @@ __global__ __launch_bounds__(64 * NW, 1) __attribute__((amdgpu_waves_per_eu(NW /
       });
 }
 
+// ------------------------------------------------------------------------------------
+// Few rows (at most FEW_ROWS_MAX): the weight's bytes bound the forward, so nothing is staged. A
+// workgroup takes one vocabulary tile; a wave takes 16 IB columns x all rows (NB blocks of 16)
+// over one of KS parts of K, loads its operands straight into MFMA registers and refills a block's
+// registers as soon as its MFMAs have read them, so its loads never drain.
+//
+// v_mfma_i32_16x16x64_i8: lane l supplies A[l % 16][k] and B[k][l % 16] for k = 16 (l / 16) +
+// 0..15, and holds D[4 (l / 16) + r][l % 16]. A load instruction then takes 64 consecutive bytes
+// of each of 16 weight rows, and the next one the rest of the same 128-byte lines; with the wide
+// tile's 32 x 32 blocks it would take 16 bytes at 64 places, and the L1's request rate bounds
+// the stream (measured, 37 rows of a 37717-column shard: 71 us).
+//
+// The int32 sums of the K parts meet in LDS (exact in any order), and from there the epilogue's
+// waves take them in the wide tile's register layout: its sums run in the same order, so every
+// row gets the wide tile's bits.
+// ------------------------------------------------------------------------------------
+constexpr int FEW_ROWS_MAX = 64;
+
+template <int BMODE, int NB, int IB, int KS, int BUFS>
+__global__ __launch_bounds__(1024 / IB * KS) __attribute__((amdgpu_waves_per_eu(KS * 16 / IB == 4 ? 3 : 2))) void k_fwd8_few(Fwd8Args a) {
+  constexpr int CG = 16 / IB;   // column groups
+  constexpr int THREADS = 64 * CG * KS, LDT = BM + 4;   // LDT: ints per row of sums, off the bank stride
+  __shared__ __attribute__((aligned(16))) float red[6 * 256];
+  __shared__ __attribute__((aligned(16))) float sc[3 * 256];
+  __shared__ __attribute__((aligned(16))) int sums[BUFS][16 * NB][LDT];
+  const int Ts = *a.f.count;
+  if (Ts <= 0) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int cg = wave % CG, ks = wave / CG;
+  const int vt = blockIdx.x, v0 = vt * BM;
+  const int64_t ldw = a.f.ldw * 2, ldh = a.f.ldh * 2;   // bytes
+  const char* const W = reinterpret_cast<const char*>(a.f.W) + (int64_t)v0 * ldw;
+  const char* const h = reinterpret_cast<const char*>(a.f.h);
+  const int rows = a.f.n_real - v0 < BM ? (int)(a.f.n_real - v0) : BM;
+  const int l16 = lane & 15;
+  const int lr = lane >> 2, kb = (lane & 3) * 16;   // row and bytes this lane loads
+  const int from = 4 * (l16 * 4 + (lane >> 4));     // and where its MFMA operand is (bpermute)
+  uint32_t oa[IB], ob[NB];
+#pragma unroll
+  for (int i = 0; i < IB; ++i) {
+    const int r = cg * 16 * IB + i * 16 + lr;
+    oa[i] = (uint32_t)((r < rows ? r : rows - 1) * ldw) + kb;
+  }
+#pragma unroll
+  for (int n = 0; n < NB; ++n) {
+    const int j = n * 16 + lr;
+    ob[n] = (uint32_t)(a.f.scored[j < Ts ? j : Ts - 1] * ldh) + kb;
+  }
+  const int steps = a.f.H / KSTEP;   // of 128 bytes
+  const int s0 = steps * ks / KS, s1 = steps * (ks + 1) / KS;
+  i32x4 acc[IB][NB], A[IB][2], B[NB][2], Bn[NB][2];
+#pragma unroll
+  for (int i = 0; i < IB; ++i)
+#pragma unroll
+    for (int n = 0; n < NB; ++n) acc[i][n] = i32x4{0, 0, 0, 0};
+  auto load = [&](i32x4 (&x)[2], const char* base, uint32_t off, int s) {
+    const char* p = base + (size_t)(off + (uint32_t)s * 128u);
+    x[0] = *reinterpret_cast<const i32x4*>(p);
+    x[1] = *reinterpret_cast<const i32x4*>(p + 64);
+  };
+  auto placed = [&](const i32x4& x) {
+    i32x4 y;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) y[u] = __builtin_amdgcn_ds_bpermute(from, x[u]);
+    return y;
+  };
+  auto products = [&](int i) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const i32x4 x = placed(A[i][q]);
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+        acc[i][n] = __builtin_amdgcn_mfma_i32_16x16x64_i8(x, B[n][q], acc[i][n], 0, 0, 0);
+    }
+  };
+  if (s0 < s1) {
+    // Issued in the order they are used: a wait for the first then leaves the rest in flight.
+#pragma unroll
+    for (int n = 0; n < NB; ++n) load(Bn[n], h, ob[n], s0);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < IB; ++i) {
+      load(A[i], W, oa[i], s0);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    for (int s = s0; s + 1 < s1; ++s) {
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) B[n][q] = placed(Bn[n][q]);
+#pragma unroll
+      for (int n = 0; n < NB; ++n) load(Bn[n], h, ob[n], s + 1);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < IB; ++i) {
+        products(i);
+        load(A[i], W, oa[i], s + 1);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) B[n][q] = placed(Bn[n][q]);
+#pragma unroll
+    for (int i = 0; i < IB; ++i) products(i);
+  }
+  // Scales of the tile's columns and of the rows.
+  for (int i = threadIdx.x; i < 256; i += THREADS) {
+    const int v = v0 + i;
+    const bool in = v < a.f.n_real;
+    sc[i] = in ? a.ws[v] : 0.f;
+    if constexpr (BMODE == BIAS_F32)
+      sc[256 + i] = in ? reinterpret_cast<const float*>(a.f.bias)[v] : 0.f;
+    if constexpr (BMODE == BIAS_BF16)
+      sc[256 + i] = in ? bf16_to_f32(reinterpret_cast<const uint16_t*>(a.f.bias)[v]) : 0.f;
+    if (i < FEW_ROWS_MAX) sc[512 + i] = a.hs[a.f.scored[i < Ts ? i : Ts - 1]];
+  }
+  // K parts p, p + BUFS, ... share buffer p: the first writes, the others add in turn.
+#pragma unroll
+  for (int ph = 0; ph < KS / BUFS; ++ph) {
+    if (ks / BUFS == ph) {
+#pragma unroll
+      for (int i = 0; i < IB; ++i)
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+          i32x4* p = reinterpret_cast<i32x4*>(&sums[ks % BUFS][n * 16 + l16][cg * 16 * IB + i * 16 + (lane >> 4) * 4]);
+          *p = ph == 0 ? acc[i][n] : *p + acc[i][n];
+        }
+    }
+    __syncthreads();
+  }
+  if (wave >= 2 * ((NB + 1) / 2)) {
+    // The epilogue's two barriers.
+    dma::lds_barrier();
+    dma::lds_barrier();
+    return;
+  }
+  const int wm = wave & 1;
+  const int token = ((wave >> 1) * 32 + (lane & 31)) % (16 * NB);
+  i32x16 x[4][1];
+#pragma unroll
+  for (int mi = 0; mi < 4; ++mi)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int v = wm * 128 + mi * 32 + 8 * g + 4 * (lane >> 5);   // rows v .. v + 3 (mfma_row)
+      i32x4 y = *reinterpret_cast<const i32x4*>(&sums[0][token][v]);
+#pragma unroll
+      for (int p = 1; p < BUFS; ++p) y += *reinterpret_cast<const i32x4*>(&sums[p][token][v]);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) x[mi][0][4 * g + u] = y[u];
+    }
+  int8_epilogue<BMODE, 1>(x, a, vt, 0, Ts, red, sc);
+}
+
+template <int NB, int IB, int KS, int BUFS>
+static void launch_few(const Fwd8Args& a, hipStream_t s) {
+  const dim3 grid((unsigned)a.f.nvt), block(1024 / IB * KS);
+  if (a.f.bias == nullptr) hipLaunchKernelGGL((k_fwd8_few<BIAS_NONE, NB, IB, KS, BUFS>), grid, block, 0, s, a);
+  else if (a.f.bias_f32) hipLaunchKernelGGL((k_fwd8_few<BIAS_F32, NB, IB, KS, BUFS>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((k_fwd8_few<BIAS_BF16, NB, IB, KS, BUFS>), grid, block, 0, s, a);
+}
+
 hipError_t launch_fwd8(const Fwd8Args& a, hipStream_t s) {
   if (a.f.nvt <= 0 || a.f.ntb <= 0) return hipGetLastError();
+  if (a.rows <= FEW_ROWS_MAX) {
+    // 4 waves per tile keep every tile of a large vocabulary resident at once (3 per compute
+    // unit); with at most one tile per compute unit, 8 waves have more loads in flight.
+    const bool small = a.f.nvt <= a.f.workers;
+    if (a.rows <= 16) small ? launch_few<1, 8, 4, 2>(a, s) : launch_few<1, 8, 2, 2>(a, s);
+    else if (a.rows <= 32) small ? launch_few<2, 8, 4, 2>(a, s) : launch_few<2, 4, 1, 1>(a, s);
+    else launch_few<4, 4, 2, 2>(a, s);
+    return hipGetLastError();
+  }
   const int64_t ntiles = (int64_t)a.f.nvt * a.f.ntb;
   const int n = a.f.H / KSTEP;
   const dim3 block(64 * FWD_WAVES);

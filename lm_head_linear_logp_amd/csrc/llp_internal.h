@@ -75,6 +75,7 @@ struct FwdArgs {
 
 struct CombineArgs {
   int32_t nvt;
+  int64_t rows;     // host side: the call's rows (scored or not)
   int64_t pstride;
   const int32_t* count;
   const int32_t* scored;
@@ -272,6 +273,7 @@ struct Fwd8Args {
   FwdArgs f;
   const float* hs;  // [T] scale of each hidden row
   const float* ws;  // [local vocabulary] scale of each weight row
+  int64_t rows;     // host side: the call's rows (scored or not)
 };
 
 struct EmbArgs {
@@ -291,7 +293,7 @@ struct EmbArgs {
 
 // Embedding gradient: rows are sorted by token in groups of EMB_ROWS_MAX local ids at most, and
 // summed in units of EMB_UNIT consecutive sorted rows.
-constexpr int EMB_ROWS_MAX = 2048;
+constexpr int EMB_ROWS_MAX = 1024;
 constexpr int EMB_UNIT = 32;
 struct EmbBwdArgs {
   const int64_t* ids;
@@ -307,9 +309,11 @@ struct EmbBwdArgs {
   int64_t ldo;
   float* dW;
   int64_t ldw;
+  int32_t* loc;     // [T] local row of each token, or -1
   int32_t* start;   // [n_real + 1] first sorted position of each local row
   int32_t* order;   // [T] sorted position -> row of dout
   int32_t* row;     // [T] sorted position -> local row
+  int32_t* span;    // [units] units after this one that share the token beginning here
   float* part;      // [units][2][H] sums of a unit's first and last segment (rows shared by units)
   int32_t* status;
 };

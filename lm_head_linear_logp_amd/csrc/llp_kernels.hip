@@ -191,39 +191,30 @@ __device__ __forceinline__ void fold(float& M, float& S, float& Q, float m, floa
 // (with 16 rows two workgroups each fetched half of every line: 70 MB for 29 MB of partials).
 constexpr int COMBINE_ROWS = 32, COMBINE_CHAINS = 16;
 
-__global__ __launch_bounds__(COMBINE_ROWS * COMBINE_CHAINS) void k_combine(CombineArgs a) {
-  __shared__ float rm[COMBINE_CHAINS][COMBINE_ROWS], rs[COMBINE_CHAINS][COMBINE_ROWS],
-      rq[COMBINE_CHAINS][COMBINE_ROWS];
-  const int r = threadIdx.x % COMBINE_ROWS, c = threadIdx.x / COMBINE_ROWS;
-  const int Ts = *a.count;
-  const int j = blockIdx.x * COMBINE_ROWS + r;
-  if (blockIdx.x * COMBINE_ROWS >= Ts) return;
-  float M = -INFINITY, S = 0.f, Q = 0.f;
-  if (j < Ts) {
-    // Unrolled so that each thread has several independent loads in flight.
-    float mmax = -INFINITY;
+// One chain of a row: tiles c, c + 16, ... of nvt, `get(vt, m, s, q)` reading a tile's partial.
+// Unrolled so that each thread has several independent loads in flight.
+template <class Max, class Get>
+__device__ __forceinline__ void combine_chain(int c, int nvt, Max max_of, Get get, float& M, float& S,
+                                              float& Q) {
+  float mmax = -INFINITY;
 #pragma unroll 8
-    for (int vt = c; vt < a.nvt; vt += COMBINE_CHAINS)
-      mmax = fmaxf(mmax, a.pm[(int64_t)vt * a.pstride + j]);
-    if (mmax != -INFINITY) {
+  for (int vt = c; vt < nvt; vt += COMBINE_CHAINS) mmax = fmaxf(mmax, max_of(vt));
+  if (mmax != -INFINITY) {
 #pragma unroll 8
-      for (int vt = c; vt < a.nvt; vt += COMBINE_CHAINS) {
-        const int64_t o = (int64_t)vt * a.pstride + j;
-        const float d = a.pm[o] - mmax, s = a.ps[o], q = a.pq[o];
-        const float e = expf(d);
-        S += e * s;
-        Q += e * (q + s * d * kLog2e);
-      }
-      M = mmax;
+    for (int vt = c; vt < nvt; vt += COMBINE_CHAINS) {
+      float m, s, q;
+      get(vt, m, s, q);
+      const float d = m - mmax;
+      const float e = expf(d);
+      S += e * s;
+      Q += e * (q + s * d * kLog2e);
     }
+    M = mmax;
   }
-  rm[c][r] = M;
-  rs[c][r] = S;
-  rq[c][r] = Q;
-  __syncthreads();
-  if (c != 0 || j >= Ts) return;
-  M = -INFINITY; S = 0.f; Q = 0.f;
-  for (int g = 0; g < COMBINE_CHAINS; ++g) fold(M, S, Q, rm[g][r], rs[g][r], rq[g][r]);
+}
+
+// A row's finished sums to its outputs.
+__device__ __forceinline__ void combine_out(const CombineArgs& a, int j, float M, float S, float Q) {
   float lse, ent;
   if (M == -INFINITY || !(S > 0.f)) {
     lse = -INFINITY;
@@ -241,6 +232,75 @@ __global__ __launch_bounds__(COMBINE_ROWS * COMBINE_CHAINS) void k_combine(Combi
   a.out_l[row] = lse;
   if (a.out_e) a.out_e[row] = ent;
   if (a.out_p) a.out_p[row] = hit ? tz - lse : -INFINITY;
+}
+
+__global__ __launch_bounds__(COMBINE_ROWS * COMBINE_CHAINS) void k_combine(CombineArgs a) {
+  __shared__ float rm[COMBINE_CHAINS][COMBINE_ROWS], rs[COMBINE_CHAINS][COMBINE_ROWS],
+      rq[COMBINE_CHAINS][COMBINE_ROWS];
+  const int r = threadIdx.x % COMBINE_ROWS, c = threadIdx.x / COMBINE_ROWS;
+  const int Ts = *a.count;
+  const int j = blockIdx.x * COMBINE_ROWS + r;
+  if (blockIdx.x * COMBINE_ROWS >= Ts) return;
+  float M = -INFINITY, S = 0.f, Q = 0.f;
+  if (j < Ts)
+    combine_chain(
+        c, a.nvt, [&](int vt) { return a.pm[(int64_t)vt * a.pstride + j]; },
+        [&](int vt, float& m, float& s, float& q) {
+          const int64_t o = (int64_t)vt * a.pstride + j;
+          m = a.pm[o];
+          s = a.ps[o];
+          q = a.pq[o];
+        },
+        M, S, Q);
+  rm[c][r] = M;
+  rs[c][r] = S;
+  rq[c][r] = Q;
+  __syncthreads();
+  if (c != 0 || j >= Ts) return;
+  M = -INFINITY; S = 0.f; Q = 0.f;
+  for (int g = 0; g < COMBINE_CHAINS; ++g) fold(M, S, Q, rm[g][r], rs[g][r], rq[g][r]);
+  combine_out(a, j, M, S, Q);
+}
+
+// Few rows leave k_combine one or two workgroups that wait for 2 x nvt / 16 loads one after the
+// other (17.6 us for one row of a 151669-column vocabulary). Here a workgroup takes one row, all
+// its threads fetch the row's partials to LDS at once, and the chains run from there: the same
+// arithmetic on the same values, so the same bits.
+constexpr int COMBINE_FEW_ROWS = 64, COMBINE_FEW_TILES = 2048;
+
+__global__ __launch_bounds__(256) void k_combine_few(CombineArgs a) {
+  __shared__ float pm[COMBINE_FEW_TILES], ps[COMBINE_FEW_TILES], pq[COMBINE_FEW_TILES];
+  __shared__ float rm[COMBINE_CHAINS], rs[COMBINE_CHAINS], rq[COMBINE_CHAINS];
+  const int j = blockIdx.x;
+  if (j >= *a.count) return;
+#pragma unroll 4
+  for (int vt = threadIdx.x; vt < a.nvt; vt += 256) {
+    const int64_t o = (int64_t)vt * a.pstride + j;
+    pm[vt] = a.pm[o];
+    ps[vt] = a.ps[o];
+    pq[vt] = a.pq[o];
+  }
+  __syncthreads();
+  const int c = threadIdx.x;
+  if (c < COMBINE_CHAINS) {
+    float M = -INFINITY, S = 0.f, Q = 0.f;
+    combine_chain(
+        c, a.nvt, [&](int vt) { return pm[vt]; },
+        [&](int vt, float& m, float& s, float& q) {
+          m = pm[vt];
+          s = ps[vt];
+          q = pq[vt];
+        },
+        M, S, Q);
+    rm[c] = M;
+    rs[c] = S;
+    rq[c] = Q;
+  }
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  float M = -INFINITY, S = 0.f, Q = 0.f;
+  for (int g = 0; g < COMBINE_CHAINS; ++g) fold(M, S, Q, rm[g], rs[g], rq[g]);
+  combine_out(a, j, M, S, Q);
 }
 
 // ------------------------------------------------------------------------------------
@@ -1182,7 +1242,9 @@ hipError_t launch_fwd(const FwdArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_combine(const CombineArgs& a, int64_t T_cap, hipStream_t s) {
-  if (T_cap > 0)
+  if (a.rows > 0 && a.rows <= COMBINE_FEW_ROWS && a.nvt <= COMBINE_FEW_TILES)
+    hipLaunchKernelGGL(k_combine_few, dim3((unsigned)a.rows), dim3(256), 0, s, a);
+  else if (T_cap > 0)
     hipLaunchKernelGGL(k_combine, dim3(ceil_div64(T_cap, COMBINE_ROWS)),
                        dim3(COMBINE_ROWS * COMBINE_CHAINS), 0, s, a);
   return hipGetLastError();

@@ -34,19 +34,31 @@ def _tensor(t, name):
     return t
 
 
-def _opt(t, name, dtype, n, dev):
-    """Pointer of an optional contiguous 1-d tensor of n elements."""
-    if t is None:
-        return None
-    _vec(t, name, dtype, n, dev)
+def _at(t, name, dtype, n, dev):
+    """Pointer of a contiguous 1-d tensor of n elements (_vec, which words the refusal, is the
+    slower test: these calls are short enough for it to show)."""
+    if not (type(t) is torch.Tensor and t.dtype is dtype and t.shape == (n,) and t.device == dev
+            and t.is_contiguous()):
+        _vec(t, name, dtype, n, dev)
     return t.data_ptr()
+
+
+def _opt(t, name, dtype, n, dev):
+    """The same of an optional tensor."""
+    return None if t is None else _at(t, name, dtype, n, dev)
+
+
+_ready_devices = set()
 
 
 def _ready(dev):
     """The tensors' device, opened (the last check before the library is called)."""
+    if dev in _ready_devices:
+        return
     if dev.type != "cuda":
         raise RuntimeError(f"tensors are on {dev}: the kernels run on a gfx950 GPU only")
     open(dev.index)
+    _ready_devices.add(dev)
 
 
 def _call(dev, name, *args):
@@ -128,22 +140,20 @@ def forward_int8(hidden: torch.Tensor, hidden_scale: torch.Tensor, weight: torch
     T, K = hidden.shape
     _need(weight, "weight", _I8, 2, dev, (None, K))
     V = weight.shape[0]
-    _vec(hidden_scale, "hidden_scale", _F32, T, dev)
-    _vec(weight_scale, "weight_scale", _F32, V, dev)
-    _vec(target_ids, "target_ids", _I64, T, dev)
     r = A.llp_int8_request()
-    r.hidden, r.hidden_stride, r.hidden_scale = _ptr(hidden), _stride(hidden, T, K), _ptr(hidden_scale)
-    r.weight, r.weight_stride, r.weight_scale = _ptr(weight), _stride(weight, V, K), _ptr(weight_scale)
+    r.hidden, r.hidden_stride = hidden.data_ptr(), _stride(hidden, T, K)
+    r.hidden_scale = _at(hidden_scale, "hidden_scale", _F32, T, dev)
+    r.weight, r.weight_stride = weight.data_ptr(), _stride(weight, V, K)
+    r.weight_scale = _at(weight_scale, "weight_scale", _F32, V, dev)
+    r.target_ids = _at(target_ids, "target_ids", _I64, T, dev)
     if bias is not None:
         if not isinstance(bias, torch.Tensor) or bias.dtype not in _DTYPE:
             raise TypeError("bias must be a bf16 or fp32 tensor")
-        _vec(bias, "bias", bias.dtype, V, dev)
-        r.bias, r.bias_dtype = _ptr(bias), _DTYPE[bias.dtype]
+        r.bias, r.bias_dtype = _at(bias, "bias", bias.dtype, V, dev), _DTYPE[bias.dtype]
     r.flags = A.LLP_FLAG_WANT_ENTROPY if want_entropy else 0
     r.hidden_size = K
     _vocab(r.vocab, offset, V, real_vocab, padded_vocab, rank, world)
     _layout(r.layout, T, loss_mask, cu_seqlens, dev)
-    r.target_ids = _ptr(target_ids)
     r.temperature = float(temperature)
     _status(status, dev)
     r.status_word = _ptr(status)
@@ -194,10 +204,10 @@ def policy_grads(logp: torch.Tensor, old_logp: torch.Tensor, advantages: torch.T
     dev = _tensor(logp, "logp").device
     _need(logp, "logp", _F32, 1, dev)
     T = logp.shape[0]
-    _vec(old_logp, "old_logp", _F32, T, dev)
-    _vec(advantages, "advantages", _F32, T, dev)
     r = A.llp_policy_request()
-    r.logp, r.old_logp, r.advantages = logp.data_ptr(), old_logp.data_ptr(), advantages.data_ptr()
+    r.logp = logp.data_ptr()
+    r.old_logp = _at(old_logp, "old_logp", _F32, T, dev)
+    r.advantages = _at(advantages, "advantages", _F32, T, dev)
     r.ref_logp = _opt(ref_logp, "ref_logp", _F32, T, dev)
     r.entropy = _opt(entropy, "entropy", _F32, T, dev)
     if ref_logp is None and kl_coef:
@@ -436,7 +446,7 @@ def embedding_backward(token_ids: torch.Tensor, dout: torch.Tensor, *,
         raise TypeError(f"dout must be a bf16 or fp32 tensor, got {dout.dtype}")
     _need(dout, "dout", dout.dtype, 2, dev)
     T, H = dout.shape
-    _vec(token_ids, "token_ids", _I64, T, dev)
+    _at(token_ids, "token_ids", _I64, T, dev)
     if dweight is not None:
         _need(dweight, "dweight", _F32, 2, dev, (local_size, H))
         local_size = dweight.shape[0]

@@ -9,7 +9,7 @@ LOG_RATIO_MAX = 20.0
 
 def quantize(x):
     """int8 rows (columns padded to a multiple of 128) and fp32 scales of fp32 rows `x`. The
-    definition fixes two fp32 divisions, so these are carried out in fp32."""
+    definition fixes an fp32 product and an fp32 division, so these are carried out in fp32."""
     x = np.asarray(x, dtype=np.float32)
     R, K = x.shape
     q = np.zeros((R, -(-K // 128) * 128), dtype=np.int8)
@@ -18,7 +18,7 @@ def quantize(x):
         if not np.isfinite(x[r]).all():
             scale[r] = np.nan
             continue
-        scale[r] = np.maximum(np.abs(x[r]).max(), np.float32(1e-30)) / np.float32(127)
+        scale[r] = np.maximum(np.abs(x[r]).max(), np.float32(1e-30)) * (np.float32(1) / np.float32(127))
         q[r, :K] = np.rint(x[r] / scale[r]).astype(np.int8)
     return q, scale
 
