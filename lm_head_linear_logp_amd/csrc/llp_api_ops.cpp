@@ -133,15 +133,20 @@ struct PolicyWs {
 PolicyWs policy_ws(const llp_policy_request& r) {
   PolicyWs w{};
   const int64_t T = r.layout.num_tokens;
-  if (r.reduction == LLP_REDUCE_SEQ_MEAN) w.ncount = r.layout.num_seqs;
+  const bool by_seq = r.reduction == LLP_REDUCE_SEQ_MEAN;
+  if (T <= POLICY_SOLO_ROWS && !(by_seq && r.layout.num_seqs > POLICY_SOLO_SEQS)) {
+    w.total = 256;   // one workgroup, nothing in the workspace
+    return w;
+  }
+  if (by_seq) w.ncount = r.layout.num_seqs;
   else if (r.reduction == LLP_REDUCE_TOKEN_MEAN && r.layout.loss_mask && !r.denominator)
     w.ncount = (int32_t)((T + kPolicyCountRows - 1) / kPolicyCountRows);
   int64_t nb = (T + kPolicyBlockRows - 1) / kPolicyBlockRows;
-  if (nb < 1) nb = 1;
+  if (nb < 1) nb = 1;   // no rows in many sequences
   w.nblocks = (int32_t)(nb < kPolicyBlocks ? nb : kPolicyBlocks);
   Regions g;
   w.count = g.take((size_t)w.ncount * 4);
-  w.meta = g.take(8);
+  w.meta = g.take(4);
   w.part = g.take((size_t)w.nblocks * LLP_POLICY_STATS * 8);
   w.total = g.off;
   return w;
@@ -362,7 +367,6 @@ LLP_API llp_status llp_policy_loss(const llp_policy_request* req, const llp_poli
   a.klc64 = req->kl_coef;
   a.entc64 = req->entropy_coef;
   a.klc = (float)req->kl_coef;
-  a.entc = (float)req->entropy_coef;
   a.kl_kind = req->kl_kind;
   a.reduction = req->reduction;
   a.denom = req->denominator;

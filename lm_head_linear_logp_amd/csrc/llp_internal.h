@@ -318,6 +318,9 @@ struct EmbBwdArgs {
   int32_t* status;
 };
 
+// Rows and sequences up to which one workgroup computes a policy loss in one launch.
+constexpr int64_t POLICY_SOLO_ROWS = 8192;
+constexpr int POLICY_SOLO_SEQS = 1024;
 struct PolicyArgs {
   int64_t T;
   const float* logp;
@@ -330,13 +333,13 @@ struct PolicyArgs {
   int32_t S;
   double log_lo, log_hi, log_dual;     // borders of d = logp - old_logp
   float lo, hi, dual;                  // the clipped ratios
-  float klc, entc;
+  float klc;
   int32_t kl_kind, reduction;
   const float* denom;
-  int32_t nblocks;                     // blocks of the loss kernel
+  int32_t nblocks;                     // blocks of the loss kernel; 0: one workgroup does it all
   int32_t ncount;                      // blocks of the count kernel (0: nothing to count)
   int32_t* count;                      // [ncount] scored rows, or [S] for SEQ_MEAN
-  int32_t* meta;                       // [2] sequences with scored rows, malformed cu_seqlens
+  int32_t* meta;                       // [1] sequences with scored rows, -1: malformed cu_seqlens
   double* part;                        // [nblocks][LLP_POLICY_STATS]
   float* loss;
   float* stats;

@@ -47,23 +47,44 @@ __device__ __forceinline__ int seq_of(const int32_t* cu, int64_t t, int lo, int 
   return lo;
 }
 
+// The same for the whole wave (t uniform), 64 probes at a time: two rounds for 4096 sequences.
+__device__ __forceinline__ int seq_of_wave(const int32_t* cu, int64_t t, int hi) {
+  const int lane = threadIdx.x & 63;
+  int lo = 0;
+  while (lo < hi) {
+    const int step = (hi - lo + 64) / 64;   // ceil((hi - lo + 1) / 64)
+    const int at = lo + lane * step;
+    const uint64_t below = __builtin_amdgcn_ballot_w64(at <= hi && (lane == 0 || cu[at <= hi ? at : hi] <= t));
+    const int k = 63 - __builtin_clzll(below);
+    lo += k * step;
+    hi = lo + step - 1 < hi ? lo + step - 1 : hi;
+  }
+  return lo;
+}
+
 __device__ __forceinline__ bool cu_bad(const int32_t* cu, int S, int64_t T, int i) {
   const int c = cu[i];
   return (i == 0 && c != 0) || (i == S && (int64_t)c != T) || (i < S && cu[i + 1] < c);
 }
 
 // ------------------------------------------------------------------------------------
-// Clipped policy loss. Launches: scored rows counted per block of POLICY_COUNT_ROWS (TOKEN_MEAN
-// with a mask) or per sequence (SEQ_MEAN, then one workgroup that counts the sequences with
-// scored rows and checks cu_seqlens); the loss kernel, one pass over the rows; one workgroup
-// that adds up its partial sums.
+// Clipped policy loss. Up to POLICY_SOLO_ROWS rows one workgroup does it all in one launch.
+// Beyond, launches: scored rows counted per block of POLICY_COUNT_ROWS (TOKEN_MEAN with a mask)
+// or per sequence (SEQ_MEAN); the loss kernel, one pass over the rows; one workgroup that adds
+// up its partial sums. With more than POLICY_SEQS sequences one more workgroup, after the count,
+// finds the number of sequences with scored rows; up to that many every block of the loss kernel
+// looks through the counts itself.
 // ------------------------------------------------------------------------------------
-constexpr int POLICY_COUNT_ROWS = 16384;
+constexpr int POLICY_COUNT_ROWS = 16384, POLICY_SEQS = 2048;
+constexpr int SOLO_THREADS = 1024;
 
+// SEQ_MEAN counts carry a malformed cu_seqlens as -1.
 __global__ __launch_bounds__(LOSS_THREADS) void k_policy_count(PolicyArgs a) {
   __shared__ int sh[LOSS_THREADS / 64];
   int64_t b, e;
+  bool bad = false;
   if (a.reduction == LLP_REDUCE_SEQ_MEAN) {
+    bad = cu_bad(a.cu, a.S, a.T, blockIdx.x) || cu_bad(a.cu, a.S, a.T, blockIdx.x + 1);
     b = a.cu[blockIdx.x] > 0 ? a.cu[blockIdx.x] : 0;
     e = a.cu[blockIdx.x + 1] < a.T ? a.cu[blockIdx.x + 1] : a.T;
   } else {
@@ -74,28 +95,35 @@ __global__ __launch_bounds__(LOSS_THREADS) void k_policy_count(PolicyArgs a) {
   if (a.mask == nullptr) {
     if (threadIdx.x == 0 && e > b) n = (int)(e - b);
   } else {
-#pragma unroll 8
+#pragma unroll 16
     for (int64_t t = b + threadIdx.x; t < e; t += LOSS_THREADS) n += a.mask[t] != 0 ? 1 : 0;
   }
   n = block_sum<LOSS_THREADS / 64>(n, sh);
-  if (threadIdx.x == 0) a.count[blockIdx.x] = n;
-}
-
-// SEQ_MEAN: meta[0] = sequences with scored rows, meta[1] = 1 for a malformed cu_seqlens.
-__global__ __launch_bounds__(1024) void k_policy_seqs(PolicyArgs a) {
-  __shared__ int sh[16];
-  int n = 0, bad = 0;
-  for (int i = threadIdx.x; i <= a.S; i += 1024) {
-    if (i < a.S) n += a.count[i] > 0 ? 1 : 0;
-    bad += cu_bad(a.cu, a.S, a.T, i) ? 1 : 0;
-  }
-  n = block_sum<16>(n, sh);
-  bad = block_sum<16>(bad, sh);
   if (threadIdx.x == 0) {
-    a.meta[0] = n;
-    a.meta[1] = bad ? 1 : 0;
+    a.count[blockIdx.x] = bad ? -1 : n;
     if (bad && a.status) atomicOr(a.status, LLP_STATUS_LAYOUT_INVALID);
   }
+}
+
+// SEQ_MEAN: the number of sequences with scored rows, or -1 for a malformed cu_seqlens, from the
+// counts (NW waves, the result in every thread).
+template <int NW>
+__device__ __forceinline__ int policy_seqs(const PolicyArgs& a, int* sh) {
+  int n = 0, bad = 0;
+  for (int i = threadIdx.x; i < a.S; i += 64 * NW) {
+    const int c = a.count[i];
+    n += c > 0 ? 1 : 0;
+    bad += c < 0 ? 1 : 0;
+  }
+  n = block_sum<NW>(n, sh);
+  bad = block_sum<NW>(bad, sh);
+  return bad ? -1 : n;
+}
+
+__global__ __launch_bounds__(1024) void k_policy_seqs(PolicyArgs a) {
+  __shared__ int sh[16];
+  const int n = policy_seqs<16>(a, sh);
+  if (threadIdx.x == 0) a.meta[0] = n;
 }
 
 // exp(y) - y - 1 without the cancellation near 0: below 0.5 its series, y^2 (1/2 + y/6 + ...).
@@ -162,22 +190,11 @@ __device__ __forceinline__ PolicyRow policy_row(const PolicyArgs& a, float lp, f
   return o;
 }
 
-// One over the number of rows (or sequences) that the loss is a mean of; 0 when there are none.
-__device__ __forceinline__ double policy_norm(const PolicyArgs& a, int* sh) {
+// One over the number n of rows (or sequences) that the loss is a mean of; 0 when there are none.
+__device__ __forceinline__ double policy_norm(const PolicyArgs& a, int n) {
   if (a.reduction == LLP_REDUCE_SUM) return 1.0;
-  double n;
-  if (a.denom != nullptr) {
-    n = (double)a.denom[0];
-  } else if (a.reduction == LLP_REDUCE_SEQ_MEAN) {
-    n = (double)a.meta[0];
-  } else if (a.mask == nullptr) {
-    n = (double)a.T;
-  } else {
-    int c = 0;
-    for (int i = threadIdx.x; i < a.ncount; i += LOSS_THREADS) c += a.count[i];
-    n = (double)block_sum<LOSS_THREADS / 64>(c, sh);
-  }
-  return n > 0.0 && n < INFINITY ? 1.0 / n : 0.0;
+  const double d = a.denom != nullptr ? (double)a.denom[0] : (double)n;
+  return d > 0.0 && d < INFINITY ? 1.0 / d : 0.0;
 }
 
 // Rows 4 per thread and pass: VEC (every array 16-byte aligned) with one load per array.
@@ -217,85 +234,220 @@ __device__ __forceinline__ void mask4(const uint8_t* p, int64_t t, int64_t T, bo
   }
 }
 
+// Four rows of one thread.
+struct PolicyRows {
+  float lp[4], old[4], adv[4], ref[4], ent[4];
+  bool m[4];
+};
+
+template <bool VEC>
+__device__ __forceinline__ void policy_load(const PolicyArgs& a, int64_t t, PolicyRows& x) {
+  mask4<VEC>(a.mask, t, a.T, x.m);
+  load4<VEC>(a.logp, t, a.T, x.lp);
+  load4<VEC>(a.old, t, a.T, x.old);
+  load4<VEC>(a.adv, t, a.T, x.adv);
+  load4<VEC>(a.ref, t, a.T, x.ref);
+  load4<VEC>(a.ent, t, a.T, x.ent);
+}
+
+constexpr int POLICY_SUMS = LLP_POLICY_STATS - 1;   // after the loss
+
+// Their terms into `sum` and their gradients out. by_seq: w = norm / the sequence's count, its
+// sequence looked for in [s_lo, s_hi].
+template <bool VEC>
+__device__ __forceinline__ void policy_rows(const PolicyArgs& a, int64_t t, const PolicyRows& x, double norm,
+                                            double up, bool by_seq, const int* count, int s_lo, int s_hi,
+                                            double (&sum)[POLICY_SUMS], int& status) {
+  float dl[4], de[4];
+  int s = -1, s_end = 0;   // this thread's sequence and its end
+  double w = norm;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    dl[i] = de[i] = 0.f;
+    if (!x.m[i]) continue;
+    if (by_seq && (s < 0 || t + i >= s_end)) {
+      s = seq_of(a.cu, t + i, s < 0 ? s_lo : s, s_hi);
+      s_end = a.cu[s + 1];
+      w = norm / (double)count[s];
+    }
+    sum[6] += 1.0;
+    const bool fine = fabsf(x.lp[i]) < INFINITY && fabsf(x.old[i]) < INFINITY &&
+                      fabsf(x.adv[i]) < INFINITY && fabsf(x.ref[i]) < INFINITY &&
+                      fabsf(x.ent[i]) < INFINITY;
+    if (!fine) {
+      status |= LLP_STATUS_VALUE_NOT_FINITE;
+      continue;
+    }
+    const PolicyRow r = policy_row(a, x.lp[i], x.old[i], x.adv[i], x.ref[i]);
+    sum[0] += w * (double)r.pg;
+    sum[1] += w * (double)r.kl;
+    sum[2] += w * (double)x.ent[i];
+    sum[3] += r.clipped ? w : 0.0;
+    sum[4] += w * (double)r.ratio;
+    sum[5] += w * ((double)x.old[i] - (double)x.lp[i]);
+    dl[i] = (float)(up * w * (double)r.grad);
+    de[i] = (float)(up * w * -a.entc64);
+  }
+  store4<VEC>(a.dlogp, t, a.T, dl);
+  store4<VEC>(a.dent, t, a.T, de);
+}
+
+// The threads' sums over a workgroup of NW waves: sum k in thread k (k < POLICY_SUMS).
+template <int NW>
+__device__ __forceinline__ double policy_total(const double (&sum)[POLICY_SUMS], double (*sh)[POLICY_SUMS]) {
+#pragma unroll
+  for (int k = 0; k < POLICY_SUMS; ++k) {
+    const double x = wave_sum(sum[k]);
+    if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6][k] = x;
+  }
+  __syncthreads();
+  double x = 0.0;
+  if (threadIdx.x < POLICY_SUMS)
+    for (int w = 0; w < NW; ++w) x += sh[w][threadIdx.x];
+  return x;
+}
+
+// The finished sums (sum k in thread k) to loss and statistics; sh: POLICY_SUMS entries.
+__device__ __forceinline__ void policy_finish(const PolicyArgs& a, double x, double* sh) {
+  if (threadIdx.x < POLICY_SUMS) {
+    sh[threadIdx.x] = x;
+    if (a.stats) a.stats[1 + threadIdx.x] = (float)x;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    const double loss = sh[0] + a.klc64 * sh[1] - a.entc64 * sh[2];
+    a.loss[0] = (float)loss;
+    if (a.stats) a.stats[0] = (float)loss;
+  }
+}
+
 template <bool VEC>
 __global__ __launch_bounds__(LOSS_THREADS) void k_policy(PolicyArgs a) {
-  __shared__ double shd[LOSS_THREADS / 64];
-  __shared__ int shi[LOSS_THREADS / 64];
+  constexpr int NW = LOSS_THREADS / 64;
+  __shared__ double shd[NW][POLICY_SUMS];
+  __shared__ int shi[NW], ends[2];
+  const int64_t step = (int64_t)gridDim.x * LOSS_THREADS * 4;
+  int64_t t0 = (int64_t)blockIdx.x * LOSS_THREADS * 4;
+  PolicyRows x;
+  policy_load<VEC>(a, t0 + threadIdx.x * 4, x);   // in flight while the weights are found
   const bool by_seq = a.reduction == LLP_REDUCE_SEQ_MEAN;
-  const bool void_layout = by_seq && a.meta[1] != 0;
-  const double norm = void_layout ? 0.0 : policy_norm(a, shi);
+  int n = 0;
+  if (by_seq) {
+    n = a.S <= POLICY_SEQS ? policy_seqs<NW>(a, shi) : a.meta[0];
+  } else if (a.ncount > 0) {
+    for (int i = threadIdx.x; i < a.ncount; i += LOSS_THREADS) n += a.count[i];
+    n = block_sum<NW>(n, shi);
+  } else {
+    n = (int)a.T;   // no mask (or a denominator, or a sum)
+  }
+  const bool void_layout = by_seq && n < 0;
+  const double norm = policy_norm(a, n);
   const double up = a.dloss != nullptr ? (double)a.dloss[0] : 1.0;
-  double sum[LLP_POLICY_STATS - 1] = {0.0, 0.0, 0.0, 0.0, 0.0, 0.0, 0.0};   // after the loss
+  double sum[POLICY_SUMS] = {0.0, 0.0, 0.0, 0.0, 0.0, 0.0, 0.0};
   int status = 0;
   if (!by_seq && a.cu != nullptr && blockIdx.x == 0)
     for (int i = threadIdx.x; i <= a.S; i += LOSS_THREADS)
       if (cu_bad(a.cu, a.S, a.T, i)) status |= LLP_STATUS_LAYOUT_INVALID;
-  const int64_t step = (int64_t)gridDim.x * LOSS_THREADS * 4;
-  for (int64_t t0 = (int64_t)blockIdx.x * LOSS_THREADS * 4; t0 < a.T; t0 += step) {
+  for (;;) {
     const int64_t t = t0 + threadIdx.x * 4;
-    float lp[4], old[4], adv[4], ref[4], ent[4], dl[4], de[4];
-    bool m[4];
-    mask4<VEC>(a.mask, t, a.T, m);
-    load4<VEC>(a.logp, t, a.T, lp);
-    load4<VEC>(a.old, t, a.T, old);
-    load4<VEC>(a.adv, t, a.T, adv);
-    load4<VEC>(a.ref, t, a.T, ref);
-    load4<VEC>(a.ent, t, a.T, ent);
-    int s = -1, s_end = 0;   // this thread's sequence and its end
-    double w_seq = norm;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      dl[i] = de[i] = 0.f;
-      if (!m[i] || void_layout) continue;
-      if (by_seq && (s < 0 || t + i >= s_end)) {
-        s = seq_of(a.cu, t + i, s < 0 ? 0 : s, a.S - 1);
-        s_end = a.cu[s + 1];
-        w_seq = norm / (double)a.count[s];
+    if (by_seq && !void_layout) {
+      // The sequences of the block's first and last rows bound every thread's search.
+      const int w = threadIdx.x >> 6;
+      if (w < 2) {
+        const int64_t last = t0 + LOSS_THREADS * 4 - 1 < a.T - 1 ? t0 + LOSS_THREADS * 4 - 1 : a.T - 1;
+        const int s = seq_of_wave(a.cu, w == 0 ? t0 : last, a.S - 1);
+        if ((threadIdx.x & 63) == 0) ends[w] = s;
       }
-      sum[6] += 1.0;
-      const bool fine = fabsf(lp[i]) < INFINITY && fabsf(old[i]) < INFINITY &&
-                        fabsf(adv[i]) < INFINITY && fabsf(ref[i]) < INFINITY &&
-                        fabsf(ent[i]) < INFINITY;
-      if (!fine) {
-        status |= LLP_STATUS_VALUE_NOT_FINITE;
-        continue;
-      }
-      const PolicyRow r = policy_row(a, lp[i], old[i], adv[i], ref[i]);
-      sum[0] += w_seq * (double)r.pg;
-      sum[1] += w_seq * (double)r.kl;
-      sum[2] += w_seq * (double)ent[i];
-      sum[3] += r.clipped ? w_seq : 0.0;
-      sum[4] += w_seq * (double)r.ratio;
-      sum[5] += w_seq * ((double)old[i] - (double)lp[i]);
-      dl[i] = (float)(up * w_seq * (double)r.grad);
-      de[i] = (float)(up * w_seq * -a.entc64);
+      __syncthreads();
     }
-    store4<VEC>(a.dlogp, t, a.T, dl);
-    store4<VEC>(a.dent, t, a.T, de);
+    if (void_layout) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x.m[i] = false;
+    }
+    policy_rows<VEC>(a, t, x, norm, up, by_seq, a.count, by_seq ? ends[0] : 0, by_seq ? ends[1] : 0, sum, status);
+    t0 += step;
+    if (t0 >= a.T) break;
+    __syncthreads();   // `ends` is read by all before the next search writes it
+    policy_load<VEC>(a, t0 + threadIdx.x * 4, x);
   }
   if (status && a.status) atomicOr(a.status, status);
-#pragma unroll
-  for (int k = 0; k < LLP_POLICY_STATS - 1; ++k) {
-    const double x = block_sum<LOSS_THREADS / 64>(sum[k], shd);
-    if (threadIdx.x == 0) a.part[(int64_t)blockIdx.x * LLP_POLICY_STATS + 1 + k] = x;
-  }
+  const double total = policy_total<NW>(sum, shd);
+  if (threadIdx.x < POLICY_SUMS) a.part[(int64_t)blockIdx.x * LLP_POLICY_STATS + threadIdx.x] = total;
 }
 
 __global__ __launch_bounds__(LOSS_THREADS) void k_policy_sum(PolicyArgs a) {
-  __shared__ double shd[LOSS_THREADS / 64];
-  double sum[LLP_POLICY_STATS - 1] = {0.0, 0.0, 0.0, 0.0, 0.0, 0.0, 0.0};
+  constexpr int NW = LOSS_THREADS / 64;
+  __shared__ double shd[NW][POLICY_SUMS], fin[POLICY_SUMS];
+  double sum[POLICY_SUMS] = {0.0, 0.0, 0.0, 0.0, 0.0, 0.0, 0.0};
+#pragma unroll 4
   for (int b = threadIdx.x; b < a.nblocks; b += LOSS_THREADS)
 #pragma unroll
-    for (int k = 0; k < LLP_POLICY_STATS - 1; ++k) sum[k] += a.part[(int64_t)b * LLP_POLICY_STATS + 1 + k];
+    for (int k = 0; k < POLICY_SUMS; ++k) sum[k] += a.part[(int64_t)b * LLP_POLICY_STATS + k];
+  policy_finish(a, policy_total<NW>(sum, shd), fin);
+}
+
+// Few rows, and few sequences: everything in one workgroup.
+template <bool VEC>
+__global__ __launch_bounds__(SOLO_THREADS) void k_policy_solo(PolicyArgs a) {
+  constexpr int NW = SOLO_THREADS / 64;
+  __shared__ double shd[NW][POLICY_SUMS], fin[POLICY_SUMS];
+  __shared__ int shi[NW], count[POLICY_SOLO_SEQS];
+  const bool by_seq = a.reduction == LLP_REDUCE_SEQ_MEAN;
+  int status = 0, n = 0;
+  PolicyRows x;
+  policy_load<VEC>(a, threadIdx.x * 4, x);
+  bool bad = false;
+  if (a.cu != nullptr)
+    for (int i = threadIdx.x; i <= a.S; i += SOLO_THREADS) bad |= cu_bad(a.cu, a.S, a.T, i);
+  if (bad) status |= LLP_STATUS_LAYOUT_INVALID;
+  bool void_layout = false;
+  if (by_seq) {
+    for (int i = threadIdx.x; i < a.S; i += SOLO_THREADS) count[i] = 0;
+    void_layout = block_sum<NW>(bad ? 1 : 0, shi) != 0;
+    if (!void_layout) {
+      // Whole numbers: the order of the additions is free. A run of rows of one sequence is one.
+      for (int64_t t0 = 0; t0 < a.T; t0 += SOLO_THREADS * 4) {
+        const int64_t t = t0 + threadIdx.x * 4;
+        if (t0 > 0) mask4<VEC>(a.mask, t, a.T, x.m);
+        int s = -1, s_end = 0, run = 0;
 #pragma unroll
-  for (int k = 0; k < LLP_POLICY_STATS - 1; ++k) sum[k] = block_sum<LOSS_THREADS / 64>(sum[k], shd);
-  if (threadIdx.x != 0) return;
-  const double loss = sum[0] + a.klc64 * sum[1] - a.entc64 * sum[2];
-  a.loss[0] = (float)loss;
-  if (a.stats == nullptr) return;
-  a.stats[0] = (float)loss;
+        for (int i = 0; i < 4; ++i) {
+          if (!x.m[i]) continue;
+          if (s < 0 || t + i >= s_end) {
+            if (run) atomicAdd(count + s, run);
+            s = seq_of(a.cu, t + i, s < 0 ? 0 : s, a.S - 1);
+            s_end = a.cu[s + 1];
+            run = 0;
+          }
+          ++run;
+        }
+        if (run) atomicAdd(count + s, run);
+      }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.S; i += SOLO_THREADS) n += count[i] > 0 ? 1 : 0;
+  } else if (a.reduction == LLP_REDUCE_TOKEN_MEAN && a.denom == nullptr) {
+    for (int64_t t0 = 0; t0 < a.T; t0 += SOLO_THREADS * 4) {
+      if (t0 > 0) mask4<VEC>(a.mask, t0 + threadIdx.x * 4, a.T, x.m);
 #pragma unroll
-  for (int k = 0; k < LLP_POLICY_STATS - 1; ++k) a.stats[1 + k] = (float)sum[k];
+      for (int i = 0; i < 4; ++i) n += x.m[i] ? 1 : 0;
+    }
+  }
+  n = block_sum<NW>(n, shi);
+  const double norm = policy_norm(a, n);
+  const double up = a.dloss != nullptr ? (double)a.dloss[0] : 1.0;
+  double sum[POLICY_SUMS] = {0.0, 0.0, 0.0, 0.0, 0.0, 0.0, 0.0};
+  for (int64_t t0 = 0; t0 < a.T; t0 += SOLO_THREADS * 4) {
+    const int64_t t = t0 + threadIdx.x * 4;
+    if (a.T > SOLO_THREADS * 4) policy_load<VEC>(a, t, x);
+    if (void_layout) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x.m[i] = false;
+    }
+    policy_rows<VEC>(a, t, x, norm, up, by_seq, count, 0, a.S - 1, sum, status);
+  }
+  if (status && a.status) atomicOr(a.status, status);
+  policy_finish(a, policy_total<NW>(sum, shd), fin);
 }
 
 static bool all_aligned(std::initializer_list<const void*> ps, size_t n) {
@@ -306,18 +458,23 @@ static bool all_aligned(std::initializer_list<const void*> ps, size_t n) {
 
 hipError_t launch_policy(const PolicyArgs& a, hipStream_t s) {
   const dim3 block(LOSS_THREADS);
+  const bool vec = all_aligned({a.logp, a.old, a.adv, a.ref, a.ent, a.dlogp, a.dent}, 16) &&
+                   all_aligned({a.mask}, 4);
+  if (a.nblocks == 0) {
+    if (vec) hipLaunchKernelGGL(k_policy_solo<true>, dim3(1), dim3(SOLO_THREADS), 0, s, a);
+    else hipLaunchKernelGGL(k_policy_solo<false>, dim3(1), dim3(SOLO_THREADS), 0, s, a);
+    return hipGetLastError();
+  }
   if (a.ncount > 0) {
     hipLaunchKernelGGL(k_policy_count, dim3((unsigned)a.ncount), block, 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (a.reduction == LLP_REDUCE_SEQ_MEAN) {
+  if (a.reduction == LLP_REDUCE_SEQ_MEAN && a.S > POLICY_SEQS) {
     hipLaunchKernelGGL(k_policy_seqs, dim3(1), dim3(1024), 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  const bool vec = all_aligned({a.logp, a.old, a.adv, a.ref, a.ent, a.dlogp, a.dent}, 16) &&
-                   all_aligned({a.mask}, 4);
   if (vec) hipLaunchKernelGGL(k_policy<true>, dim3((unsigned)a.nblocks), block, 0, s, a);
   else hipLaunchKernelGGL(k_policy<false>, dim3((unsigned)a.nblocks), block, 0, s, a);
   const hipError_t e = hipGetLastError();
@@ -329,9 +486,9 @@ hipError_t launch_policy(const PolicyArgs& a, hipStream_t s) {
 // ------------------------------------------------------------------------------------
 // Preference loss. First launch: the sum of logp - ref_logp over each sequence's scored rows;
 // PREF_SPLIT workgroups share a sequence, workgroup y taking its chunks y, y + PREF_SPLIT, ... of
-// PREF_CHUNK rows, so that a sum's order depends on its sequence alone. Second: one workgroup turns
-// the sums into each pair's loss and gradient coefficient and adds up the losses. Third: the
-// coefficients are spread over the scored rows.
+// PREF_CHUNK rows, so that a sum's order depends on its sequence alone. Second: the sums become each
+// pair's loss and gradient coefficient, and the losses are added up. Third (with few pairs, in
+// one launch with the second): the coefficients are spread over the scored rows.
 // ------------------------------------------------------------------------------------
 __global__ __launch_bounds__(LOSS_THREADS) void k_pref_sum(PrefArgs a) {
   __shared__ double shd[LOSS_THREADS / 64];
@@ -343,11 +500,22 @@ __global__ __launch_bounds__(LOSS_THREADS) void k_pref_sum(PrefArgs a) {
   int n = 0, bad = 0;
   for (int64_t c = b + (int64_t)blockIdx.y * PREF_CHUNK; c < e; c += PREF_SPLIT * PREF_CHUNK) {
     const int64_t ce = c + PREF_CHUNK < e ? c + PREF_CHUNK : e;
-#pragma unroll 8
-    for (int64_t t = c + threadIdx.x; t < ce; t += LOSS_THREADS) {
-      if (a.mask != nullptr && a.mask[t] == 0) continue;
-      const float lp = a.logp[t], rf = a.ref != nullptr ? a.ref[t] : 0.f;
-      if (fabsf(lp) < INFINITY && fabsf(rf) < INFINITY) sum += (double)lp - (double)rf;
+    constexpr int N = PREF_CHUNK / LOSS_THREADS;
+    // A chunk's loads all in flight; the rows' order does not depend on their alignment.
+    float lp[N], rf[N];
+    bool m[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int64_t t = c + i * LOSS_THREADS + threadIdx.x;
+      const bool in = t < ce;
+      m[i] = in && (a.mask == nullptr || a.mask[t] != 0);
+      lp[i] = in ? a.logp[t] : 0.f;
+      rf[i] = in && a.ref != nullptr ? a.ref[t] : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (!m[i]) continue;
+      if (fabsf(lp[i]) < INFINITY && fabsf(rf[i]) < INFINITY) sum += (double)lp[i] - (double)rf[i];
       else bad = 1;
       ++n;
     }
@@ -372,63 +540,83 @@ __device__ __forceinline__ double sigmoid(double x) {
 
 constexpr int PAIR_THREADS = 1024;
 
-__global__ __launch_bounds__(PAIR_THREADS) void k_pref_pairs(PrefArgs a) {
-  __shared__ double shd[PAIR_THREADS / 64];
-  __shared__ int shi[PAIR_THREADS / 64];
+struct PairOut {
+  double loss;       // weighted
+  float coef[2];     // of the scored rows of the chosen and of the rejected response
+  float l, chosen, rejected;
+  bool unfit;        // a value that is not finite was met
+};
+
+// Pair p from its sums; `up` is the upstream gradient over the number of pairs (for the mean).
+__device__ __forceinline__ PairOut pref_pair(const PrefArgs& a, int p, double up) {
+  double R[2] = {0.0, 0.0}, per[2] = {1.0, 1.0};
+  const float w = a.weight != nullptr ? a.weight[p] : 1.f;
+  bool odd = false;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    int n = 0;
+#pragma unroll
+    for (int y = 0; y < PREF_SPLIT; ++y) {
+      const int64_t o = ((int64_t)2 * p + k) * PREF_SPLIT + y;
+      R[k] += a.sum[o];
+      const int c = a.cnt[o];
+      if (c < 0) odd = true;
+      n += c;
+    }
+    if (a.average) {
+      per[k] = n > 0 ? 1.0 / (double)n : 0.0;
+      R[k] *= per[k];
+    }
+  }
+  PairOut o;
+  o.unfit = w != 0.f && (odd || !(fabsf(w) < INFINITY));
+  const bool ok = w != 0.f && !o.unfit;
+  const double h = R[0] - R[1], m = a.beta * h - a.gamma;
+  double l, g;   // the pair's loss and its derivative by h
+  if (a.kind == LLP_PREF_SIGMOID) {
+    l = (1.0 - a.smooth) * softplus(-m) + a.smooth * softplus(m);
+    g = a.beta * (a.smooth - sigmoid(-m));
+  } else if (a.kind == LLP_PREF_HINGE) {
+    l = fmax(0.0, 1.0 - m);
+    g = m < 1.0 ? -a.beta : 0.0;
+  } else {
+    const double x = h - 0.5 / a.beta;
+    l = x * x;
+    g = 2.0 * x;
+  }
+  const double c = ok ? up * (double)w * g : 0.0;
+  o.coef[0] = (float)(c * per[0]);
+  o.coef[1] = (float)(-c * per[1]);
+  o.loss = ok ? (double)w * l : 0.0;
+  o.l = ok ? (float)l : 0.f;
+  o.chosen = ok ? (float)(a.beta * R[0]) : 0.f;
+  o.rejected = ok ? (float)(a.beta * R[1]) : 0.f;
+  return o;
+}
+
+// All pairs, by a workgroup of NW waves: coefficients to `coef`, and, with `write`, the outputs. A
+// malformed layout makes everything 0.
+template <int NW>
+__device__ __forceinline__ void pref_pairs(const PrefArgs& a, float* coef, bool write, double* shd, int* shi) {
   int bad = 0;
-  for (int i = threadIdx.x; i <= 2 * a.P; i += PAIR_THREADS) bad += cu_bad(a.cu, 2 * a.P, a.T, i) ? 1 : 0;
-  const bool void_layout = block_sum<PAIR_THREADS / 64>(bad, shi) != 0;
+  for (int i = threadIdx.x; i <= 2 * a.P; i += 64 * NW) bad += cu_bad(a.cu, 2 * a.P, a.T, i) ? 1 : 0;
+  const bool void_layout = block_sum<NW>(bad, shi) != 0;
   const double up = (a.dloss != nullptr ? (double)a.dloss[0] : 1.0) / (a.mean ? (double)a.P : 1.0);
   double total = 0.0;
   bool unfit = false;
-  for (int p = threadIdx.x; p < a.P; p += PAIR_THREADS) {
-    double R[2] = {0.0, 0.0}, per[2] = {1.0, 1.0};
-    bool ok = !void_layout;
-    const float w = a.weight != nullptr ? a.weight[p] : 1.f;
-    bool odd = false;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      int n = 0;
-#pragma unroll
-      for (int y = 0; y < PREF_SPLIT; ++y) {
-        const int64_t o = ((int64_t)2 * p + k) * PREF_SPLIT + y;
-        R[k] += a.sum[o];
-        const int c = a.cnt[o];
-        if (c < 0) odd = true;
-        n += c;
-      }
-      if (a.average) {
-        per[k] = n > 0 ? 1.0 / (double)n : 0.0;
-        R[k] *= per[k];
-      }
-    }
-    if (w == 0.f) ok = false;
-    else if (odd || !(fabsf(w) < INFINITY)) {
-      if (ok) unfit = true;
-      ok = false;
-    }
-    const double h = R[0] - R[1], m = a.beta * h - a.gamma;
-    double l, g;   // the pair's loss and its derivative by h
-    if (a.kind == LLP_PREF_SIGMOID) {
-      l = (1.0 - a.smooth) * softplus(-m) + a.smooth * softplus(m);
-      g = a.beta * (a.smooth - sigmoid(-m));
-    } else if (a.kind == LLP_PREF_HINGE) {
-      l = fmax(0.0, 1.0 - m);
-      g = m < 1.0 ? -a.beta : 0.0;
-    } else {
-      const double x = h - 0.5 / a.beta;
-      l = x * x;
-      g = 2.0 * x;
-    }
-    const double c = ok ? up * (double)w * g : 0.0;
-    a.coef[2 * p] = (float)(c * per[0]);
-    a.coef[2 * p + 1] = (float)(-c * per[1]);
-    if (ok) total += (double)w * l;
-    if (a.pair_loss != nullptr) a.pair_loss[p] = ok ? (float)l : 0.f;
-    if (a.chosen != nullptr) a.chosen[p] = ok ? (float)(a.beta * R[0]) : 0.f;
-    if (a.rejected != nullptr) a.rejected[p] = ok ? (float)(a.beta * R[1]) : 0.f;
+  for (int p = threadIdx.x; p < a.P; p += 64 * NW) {
+    PairOut o{};
+    if (!void_layout) o = pref_pair(a, p, up);
+    unfit |= o.unfit;
+    total += o.loss;
+    coef[2 * p] = o.coef[0];
+    coef[2 * p + 1] = o.coef[1];
+    if (write && a.pair_loss != nullptr) a.pair_loss[p] = o.l;
+    if (write && a.chosen != nullptr) a.chosen[p] = o.chosen;
+    if (write && a.rejected != nullptr) a.rejected[p] = o.rejected;
   }
-  total = block_sum<PAIR_THREADS / 64>(total, shd);
+  if (!write) return;
+  total = block_sum<NW>(total, shd);
   if (unfit && a.status) atomicOr(a.status, LLP_STATUS_VALUE_NOT_FINITE);
   if (threadIdx.x == 0) {
     a.loss[0] = (float)(a.mean && a.P > 0 ? total / (double)a.P : total);
@@ -436,21 +624,42 @@ __global__ __launch_bounds__(PAIR_THREADS) void k_pref_pairs(PrefArgs a) {
   }
 }
 
-template <bool VEC>
+__global__ __launch_bounds__(PAIR_THREADS) void k_pref_pairs(PrefArgs a) {
+  __shared__ double shd[PAIR_THREADS / 64];
+  __shared__ int shi[PAIR_THREADS / 64];
+  pref_pairs<PAIR_THREADS / 64>(a, a.coef, true, shd, shi);
+}
+
+// FEW (at most PREF_FEW pairs): every workgroup works the pairs out for itself, the first one
+// writes them out, and the launch in between is saved.
+constexpr int PREF_FEW = 128;
+
+template <bool VEC, bool FEW>
 __global__ __launch_bounds__(LOSS_THREADS) void k_pref_grad(PrefArgs a) {
-  const int64_t t0 = (int64_t)blockIdx.x * LOSS_THREADS * 4;
+  constexpr int NW = LOSS_THREADS / 64;
   __shared__ int ends[2];
-  // The sequences this workgroup's rows lie in bound every thread's search.
-  if (threadIdx.x < 2) {
-    const int64_t t = threadIdx.x == 0 ? t0 : (t0 + LOSS_THREADS * 4 - 1 < a.T - 1 ? t0 + LOSS_THREADS * 4 - 1 : a.T - 1);
-    ends[threadIdx.x] = seq_of(a.cu, t, 0, 2 * a.P - 1);
+  __shared__ float own[FEW ? 2 * PREF_FEW : 1];
+  const int64_t t0 = (int64_t)blockIdx.x * LOSS_THREADS * 4;
+  const int64_t t = t0 + threadIdx.x * 4;
+  bool m[4];
+  mask4<VEC>(a.mask, t, a.T, m);
+  // The sequences of the workgroup's first and last rows bound every thread's search.
+  const int w = threadIdx.x >> 6;
+  if (w < 2 && t0 < a.T) {
+    const int64_t last = t0 + LOSS_THREADS * 4 - 1 < a.T - 1 ? t0 + LOSS_THREADS * 4 - 1 : a.T - 1;
+    const int s = seq_of_wave(a.cu, w == 0 ? t0 : last, 2 * a.P - 1);
+    if ((threadIdx.x & 63) == 0) ends[w] = s;
+  }
+  if constexpr (FEW) {
+    __shared__ double shd[NW];
+    __shared__ int shi[NW];
+    pref_pairs<NW>(a, own, blockIdx.x == 0, shd, shi);
   }
   __syncthreads();
-  const int64_t t = t0 + threadIdx.x * 4;
-  if (t >= a.T) return;
-  bool m[4];
+  if (t >= a.T || a.dlogp == nullptr) return;
+  const float* coef = FEW ? own : a.coef;
+  const int lo = ends[0], hi = ends[1] > lo ? ends[1] : lo;
   float g[4];
-  mask4<VEC>(a.mask, t, a.T, m);
   int s = -1, s_end = 0;
   float c = 0.f;
 #pragma unroll
@@ -458,13 +667,23 @@ __global__ __launch_bounds__(LOSS_THREADS) void k_pref_grad(PrefArgs a) {
     g[i] = 0.f;
     if (!m[i]) continue;
     if (s < 0 || t + i >= s_end) {
-      s = seq_of(a.cu, t + i, s < 0 ? ends[0] : s, ends[1] > ends[0] ? ends[1] : ends[0]);
+      s = seq_of(a.cu, t + i, s < 0 ? lo : s, hi);
       s_end = a.cu[s + 1];
-      c = a.coef[s];
+      c = coef[s];
     }
     g[i] = c;
   }
   store4<VEC>(a.dlogp, t, a.T, g);
+}
+
+template <bool FEW>
+static void launch_pref_grad(const PrefArgs& a, hipStream_t s) {
+  const int64_t n = a.dlogp != nullptr && a.T > 0 ? (a.T + LOSS_THREADS * 4 - 1) / (LOSS_THREADS * 4) : 1;
+  const dim3 grid((unsigned)n), block(LOSS_THREADS);
+  if (all_aligned({a.dlogp}, 16) && all_aligned({a.mask}, 4))
+    hipLaunchKernelGGL((k_pref_grad<true, FEW>), grid, block, 0, s, a);
+  else
+    hipLaunchKernelGGL((k_pref_grad<false, FEW>), grid, block, 0, s, a);
 }
 
 hipError_t launch_preference(const PrefArgs& a, hipStream_t s) {
@@ -473,12 +692,14 @@ hipError_t launch_preference(const PrefArgs& a, hipStream_t s) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
+  if (a.P <= PREF_FEW) {
+    launch_pref_grad<true>(a, s);
+    return hipGetLastError();
+  }
   hipLaunchKernelGGL(k_pref_pairs, dim3(1), dim3(PAIR_THREADS), 0, s, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.dlogp == nullptr || a.T == 0) return e;
-  const dim3 grid((unsigned)((a.T + LOSS_THREADS * 4 - 1) / (LOSS_THREADS * 4))), block(LOSS_THREADS);
-  if (all_aligned({a.dlogp}, 16) && all_aligned({a.mask}, 4)) hipLaunchKernelGGL(k_pref_grad<true>, grid, block, 0, s, a);
-  else hipLaunchKernelGGL(k_pref_grad<false>, grid, block, 0, s, a);
+  launch_pref_grad<false>(a, s);
   return hipGetLastError();
 }
 

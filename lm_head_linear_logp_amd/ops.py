@@ -61,15 +61,24 @@ def _ready(dev):
     _ready_devices.add(dev)
 
 
+_fns = {}
+
+
+def _fn(name):
+    f = _fns.get(name)
+    if f is None:
+        f = _fns[name] = getattr(A.load(), name)
+    return f
+
+
 def _call(dev, name, *args):
     """One execution call of the library on `dev`'s current stream, with `dev` current."""
-    fn = getattr(A.load(), name)
     stream = torch.cuda.current_stream(dev).cuda_stream
     if torch.cuda.current_device() == dev.index:
-        st = fn(*args, stream)
+        st = _fn(name)(*args, stream)
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, stream)
+            st = _fn(name)(*args, stream)
     if st != A.LLP_OK:
         _check(st, name)
 
@@ -77,7 +86,7 @@ def _call(dev, name, *args):
 def _space(name, req, dev, workspace):
     """The call's workspace: the caller's when it is large enough, else a new one."""
     n = C.c_size_t(0)
-    st = getattr(A.load(), name)(C.byref(req), C.byref(n))
+    st = _fn(name)(C.byref(req), C.byref(n))
     if st != A.LLP_OK:
         _check(st, name)
     if workspace is None or workspace.numel() < n.value:
@@ -153,7 +162,7 @@ def forward_int8(hidden: torch.Tensor, hidden_scale: torch.Tensor, weight: torch
     r.flags = A.LLP_FLAG_WANT_ENTROPY if want_entropy else 0
     r.hidden_size = K
     _vocab(r.vocab, offset, V, real_vocab, padded_vocab, rank, world)
-    _layout(r.layout, T, loss_mask, cu_seqlens, dev)
+    r.layout = _layout(T, loss_mask, cu_seqlens, dev)
     r.temperature = float(temperature)
     _status(status, dev)
     r.status_word = _ptr(status)
@@ -170,15 +179,25 @@ def forward_int8(hidden: torch.Tensor, hidden_scale: torch.Tensor, weight: torch
     return out
 
 
-def _layout(l, T, loss_mask, cu_seqlens, dev):
-    l.num_tokens = T
-    l.loss_mask = _opt(loss_mask, "loss_mask", _U8, T, dev)
-    if cu_seqlens is not None:
+def _layout(T, loss_mask, cu_seqlens, dev):
+    mask = _opt(loss_mask, "loss_mask", _U8, T, dev)
+    if cu_seqlens is None:
+        return A.llp_token_layout(T, 0, 0, None, mask)
+    if not (type(cu_seqlens) is torch.Tensor and cu_seqlens.dtype is _I32 and cu_seqlens.dim() == 1
+            and cu_seqlens.device == dev and cu_seqlens.is_contiguous()):
         _need(cu_seqlens, "cu_seqlens", _I32, 1, dev)
-        if cu_seqlens.shape[0] < 1:
-            raise ValueError("cu_seqlens needs at least one entry")
-        l.cu_seqlens = cu_seqlens.data_ptr()
-        l.num_seqs = cu_seqlens.shape[0] - 1
+    n = cu_seqlens.shape[0]
+    if n < 1:
+        raise ValueError("cu_seqlens needs at least one entry")
+    return A.llp_token_layout(T, n - 1, 0, cu_seqlens.data_ptr(), mask)
+
+
+def _len(t, name, dtype):
+    """Device and length of the 1-d tensor that sets a call's row count."""
+    dev = _tensor(t, name).device
+    if not (t.dtype is dtype and t.dim() == 1 and t.is_contiguous()):
+        _need(t, name, dtype, 1, dev)
+    return dev, t.shape[0]
 
 
 # ---- Losses ----------------------------------------------------------------------------------
@@ -201,29 +220,21 @@ def policy_grads(logp: torch.Tensor, old_logp: torch.Tensor, advantages: torch.T
     Returns loss [1], stats [8] (loss, policy, kl, entropy, clipped, ratio, old_logp - logp as
     means, then the number of scored rows), dlogp [T] and dentropy [T] (None without `entropy`;
     both None unless want_grad)."""
-    dev = _tensor(logp, "logp").device
-    _need(logp, "logp", _F32, 1, dev)
-    T = logp.shape[0]
-    r = A.llp_policy_request()
-    r.logp = logp.data_ptr()
-    r.old_logp = _at(old_logp, "old_logp", _F32, T, dev)
-    r.advantages = _at(advantages, "advantages", _F32, T, dev)
-    r.ref_logp = _opt(ref_logp, "ref_logp", _F32, T, dev)
-    r.entropy = _opt(entropy, "entropy", _F32, T, dev)
+    dev, T = _len(logp, "logp", _F32)
     if ref_logp is None and kl_coef:
         raise ValueError("kl_coef needs ref_logp")
     if entropy is None and entropy_coef:
         raise ValueError("entropy_coef needs entropy")
-    _layout(r.layout, T, loss_mask, cu_seqlens, dev)
-    r.clip_low, r.clip_high, r.dual_clip = float(clip_low), float(clip_high), float(dual_clip)
-    r.kl_coef, r.entropy_coef = float(kl_coef), float(entropy_coef)
-    r.kl_kind = _choice(_KL, kl, "kl")
-    r.reduction = _choice(_REDUCE, reduction, "reduction")
     if reduction == "seq_mean" and cu_seqlens is None:
         raise ValueError("reduction 'seq_mean' needs cu_seqlens")
-    r.denominator = _opt(denominator, "denominator", _F32, 1, dev)
     _status(status, dev)
-    r.status_word = _ptr(status)
+    r = A.llp_policy_request(
+        logp.data_ptr(), _at(old_logp, "old_logp", _F32, T, dev),
+        _at(advantages, "advantages", _F32, T, dev), _opt(ref_logp, "ref_logp", _F32, T, dev),
+        _opt(entropy, "entropy", _F32, T, dev), _layout(T, loss_mask, cu_seqlens, dev), clip_low,
+        clip_high, dual_clip, kl_coef, entropy_coef, _choice(_KL, kl, "kl"),
+        _choice(_REDUCE, reduction, "reduction"),
+        _opt(denominator, "denominator", _F32, 1, dev), _ptr(status))
     dl = _opt(dloss, "dloss", _F32, 1, dev)
     has_ent = entropy is not None and want_grad
     if out is not None:
@@ -236,10 +247,9 @@ def policy_grads(logp: torch.Tensor, old_logp: torch.Tensor, advantages: torch.T
     _check_space(workspace, dev)
     _ready(dev)
     if out is None:
-        out = dict(loss=torch.empty(1, dtype=_F32, device=dev),
-                   stats=torch.empty(A.LLP_POLICY_STATS, dtype=_F32, device=dev),
-                   dlogp=torch.empty(T, dtype=_F32, device=dev) if want_grad else None,
-                   dentropy=torch.empty(T, dtype=_F32, device=dev) if has_ent else None)
+        new = logp.new_empty
+        out = dict(loss=new(1), stats=new(A.LLP_POLICY_STATS), dlogp=new(T) if want_grad else None,
+                   dentropy=new(T) if has_ent else None)
     o = A.llp_policy_out(out["loss"].data_ptr(), out["stats"].data_ptr(), dl,
                          out["dlogp"].data_ptr() if want_grad else None,
                          out["dentropy"].data_ptr() if has_ent else None)
@@ -264,26 +274,19 @@ def preference_grads(logp: torch.Tensor, cu_seqlens: torch.Tensor, *,
     average: mean log ratio per response instead of the sum. Returns loss [1], pair_loss [P],
     chosen [P] and rejected [P] (beta times the responses' log ratios) and dlogp [T] (None
     unless want_grad)."""
-    dev = _tensor(logp, "logp").device
-    _need(logp, "logp", _F32, 1, dev)
-    T = logp.shape[0]
-    r = A.llp_pref_request()
-    r.logp = logp.data_ptr()
-    r.ref_logp = _opt(ref_logp, "ref_logp", _F32, T, dev)
-    _need(cu_seqlens, "cu_seqlens", _I32, 1, dev)
-    if cu_seqlens.shape[0] % 2 == 0:
-        raise ValueError(f"cu_seqlens has {cu_seqlens.shape[0]} entries; 2 * pairs + 1 expected")
-    P = (cu_seqlens.shape[0] - 1) // 2
+    dev, T = _len(logp, "logp", _F32)
+    layout = _layout(T, loss_mask, _tensor(cu_seqlens, "cu_seqlens"), dev)
+    if layout.num_seqs % 2:
+        raise ValueError(f"cu_seqlens has {layout.num_seqs + 1} entries; 2 * pairs + 1 expected")
+    P = layout.num_seqs // 2
     if P == 0 and T > 0:
         raise ValueError("cu_seqlens holds no pair")
-    _layout(r.layout, T, loss_mask, cu_seqlens, dev)
-    r.pair_weight = _opt(pair_weight, "pair_weight", _F32, P, dev)
-    r.beta, r.gamma, r.label_smoothing = float(beta), float(gamma), float(label_smoothing)
-    r.kind = _choice(_PREF, kind, "kind")
-    r.average = 1 if average else 0
-    r.reduction = _choice(_PREF_REDUCE, reduction, "reduction")
     _status(status, dev)
-    r.status_word = _ptr(status)
+    r = A.llp_pref_request(
+        logp.data_ptr(), _opt(ref_logp, "ref_logp", _F32, T, dev),
+        _opt(pair_weight, "pair_weight", _F32, P, dev), layout, beta, gamma, label_smoothing,
+        _choice(_PREF, kind, "kind"), 1 if average else 0,
+        _choice(_PREF_REDUCE, reduction, "reduction"), 0, _ptr(status))
     dl = _opt(dloss, "dloss", _F32, 1, dev)
     if out is not None:
         _vec(out["loss"], "out['loss']", _F32, 1, dev)
@@ -294,11 +297,9 @@ def preference_grads(logp: torch.Tensor, cu_seqlens: torch.Tensor, *,
     _check_space(workspace, dev)
     _ready(dev)
     if out is None:
-        out = dict(loss=torch.empty(1, dtype=_F32, device=dev),
-                   pair_loss=torch.empty(P, dtype=_F32, device=dev),
-                   chosen=torch.empty(P, dtype=_F32, device=dev),
-                   rejected=torch.empty(P, dtype=_F32, device=dev),
-                   dlogp=torch.empty(T, dtype=_F32, device=dev) if want_grad else None)
+        new = logp.new_empty
+        out = dict(loss=new(1), pair_loss=new(P), chosen=new(P), rejected=new(P),
+                   dlogp=new(T) if want_grad else None)
     o = A.llp_pref_out(out["loss"].data_ptr(), _ptr(out["pair_loss"]), _ptr(out["chosen"]),
                        _ptr(out["rejected"]), dl, out["dlogp"].data_ptr() if want_grad else None)
     ws = _space("llp_preference_workspace_bytes", r, dev, workspace)
@@ -393,12 +394,12 @@ def preference_loss(logp: torch.Tensor, cu_seqlens: torch.Tensor, *,
 def _embedding_request(token_ids, token_mask, T, H, local_size, scale, offset, real_vocab,
                        padded_vocab, rank, world, status, dev):
     r = A.llp_embedding_request()
-    r.token_ids = _ptr(token_ids)
+    r.token_ids = token_ids.data_ptr()
     r.token_mask = _opt(token_mask, "token_mask", _U8, T, dev)
     r.num_tokens = T
     _vocab(r.vocab, offset, local_size, real_vocab, padded_vocab, rank, world)
     r.hidden_size = H
-    r.scale = float(scale)
+    r.scale = scale
     _status(status, dev)
     r.status_word = _ptr(status)
     return r
