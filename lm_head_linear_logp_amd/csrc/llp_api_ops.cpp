@@ -235,7 +235,7 @@ struct EmbWs {
 EmbWs embedding_ws(const llp_embedding_request& r) {
   EmbWs w{};
   Regions g;
-  const int64_t T = r.num_tokens, units = (T + EMB_UNIT - 1) / EMB_UNIT;
+  const int64_t T = r.num_tokens, units = (T + emb_unit(T) - 1) / emb_unit(T);
   w.loc = g.take((size_t)T * 4);
   w.start = g.take((size_t)(local_real(r.vocab) + 1) * 4);
   w.order = g.take((size_t)T * 4);
@@ -499,6 +499,7 @@ LLP_API llp_status llp_embedding_backward(const llp_embedding_request* req, cons
   // One group of local rows per compute unit, within what the sort's counters hold.
   const int64_t R = (a.n_real + 255) / 256;
   a.rows_per_group = (int32_t)(R < 1 ? 1 : R > EMB_ROWS_MAX ? EMB_ROWS_MAX : R);
+  a.unit = emb_unit(T);
   a.scale = req->scale;
   a.overwrite = (req->flags & LLP_FLAG_OVERWRITE_GRADS) != 0;
   a.dout = dout;

@@ -6,6 +6,8 @@
 
 namespace llp {
 
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
 // Local row of token t, or -1 (masked, another shard's, or out of range: then *status).
 template <class Args>
 __device__ __forceinline__ int emb_local(const Args& a, int64_t t, int& status) {
@@ -68,7 +70,9 @@ __global__ __launch_bounds__(64 * EMB_WAVES) void k_embed(EmbArgs a, int chunks,
 #pragma unroll
     for (int i = 0; i < EMB_PIECE; ++i) {
       const int c = c0 + i * 64 + lane;
-      if (c < end) dst[c] = loc >= 0 ? emb_scale<BF16>(v[i], a.scale) : v[i];
+      // Past the caches, which hold the rows that other tokens read again (129 -> 119 us for 56583
+      // tokens of 4096 columns).
+      if (c < end) __builtin_nontemporal_store(loc >= 0 ? emb_scale<BF16>(v[i], a.scale) : v[i], dst + c);
     }
   }
 }
@@ -109,7 +113,7 @@ __global__ __launch_bounds__(256) void k_embed_ids(EmbBwdArgs a) {
   if (status && a.status) atomicOr(a.status, status);
 }
 
-constexpr int SORT_WAVES = 16, SORT_UNROLL = 8, SORT_LIST = 256;
+constexpr int SORT_WAVES = 16, SORT_UNROLL = 16, SORT_LIST = 256;
 
 // Hands out positions, in lane order, to the lanes with `in` (local row r of the group, token t).
 __device__ __forceinline__ void sort_place(const EmbBwdArgs& a, volatile int* next, int lo, bool in,
@@ -132,6 +136,8 @@ __device__ __forceinline__ void sort_place(const EmbBwdArgs& a, volatile int* ne
   }
 }
 
+// RAW: from the caller's ids (few tokens: one launch less); else from k_embed_ids.
+template <bool RAW>
 __global__ __launch_bounds__(64 * SORT_WAVES) void k_embed_sort(EmbBwdArgs a) {
   __shared__ int cnt[SORT_WAVES * EMB_ROWS_MAX];   // [wave][row]
   __shared__ int2 list[SORT_WAVES][SORT_LIST];     // token, row
@@ -145,13 +151,15 @@ __global__ __launch_bounds__(64 * SORT_WAVES) void k_embed_sort(EmbBwdArgs a) {
   int* const mine = cnt + w * R;
   for (int i = lane; i < nr; i += 64) mine[i] = 0;
   __builtin_amdgcn_wave_barrier();
+  int status = 0;
+  auto local = [&](int t) { return RAW ? emb_local(a, t, status) : a.loc[t]; };
   int below = 0, found = 0, resume = te;   // resume: the tokens from here on are not in the list
   for (int t0 = tb; t0 < te; t0 += 64 * SORT_UNROLL) {
     int loc[SORT_UNROLL];
 #pragma unroll
     for (int u = 0; u < SORT_UNROLL; ++u) {
       const int t = t0 + u * 64 + lane;
-      loc[u] = t < te ? a.loc[t] : -1;
+      loc[u] = t < te ? local(t) : -1;
     }
 #pragma unroll
     for (int u = 0; u < SORT_UNROLL; ++u) {
@@ -175,6 +183,7 @@ __global__ __launch_bounds__(64 * SORT_WAVES) void k_embed_sort(EmbBwdArgs a) {
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) below += __shfl_xor(below, off);
   if (lane == 0) wbelow[w] = below;
+  if (RAW && blockIdx.x == 0 && status && a.status) atomicOr(a.status, status);
   __syncthreads();
   // Exclusive scan of the rows' totals, one row per thread.
   static_assert(EMB_ROWS_MAX <= 64 * SORT_WAVES, "one row per thread");
@@ -212,48 +221,61 @@ __global__ __launch_bounds__(64 * SORT_WAVES) void k_embed_sort(EmbBwdArgs a) {
   }
   for (int t0 = resume; t0 < te; t0 += 64) {
     const int t = t0 + lane;
-    const int loc = t < te ? a.loc[t] : -1;
+    const int loc = t < te ? local(t) : -1;
     const uint32_t q = (uint32_t)loc - (uint32_t)lo;
     sort_place(a, mine, lo, loc >= 0 && q < (uint32_t)nr, (int)q, t, lane);
   }
 }
 
+constexpr int64_t SORT_RAW_TOKENS = 8192;
+
 hipError_t launch_embedding_sort(const EmbBwdArgs& a, hipStream_t s) {
   if (a.T <= 0) return hipGetLastError();
+  const int64_t groups = (a.n_real + a.rows_per_group - 1) / a.rows_per_group;
+  const dim3 block(64 * SORT_WAVES);
+  if (a.T <= SORT_RAW_TOKENS) {
+    // A shard without real rows still reports ids out of range (a group with no rows).
+    hipLaunchKernelGGL(k_embed_sort<true>, dim3((unsigned)(groups > 0 ? groups : 1)), block, 0, s, a);
+    return hipGetLastError();
+  }
   hipLaunchKernelGGL(k_embed_ids, dim3((unsigned)((a.T + 255) / 256)), dim3(256), 0, s, a);
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || a.n_real <= 0) return e;
-  const int64_t groups = (a.n_real + a.rows_per_group - 1) / a.rows_per_group;
-  hipLaunchKernelGGL(k_embed_sort, dim3((unsigned)groups), dim3(64 * SORT_WAVES), 0, s, a);
+  if (e != hipSuccess || groups == 0) return e;
+  hipLaunchKernelGGL(k_embed_sort<false>, dim3((unsigned)groups), block, 0, s, a);
   return hipGetLastError();
 }
 
 // ------------------------------------------------------------------------------------
-// The sums: the sorted rows are cut into units of EMB_UNIT, whatever tokens they hold, so a token
+// The sums: the sorted rows are cut into units of a.unit, whatever tokens they hold, so a token
 // that fills half the batch costs no more than any other. A unit adds up its rows in order, 8
 // columns per thread in fp32, and writes each token's sum when the token changes; the sums of a
 // token whose rows reach into another unit go to `part` (slot 0: it began in an earlier unit;
 // slot 1: it begins here), and the unit where such a token begins notes in `span` how many units
 // follow. Behind the units, when the gradient is overwritten, workgroups write the rows that no
-// token names as 0. Bound by memory: one read of dout, one write (or read and write) of the
-// touched rows.
+// token names as 0, beside the units' reads. Bound by memory: one read of dout, one write (or
+// read and write) of the touched rows.
 // ------------------------------------------------------------------------------------
 constexpr int EMB_ZERO_ROWS = 16;
 
-template <bool BF16>
+// NT (bf16): read once, not kept in the caches.
+template <bool BF16, bool NT = false>
 __device__ __forceinline__ void emb_load8(const void* base, int64_t off, float (&v)[8]) {
   if constexpr (BF16) {
-    const u32x4 u = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(base) + off);
+    const u32x4* p = reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(base) + off);
+    const u32x4 u = NT ? __builtin_nontemporal_load(p) : *p;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       v[2 * i] = __builtin_bit_cast(float, u[i] << 16);
       v[2 * i + 1] = __builtin_bit_cast(float, u[i] & 0xFFFF0000u);
     }
   } else {
-    const float4 x = *reinterpret_cast<const float4*>(static_cast<const float*>(base) + off);
-    const float4 y = *reinterpret_cast<const float4*>(static_cast<const float*>(base) + off + 4);
-    v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-    v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
+    const f32x4* p = reinterpret_cast<const f32x4*>(static_cast<const float*>(base) + off);
+    const f32x4 x = p[0], y = p[1];   // half lines each: the caches put them together
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = x[i];
+      v[4 + i] = y[i];
+    }
   }
 }
 
@@ -262,7 +284,9 @@ __device__ __forceinline__ void emb_store8(float* p, const float (&v)[8]) {
   *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
 }
 
-// dweight row of a finished sum: scale * sum, added to what is there or not.
+// dweight row of a finished sum: scale * sum, added to what is there or not. (Past the caches
+// these half-line stores were slow, 145 us a call for 4096 tokens over 37984 rows against 130;
+// swapped between lanes so that each took 1 KB in a row, they ran no faster than this.)
 __device__ __forceinline__ void emb_finish(const EmbBwdArgs& a, int row, int c, float (&v)[8]) {
   float* p = a.dW + (int64_t)row * a.ldw + c;
 #pragma unroll
@@ -276,8 +300,10 @@ __device__ __forceinline__ void emb_finish(const EmbBwdArgs& a, int row, int c, 
   emb_store8(p, v);
 }
 
-// Rows v0 .. v0 + EMB_ZERO_ROWS - 1 without a token become 0: whole cache lines per wave and store.
-// (The workgroups of one v0 share the columns.)
+// Rows v0 .. v0 + EMB_ZERO_ROWS - 1 without a token become 0, whole cache lines per wave and
+// store, past the caches (a shard of 37984 rows, 4096 tokens: 143 -> 130 us a call). The
+// workgroups of one v0 share the columns. In a launch of its own, with one store per thread,
+// this part reaches 6.7 TB/s, but then nothing runs beside it: 137 us.
 __device__ __forceinline__ void emb_zero(const EmbBwdArgs& a, int64_t v0) {
   const int lane = threadIdx.x & 63;
   const int64_t mine = v0 + lane;
@@ -289,11 +315,14 @@ __device__ __forceinline__ void emb_zero(const EmbBwdArgs& a, int64_t v0) {
     rows &= rows - 1;
     float* p = a.dW + (v0 + i) * a.ldw;
     for (int c = (blockIdx.y * blockDim.x + threadIdx.x) * 4; c < a.H; c += gridDim.y * blockDim.x * 4)
-      *reinterpret_cast<float4*>(p + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+      __builtin_nontemporal_store(f32x4{0.f, 0.f, 0.f, 0.f}, reinterpret_cast<f32x4*>(p + c));
   }
 }
 
-template <bool BF16>
+// NT: dout is larger than the 256 MB of the last-level cache, so nothing of it is still there from
+// its producer, and what else is there is worth keeping (56583 x 4096 bf16: 614 -> 595 us a call;
+// 4096 x 4096, which the cache holds: 129 -> 135 us the other way round).
+template <bool BF16, bool NT>
 __global__ __launch_bounds__(256) void k_embed_sum(EmbBwdArgs a, int units) {
   if ((int)blockIdx.x >= units) {
     emb_zero(a, ((int64_t)blockIdx.x - units) * EMB_ZERO_ROWS);
@@ -301,15 +330,15 @@ __global__ __launch_bounds__(256) void k_embed_sum(EmbBwdArgs a, int units) {
   }
   const int c = ((int)blockIdx.y * (int)blockDim.x + (int)threadIdx.x) * 8;
   const int N = a.start[a.n_real];
-  const int u = blockIdx.x, s0 = u * EMB_UNIT;
-  const int s1 = s0 + EMB_UNIT < N ? s0 + EMB_UNIT : N;
+  const int u = blockIdx.x, s0 = u * a.unit;
+  const int s1 = s0 + a.unit < N ? s0 + a.unit : N;
   const bool began = s0 < N && s0 > 0 && a.row[s0 - 1] == a.row[s0];
   const bool goes_on = s0 < N && s1 < N && a.row[s1 - 1] == a.row[s1];
   if (blockIdx.y == 0 && threadIdx.x == 0) {
     int n = 0;
     if (goes_on) {
       const int r = a.row[s1];
-      if (a.start[r] >= s0) n = (a.start[r + 1] - 1) / EMB_UNIT - u;
+      if (a.start[r] >= s0) n = (a.start[r + 1] - 1) / a.unit - u;
     }
     a.span[u] = n;
   }
@@ -322,7 +351,7 @@ __global__ __launch_bounds__(256) void k_embed_sum(EmbBwdArgs a, int units) {
 #pragma unroll
     for (int i = 0; i < B; ++i) {
       const int k = s + i < s1 ? s + i : s1 - 1;
-      emb_load8<BF16>(a.dout, (int64_t)a.order[k] * a.ldo + c, v[i]);
+      emb_load8<BF16, NT>(a.dout, (int64_t)a.order[k] * a.ldo + c, v[i]);
     }
 #pragma unroll
     for (int i = 0; i < B; ++i) {
@@ -346,7 +375,7 @@ __global__ __launch_bounds__(256) void k_embed_sum(EmbBwdArgs a, int units) {
 // Tokens shared by several units: a workgroup looks through FIX_UNITS units and, where such a
 // token begins, adds its partial sums: 8 waves take consecutive eighths of the units, then their
 // sums are added in order.
-constexpr int FIX_WAVES = 8, FIX_UNITS = 4;
+constexpr int FIX_WAVES = 8, FIX_UNITS = 2;
 
 __global__ __launch_bounds__(64 * FIX_WAVES) void k_embed_fix(EmbBwdArgs a, int units) {
   __shared__ float sh[FIX_WAVES][64][8];
@@ -378,20 +407,22 @@ __global__ __launch_bounds__(64 * FIX_WAVES) void k_embed_fix(EmbBwdArgs a, int 
       for (int k = 1; k < FIX_WAVES; ++k)
 #pragma unroll
         for (int x = 0; x < 8; ++x) acc[x] += sh[k][lane][x];
-      emb_finish(a, a.row[u * EMB_UNIT + EMB_UNIT], c, acc);
+      emb_finish(a, a.row[(u + 1) * a.unit], c, acc);
     }
     __syncthreads();
   }
 }
 
 hipError_t launch_embedding_sum(const EmbBwdArgs& a, hipStream_t s) {
-  const int units = a.n_real > 0 ? (int)((a.T + EMB_UNIT - 1) / EMB_UNIT) : 0;
+  const int units = a.n_real > 0 ? (int)((a.T + a.unit - 1) / a.unit) : 0;
   const int64_t zero = a.overwrite ? (a.local_size + EMB_ZERO_ROWS - 1) / EMB_ZERO_ROWS : 0;
   if (units + zero == 0) return hipGetLastError();
   const int threads = a.H / 8 >= 256 ? 256 : (a.H / 8 + 63) / 64 * 64;
   const dim3 grid((unsigned)(units + zero), (unsigned)((a.H / 8 + threads - 1) / threads));
-  if (a.bf16) hipLaunchKernelGGL(k_embed_sum<true>, grid, dim3(threads), 0, s, a, units);
-  else hipLaunchKernelGGL(k_embed_sum<false>, grid, dim3(threads), 0, s, a, units);
+  const bool nt = a.T * a.H * (a.bf16 ? 2 : 4) > (int64_t(256) << 20);
+  if (a.bf16 && nt) hipLaunchKernelGGL((k_embed_sum<true, true>), grid, dim3(threads), 0, s, a, units);
+  else if (a.bf16) hipLaunchKernelGGL((k_embed_sum<true, false>), grid, dim3(threads), 0, s, a, units);
+  else hipLaunchKernelGGL((k_embed_sum<false, false>), grid, dim3(threads), 0, s, a, units);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || units <= 1) return e;
   hipLaunchKernelGGL(k_embed_fix, dim3((unsigned)((units + FIX_UNITS - 1) / FIX_UNITS), (unsigned)((a.H / 8 + 63) / 64)),

@@ -292,9 +292,10 @@ struct EmbArgs {
 };
 
 // Embedding gradient: rows are sorted by token in groups of EMB_ROWS_MAX local ids at most, and
-// summed in units of EMB_UNIT consecutive sorted rows.
+// summed in units of emb_unit(T) consecutive sorted rows: small ones spread few tokens over the
+// compute units, large ones leave fewer tokens shared between units.
 constexpr int EMB_ROWS_MAX = 1024;
-constexpr int EMB_UNIT = 32;
+inline int emb_unit(int64_t T) { return T <= 4096 ? 16 : 32; }
 struct EmbBwdArgs {
   const int64_t* ids;
   const uint8_t* mask;
@@ -302,6 +303,7 @@ struct EmbBwdArgs {
   int64_t offset, n_real, real_vocab, local_size;
   int32_t H;
   int32_t rows_per_group;
+  int32_t unit;     // emb_unit(T)
   float scale;
   int32_t overwrite;
   const void* dout;
