@@ -381,17 +381,19 @@ llp_status forward_impl(const llp_request* req, const llp_partials* out, void* w
   if (st != LLP_OK) return st;
   if (T == 0) return LLP_OK;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  return run_forward(req->vocab, req->layout, req->target_ids, req->temperature, want_ent,
-                     req->status_word, w, out, workspace, num_cus, s, [&](FwdArgs& fa) {
-    fa.W = static_cast<const uint16_t*>(req->proj.weight);
-    fa.ldw = req->proj.weight_stride;
-    fa.h = static_cast<const uint16_t*>(req->proj.hidden);
-    fa.ldh = req->proj.hidden_stride;
-    fa.bias = req->proj.bias;
-    fa.bias_f32 = req->proj.bias_dtype == LLP_DTYPE_F32;
-    fa.H = (int32_t)H;
-    return launch_fwd(fa, s);
-  });
+  ForwardArgs f = forward_args(req->vocab, req->layout, req->target_ids, req->temperature, want_ent,
+                               req->status_word, w, out, workspace, num_cus);
+  f.fa.W = static_cast<const uint16_t*>(req->proj.weight);
+  f.fa.ldw = req->proj.weight_stride;
+  f.fa.h = static_cast<const uint16_t*>(req->proj.hidden);
+  f.fa.ldh = req->proj.hidden_stride;
+  f.fa.bias = req->proj.bias;
+  f.fa.bias_f32 = req->proj.bias_dtype == LLP_DTYPE_F32;
+  f.fa.H = (int32_t)H;
+  LLP_HIP(launch_layout(f.la, s), "layout kernel launch");
+  LLP_HIP(launch_fwd(f.fa, s), "forward kernel launch");
+  LLP_HIP(launch_combine(f.ca, w.T_cap, s), "combine kernel launch");
+  return LLP_OK;
 }
 
 }  // namespace

@@ -310,22 +310,29 @@ LLP_API llp_status llp_forward_int8(const llp_int8_request* req, const llp_parti
   if (st != LLP_OK) return st;
   if (T == 0) return LLP_OK;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  return run_forward(req->vocab, req->layout, req->target_ids, req->temperature, want_ent,
-                     req->status_word, w, out, workspace, num_cus, s, [&](FwdArgs& fa) {
-    fa.W = reinterpret_cast<const uint16_t*>(req->weight);
-    fa.ldw = req->weight_stride / 2;
-    fa.h = reinterpret_cast<const uint16_t*>(req->hidden);
-    fa.ldh = req->hidden_stride / 2;
-    fa.bias = req->bias;
-    fa.bias_f32 = req->bias_dtype == LLP_DTYPE_F32;
-    fa.H = (int32_t)(req->hidden_size / 2);
-    Fwd8Args a{};
-    a.f = fa;
-    a.hs = req->hidden_scale;
-    a.ws = req->weight_scale;
-    a.rows = T;
-    return launch_fwd8(a, s);
-  });
+  const ForwardArgs f = forward_args(req->vocab, req->layout, req->target_ids, req->temperature,
+                                     want_ent, req->status_word, w, out, workspace, num_cus);
+  Fwd8Args a{};
+  a.f = f.fa;
+  a.f.W = reinterpret_cast<const uint16_t*>(req->weight);
+  a.f.ldw = req->weight_stride / 2;
+  a.f.h = reinterpret_cast<const uint16_t*>(req->hidden);
+  a.f.ldh = req->hidden_stride / 2;
+  a.f.bias = req->bias;
+  a.f.bias_f32 = req->bias_dtype == LLP_DTYPE_F32;
+  a.f.H = (int32_t)(req->hidden_size / 2);
+  a.la = f.la;
+  a.ca = f.ca;
+  a.hs = req->hidden_scale;
+  a.ws = req->weight_scale;
+  if (T <= FEW_ROWS) {
+    LLP_HIP(launch_fwd8_few(a, s), "few-row forward kernel launch");
+    return LLP_OK;
+  }
+  LLP_HIP(launch_layout(f.la, s), "layout kernel launch");
+  LLP_HIP(launch_fwd8(a, s), "forward kernel launch");
+  LLP_HIP(launch_combine(f.ca, w.T_cap, s), "combine kernel launch");
+  return LLP_OK;
 }
 
 LLP_API llp_status llp_policy_workspace_bytes(const llp_policy_request* req, size_t* bytes) {

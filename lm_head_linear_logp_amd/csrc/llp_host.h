@@ -1,6 +1,6 @@
 // llp_host.h -- host-side helpers shared by the C-ABI entry points (llp_api.cpp,
-// llp_api_ops.cpp): status reporting, request checks, the forward's workspace layout and its
-// launch sequence. Not part of the public ABI.
+// llp_api_ops.cpp): status reporting, request checks, the forward's workspace layout and
+// kernel arguments. Not part of the public ABI.
 #pragma once
 
 #include <hip/hip_runtime_api.h>
@@ -71,15 +71,20 @@ Ws ws_layout(int64_t T, int64_t n_real, int64_t H, int op, bool slabs = false);
 llp_status check_forward_out(int64_t T, bool want_ent, const llp_partials* out, const Ws& w,
                              const void* workspace, size_t workspace_bytes);
 
-// The forward of one shard on `stream`: layout, the fused tiles, the cross-tile combine. `tiles`
-// launches the tiles given the fields of FwdArgs that do not describe the operands.
-template <class Tiles>
-llp_status run_forward(const llp_vocab_partition& vocab, const llp_token_layout& layout,
-                       const int64_t* target_ids, float temperature, bool want_ent,
-                       int32_t* status_word, const Ws& w, const llp_partials* out,
-                       void* workspace, int num_cus, hipStream_t s, Tiles&& tiles) {
-  float* ent = want_ent ? out->entropy : nullptr;
+// The forward's launches over a workspace, but for what describes the operands.
+struct ForwardArgs {
   LayoutArgs la{};
+  FwdArgs fa{};
+  CombineArgs ca{};
+};
+
+inline ForwardArgs forward_args(const llp_vocab_partition& vocab, const llp_token_layout& layout,
+                                const int64_t* target_ids, float temperature, bool want_ent,
+                                int32_t* status_word, const Ws& w, const llp_partials* out,
+                                void* workspace, int num_cus) {
+  float* ent = want_ent ? out->entropy : nullptr;
+  ForwardArgs f;
+  LayoutArgs& la = f.la;
   la.T = layout.num_tokens;
   la.mask = layout.loss_mask;
   la.cu_seqlens = layout.cu_seqlens;
@@ -101,9 +106,8 @@ llp_status run_forward(const llp_vocab_partition& vocab, const llp_token_layout&
   la.status = status_word;
   la.qctr = at<int32_t>(workspace, w.qctr);   // the forward kernel's tile-queue counters
   la.nqctr = QCTR_INTS;
-  LLP_HIP(launch_layout(la, s), "layout kernel launch");
 
-  FwdArgs fa{};
+  FwdArgs& fa = f.fa;
   fa.n_real = la.n_real;
   fa.nvt = (int32_t)w.nvt;
   fa.ntb = (int32_t)(w.T_cap / TILE);
@@ -118,9 +122,8 @@ llp_status run_forward(const llp_vocab_partition& vocab, const llp_token_layout&
   fa.pstride = w.T_cap;
   fa.qctr = la.qctr;
   fa.workers = num_cus;
-  LLP_HIP(tiles(fa), "forward kernel launch");
 
-  CombineArgs ca{};
+  CombineArgs& ca = f.ca;
   ca.nvt = (int32_t)w.nvt;
   ca.rows = layout.num_tokens;
   ca.pstride = w.T_cap;
@@ -136,8 +139,7 @@ llp_status run_forward(const llp_vocab_partition& vocab, const llp_token_layout&
   ca.out_l = out->lse;
   ca.out_e = ent;
   ca.out_p = out->logp;
-  LLP_HIP(launch_combine(ca, w.T_cap, s), "combine kernel launch");
-  return LLP_OK;
+  return f;
 }
 
 }  // namespace llp

@@ -1,5 +1,6 @@
 // llp_int8.hip -- scoring with a head in 8-bit integers: the quantisation of rows and the fused
 // forward on int8 operands.
+#include "llp_combine.hpp"
 #include "llp_fwd_tile.hpp"
 #include "llp_internal.h"
 #include "llp_tile.hpp"
@@ -229,7 +230,7 @@ __global__ __launch_bounds__(64 * NW, 1) __attribute__((amdgpu_waves_per_eu(NW /
 }
 
 // ------------------------------------------------------------------------------------
-// Few rows (at most FEW_ROWS_MAX): the weight's bytes bound the forward, so nothing is staged. A
+// Few rows (at most FEW_ROWS, one wave's lanes): the weight's bytes bound the forward, so nothing is staged. A
 // workgroup takes one vocabulary tile; a wave takes 16 IB columns x all rows (NB blocks of 16)
 // over one of KS parts of K, loads its operands straight into MFMA registers and refills a block's
 // registers as soon as its MFMAs have read them, so its loads never drain.
@@ -244,7 +245,23 @@ __global__ __launch_bounds__(64 * NW, 1) __attribute__((amdgpu_waves_per_eu(NW /
 // waves take them in the wide tile's register layout: its sums run in the same order, so every
 // row gets the wide tile's bits.
 // ------------------------------------------------------------------------------------
-constexpr int FEW_ROWS_MAX = 64;
+// The layout of so few rows is a ballot: every workgroup works it out for itself, which saves a
+// launch in front. Returns the wave's mask of scored rows.
+__device__ __forceinline__ uint64_t few_scored(const LayoutArgs& la) {
+  const int lane = threadIdx.x & 63;
+  return __builtin_amdgcn_ballot_w64(lane < la.T && (la.mask == nullptr || la.mask[lane < la.T ? lane : 0] != 0));
+}
+
+// Local column of row t's target, or -1, and the status bits it raises.
+__device__ __forceinline__ int few_target(const LayoutArgs& la, int t, int& status) {
+  const int64_t tg = la.targets[t];
+  const bool valid = tg >= 0 && tg < la.real_vocab;
+  if (!valid) status |= LLP_STATUS_TARGET_OUT_OF_RANGE;
+  const int64_t loc = tg - la.offset;
+  const bool hit = valid && loc >= 0 && loc < la.n_real;
+  if (!hit && la.world == 1) status |= LLP_STATUS_TARGET_NOT_FOUND;
+  return hit ? (int)loc : -1;
+}
 
 template <int BMODE, int NB, int IB, int KS, int BUFS>
 __global__ __launch_bounds__(1024 / IB * KS) __attribute__((amdgpu_waves_per_eu(KS * 16 / IB == 4 ? 3 : 2))) void k_fwd8_few(Fwd8Args a) {
@@ -253,9 +270,18 @@ __global__ __launch_bounds__(1024 / IB * KS) __attribute__((amdgpu_waves_per_eu(
   __shared__ __attribute__((aligned(16))) float red[6 * 256];
   __shared__ __attribute__((aligned(16))) float sc[3 * 256];
   __shared__ __attribute__((aligned(16))) int sums[BUFS][16 * NB][LDT];
-  const int Ts = *a.f.count;
-  if (Ts <= 0) return;
+  __shared__ int scored[FEW_ROWS], tloc[FEW_ROWS];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint64_t on = few_scored(a.la);
+  const int Ts = __popcll(on);
+  if (Ts == 0) return;
+  if (wave == 0 && ((on >> lane) & 1) != 0) {
+    const int j = __popcll(on & ((1ull << lane) - 1));
+    int status = 0;
+    scored[j] = lane;
+    tloc[j] = few_target(a.la, lane, status);
+  }
+  __syncthreads();
   const int cg = wave % CG, ks = wave / CG;
   const int vt = blockIdx.x, v0 = vt * BM;
   const int64_t ldw = a.f.ldw * 2, ldh = a.f.ldh * 2;   // bytes
@@ -274,7 +300,7 @@ __global__ __launch_bounds__(1024 / IB * KS) __attribute__((amdgpu_waves_per_eu(
 #pragma unroll
   for (int n = 0; n < NB; ++n) {
     const int j = n * 16 + lr;
-    ob[n] = (uint32_t)(a.f.scored[j < Ts ? j : Ts - 1] * ldh) + kb;
+    ob[n] = (uint32_t)(scored[j < Ts ? j : Ts - 1] * ldh) + kb;
   }
   const int steps = a.f.H / KSTEP;   // of 128 bytes
   const int s0 = steps * ks / KS, s1 = steps * (ks + 1) / KS;
@@ -344,7 +370,7 @@ __global__ __launch_bounds__(1024 / IB * KS) __attribute__((amdgpu_waves_per_eu(
       sc[256 + i] = in ? reinterpret_cast<const float*>(a.f.bias)[v] : 0.f;
     if constexpr (BMODE == BIAS_BF16)
       sc[256 + i] = in ? bf16_to_f32(reinterpret_cast<const uint16_t*>(a.f.bias)[v]) : 0.f;
-    if (i < FEW_ROWS_MAX) sc[512 + i] = a.hs[a.f.scored[i < Ts ? i : Ts - 1]];
+    if (i < FEW_ROWS) sc[512 + i] = a.hs[scored[i < Ts ? i : Ts - 1]];
   }
   // K parts p, p + BUFS, ... share buffer p: the first writes, the others add in turn.
 #pragma unroll
@@ -380,7 +406,66 @@ __global__ __launch_bounds__(1024 / IB * KS) __attribute__((amdgpu_waves_per_eu(
 #pragma unroll
       for (int u = 0; u < 4; ++u) x[mi][0][4 * g + u] = y[u];
     }
-  int8_epilogue<BMODE, 1>(x, a, vt, 0, Ts, red, sc);
+  Fwd8Args own = a;
+  own.f.tloc = tloc;
+  int8_epilogue<BMODE, 1>(x, own, vt, 0, Ts, red, sc);
+}
+
+// The rest of a few-row forward: a workgroup per row, scored or not, combines its partials and writes
+// its outputs and status; the first one checks cu_seqlens.
+__global__ __launch_bounds__(COMBINE_FEW_THREADS) void k_fwd8_few_out(Fwd8Args a) {
+  __shared__ CombineFewLds lds;
+  const LayoutArgs& la = a.la;
+  const int t = blockIdx.x;
+  int status = 0;
+  if (t == 0 && la.cu_seqlens != nullptr)
+    for (int i = threadIdx.x; i <= la.num_seqs; i += COMBINE_FEW_THREADS) {
+      const int c = la.cu_seqlens[i];
+      if ((i == 0 && c != 0) || (i == la.num_seqs && (int64_t)c != la.T) ||
+          (i < la.num_seqs && la.cu_seqlens[i + 1] < c))
+        status |= LLP_STATUS_LAYOUT_INVALID;
+    }
+  const uint64_t on = few_scored(la);
+  if (((on >> t) & 1) == 0) {
+    if (threadIdx.x == 0) {
+      la.out_t[t] = 0.f;
+      la.out_f[t] = 0;
+      la.out_l[t] = 0.f;
+      if (la.out_e) la.out_e[t] = 0.f;
+      if (la.out_p) la.out_p[t] = 0.f;
+    }
+  } else {
+    const int j = __popcll(on & ((1ull << t) - 1));
+    const int loc = few_target(la, t, status);
+    const float target = loc >= 0 ? a.ca.tz[j] : 0.f;
+    float M = -INFINITY, S = 0.f, Q = 0.f;
+    if (a.ca.nvt <= COMBINE_FEW_TILES) {
+      combine_few(a.ca, j, lds, M, S, Q);
+    } else {
+      // More tiles than the LDS takes: the chains read their partials themselves.
+      const int c = threadIdx.x;
+      if (c < COMBINE_CHAINS) {
+        combine_chain(
+            c, a.ca.nvt, [&](int vt) { return a.ca.pm[(int64_t)vt * a.ca.pstride + j]; },
+            [&](int vt, float& m, float& s, float& q) {
+              const int64_t o = (int64_t)vt * a.ca.pstride + j;
+              m = a.ca.pm[o];
+              s = a.ca.ps[o];
+              q = a.ca.pq[o];
+            },
+            M, S, Q);
+        lds.rm[c] = M;
+        lds.rs[c] = S;
+        lds.rq[c] = Q;
+      }
+      __syncthreads();
+      M = -INFINITY; S = 0.f; Q = 0.f;
+      if (threadIdx.x == 0)
+        for (int g = 0; g < COMBINE_CHAINS; ++g) fold(M, S, Q, lds.rm[g], lds.rs[g], lds.rq[g]);
+    }
+    if (threadIdx.x == 0) combine_out(a.ca, t, loc >= 0, target, M, S, Q);
+  }
+  if (status && la.status) atomicOr(la.status, status);
 }
 
 template <int NB, int IB, int KS, int BUFS>
@@ -391,17 +476,23 @@ static void launch_few(const Fwd8Args& a, hipStream_t s) {
   else hipLaunchKernelGGL((k_fwd8_few<BIAS_BF16, NB, IB, KS, BUFS>), grid, block, 0, s, a);
 }
 
-hipError_t launch_fwd8(const Fwd8Args& a, hipStream_t s) {
-  if (a.f.nvt <= 0 || a.f.ntb <= 0) return hipGetLastError();
-  if (a.rows <= FEW_ROWS_MAX) {
+hipError_t launch_fwd8_few(const Fwd8Args& a, hipStream_t s) {
+  if (a.f.nvt > 0) {
     // 4 waves per tile keep every tile of a large vocabulary resident at once (3 per compute
     // unit); with at most one tile per compute unit, 8 waves have more loads in flight.
     const bool small = a.f.nvt <= a.f.workers;
-    if (a.rows <= 16) small ? launch_few<1, 8, 4, 2>(a, s) : launch_few<1, 8, 2, 2>(a, s);
-    else if (a.rows <= 32) small ? launch_few<2, 8, 4, 2>(a, s) : launch_few<2, 4, 1, 1>(a, s);
+    if (a.la.T <= 16) small ? launch_few<1, 8, 4, 2>(a, s) : launch_few<1, 8, 2, 2>(a, s);
+    else if (a.la.T <= 32) small ? launch_few<2, 8, 4, 2>(a, s) : launch_few<2, 4, 1, 1>(a, s);
     else launch_few<4, 4, 2, 2>(a, s);
-    return hipGetLastError();
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
   }
+  hipLaunchKernelGGL(k_fwd8_few_out, dim3((unsigned)a.la.T), dim3(COMBINE_FEW_THREADS), 0, s, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_fwd8(const Fwd8Args& a, hipStream_t s) {
+  if (a.f.nvt <= 0 || a.f.ntb <= 0) return hipGetLastError();
   const int64_t ntiles = (int64_t)a.f.nvt * a.f.ntb;
   const int n = a.f.H / KSTEP;
   const dim3 block(64 * FWD_WAVES);

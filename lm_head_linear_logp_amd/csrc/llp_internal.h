@@ -28,6 +28,9 @@ inline int64_t layout_blocks(int64_t T) {
   return T > LAYOUT_BLOCK_ROWS ? (T + LAYOUT_BLOCK_ROWS - 1) / LAYOUT_BLOCK_ROWS : 1;
 }
 
+// Rows up to which a forward is one of few rows.
+constexpr int64_t FEW_ROWS = 64;
+
 struct LayoutArgs {
   int64_t T;
   const uint8_t* mask;
@@ -271,9 +274,10 @@ struct QuantArgs {
 // count pairs of columns).
 struct Fwd8Args {
   FwdArgs f;
+  LayoutArgs la;    // few rows: the layout, which the kernels work out themselves
+  CombineArgs ca;   // few rows: the outputs
   const float* hs;  // [T] scale of each hidden row
   const float* ws;  // [local vocabulary] scale of each weight row
-  int64_t rows;     // host side: the call's rows (scored or not)
 };
 
 struct EmbArgs {
@@ -394,6 +398,7 @@ hipError_t launch_logits(const LogitsArgs& a, hipStream_t s);
 hipError_t launch_keep(const KeepArgs& a, hipStream_t s);
 hipError_t launch_quant(const QuantArgs& a, hipStream_t s);
 hipError_t launch_fwd8(const Fwd8Args& a, hipStream_t s);
+hipError_t launch_fwd8_few(const Fwd8Args& a, hipStream_t s);
 hipError_t launch_embedding(const EmbArgs& a, hipStream_t s);
 hipError_t launch_embedding_sort(const EmbBwdArgs& a, hipStream_t s);
 hipError_t launch_embedding_sum(const EmbBwdArgs& a, hipStream_t s);

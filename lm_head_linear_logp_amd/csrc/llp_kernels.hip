@@ -6,6 +6,7 @@
 // Sources: [CUDA provider] "feat(rl-kernel): add CUDA linear logp provider integration",
 // [ROCm provider] "feat(rl-kernel): add ROCm linear logp provider integration",
 // [top-p replay] "Perf/cuda compact top p replay".
+#include "llp_combine.hpp"
 #include "llp_fwd_tile.hpp"
 #include "llp_internal.h"
 #include "llp_tile.hpp"
@@ -164,76 +165,8 @@ __global__ __launch_bounds__(64 * NW, 1) __attribute__((amdgpu_waves_per_eu(NW /
 }
 
 // ------------------------------------------------------------------------------------
-// Cross-tile combine, in vocabulary-tile order: chain c of 16 folds tiles c, c+16, ... of a row,
-// then the row's 16 chains are folded in order c = 0..15. A workgroup takes 32 rows x 16 chains
-// (thread = chain * 32 + row), so the 4096 rows of a chunk spread over 128 workgroups; the
-// arithmetic of a row does not depend on that grouping. With d_k = m_k - M:
-// S = sum_k s_k e^{d_k}, Q = sum_k e^{d_k}(q_k + s_k d_k log2 e); lse = M + ln S and
-// entropy = ln S - ln2 * Q / S. An empty shard gives lse = -inf, entropy 0, target logit 0,
-// in_range 0 and logp -inf ([top-p replay, "Changes" table]: empty vocabulary rows).
+// Cross-tile combine (llp_combine.hpp).
 // ------------------------------------------------------------------------------------
-__device__ __forceinline__ void fold(float& M, float& S, float& Q, float m, float s, float q) {
-  // Combine (M, S, Q) with a partial (m, s, q); both may be empty (-inf max, zero sums).
-  if (m == -INFINITY) return;
-  if (M == -INFINITY) {
-    M = m; S = s; Q = q;
-    return;
-  }
-  const float N = fmaxf(M, m);
-  const float da = M - N, db = m - N;
-  const float wa = expf(da), wb = expf(db);
-  Q = wa * (Q + S * da * kLog2e) + wb * (q + s * db * kLog2e);
-  S = wa * S + wb * s;
-  M = N;
-}
-
-// 32 rows: a wave's loads of one partial are 32 consecutive floats, a whole 128-byte line
-// (with 16 rows two workgroups each fetched half of every line: 70 MB for 29 MB of partials).
-constexpr int COMBINE_ROWS = 32, COMBINE_CHAINS = 16;
-
-// One chain of a row: tiles c, c + 16, ... of nvt, `get(vt, m, s, q)` reading a tile's partial.
-// Unrolled so that each thread has several independent loads in flight.
-template <class Max, class Get>
-__device__ __forceinline__ void combine_chain(int c, int nvt, Max max_of, Get get, float& M, float& S,
-                                              float& Q) {
-  float mmax = -INFINITY;
-#pragma unroll 8
-  for (int vt = c; vt < nvt; vt += COMBINE_CHAINS) mmax = fmaxf(mmax, max_of(vt));
-  if (mmax != -INFINITY) {
-#pragma unroll 8
-    for (int vt = c; vt < nvt; vt += COMBINE_CHAINS) {
-      float m, s, q;
-      get(vt, m, s, q);
-      const float d = m - mmax;
-      const float e = expf(d);
-      S += e * s;
-      Q += e * (q + s * d * kLog2e);
-    }
-    M = mmax;
-  }
-}
-
-// A row's finished sums to its outputs.
-__device__ __forceinline__ void combine_out(const CombineArgs& a, int j, float M, float S, float Q) {
-  float lse, ent;
-  if (M == -INFINITY || !(S > 0.f)) {
-    lse = -INFINITY;
-    ent = 0.f;
-  } else {
-    const float ls = logf(S);
-    lse = M + ls;
-    ent = ls - kLn2 * (Q / S);
-  }
-  const int row = a.scored[j];
-  const bool hit = a.tloc[j] >= 0;
-  const float tz = hit ? a.tz[j] : 0.f;
-  a.out_t[row] = tz;
-  a.out_f[row] = hit ? 1 : 0;
-  a.out_l[row] = lse;
-  if (a.out_e) a.out_e[row] = ent;
-  if (a.out_p) a.out_p[row] = hit ? tz - lse : -INFINITY;
-}
-
 __global__ __launch_bounds__(COMBINE_ROWS * COMBINE_CHAINS) void k_combine(CombineArgs a) {
   __shared__ float rm[COMBINE_CHAINS][COMBINE_ROWS], rs[COMBINE_CHAINS][COMBINE_ROWS],
       rq[COMBINE_CHAINS][COMBINE_ROWS];
@@ -259,48 +192,17 @@ __global__ __launch_bounds__(COMBINE_ROWS * COMBINE_CHAINS) void k_combine(Combi
   if (c != 0 || j >= Ts) return;
   M = -INFINITY; S = 0.f; Q = 0.f;
   for (int g = 0; g < COMBINE_CHAINS; ++g) fold(M, S, Q, rm[g][r], rs[g][r], rq[g][r]);
-  combine_out(a, j, M, S, Q);
+  combine_out(a, a.scored[j], a.tloc[j] >= 0, a.tz[j], M, S, Q);
 }
 
-// Few rows leave k_combine one or two workgroups that wait for 2 x nvt / 16 loads one after the
-// other (17.6 us for one row of a 151669-column vocabulary). Here a workgroup takes one row, all
-// its threads fetch the row's partials to LDS at once, and the chains run from there: the same
-// arithmetic on the same values, so the same bits.
-constexpr int COMBINE_FEW_ROWS = 64, COMBINE_FEW_TILES = 2048;
-
-__global__ __launch_bounds__(256) void k_combine_few(CombineArgs a) {
-  __shared__ float pm[COMBINE_FEW_TILES], ps[COMBINE_FEW_TILES], pq[COMBINE_FEW_TILES];
-  __shared__ float rm[COMBINE_CHAINS], rs[COMBINE_CHAINS], rq[COMBINE_CHAINS];
+// Few rows: one workgroup each.
+__global__ __launch_bounds__(COMBINE_FEW_THREADS) void k_combine_few(CombineArgs a) {
+  __shared__ CombineFewLds lds;
   const int j = blockIdx.x;
   if (j >= *a.count) return;
-#pragma unroll 4
-  for (int vt = threadIdx.x; vt < a.nvt; vt += 256) {
-    const int64_t o = (int64_t)vt * a.pstride + j;
-    pm[vt] = a.pm[o];
-    ps[vt] = a.ps[o];
-    pq[vt] = a.pq[o];
-  }
-  __syncthreads();
-  const int c = threadIdx.x;
-  if (c < COMBINE_CHAINS) {
-    float M = -INFINITY, S = 0.f, Q = 0.f;
-    combine_chain(
-        c, a.nvt, [&](int vt) { return pm[vt]; },
-        [&](int vt, float& m, float& s, float& q) {
-          m = pm[vt];
-          s = ps[vt];
-          q = pq[vt];
-        },
-        M, S, Q);
-    rm[c] = M;
-    rs[c] = S;
-    rq[c] = Q;
-  }
-  __syncthreads();
-  if (threadIdx.x != 0) return;
-  float M = -INFINITY, S = 0.f, Q = 0.f;
-  for (int g = 0; g < COMBINE_CHAINS; ++g) fold(M, S, Q, rm[g], rs[g], rq[g]);
-  combine_out(a, j, M, S, Q);
+  float M, S, Q;
+  combine_few(a, j, lds, M, S, Q);
+  if (threadIdx.x == 0) combine_out(a, a.scored[j], a.tloc[j] >= 0, a.tz[j], M, S, Q);
 }
 
 // ------------------------------------------------------------------------------------
@@ -1242,8 +1144,8 @@ hipError_t launch_fwd(const FwdArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_combine(const CombineArgs& a, int64_t T_cap, hipStream_t s) {
-  if (a.rows > 0 && a.rows <= COMBINE_FEW_ROWS && a.nvt <= COMBINE_FEW_TILES)
-    hipLaunchKernelGGL(k_combine_few, dim3((unsigned)a.rows), dim3(256), 0, s, a);
+  if (a.rows > 0 && a.rows <= FEW_ROWS && a.nvt <= COMBINE_FEW_TILES)
+    hipLaunchKernelGGL(k_combine_few, dim3((unsigned)a.rows), dim3(COMBINE_FEW_THREADS), 0, s, a);
   else if (T_cap > 0)
     hipLaunchKernelGGL(k_combine, dim3(ceil_div64(T_cap, COMBINE_ROWS)),
                        dim3(COMBINE_ROWS * COMBINE_CHAINS), 0, s, a);

@@ -128,6 +128,24 @@ def test_forward_int8_parity(llp, T, H, real, pad, bias, mask, tau):
             assert not host(out[k])[off].any(), k
 
 
+@pytest.mark.parametrize("T", [3, 30, 64, 70])
+def test_forward_int8_many_tiles_and_few_rows(llp, T):
+    # 2344 vocabulary tiles: more than a few-row combine holds in LDS; masked rows among them.
+    H, real, pad = 128, 600000, 600064
+    g = np.random.default_rng(T)
+    h = g.standard_normal((T, H)).astype(np.float32)
+    hq, hs = O.quantize(h)
+    wq = torch.randint(-127, 128, (pad, H), dtype=torch.int8, device="cuda",
+                       generator=torch.Generator(device="cuda").manual_seed(T))
+    ws = torch.rand(pad, device="cuda") * 1e-3
+    mask = (np.arange(T) % 7 != 2).astype(np.uint8)
+    tg = g.integers(0, real, T)
+    out = llp.forward_int8(dev(hq), dev(hs), wq, ws, dev(tg), temperature=0.9, real_vocab=real,
+                           padded_vocab=pad, loss_mask=dev(mask))
+    z = O.int8_logits(hq, hs, host(wq), host(ws), None, 0.9, real)
+    _close(out, O.score(z, tg, mask), z)
+
+
 def test_forward_int8_extreme_values(llp):
     # Every product at its largest: sums of +-127 * 127 * 4096 (past 2^24) and -128 as stored.
     T, K, V = 5, 4096, 300
