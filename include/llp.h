@@ -355,7 +355,8 @@ typedef struct {
  *                 [local_size, hidden_size], row stride weight_stride bytes: strides >=
  *                 hidden_size and multiples of 16, 16-byte aligned bases. As
  *                 llp_quantize_rows writes them (values in [-127, 127]; -128 is read as such).
- *   hidden_scale  fp32 [T]; weight_scale fp32 [local_size] (16-byte aligned base).
+ *   hidden_scale  fp32 [T]; weight_scale fp32 [local_size]; bias as in llp_projection, aligned
+ *                 to its element type.
  *   hidden_size   the padded width: a positive multiple of LLP_INT8_COLUMNS, at most 2^17 - 128
  *                 (the int32 sums cannot overflow; else LLP_ERR_UNSUPPORTED).
  *   hidden_stride and weight_stride < 2^24, T * hidden_stride < 2^31 and the row limits of
@@ -407,7 +408,8 @@ enum { LLP_REDUCE_TOKEN_MEAN = 1, LLP_REDUCE_SEQ_MEAN = 2, LLP_REDUCE_SUM = 3 };
  *   logp, old_logp, advantages   fp32 [T]
  *   ref_logp   fp32 [T], or NULL (then no KL term; kl_coef must be 0)
  *   entropy    fp32 [T], or NULL (then no bonus; entropy_coef must be 0)
- *   layout     T < 2^31; cu_seqlens is required for SEQ_MEAN. A malformed cu_seqlens sets
+ *   layout     T < 2^31, num_seqs <= 2^23 (else LLP_ERR_UNSUPPORTED); cu_seqlens is required
+ *              for SEQ_MEAN. A malformed cu_seqlens sets
  *              LLP_STATUS_LAYOUT_INVALID, and with SEQ_MEAN every output is 0 then.
  *   0 <= clip_low <= 1, clip_high >= 0, dual_clip 0 (none) or > 1, all coefficients finite.
  * A scored row holding a value that is not finite (of the arrays that are used) sets
@@ -447,7 +449,7 @@ typedef struct {
 enum { LLP_PREF_SIGMOID = 1, LLP_PREF_HINGE = 2, LLP_PREF_IPO = 3 };
 
 /* Preference loss of P pairs of packed sequences: sequence 2i is pair i's chosen response, 2i + 1
- * the rejected one (layout.num_seqs = 2 P, cu_seqlens required). For each sequence R = the sum,
+ * the rejected one (layout.num_seqs = 2 P <= 2^23, cu_seqlens required). For each sequence R = the sum,
  * or with `average` the mean, of logp - ref_logp over its scored rows (0 when it has none), and
  * h = R_chosen - R_rejected:
  *   SIGMOID  (1 - e) softplus(-m) + e softplus(m), m = beta h - gamma, e = label_smoothing

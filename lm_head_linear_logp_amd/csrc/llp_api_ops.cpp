@@ -58,14 +58,15 @@ llp_status check_int8(const llp_int8_request* req) {
   if (local_real(p.vocab) > 0) {
     LLP_CHECK(p.weight && p.weight_scale, LLP_ERR_INVALID_ARGUMENT,
               "weight and weight_scale are required");
-    LLP_CHECK(aligned(p.weight, 16) && aligned(p.weight_scale, 16), LLP_ERR_INVALID_ARGUMENT,
-              "weight and weight_scale must be 16-byte aligned");
+    LLP_CHECK(aligned(p.weight, 16), LLP_ERR_INVALID_ARGUMENT, "weight not 16-byte aligned");
   }
+  LLP_CHECK(aligned(p.hidden_scale, 4) && aligned(p.weight_scale, 4), LLP_ERR_INVALID_ARGUMENT,
+            "hidden_scale and weight_scale must be aligned to fp32");
   if (p.bias != nullptr) {
     LLP_CHECK(p.bias_dtype == LLP_DTYPE_BF16 || p.bias_dtype == LLP_DTYPE_F32,
               LLP_ERR_INVALID_ARGUMENT, "bias_dtype %d is not BF16 or F32", p.bias_dtype);
-    LLP_CHECK(aligned(p.bias, p.bias_dtype == LLP_DTYPE_F32 ? 16 : 8), LLP_ERR_INVALID_ARGUMENT,
-              "bias not %d-byte aligned", p.bias_dtype == LLP_DTYPE_F32 ? 16 : 8);
+    LLP_CHECK(aligned(p.bias, p.bias_dtype == LLP_DTYPE_F32 ? 4 : 2), LLP_ERR_INVALID_ARGUMENT,
+              "bias not aligned to its element type");
   }
   LLP_CHECK(isfinite(p.temperature) && p.temperature > 0.f, LLP_ERR_INVALID_ARGUMENT,
             "temperature must be finite and > 0");
@@ -80,11 +81,16 @@ llp_status check_int8(const llp_int8_request* req) {
 constexpr int64_t kPolicyBlockRows = 1024, kPolicyCountRows = 16384;
 constexpr int64_t kPolicyBlocks = 1024;
 
+// One workgroup per sequence: a launch holds fewer than 2^32 threads.
+constexpr int32_t kMaxSeqs = 1 << 23;
+
 llp_status check_loss_layout(const llp_token_layout& l) {
   LLP_CHECK(l.num_tokens >= 0 && l.num_tokens < (int64_t(1) << 31), LLP_ERR_INVALID_ARGUMENT,
             "num_tokens out of range");
-  if (l.cu_seqlens != nullptr)
+  if (l.cu_seqlens != nullptr) {
     LLP_CHECK(l.num_seqs >= 0, LLP_ERR_INVALID_ARGUMENT, "num_seqs < 0");
+    LLP_CHECK(l.num_seqs <= kMaxSeqs, LLP_ERR_UNSUPPORTED, "num_seqs %d exceeds 2^23", l.num_seqs);
+  }
   return LLP_OK;
 }
 
@@ -158,8 +164,7 @@ llp_status check_pref(const llp_pref_request* req) {
   if (st != LLP_OK) return st;
   const int64_t T = req->layout.num_tokens;
   LLP_CHECK(req->layout.cu_seqlens != nullptr, LLP_ERR_INVALID_ARGUMENT, "cu_seqlens is required");
-  LLP_CHECK(req->layout.num_seqs % 2 == 0 && req->layout.num_seqs <= (1 << 30),
-            LLP_ERR_INVALID_ARGUMENT, "num_seqs %d is not twice a number of pairs",
+  LLP_CHECK(req->layout.num_seqs % 2 == 0, LLP_ERR_INVALID_ARGUMENT, "num_seqs %d is not twice a number of pairs",
             req->layout.num_seqs);
   LLP_CHECK(req->layout.num_seqs > 0 || T == 0, LLP_ERR_INVALID_ARGUMENT,
             "rows without a sequence (num_seqs = 0)");

@@ -75,57 +75,60 @@ __global__ __launch_bounds__(64 * QUANT_WAVES) void k_quant(QuantArgs a) {
   __shared__ float tops[QUANT_WAVES];
   constexpr int STEP = 64 * WPR * 8;   // columns per pass
   const int lane = threadIdx.x % (64 * WPR);
-  const int64_t r = (int64_t)blockIdx.x * (QUANT_WAVES / WPR) + threadIdx.x / (64 * WPR);
-  if (r >= a.rows) return;
-  const void* row = static_cast<const char*>(a.x) + r * a.ldx * (BF16 ? 2 : 4);
-  float v[QUANT_PASSES][8];
-  float top = 0.f;   // becomes infinite with an infinity or NaN in the row
-  for (int c0 = 0; c0 < a.cols; c0 += QUANT_PASSES * STEP) {
+  const int64_t step = (int64_t)gridDim.x * (QUANT_WAVES / WPR);
+  for (int64_t r = (int64_t)blockIdx.x * (QUANT_WAVES / WPR) + threadIdx.x / (64 * WPR); r < a.rows; r += step) {
+    const void* row = static_cast<const char*>(a.x) + r * a.ldx * (BF16 ? 2 : 4);
+    float v[QUANT_PASSES][8];
+    float top = 0.f;   // becomes infinite with an infinity or NaN in the row
+    for (int c0 = 0; c0 < a.cols; c0 += QUANT_PASSES * STEP) {
 #pragma unroll
-    for (int p = 0; p < QUANT_PASSES; ++p) quant_load<BF16, VEC>(row, c0 + p * STEP + lane * 8, a.cols, v[p]);
+      for (int p = 0; p < QUANT_PASSES; ++p) quant_load<BF16, VEC>(row, c0 + p * STEP + lane * 8, a.cols, v[p]);
 #pragma unroll
-    for (int p = 0; p < QUANT_PASSES; ++p)
+      for (int p = 0; p < QUANT_PASSES; ++p)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float m = fabsf(v[p][i]);
-        top = m <= top ? top : m < INFINITY ? m : INFINITY;
+        for (int i = 0; i < 8; ++i) {
+          const float m = fabsf(v[p][i]);
+          top = m <= top ? top : m < INFINITY ? m : INFINITY;
+        }
+    }
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off));
+    if constexpr (WPR > 1) {
+      if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < WPR; ++w) top = fmaxf(top, tops[w]);
+      __syncthreads();   // read by all before the next row's are written
+    }
+    const bool bad = !(top < INFINITY);
+    const float scale = fmaxf(top, 1e-30f) * (1.f / 127.f);
+    const float inv = 1.f / scale;
+    if (lane == 0) a.scale[r] = bad ? __builtin_nanf("") : scale;
+    int8_t* q = a.q + r * a.ldq;
+    const bool held = a.cols <= QUANT_PASSES * STEP;
+    for (int c0 = 0; c0 < a.colsp; c0 += QUANT_PASSES * STEP) {
+#pragma unroll
+      for (int p = 0; p < QUANT_PASSES; ++p) {
+        const int c = c0 + p * STEP + lane * 8;
+        if (c >= a.colsp) continue;
+        if (!held) quant_load<BF16, VEC>(row, c, a.cols, v[p]);
+        uint2 w = quant_pack(v[p], scale, inv);
+        if (bad) w = make_uint2(0, 0);
+        *reinterpret_cast<uint2*>(q + c) = w;
       }
-  }
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off));
-  if constexpr (WPR > 1) {
-    if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < WPR; ++w) top = fmaxf(top, tops[w]);
-  }
-  const bool bad = !(top < INFINITY);
-  const float scale = fmaxf(top, 1e-30f) * (1.f / 127.f);
-  const float inv = 1.f / scale;
-  if (lane == 0) a.scale[r] = bad ? __builtin_nanf("") : scale;
-  int8_t* q = a.q + r * a.ldq;
-  const bool held = a.cols <= QUANT_PASSES * STEP;
-  for (int c0 = 0; c0 < a.colsp; c0 += QUANT_PASSES * STEP) {
-#pragma unroll
-    for (int p = 0; p < QUANT_PASSES; ++p) {
-      const int c = c0 + p * STEP + lane * 8;
-      if (c >= a.colsp) continue;
-      if (!held) quant_load<BF16, VEC>(row, c, a.cols, v[p]);
-      uint2 w = quant_pack(v[p], scale, inv);
-      if (bad) w = make_uint2(0, 0);
-      *reinterpret_cast<uint2*>(q + c) = w;
     }
   }
 }
 
 template <bool BF16, bool VEC>
 static void launch_quant_as(const QuantArgs& a, hipStream_t s) {
-  // Rows wider than one wave's registers go to the whole workgroup.
-  if (a.cols > QUANT_PASSES * 512)
-    hipLaunchKernelGGL((k_quant<BF16, VEC, QUANT_WAVES>), dim3((unsigned)a.rows), dim3(64 * QUANT_WAVES), 0, s, a);
-  else
-    hipLaunchKernelGGL((k_quant<BF16, VEC, 1>), dim3((unsigned)((a.rows + QUANT_WAVES - 1) / QUANT_WAVES)),
-                       dim3(64 * QUANT_WAVES), 0, s, a);
+  // Rows wider than one wave's registers go to the whole workgroup. A launch holds fewer than
+  // 2^32 threads: past 2^22 workgroups each takes several rows.
+  const int per = a.cols > QUANT_PASSES * 512 ? 1 : QUANT_WAVES;
+  const int64_t n = (a.rows + per - 1) / per;
+  const dim3 grid((unsigned)(n < (1 << 22) ? n : 1 << 22)), block(64 * QUANT_WAVES);
+  if (per == 1) hipLaunchKernelGGL((k_quant<BF16, VEC, QUANT_WAVES>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((k_quant<BF16, VEC, 1>), grid, block, 0, s, a);
 }
 
 hipError_t launch_quant(const QuantArgs& a, hipStream_t s) {

@@ -8,6 +8,7 @@ import ctypes as C
 from typing import Optional
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _capi as A
 from . import (_check, _need, _partials_alloc, _partials_out, _ptr, _status, _vec, _vocab, open)
@@ -330,6 +331,7 @@ class _PolicyLoss(torch.autograd.Function):
         return o["loss"].reshape(()), o["stats"]
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dloss, _dstats):
         logp, entropy, old_logp, advantages, ref_logp, mask, cu, denominator = ctx.saved_tensors
         g = policy_grads(logp, old_logp, advantages, ref_logp=ref_logp, entropy=entropy,
@@ -368,6 +370,7 @@ class _PreferenceLoss(torch.autograd.Function):
         return o["loss"].reshape(()), o["chosen"], o["rejected"]
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dloss, _dc, _dr):
         logp, cu_seqlens, ref_logp, loss_mask, pair_weight = ctx.saved_tensors
         g = preference_grads(logp, cu_seqlens, ref_logp=ref_logp, loss_mask=loss_mask,
@@ -479,6 +482,7 @@ class _Embedding(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         token_ids, token_mask = ctx.saved_tensors
         scale, real_vocab, V, dtype = ctx.cfg

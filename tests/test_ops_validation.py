@@ -126,14 +126,14 @@ NAN, INF = float("nan"), float("inf")
     (int8, dict(hidden_stride=1 << 24), UNS), (int8, dict(weight_stride=1 << 24), UNS),
     (int8, dict(T=1 << 20, hidden_stride=2048), UNS), (int8, dict(V=1 << 23), UNS),
     (int8, dict(hidden=None), INV), (int8, dict(hidden_scale=None), INV), (int8, dict(weight=None), INV),
-    (int8, dict(weight_scale=None), INV), (int8, dict(weight_scale=FAKE + 4), INV),
+    (int8, dict(weight_scale=None), INV), (int8, dict(weight_scale=FAKE + 2), INV), (int8, dict(hidden_scale=FAKE + 1), INV),
     (int8, dict(hidden=FAKE + 8), INV), (int8, dict(weight=FAKE + 8), INV), (int8, dict(target_ids=None), INV),
-    (int8, dict(bias=FAKE, bias_dtype=9), INV), (int8, dict(bias=FAKE + 4, bias_dtype=2), INV),
+    (int8, dict(bias=FAKE, bias_dtype=9), INV), (int8, dict(bias=FAKE + 2, bias_dtype=2), INV), (int8, dict(bias=FAKE + 1, bias_dtype=1), INV),
     (int8, dict(temperature=0.0), INV), (int8, dict(temperature=NAN), INV), (int8, dict(flags=2), INV),
     (int8, dict(ws=100), INV), (int8, dict(wsp=None), INV), (int8, dict(wsp=FAKE + 16), INV),
     (int8, dict(out=A.llp_partials(FAKE, FAKE, FAKE, None, FAKE)), INV),
     (int8, dict(cu=FAKE, seqs=-1), INV),
-    (policy, dict(T=-1), INV), (policy, dict(T=1 << 31), INV), (policy, dict(seqs=-1), INV),
+    (policy, dict(T=-1), INV), (policy, dict(T=1 << 31), INV), (policy, dict(seqs=-1), INV), (policy, dict(seqs=(1 << 23) + 1), UNS),
     (policy, dict(reduction=0), INV), (policy, dict(reduction=4), INV), (policy, dict(clip_low=-0.1), INV),
     (policy, dict(clip_low=1.1), INV), (policy, dict(clip_low=NAN), INV), (policy, dict(clip_high=-0.1), INV),
     (policy, dict(clip_high=INF), INV), (policy, dict(dual_clip=1.0), INV), (policy, dict(dual_clip=-2.0), INV),
@@ -144,7 +144,7 @@ NAN, INF = float("nan"), float("inf")
     (policy, dict(reduction=3, denominator=FAKE), INV), (policy, dict(ws=16), INV), (policy, dict(wsp=None), INV),
     (policy, dict(out=A.llp_policy_out(None, FAKE, None, FAKE, FAKE)), INV),
     (policy, dict(entropy=None, entropy_coef=0.0), INV),           # dentropy without entropy
-    (pref, dict(T=-1), INV), (pref, dict(cu=None), INV), (pref, dict(seqs=3), INV), (pref, dict(seqs=0), INV),
+    (pref, dict(T=-1), INV), (pref, dict(cu=None), INV), (pref, dict(seqs=3), INV), (pref, dict(seqs=(1 << 23) + 2), UNS), (pref, dict(seqs=0), INV),
     (pref, dict(logp=None), INV), (pref, dict(kind=0), INV), (pref, dict(kind=4), INV), (pref, dict(reduction=2), INV),
     (pref, dict(beta=0.0), INV), (pref, dict(beta=NAN), INV), (pref, dict(gamma=INF), INV),
     (pref, dict(kind=3, gamma=0.5), INV), (pref, dict(label_smoothing=1.0), INV),
