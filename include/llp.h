@@ -595,7 +595,8 @@ LLP_API llp_status llp_forward_int8(const llp_int8_request* req, const llp_parti
                                     void* workspace, size_t workspace_bytes, void* stream);
 
 /* The losses (see llp_policy_request and llp_pref_request): the loss and, where out->dlogp (and
- * out->dentropy) is given, its gradient. Workspace: device memory, 256-byte aligned. */
+ * out->dentropy) is given, its gradient. Workspace: device memory, 256-byte aligned; where the
+ * size is 0 (small calls) none is taken and it may be NULL. */
 LLP_API llp_status llp_policy_workspace_bytes(const llp_policy_request* req, size_t* bytes);
 LLP_API llp_status llp_policy_loss(const llp_policy_request* req, const llp_policy_out* out,
                                    void* workspace, size_t workspace_bytes, void* stream);

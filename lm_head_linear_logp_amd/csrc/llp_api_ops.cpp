@@ -14,7 +14,9 @@ namespace {
 
 constexpr int64_t kMaxRows = (int64_t(1) << 23) - 256;
 
+// `need` 0: the call takes no workspace.
 llp_status check_workspace(const void* workspace, size_t bytes, size_t need) {
+  if (need == 0) return LLP_OK;
   LLP_CHECK(bytes >= need, LLP_ERR_INVALID_ARGUMENT,
             "workspace of %zu bytes is smaller than the %zu required", bytes, need);
   LLP_CHECK(workspace != nullptr && aligned(workspace, 256), LLP_ERR_INVALID_ARGUMENT,
@@ -140,10 +142,8 @@ PolicyWs policy_ws(const llp_policy_request& r) {
   PolicyWs w{};
   const int64_t T = r.layout.num_tokens;
   const bool by_seq = r.reduction == LLP_REDUCE_SEQ_MEAN;
-  if (T <= POLICY_SOLO_ROWS && !(by_seq && r.layout.num_seqs > POLICY_SOLO_SEQS)) {
-    w.total = 256;   // one workgroup, nothing in the workspace
-    return w;
-  }
+  if (T <= POLICY_SOLO_ROWS && !(by_seq && r.layout.num_seqs > POLICY_SOLO_SEQS))
+    return w;   // one workgroup, no workspace
   if (by_seq) w.ncount = r.layout.num_seqs;
   else if (r.reduction == LLP_REDUCE_TOKEN_MEAN && r.layout.loss_mask && !r.denominator)
     w.ncount = (int32_t)((T + kPolicyCountRows - 1) / kPolicyCountRows);
@@ -190,6 +190,8 @@ struct PrefWs {
 
 PrefWs pref_ws(const llp_pref_request& r) {
   PrefWs w{};
+  if (r.layout.num_tokens <= PREF_SOLO_ROWS && r.layout.num_seqs <= 2 * PREF_SOLO_PAIRS)
+    return w;   // one workgroup, no workspace
   Regions g;
   const size_t n = (size_t)r.layout.num_seqs;
   w.sum = g.take(n * PREF_SPLIT * 8);
@@ -429,6 +431,7 @@ LLP_API llp_status llp_preference_loss(const llp_pref_request* req, const llp_pr
   a.kind = req->kind;
   a.average = req->average != 0;
   a.mean = req->reduction == LLP_REDUCE_TOKEN_MEAN;
+  a.solo = w.total == 0;
   a.sum = at<double>(workspace, w.sum);
   a.cnt = at<int32_t>(workspace, w.cnt);
   a.coef = at<float>(workspace, w.coef);

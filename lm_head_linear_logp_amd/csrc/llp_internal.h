@@ -360,6 +360,9 @@ struct PolicyArgs {
 // the sequence alone).
 constexpr int PREF_SPLIT = 4;
 constexpr int PREF_CHUNK = 4096;
+// Rows and pairs up to which one workgroup computes a preference loss in one launch.
+constexpr int64_t PREF_SOLO_ROWS = 8192;
+constexpr int PREF_SOLO_PAIRS = 16;
 struct PrefArgs {
   int64_t T;
   const float* logp;
@@ -370,6 +373,7 @@ struct PrefArgs {
   int32_t P;
   double beta, gamma, smooth;
   int32_t kind, average, mean;
+  int32_t solo;      // one workgroup does it all, without the workspace
   double* sum;       // [2 P][PREF_SPLIT]
   int32_t* cnt;      // [2 P][PREF_SPLIT], scored rows; -1 when one of them is not finite
   float* coef;       // [2 P] d loss / d logp of a scored row of the sequence

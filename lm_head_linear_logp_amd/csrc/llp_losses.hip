@@ -484,21 +484,21 @@ hipError_t launch_policy(const PolicyArgs& a, hipStream_t s) {
 }
 
 // ------------------------------------------------------------------------------------
-// Preference loss. First launch: the sum of logp - ref_logp over each sequence's scored rows;
+// Preference loss. Few rows in few pairs: one workgroup, one launch. Else, first launch: the sum of logp - ref_logp over each sequence's scored rows;
 // PREF_SPLIT workgroups share a sequence, workgroup y taking its chunks y, y + PREF_SPLIT, ... of
 // PREF_CHUNK rows, so that a sum's order depends on its sequence alone. Second: the sums become each
 // pair's loss and gradient coefficient, and the losses are added up. Third (with few pairs, in
 // one launch with the second): the coefficients are spread over the scored rows.
 // ------------------------------------------------------------------------------------
-__global__ __launch_bounds__(LOSS_THREADS) void k_pref_sum(PrefArgs a) {
-  __shared__ double shd[LOSS_THREADS / 64];
-  __shared__ int shi[LOSS_THREADS / 64];
-  const int s = blockIdx.x;
-  const int64_t b = a.cu[s] > 0 ? a.cu[s] : 0;
-  const int64_t e = a.cu[s + 1] < a.T ? a.cu[s + 1] : a.T;
-  double sum = 0.0;
-  int n = 0, bad = 0;
-  for (int64_t c = b + (int64_t)blockIdx.y * PREF_CHUNK; c < e; c += PREF_SPLIT * PREF_CHUNK) {
+// Sum of the scored rows' log ratios of the sequence [from, to), part y of PREF_SPLIT, by thread
+// `tid` of LOSS_THREADS; n rows, `bad` when one of them is not finite.
+__device__ __forceinline__ void pref_partial(const PrefArgs& a, int64_t from, int64_t to, int y, int tid,
+                                             double& sum, int& n, int& bad) {
+  const int64_t b = from > 0 ? from : 0;
+  const int64_t e = to < a.T ? to : a.T;
+  sum = 0.0;
+  n = bad = 0;
+  for (int64_t c = b + (int64_t)y * PREF_CHUNK; c < e; c += PREF_SPLIT * PREF_CHUNK) {
     const int64_t ce = c + PREF_CHUNK < e ? c + PREF_CHUNK : e;
     constexpr int N = PREF_CHUNK / LOSS_THREADS;
     // A chunk's loads all in flight; the rows' order does not depend on their alignment.
@@ -506,7 +506,7 @@ __global__ __launch_bounds__(LOSS_THREADS) void k_pref_sum(PrefArgs a) {
     bool m[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int64_t t = c + i * LOSS_THREADS + threadIdx.x;
+      const int64_t t = c + i * LOSS_THREADS + tid;
       const bool in = t < ce;
       m[i] = in && (a.mask == nullptr || a.mask[t] != 0);
       lp[i] = in ? a.logp[t] : 0.f;
@@ -520,12 +520,21 @@ __global__ __launch_bounds__(LOSS_THREADS) void k_pref_sum(PrefArgs a) {
       ++n;
     }
   }
+}
+
+__global__ __launch_bounds__(LOSS_THREADS) void k_pref_sum(PrefArgs a) {
+  __shared__ double shd[LOSS_THREADS / 64];
+  __shared__ int shi[LOSS_THREADS / 64];
+  double sum;
+  int n, bad;
+  pref_partial(a, a.cu[blockIdx.x], a.cu[blockIdx.x + 1], blockIdx.y, threadIdx.x, sum, n, bad);
   sum = block_sum<LOSS_THREADS / 64>(sum, shd);
   n = block_sum<LOSS_THREADS / 64>(n, shi);
   bad = block_sum<LOSS_THREADS / 64>(bad, shi);
   if (threadIdx.x == 0) {
-    a.sum[(int64_t)s * PREF_SPLIT + blockIdx.y] = sum;
-    a.cnt[(int64_t)s * PREF_SPLIT + blockIdx.y] = bad ? -1 : n;
+    const int64_t o = (int64_t)blockIdx.x * PREF_SPLIT + blockIdx.y;
+    a.sum[o] = sum;
+    a.cnt[o] = bad ? -1 : n;
   }
 }
 
@@ -630,35 +639,12 @@ __global__ __launch_bounds__(PAIR_THREADS) void k_pref_pairs(PrefArgs a) {
   pref_pairs<PAIR_THREADS / 64>(a, a.coef, true, shd, shi);
 }
 
-// FEW (at most PREF_FEW pairs): every workgroup works the pairs out for itself, the first one
-// writes them out, and the launch in between is saved.
-constexpr int PREF_FEW = 128;
-
-template <bool VEC, bool FEW>
-__global__ __launch_bounds__(LOSS_THREADS) void k_pref_grad(PrefArgs a) {
-  constexpr int NW = LOSS_THREADS / 64;
-  __shared__ int ends[2];
-  __shared__ float own[FEW ? 2 * PREF_FEW : 1];
-  const int64_t t0 = (int64_t)blockIdx.x * LOSS_THREADS * 4;
-  const int64_t t = t0 + threadIdx.x * 4;
+// Gradients of rows t .. t + 3: their sequence's coefficient where they are scored; the sequences
+// are looked for in [lo, hi].
+template <bool VEC>
+__device__ __forceinline__ void pref_spread(const PrefArgs& a, int64_t t, const float* coef, int lo, int hi) {
   bool m[4];
   mask4<VEC>(a.mask, t, a.T, m);
-  // The sequences of the workgroup's first and last rows bound every thread's search.
-  const int w = threadIdx.x >> 6;
-  if (w < 2 && t0 < a.T) {
-    const int64_t last = t0 + LOSS_THREADS * 4 - 1 < a.T - 1 ? t0 + LOSS_THREADS * 4 - 1 : a.T - 1;
-    const int s = seq_of_wave(a.cu, w == 0 ? t0 : last, 2 * a.P - 1);
-    if ((threadIdx.x & 63) == 0) ends[w] = s;
-  }
-  if constexpr (FEW) {
-    __shared__ double shd[NW];
-    __shared__ int shi[NW];
-    pref_pairs<NW>(a, own, blockIdx.x == 0, shd, shi);
-  }
-  __syncthreads();
-  if (t >= a.T || a.dlogp == nullptr) return;
-  const float* coef = FEW ? own : a.coef;
-  const int lo = ends[0], hi = ends[1] > lo ? ends[1] : lo;
   float g[4];
   int s = -1, s_end = 0;
   float c = 0.f;
@@ -676,6 +662,93 @@ __global__ __launch_bounds__(LOSS_THREADS) void k_pref_grad(PrefArgs a) {
   store4<VEC>(a.dlogp, t, a.T, g);
 }
 
+// FEW (at most PREF_FEW pairs): every workgroup works the pairs out for itself, the first one
+// writes them out, and the launch in between is saved.
+constexpr int PREF_FEW = 128;
+
+template <bool VEC, bool FEW>
+__global__ __launch_bounds__(LOSS_THREADS) void k_pref_grad(PrefArgs a) {
+  constexpr int NW = LOSS_THREADS / 64;
+  __shared__ int ends[2];
+  __shared__ float own[FEW ? 2 * PREF_FEW : 1];
+  const int64_t t0 = (int64_t)blockIdx.x * LOSS_THREADS * 4;
+  // The sequences of the workgroup's first and last rows bound every thread's search.
+  const int w = threadIdx.x >> 6;
+  if (w < 2 && t0 < a.T) {
+    const int64_t last = t0 + LOSS_THREADS * 4 - 1 < a.T - 1 ? t0 + LOSS_THREADS * 4 - 1 : a.T - 1;
+    const int s = seq_of_wave(a.cu, w == 0 ? t0 : last, 2 * a.P - 1);
+    if ((threadIdx.x & 63) == 0) ends[w] = s;
+  }
+  if constexpr (FEW) {
+    __shared__ double shd[NW];
+    __shared__ int shi[NW];
+    pref_pairs<NW>(a, own, blockIdx.x == 0, shd, shi);
+  }
+  __syncthreads();
+  const int64_t t = t0 + threadIdx.x * 4;
+  if (t >= a.T || a.dlogp == nullptr) return;
+  const int lo = ends[0], hi = ends[1] > lo ? ends[1] : lo;
+  pref_spread<VEC>(a, t, FEW ? own : a.coef, lo, hi);
+}
+
+// Few rows in few pairs: everything in one workgroup, each group of 256 threads summing whole
+// sequences exactly as k_pref_sum's workgroups do (a sum's bits do not depend on the batch).
+constexpr int PREF_SOLO_SEQS = 2 * PREF_SOLO_PAIRS;
+
+template <bool VEC>
+__global__ __launch_bounds__(PAIR_THREADS) void k_pref_solo(PrefArgs a) {
+  constexpr int NW = PAIR_THREADS / 64, GROUPS = PAIR_THREADS / LOSS_THREADS, GW = LOSS_THREADS / 64;
+  __shared__ double wsum[PREF_SOLO_SEQS][PREF_SPLIT][GW], sums[PREF_SOLO_SEQS][PREF_SPLIT], shd[NW];
+  __shared__ int wcnt[PREF_SOLO_SEQS][PREF_SPLIT][GW], cnts[PREF_SOLO_SEQS][PREF_SPLIT], shi[NW];
+  __shared__ float coef[PREF_SOLO_SEQS];
+  __shared__ int cu[PREF_SOLO_SEQS + 1];
+  const int group = threadIdx.x / LOSS_THREADS, tid = threadIdx.x % LOSS_THREADS;
+  for (int i = threadIdx.x; i <= 2 * a.P; i += PAIR_THREADS) cu[i] = a.cu[i];
+  __syncthreads();
+  for (int s = group; s < 2 * a.P; s += GROUPS)
+    for (int y = 0; y < PREF_SPLIT; ++y) {
+      double sum = 0.0;
+      int n = 0, bad = 0;
+      // Most responses end before their later parts begin.
+      if ((int64_t)cu[s + 1] - cu[s] > (int64_t)y * PREF_CHUNK) {
+        pref_partial(a, cu[s], cu[s + 1], y, tid, sum, n, bad);
+        sum = wave_sum(sum);
+        static_assert(PREF_SOLO_ROWS < 1 << 16, "count and flags share a word");
+        n = wave_sum(n + (bad << 16));
+        bad = n >> 16;
+        n &= 0xFFFF;
+      }
+      if ((tid & 63) == 0) {
+        wsum[s][y][tid >> 6] = sum;
+        wcnt[s][y][tid >> 6] = bad ? -1 : n;
+      }
+    }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 2 * a.P * PREF_SPLIT; i += PAIR_THREADS) {
+    const int s = i / PREF_SPLIT, y = i % PREF_SPLIT;
+    double t = 0;
+    int n = 0;
+    bool bad = false;
+#pragma unroll
+    for (int w = 0; w < GW; ++w) {
+      t += wsum[s][y][w];
+      bad |= wcnt[s][y][w] < 0;
+      n += wcnt[s][y][w];
+    }
+    sums[s][y] = t;
+    cnts[s][y] = bad ? -1 : n;
+  }
+  __syncthreads();
+  PrefArgs own = a;
+  own.cu = cu;
+  own.sum = &sums[0][0];
+  own.cnt = &cnts[0][0];
+  pref_pairs<NW>(own, coef, true, shd, shi);
+  __syncthreads();
+  if (a.dlogp == nullptr) return;
+  for (int64_t t = threadIdx.x * 4; t < a.T; t += PAIR_THREADS * 4) pref_spread<VEC>(own, t, coef, 0, 2 * a.P - 1);
+}
+
 template <bool FEW>
 static void launch_pref_grad(const PrefArgs& a, hipStream_t s) {
   const int64_t n = a.dlogp != nullptr && a.T > 0 ? (a.T + LOSS_THREADS * 4 - 1) / (LOSS_THREADS * 4) : 1;
@@ -687,6 +760,13 @@ static void launch_pref_grad(const PrefArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_preference(const PrefArgs& a, hipStream_t s) {
+  if (a.solo) {
+    if (all_aligned({a.dlogp}, 16) && all_aligned({a.mask}, 4))
+      hipLaunchKernelGGL(k_pref_solo<true>, dim3(1), dim3(PAIR_THREADS), 0, s, a);
+    else
+      hipLaunchKernelGGL(k_pref_solo<false>, dim3(1), dim3(PAIR_THREADS), 0, s, a);
+    return hipGetLastError();
+  }
   if (a.P > 0) {
     hipLaunchKernelGGL(k_pref_sum, dim3((unsigned)(2 * a.P), PREF_SPLIT), dim3(LOSS_THREADS), 0, s, a);
     const hipError_t e = hipGetLastError();

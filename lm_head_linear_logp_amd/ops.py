@@ -63,6 +63,8 @@ def _ready(dev):
 
 
 _fns = {}
+# The current stream's handle without the Stream object around it (1.8 us of a 10 us call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _fn(name):
@@ -74,7 +76,8 @@ def _fn(name):
 
 def _call(dev, name, *args):
     """One execution call of the library on `dev`'s current stream, with `dev` current."""
-    stream = torch.cuda.current_stream(dev).cuda_stream
+    stream = (_raw_stream(dev.index) if _raw_stream is not None
+              else torch.cuda.current_stream(dev).cuda_stream)
     if torch.cuda.current_device() == dev.index:
         st = _fn(name)(*args, stream)
     else:
@@ -85,14 +88,17 @@ def _call(dev, name, *args):
 
 
 def _space(name, req, dev, workspace):
-    """The call's workspace: the caller's when it is large enough, else a new one."""
+    """Pointer and size of the call's workspace: the caller's when it is large enough, else a new
+    one (which the caching allocator hands on in stream order), or none where none is needed."""
     n = C.c_size_t(0)
     st = _fn(name)(C.byref(req), C.byref(n))
     if st != A.LLP_OK:
         _check(st, name)
+    if n.value == 0:
+        return None, 0, None
     if workspace is None or workspace.numel() < n.value:
         workspace = torch.empty(n.value, dtype=_U8, device=dev)
-    return workspace
+    return workspace.data_ptr(), workspace.numel(), workspace
 
 
 def _check_space(workspace, dev):
@@ -175,8 +181,8 @@ def forward_int8(hidden: torch.Tensor, hidden_scale: torch.Tensor, weight: torch
         out = _partials_alloc(T, dev, want_entropy)
     o = A.llp_partials(_ptr(out["target_logit"]), _ptr(out["in_range"]), _ptr(out["lse"]),
                        _ptr(out.get("entropy")), _ptr(out.get("logp")))
-    ws = _space("llp_int8_workspace_bytes", r, dev, workspace)
-    _call(dev, "llp_forward_int8", C.byref(r), C.byref(o), ws.data_ptr(), ws.numel())
+    ws, size, _keep = _space("llp_int8_workspace_bytes", r, dev, workspace)
+    _call(dev, "llp_forward_int8", C.byref(r), C.byref(o), ws, size)
     return out
 
 
@@ -254,8 +260,8 @@ def policy_grads(logp: torch.Tensor, old_logp: torch.Tensor, advantages: torch.T
     o = A.llp_policy_out(out["loss"].data_ptr(), out["stats"].data_ptr(), dl,
                          out["dlogp"].data_ptr() if want_grad else None,
                          out["dentropy"].data_ptr() if has_ent else None)
-    ws = _space("llp_policy_workspace_bytes", r, dev, workspace)
-    _call(dev, "llp_policy_loss", C.byref(r), C.byref(o), ws.data_ptr(), ws.numel())
+    ws, size, _keep = _space("llp_policy_workspace_bytes", r, dev, workspace)
+    _call(dev, "llp_policy_loss", C.byref(r), C.byref(o), ws, size)
     return out
 
 
@@ -303,8 +309,8 @@ def preference_grads(logp: torch.Tensor, cu_seqlens: torch.Tensor, *,
                    dlogp=new(T) if want_grad else None)
     o = A.llp_pref_out(out["loss"].data_ptr(), _ptr(out["pair_loss"]), _ptr(out["chosen"]),
                        _ptr(out["rejected"]), dl, out["dlogp"].data_ptr() if want_grad else None)
-    ws = _space("llp_preference_workspace_bytes", r, dev, workspace)
-    _call(dev, "llp_preference_loss", C.byref(r), C.byref(o), ws.data_ptr(), ws.numel())
+    ws, size, _keep = _space("llp_preference_workspace_bytes", r, dev, workspace)
+    _call(dev, "llp_preference_loss", C.byref(r), C.byref(o), ws, size)
     return out
 
 
@@ -466,9 +472,9 @@ def embedding_backward(token_ids: torch.Tensor, dout: torch.Tensor, *,
     _ready(dev)
     if dweight is None:
         dweight = (torch.empty if overwrite else torch.zeros)((V, H), dtype=_F32, device=dev)
-    ws = _space("llp_embedding_workspace_bytes", r, dev, workspace)
+    ws, size, _keep = _space("llp_embedding_workspace_bytes", r, dev, workspace)
     _call(dev, "llp_embedding_backward", C.byref(r), _ptr(dout), _DTYPE[dout.dtype],
-          _stride(dout, T, H), _ptr(dweight), _stride(dweight, V, H), ws.data_ptr(), ws.numel())
+          _stride(dout, T, H), _ptr(dweight), _stride(dweight, V, H), ws, size)
     return dweight
 
 

@@ -83,7 +83,7 @@ void policy(int64_t T, int32_t S, int red, bool mask, bool full) {
   check("policy workspace", llp_policy_workspace_bytes(&r, &b), LLP_OK);
   void* ws = mem((int64_t)b);
   check("policy", llp_policy_loss(&r, &o, ws, b, nullptr), LLP_OK);
-  check("policy short workspace", llp_policy_loss(&r, &o, ws, b - 1, nullptr), LLP_ERR_INVALID_ARGUMENT);
+  if (b > 0) check("policy short workspace", llp_policy_loss(&r, &o, ws, b - 1, nullptr), LLP_ERR_INVALID_ARGUMENT);
   o.loss = nullptr;
   check("policy without loss", llp_policy_loss(&r, &o, ws, b, nullptr), LLP_ERR_INVALID_ARGUMENT);
   done();
@@ -99,7 +99,7 @@ void pref(int64_t T, int32_t P) {
   check("pref workspace", llp_preference_workspace_bytes(&r, &b), LLP_OK);
   void* ws = mem((int64_t)b);
   check("pref", llp_preference_loss(&r, &o, ws, b, nullptr), LLP_OK);
-  check("pref short workspace", llp_preference_loss(&r, &o, ws, b - 1, nullptr), LLP_ERR_INVALID_ARGUMENT);
+  if (b > 0) check("pref short workspace", llp_preference_loss(&r, &o, ws, b - 1, nullptr), LLP_ERR_INVALID_ARGUMENT);
   r.layout.num_seqs = 2 * P + 1;
   check("pref odd sequences", llp_preference_loss(&r, &o, ws, b, nullptr), LLP_ERR_INVALID_ARGUMENT);
   done();

@@ -117,9 +117,13 @@ hipError_t launch_preference(const PrefArgs& a, hipStream_t) {
   extent(a.logp, a.T); extent(a.ref, a.T); extent(a.mask, a.T);
   extent(a.cu, 2 * (int64_t)a.P + 1);
   extent(a.weight, a.P);
-  extent(a.sum, 2 * (int64_t)a.P * PREF_SPLIT);
-  extent(a.cnt, 2 * (int64_t)a.P * PREF_SPLIT);
-  extent(a.coef, 2 * (int64_t)a.P);
+  if (!a.solo) {
+    extent(a.sum, 2 * (int64_t)a.P * PREF_SPLIT);
+    extent(a.cnt, 2 * (int64_t)a.P * PREF_SPLIT);
+    extent(a.coef, 2 * (int64_t)a.P);
+  } else if (a.P > PREF_SOLO_PAIRS || a.T > PREF_SOLO_ROWS) {
+    return hipErrorInvalidValue;
+  }
   extent(a.loss, 1);
   extent(a.pair_loss, a.P); extent(a.chosen, a.P); extent(a.rejected, a.P);
   extent(a.dlogp, a.T);

@@ -141,7 +141,7 @@ NAN, INF = float("nan"), float("inf")
     (policy, dict(kl_kind=0), INV), (policy, dict(ref_logp=None), INV), (policy, dict(entropy=None), INV),
     (policy, dict(logp=None), INV), (policy, dict(old_logp=None), INV), (policy, dict(advantages=None), INV),
     (policy, dict(reduction=2, cu=None), INV), (policy, dict(reduction=2, seqs=0), INV),
-    (policy, dict(reduction=3, denominator=FAKE), INV), (policy, dict(ws=16), INV), (policy, dict(wsp=None), INV),
+    (policy, dict(reduction=3, denominator=FAKE), INV), (policy, dict(T=9000, ws=16), INV), (policy, dict(T=9000, wsp=None), INV),
     (policy, dict(out=A.llp_policy_out(None, FAKE, None, FAKE, FAKE)), INV),
     (policy, dict(entropy=None, entropy_coef=0.0), INV),           # dentropy without entropy
     (pref, dict(T=-1), INV), (pref, dict(cu=None), INV), (pref, dict(seqs=3), INV), (pref, dict(seqs=(1 << 23) + 2), UNS), (pref, dict(seqs=0), INV),
@@ -149,7 +149,7 @@ NAN, INF = float("nan"), float("inf")
     (pref, dict(beta=0.0), INV), (pref, dict(beta=NAN), INV), (pref, dict(gamma=INF), INV),
     (pref, dict(kind=3, gamma=0.5), INV), (pref, dict(label_smoothing=1.0), INV),
     (pref, dict(label_smoothing=-0.1), INV), (pref, dict(kind=2, label_smoothing=0.1), INV),
-    (pref, dict(ws=8), INV), (pref, dict(wsp=FAKE + 8), INV),
+    (pref, dict(T=9000, ws=8), INV), (pref, dict(T=9000, wsp=FAKE + 8), INV),
     (pref, dict(out=A.llp_pref_out(None, None, None, None, None, None)), INV),
     (emb, dict(num_tokens=-1), INV), (emb, dict(num_tokens=1 << 23), UNS), (emb, dict(V=1 << 23), UNS),
     (emb, dict(hidden_size=0), INV), (emb, dict(hidden_size=60), UNS), (emb, dict(hidden_size=(1 << 20) + 8), UNS),
