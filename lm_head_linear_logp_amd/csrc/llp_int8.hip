@@ -239,10 +239,13 @@ __global__ __launch_bounds__(64 * NW, 1) __attribute__((amdgpu_waves_per_eu(NW /
 // registers as soon as its MFMAs have read them, so its loads never drain.
 //
 // v_mfma_i32_16x16x64_i8: lane l supplies A[l % 16][k] and B[k][l % 16] for k = 16 (l / 16) +
-// 0..15, and holds D[4 (l / 16) + r][l % 16]. A load instruction then takes 64 consecutive bytes
-// of each of 16 weight rows, and the next one the rest of the same 128-byte lines; with the wide
-// tile's 32 x 32 blocks it would take 16 bytes at 64 places, and the L1's request rate bounds
-// the stream (measured, 37 rows of a 37717-column shard: 71 us).
+// 0..15, and holds D[4 (l / 16) + r][l % 16]. Loaded as the MFMA wants them, neighbouring lanes
+// would hold neighbouring rows, every lane a request of its own, and the L1's request rate would
+// bound the stream (37 rows of a 37717-column shard: 53 us). So an instruction takes whole
+// 128-byte lines of 8 weight rows, once and past the caches, and the fragments are moved to their
+// lanes: a DPP move and a ds_bpermute per register. Measured (4096 columns of K): one row of
+// 151669 columns 102 us, 6.1 TB/s of weight (118 us with half lines kept in the caches, 116 with
+// whole ones); 37 rows of the shard 28 us.
 //
 // The int32 sums of the K parts meet in LDS (exact in any order), and from there the epilogue's
 // waves take them in the wide tile's register layout: its sums run in the same order, so every
@@ -292,14 +295,16 @@ __global__ __launch_bounds__(1024 / IB * KS) __attribute__((amdgpu_waves_per_eu(
   const char* const h = reinterpret_cast<const char*>(a.f.h);
   const int rows = a.f.n_real - v0 < BM ? (int)(a.f.n_real - v0) : BM;
   const int l16 = lane & 15;
-  const int lr = lane >> 2, kb = (lane & 3) * 16;   // row and bytes this lane loads
+  const int lr = lane >> 2, kb = (lane & 3) * 16;   // hidden row and bytes this lane loads
   const int from = 4 * (l16 * 4 + (lane >> 4));     // and where its MFMA operand is (bpermute)
-  uint32_t oa[IB], ob[NB];
+  uint32_t oa[IB][2], ob[NB];
 #pragma unroll
-  for (int i = 0; i < IB; ++i) {
-    const int r = cg * 16 * IB + i * 16 + lr;
-    oa[i] = (uint32_t)((r < rows ? r : rows - 1) * ldw) + kb;
-  }
+  for (int i = 0; i < IB; ++i)
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int r = cg * 16 * IB + i * 16 + q * 8 + (lane >> 3);
+      oa[i][q] = (uint32_t)((r < rows ? r : rows - 1) * ldw) + (lane & 7) * 16;
+    }
 #pragma unroll
   for (int n = 0; n < NB; ++n) {
     const int j = n * 16 + lr;
@@ -323,10 +328,32 @@ __global__ __launch_bounds__(1024 / IB * KS) __attribute__((amdgpu_waves_per_eu(
     for (int u = 0; u < 4; ++u) y[u] = __builtin_amdgcn_ds_bpermute(from, x[u]);
     return y;
   };
+  // The weight: instruction q takes the whole lines of rows 8 q .. 8 q + 7, lane l 16 bytes at
+  // 16 (l % 8) of row l / 8.
+  auto load_lines = [&](i32x4 (&x)[2], const uint32_t (&off)[2], int s) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+      x[q] = __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(W + (size_t)(off[q] + (uint32_t)s * 128u)));
+  };
+  // Fragment q of a block: its bytes 64 q .. 64 q + 63 of 16 rows. The lanes that hold the other
+  // half of rows 0 .. 7 take rows 8 .. 15's (q = 0), and the other way round (q = 1): a move
+  // within rows of 16 lanes. Then ds_bpermute.
+  const int from_lines = 4 * ((l16 & 7) * 8 + (l16 >> 3) * 4 + (lane >> 4));
+  auto fragment = [&](const i32x4 (&x)[2], int q) {
+    i32x4 y;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int lo = x[0][u], hi = x[1][u];
+      const int z = q == 0 ? __builtin_amdgcn_update_dpp(lo, hi, 0x114, 0xf, 0xA, false)    // row_shr:4
+                           : __builtin_amdgcn_update_dpp(hi, lo, 0x104, 0xf, 0x5, false);   // row_shl:4
+      y[u] = __builtin_amdgcn_ds_bpermute(from_lines, z);
+    }
+    return y;
+  };
   auto products = [&](int i) {
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      const i32x4 x = placed(A[i][q]);
+      const i32x4 x = fragment(A[i], q);
 #pragma unroll
       for (int n = 0; n < NB; ++n)
         acc[i][n] = __builtin_amdgcn_mfma_i32_16x16x64_i8(x, B[n][q], acc[i][n], 0, 0, 0);
@@ -339,7 +366,7 @@ __global__ __launch_bounds__(1024 / IB * KS) __attribute__((amdgpu_waves_per_eu(
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int i = 0; i < IB; ++i) {
-      load(A[i], W, oa[i], s0);
+      load_lines(A[i], oa[i], s0);
       __builtin_amdgcn_sched_barrier(0);
     }
     for (int s = s0; s + 1 < s1; ++s) {
@@ -353,7 +380,7 @@ __global__ __launch_bounds__(1024 / IB * KS) __attribute__((amdgpu_waves_per_eu(
 #pragma unroll
       for (int i = 0; i < IB; ++i) {
         products(i);
-        load(A[i], W, oa[i], s + 1);
+        load_lines(A[i], oa[i], s + 1);
         __builtin_amdgcn_sched_barrier(0);
       }
     }
