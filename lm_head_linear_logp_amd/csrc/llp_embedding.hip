@@ -251,11 +251,16 @@ hipError_t launch_embedding_sort(const EmbBwdArgs& a, hipStream_t s) {
 // columns per thread in fp32, and writes each token's sum when the token changes; the sums of a
 // token whose rows reach into another unit go to `part` (slot 0: it began in an earlier unit;
 // slot 1: it begins here), and the unit where such a token begins notes in `span` how many units
-// follow. Behind the units, when the gradient is overwritten, workgroups write the rows that no
-// token names as 0, beside the units' reads. Bound by memory: one read of dout, one write (or
-// read and write) of the touched rows.
+// follow. When the gradient is overwritten, the rows that no token names are written as 0, by
+// workgroups behind the units. Bound by memory: one read of dout, one write (or read and write) of
+// the touched rows, the zeros (us a call, and the bytes over them: 485 for 56583 x 4096 bf16 onto
+// 151936 rows, 6.1 TB/s; 100 for 4096 x 4096 onto 37984 rows, 6.6 TB/s).
 // ------------------------------------------------------------------------------------
-constexpr int EMB_ZERO_ROWS = 16;
+// Zeros are written in a launch of their own where dout is larger than this: beside many units
+// they keep the units' reads waiting (151936 x 4096, us a call, apart and beside: 407 and 495 for
+// 16000 tokens, 559 and 697 for 56583; 376 and 370 for 8000, 361 and 349 for 64; 37984 x 4096: 160
+// and 168 for 16000, 124 and 118 for 8000; 4096 x 256: 25 and 20 for 4096).
+constexpr int64_t EMB_APART_BYTES = int64_t(96) << 20;
 
 // NT (bf16): read once, not kept in the caches.
 template <bool BF16, bool NT = false>
@@ -300,41 +305,41 @@ __device__ __forceinline__ void emb_finish(const EmbBwdArgs& a, int row, int c, 
   emb_store8(p, v);
 }
 
-// Rows v0 .. v0 + EMB_ZERO_ROWS - 1 without a token become 0, whole cache lines per wave and
-// store, past the caches (a shard of 37984 rows, 4096 tokens: 143 -> 130 us a call). The
-// workgroups of one v0 share the columns. In a launch of its own, with one store per thread,
-// this part reaches 6.7 TB/s, but then nothing runs beside it: 137 us.
-__device__ __forceinline__ void emb_zero(const EmbBwdArgs& a, int64_t v0) {
-  const int lane = threadIdx.x & 63;
-  const int64_t mine = v0 + lane;
-  bool empty = lane < EMB_ZERO_ROWS && mine < a.local_size;
-  if (empty && mine < a.n_real && a.T > 0) empty = a.start[mine + 1] == a.start[mine];
-  uint64_t rows = __builtin_amdgcn_ballot_w64(empty);
-  while (rows != 0) {
-    const int i = __builtin_ctzll(rows);
-    rows &= rows - 1;
-    float* p = a.dW + (v0 + i) * a.ldw;
-    for (int c = (blockIdx.y * blockDim.x + threadIdx.x) * 4; c < a.H; c += gridDim.y * blockDim.x * 4)
-      __builtin_nontemporal_store(f32x4{0.f, 0.f, 0.f, 0.f}, reinterpret_cast<f32x4*>(p + c));
+// Rows without a token become 0: one 16-byte store per thread and step, whole cache lines per
+// wave, past the caches; workgroup b of `step` takes the pieces b, b + step, ... of all rows, so
+// that what is written at one time lies together. (Sixteen rows of one workgroup written in a loop
+// reached 5.4 TB/s instead of 7.1: 460 us instead of 348 for 151936 x 4096.)
+__device__ __forceinline__ void emb_zero(const EmbBwdArgs& a, int64_t b, int64_t step, int64_t blocks, int pieces) {
+  for (; b < blocks; b += step) {
+    const int64_t v = b / pieces;
+    const int c = ((int)(b - v * pieces) * (int)blockDim.x + (int)threadIdx.x) * 4;
+    if (v < a.n_real && a.T > 0 && a.start[v + 1] != a.start[v]) continue;
+    if (c < a.H)
+      __builtin_nontemporal_store(f32x4{0.f, 0.f, 0.f, 0.f}, reinterpret_cast<f32x4*>(a.dW + v * a.ldw + c));
   }
+}
+
+__global__ __launch_bounds__(256) void k_embed_zero(EmbBwdArgs a, int64_t blocks, int pieces) {
+  emb_zero(a, blockIdx.x, gridDim.x, blocks, pieces);
 }
 
 // NT: dout is larger than the 256 MB of the last-level cache, so nothing of it is still there from
 // its producer, and what else is there is worth keeping (56583 x 4096 bf16: 614 -> 595 us a call;
 // 4096 x 4096, which the cache holds: 129 -> 135 us the other way round).
 template <bool BF16, bool NT>
-__global__ __launch_bounds__(256) void k_embed_sum(EmbBwdArgs a, int units) {
-  if ((int)blockIdx.x >= units) {
-    emb_zero(a, ((int64_t)blockIdx.x - units) * EMB_ZERO_ROWS);
+__global__ __launch_bounds__(256) void k_embed_sum(EmbBwdArgs a, int units, int ny, int64_t blocks, int pieces) {
+  if ((int)blockIdx.x >= units * ny) {
+    emb_zero(a, (int64_t)blockIdx.x - units * ny, gridDim.x - units * ny, blocks, pieces);
     return;
   }
-  const int c = ((int)blockIdx.y * (int)blockDim.x + (int)threadIdx.x) * 8;
+  const int by = (int)blockIdx.x / units;
+  const int c = (by * (int)blockDim.x + (int)threadIdx.x) * 8;
   const int N = a.start[a.n_real];
-  const int u = blockIdx.x, s0 = u * a.unit;
+  const int u = (int)blockIdx.x - by * units, s0 = u * a.unit;
   const int s1 = s0 + a.unit < N ? s0 + a.unit : N;
   const bool began = s0 < N && s0 > 0 && a.row[s0 - 1] == a.row[s0];
   const bool goes_on = s0 < N && s1 < N && a.row[s1 - 1] == a.row[s1];
-  if (blockIdx.y == 0 && threadIdx.x == 0) {
+  if (by == 0 && threadIdx.x == 0) {
     int n = 0;
     if (goes_on) {
       const int r = a.row[s1];
@@ -415,14 +420,24 @@ __global__ __launch_bounds__(64 * FIX_WAVES) void k_embed_fix(EmbBwdArgs a, int 
 
 hipError_t launch_embedding_sum(const EmbBwdArgs& a, hipStream_t s) {
   const int units = a.n_real > 0 ? (int)((a.T + a.unit - 1) / a.unit) : 0;
-  const int64_t zero = a.overwrite ? (a.local_size + EMB_ZERO_ROWS - 1) / EMB_ZERO_ROWS : 0;
-  if (units + zero == 0) return hipGetLastError();
   const int threads = a.H / 8 >= 256 ? 256 : (a.H / 8 + 63) / 64 * 64;
-  const dim3 grid((unsigned)(units + zero), (unsigned)((a.H / 8 + threads - 1) / threads));
-  const bool nt = a.T * a.H * (a.bf16 ? 2 : 4) > (int64_t(256) << 20);
-  if (a.bf16 && nt) hipLaunchKernelGGL((k_embed_sum<true, true>), grid, dim3(threads), 0, s, a, units);
-  else if (a.bf16) hipLaunchKernelGGL((k_embed_sum<true, false>), grid, dim3(threads), 0, s, a, units);
-  else hipLaunchKernelGGL((k_embed_sum<false, false>), grid, dim3(threads), 0, s, a, units);
+  const int ny = (a.H / 8 + threads - 1) / threads;
+  const int pieces = (a.H / 4 + threads - 1) / threads;
+  int64_t blocks = a.overwrite ? a.local_size * pieces : 0;
+  if (units + blocks == 0) return hipGetLastError();
+  int wgs = (int)(blocks < 1 << 22 ? blocks : 1 << 22);
+  const int64_t bytes = a.T * a.H * (a.bf16 ? 2 : 4);
+  if (wgs > 0 && units > 0 && bytes > EMB_APART_BYTES) {
+    hipLaunchKernelGGL(k_embed_zero, dim3((unsigned)wgs), dim3(threads), 0, s, a, blocks, pieces);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    blocks = wgs = 0;
+  }
+  const dim3 grid((unsigned)(units * ny + wgs));
+  const bool nt = bytes > (int64_t(256) << 20);
+  if (a.bf16 && nt) hipLaunchKernelGGL((k_embed_sum<true, true>), grid, dim3(threads), 0, s, a, units, ny, blocks, pieces);
+  else if (a.bf16) hipLaunchKernelGGL((k_embed_sum<true, false>), grid, dim3(threads), 0, s, a, units, ny, blocks, pieces);
+  else hipLaunchKernelGGL((k_embed_sum<false, false>), grid, dim3(threads), 0, s, a, units, ny, blocks, pieces);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || units <= 1) return e;
   hipLaunchKernelGGL(k_embed_fix, dim3((unsigned)((units + FIX_UNITS - 1) / FIX_UNITS), (unsigned)((a.H / 8 + 63) / 64)),

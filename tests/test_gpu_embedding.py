@@ -116,6 +116,32 @@ def test_gradient(llp, kind, T, V, H, dtype):
     assert bytes_equal(acc[keep], old[keep])
 
 
+@pytest.mark.parametrize("T,H,dtype,kind", [(9001, 64, "f32", "skewed"), (12500, 4104, "bf16", "uniform"),
+                                            (33000, 4104, "bf16", "two"), (33000, 4104, "bf16", "skewed"),
+                                            (17000, 1544, "f32", "one"), (8193, 8, "bf16", "runs")])
+def test_gradient_of_large_batches(llp, T, H, dtype, kind):
+    # Ids in a pass of their own, zeros in a launch of their own, rows read past the caches; a shard
+    # in the middle of the table and rows of NaN where the mask is 0.
+    say(f"embedding grad, large, {kind} T={T} H={H} {dtype}")
+    g = np.random.default_rng(T + H)
+    V, lo, nl = 5000, 1200, 2600
+    ids = IDS[kind](g, T, V).astype(np.int64)
+    if kind in ("one", "two"):
+        ids = np.where(ids == V - 1, lo + nl - 1, lo)
+    mask = (g.random(T) < 0.9).astype(np.uint8)
+    dout = torch.randn(T, H, device="cuda", generator=torch.Generator("cuda").manual_seed(T)).to(DT[dtype])
+    dout[torch.from_numpy(mask == 0).cuda()] = float("nan")
+    buf = torch.full((nl, H + 8), 5.0, device="cuda")
+    kw = dict(token_mask=dev(mask), offset=lo, real_vocab=V, padded_vocab=V, rank=1, world=2, scale=0.7)
+    got = llp.embedding_backward(dev(ids), dout, dweight=buf[:, :H], overwrite=True, **kw)
+    for c in (slice(0, 8), slice(H // 2, H // 2 + 4), slice(H - 8, H)):
+        part = torch.where(dev(mask)[:, None] != 0, dout[:, c].float(), 0.0)
+        n = _check_grad(got[:, c], ids, part, 0.7, nl, nl, offset=lo, mask=mask)
+    assert not got[torch.from_numpy(n == 0).cuda()].any() and bool((buf[:, H:] == 5).all())
+    again = llp.embedding_backward(dev(ids), dout, local_size=nl, overwrite=True, **kw)
+    assert bytes_equal(got.contiguous(), again)
+
+
 def test_gradient_of_many_groups_and_rows_behind(llp):
     # More local rows than one sort group per compute unit holds, wide rows, strides.
     g = np.random.default_rng(8)
