@@ -360,7 +360,8 @@ typedef struct {
  *   hidden_size   the padded width: a positive multiple of LLP_INT8_COLUMNS, at most 2^17 - 128
  *                 (the int32 sums cannot overflow; else LLP_ERR_UNSUPPORTED).
  *   hidden_stride and weight_stride < 2^24, T * hidden_stride < 2^31 and the row limits of
- *   llp_projection (else LLP_ERR_UNSUPPORTED).
+ *   llp_projection (else LLP_ERR_UNSUPPORTED). Where hidden_size / LLP_INT8_COLUMNS is odd,
+ *   ceil(T / 256) * ceil(real columns / 256) < 2^23 (else LLP_ERR_UNSUPPORTED).
  * The other fields are those of llp_request (flags: LLP_FLAG_WANT_ENTROPY). Values that are not
  * finite (scales of rows that were not) spread as they do in llp_forward. */
 typedef struct {

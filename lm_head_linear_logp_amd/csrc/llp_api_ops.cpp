@@ -51,6 +51,12 @@ llp_status check_int8(const llp_int8_request* req) {
             (long long)(T * p.hidden_stride));
   LLP_CHECK(p.vocab.local_size <= kMaxRows, LLP_ERR_UNSUPPORTED,
             "local_size %lld exceeds 2^23 - 256", (long long)p.vocab.local_size);
+  // A K of an odd number of 128s takes a workgroup of 512 threads per tile; a launch holds fewer
+  // than 2^32 threads.
+  LLP_CHECK(K % (2 * LLP_INT8_COLUMNS) == 0 ||
+                round_up(T, 256) / 256 * (round_up(local_real(p.vocab), 256) / 256) < (int64_t(1) << 23),
+            LLP_ERR_UNSUPPORTED, "%lld tokens of %lld columns are too many tiles for this hidden_size",
+            (long long)T, (long long)local_real(p.vocab));
   if (T > 0) {
     LLP_CHECK(p.hidden && p.hidden_scale, LLP_ERR_INVALID_ARGUMENT,
               "hidden and hidden_scale are required");

@@ -133,6 +133,7 @@ NAN, INF = float("nan"), float("inf")
     (int8, dict(ws=100), INV), (int8, dict(wsp=None), INV), (int8, dict(wsp=FAKE + 16), INV),
     (int8, dict(out=A.llp_partials(FAKE, FAKE, FAKE, None, FAKE)), INV),
     (int8, dict(cu=FAKE, seqs=-1), INV),
+    (int8, dict(T=1 << 20, V=1 << 21, hidden_size=128), UNS),       # 2^25 tiles, each a workgroup
     (policy, dict(T=-1), INV), (policy, dict(T=1 << 31), INV), (policy, dict(seqs=-1), INV), (policy, dict(seqs=(1 << 23) + 1), UNS),
     (policy, dict(reduction=0), INV), (policy, dict(reduction=4), INV), (policy, dict(clip_low=-0.1), INV),
     (policy, dict(clip_low=1.1), INV), (policy, dict(clip_low=NAN), INV), (policy, dict(clip_high=-0.1), INV),
