@@ -11,12 +11,12 @@ namespace llp {
 
 // ------------------------------------------------------------------------------------
 // Row quantisation: scale = max(max |x|, 1e-30) * fl32(1/127), q = x / scale to the nearest
-// integer, ties to even. A wave takes a row and holds 8 columns per lane and pass in registers; rows of up to
-// QUANT_PASSES * 512 columns are read once, wider ones twice (the second time from L2).
-// Bound by memory: one read, half of it (bf16) written.
+// integer, ties to even. A team of lanes takes a row and holds 8 columns per lane and pass in
+// registers; only rows of more than 8192 columns are read twice (the second time from L2).
+// Bound by memory: one read, half of it (bf16) written: 97 us for 37984 x 4096 bf16, 4.8 TB/s, a
+// copy's rate.
 // ------------------------------------------------------------------------------------
-constexpr int QUANT_PASSES = 2;
-constexpr int QUANT_WAVES = 4;
+constexpr int QUANT_THREADS = 256;
 
 // Columns c .. c + 7 of a row (0 past `cols`). VEC: rows are 16-byte aligned.
 template <bool BF16, bool VEC>
@@ -69,22 +69,22 @@ __device__ __forceinline__ uint2 quant_pack(const float (&v)[8], float scale, fl
   return make_uint2(w[0], w[1]);
 }
 
-// WPR waves share a row: 1, or the whole workgroup.
-template <bool BF16, bool VEC, int WPR>
-__global__ __launch_bounds__(64 * QUANT_WAVES) void k_quant(QuantArgs a) {
-  __shared__ float tops[QUANT_WAVES];
-  constexpr int STEP = 64 * WPR * 8;   // columns per pass
-  const int lane = threadIdx.x % (64 * WPR);
-  const int64_t step = (int64_t)gridDim.x * (QUANT_WAVES / WPR);
-  for (int64_t r = (int64_t)blockIdx.x * (QUANT_WAVES / WPR) + threadIdx.x / (64 * WPR); r < a.rows; r += step) {
+// TEAM lanes share a row (half a wave, a wave or the workgroup), PASSES x 8 columns each.
+template <bool BF16, bool VEC, int TEAM, int PASSES>
+__global__ __launch_bounds__(QUANT_THREADS) void k_quant(QuantArgs a) {
+  __shared__ float tops[QUANT_THREADS / 64];
+  constexpr int STEP = TEAM * 8, ROWS = QUANT_THREADS / TEAM;   // columns per pass, rows at a time
+  const int lane = threadIdx.x % TEAM;
+  const int64_t step = (int64_t)gridDim.x * ROWS;
+  for (int64_t r = (int64_t)blockIdx.x * ROWS + threadIdx.x / TEAM; r < a.rows; r += step) {
     const void* row = static_cast<const char*>(a.x) + r * a.ldx * (BF16 ? 2 : 4);
-    float v[QUANT_PASSES][8];
+    float v[PASSES][8];
     float top = 0.f;   // becomes infinite with an infinity or NaN in the row
-    for (int c0 = 0; c0 < a.cols; c0 += QUANT_PASSES * STEP) {
+    for (int c0 = 0; c0 < a.cols; c0 += PASSES * STEP) {
 #pragma unroll
-      for (int p = 0; p < QUANT_PASSES; ++p) quant_load<BF16, VEC>(row, c0 + p * STEP + lane * 8, a.cols, v[p]);
+      for (int p = 0; p < PASSES; ++p) quant_load<BF16, VEC>(row, c0 + p * STEP + lane * 8, a.cols, v[p]);
 #pragma unroll
-      for (int p = 0; p < QUANT_PASSES; ++p)
+      for (int p = 0; p < PASSES; ++p)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float m = fabsf(v[p][i]);
@@ -92,12 +92,12 @@ __global__ __launch_bounds__(64 * QUANT_WAVES) void k_quant(QuantArgs a) {
         }
     }
 #pragma unroll
-    for (int off = 32; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off));
-    if constexpr (WPR > 1) {
+    for (int off = (TEAM < 64 ? TEAM : 64) / 2; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off));
+    if constexpr (TEAM > 64) {
       if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top;
       __syncthreads();
 #pragma unroll
-      for (int w = 0; w < WPR; ++w) top = fmaxf(top, tops[w]);
+      for (int w = 0; w < TEAM / 64; ++w) top = fmaxf(top, tops[w]);
       __syncthreads();   // read by all before the next row's are written
     }
     const bool bad = !(top < INFINITY);
@@ -105,10 +105,10 @@ __global__ __launch_bounds__(64 * QUANT_WAVES) void k_quant(QuantArgs a) {
     const float inv = 1.f / scale;
     if (lane == 0) a.scale[r] = bad ? __builtin_nanf("") : scale;
     int8_t* q = a.q + r * a.ldq;
-    const bool held = a.cols <= QUANT_PASSES * STEP;
-    for (int c0 = 0; c0 < a.colsp; c0 += QUANT_PASSES * STEP) {
+    const bool held = a.cols <= PASSES * STEP;
+    for (int c0 = 0; c0 < a.colsp; c0 += PASSES * STEP) {
 #pragma unroll
-      for (int p = 0; p < QUANT_PASSES; ++p) {
+      for (int p = 0; p < PASSES; ++p) {
         const int c = c0 + p * STEP + lane * 8;
         if (c >= a.colsp) continue;
         if (!held) quant_load<BF16, VEC>(row, c, a.cols, v[p]);
@@ -120,15 +120,25 @@ __global__ __launch_bounds__(64 * QUANT_WAVES) void k_quant(QuantArgs a) {
   }
 }
 
+template <bool BF16, bool VEC, int TEAM, int PASSES>
+static void launch_quant_team(const QuantArgs& a, hipStream_t s) {
+  // A launch holds fewer than 2^32 threads: past 2^22 workgroups each takes several rows.
+  constexpr int ROWS = QUANT_THREADS / TEAM;
+  const int64_t n = (a.rows + ROWS - 1) / ROWS;
+  const dim3 grid((unsigned)(n < (1 << 22) ? n : 1 << 22));
+  hipLaunchKernelGGL((k_quant<BF16, VEC, TEAM, PASSES>), grid, dim3(QUANT_THREADS), 0, s, a);
+}
+
 template <bool BF16, bool VEC>
 static void launch_quant_as(const QuantArgs& a, hipStream_t s) {
-  // Rows wider than one wave's registers go to the whole workgroup. A launch holds fewer than
-  // 2^32 threads: past 2^22 workgroups each takes several rows.
-  const int per = a.cols > QUANT_PASSES * 512 ? 1 : QUANT_WAVES;
-  const int64_t n = (a.rows + per - 1) / per;
-  const dim3 grid((unsigned)(n < (1 << 22) ? n : 1 << 22)), block(64 * QUANT_WAVES);
-  if (per == 1) hipLaunchKernelGGL((k_quant<BF16, VEC, QUANT_WAVES>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((k_quant<BF16, VEC, 1>), grid, block, 0, s, a);
+  // The smallest team whose registers hold the row (2^27 bf16 values, us a call: 2048 columns 84 by
+  // a wave and 117 by the workgroup, 1152 columns 105 and 184, 256 columns 136 by half a wave and
+  // 215 by one; a wave that reads the row twice takes 105 for 4096 columns, the workgroup 86).
+  if (a.cols <= 512) launch_quant_team<BF16, VEC, 32, 2>(a, s);
+  else if (a.cols <= 1024) launch_quant_team<BF16, VEC, 64, 2>(a, s);
+  else if (a.cols <= 2048) launch_quant_team<BF16, VEC, 64, 4>(a, s);
+  else if (a.cols <= 4096) launch_quant_team<BF16, VEC, 256, 2>(a, s);
+  else launch_quant_team<BF16, VEC, 256, 4>(a, s);
 }
 
 hipError_t launch_quant(const QuantArgs& a, hipStream_t s) {
@@ -142,7 +152,10 @@ hipError_t launch_quant(const QuantArgs& a, hipStream_t s) {
 // ------------------------------------------------------------------------------------
 // Fused forward on int8 operands. The tile, its walk and its epilogue are the bf16 forward's; the
 // int32 sums (exact) become z * tau = (sum * weight scale) * hidden scale + bias in fp32 before
-// the epilogue: three roundings of 2^-24 and, for sums past 2^24, the conversion's.
+// the epilogue: three roundings of 2^-24 and, for sums past 2^24, the conversion's. Bound by the
+// matrix cores: 3686 scored rows of 4096 x 151669 columns take 1994 us, 2.30 PTOP/s, with the MFMA
+// pipes busy 69 % of the time at the clock that such a load is left with; the library's plain int8
+// product of 8192^3 reaches 2.26.
 // ------------------------------------------------------------------------------------
 // The tile's 256 weight scales, 256 biases and 256 hidden scales sit behind the forward's LDS, in
 // the same array; they are written while the accumulators start (every wave has by then passed
@@ -243,9 +256,8 @@ __global__ __launch_bounds__(64 * NW, 1) __attribute__((amdgpu_waves_per_eu(NW /
 // would hold neighbouring rows, every lane a request of its own, and the L1's request rate would
 // bound the stream (37 rows of a 37717-column shard: 53 us). So an instruction takes whole
 // 128-byte lines of 8 weight rows, once and past the caches, and the fragments are moved to their
-// lanes: a DPP move and a ds_bpermute per register. Measured (4096 columns of K): one row of
-// 151669 columns 102 us, 6.1 TB/s of weight (118 us with half lines kept in the caches, 116 with
-// whole ones); 37 rows of the shard 28 us.
+// lanes: a DPP move and a ds_bpermute per register. Measured (K of 4096): one row of 151669 columns
+// 104 us, 6.0 TB/s of weight (118 us with half lines kept in the caches, 116 with whole ones).
 //
 // The int32 sums of the K parts meet in LDS (exact in any order), and from there the epilogue's
 // waves take them in the wide tile's register layout: its sums run in the same order, so every
@@ -508,11 +520,12 @@ static void launch_few(const Fwd8Args& a, hipStream_t s) {
 
 hipError_t launch_fwd8_few(const Fwd8Args& a, hipStream_t s) {
   if (a.f.nvt > 0) {
-    // 4 waves per tile keep every tile of a large vocabulary resident at once (3 per compute
-    // unit); with at most one tile per compute unit, 8 waves have more loads in flight.
-    const bool small = a.f.nvt <= a.f.workers;
-    if (a.la.T <= 16) small ? launch_few<1, 8, 4, 2>(a, s) : launch_few<1, 8, 2, 2>(a, s);
-    else if (a.la.T <= 32) small ? launch_few<2, 8, 4, 2>(a, s) : launch_few<2, 4, 1, 1>(a, s);
+    // Eight blocks of 16 columns per wave and two parts of K, in 4 waves, while the registers hold
+    // them (151936 columns of 4096, us of a replayed call: 16 rows 119, with four parts 137; 32 rows
+    // 119, with four parts 137, with four blocks a wave and one part 158); 64 rows with four blocks
+    // 140, in one part 151 (with eight they spill).
+    if (a.la.T <= 16) launch_few<1, 8, 2, 2>(a, s);
+    else if (a.la.T <= 32) launch_few<2, 8, 2, 2>(a, s);
     else launch_few<4, 4, 2, 2>(a, s);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;

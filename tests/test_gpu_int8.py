@@ -43,6 +43,22 @@ def test_quantize_rows_exactly(llp, R, K, dtype, ld):
     assert np.array_equal(host(q), rq)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("K", [511, 512, 513, 1024, 1025, 2048, 2049, 4096, 4097, 8192, 8193])
+def test_quantize_rows_where_the_team_of_lanes_changes(llp, K, dtype):
+    say(f"quantize K={K} {dtype}")
+    g = np.random.default_rng(K)
+    x = torch.from_numpy((g.standard_normal((11, K)) * 10.0 ** g.uniform(-6, 6, (11, 1))).astype(np.float32))
+    x = x.to(torch.bfloat16) if dtype == "bf16" else x
+    x[3, K - 1] = 9e8                              # the row's top in its last column
+    x[4, K // 2] = float("inf")
+    q, s = llp.quantize_rows(x.cuda())
+    rq, rs = O.quantize(x.float().numpy())
+    fine = np.arange(11) != 4
+    assert np.array_equal(host(s)[fine], rs[fine]) and np.array_equal(host(q)[fine], rq[fine])
+    assert np.isnan(host(s)[4]) and not host(q)[4].any()
+
+
 def test_quantize_rows_near_ties_and_odd_values(llp):
     # Every bf16 value of two binades against scales that put quotients next to the halves.
     bits = np.arange(0x3F80, 0x4080, dtype=np.uint16)
@@ -128,7 +144,7 @@ def test_forward_int8_parity(llp, T, H, real, pad, bias, mask, tau):
             assert not host(out[k])[off].any(), k
 
 
-@pytest.mark.parametrize("T", [3, 30, 64, 70])
+@pytest.mark.parametrize("T", [3, 16, 17, 30, 32, 33, 64, 70])
 def test_forward_int8_many_tiles_and_few_rows(llp, T):
     # 2344 vocabulary tiles: more than a few-row combine holds in LDS; masked rows among them.
     H, real, pad = 128, 600000, 600064
