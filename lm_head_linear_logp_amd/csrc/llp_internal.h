@@ -324,8 +324,10 @@ struct EmbBwdArgs {
   int32_t* status;
 };
 
-// Rows and sequences up to which one workgroup computes a policy loss in one launch.
-constexpr int64_t POLICY_SOLO_ROWS = 8192;
+// Rows and sequences up to which one workgroup computes a policy loss in one launch (us of a
+// replayed call, one launch and three: 4096 rows 9.9 and 12.5, by sequence 15.0 and 16.5; 8192
+// rows 13.4 and 12.8, by sequence 23.1 and 16.3).
+constexpr int64_t POLICY_SOLO_ROWS = 4096;
 constexpr int POLICY_SOLO_SEQS = 1024;
 struct PolicyArgs {
   int64_t T;
@@ -360,9 +362,12 @@ struct PolicyArgs {
 // the sequence alone).
 constexpr int PREF_SPLIT = 4;
 constexpr int PREF_CHUNK = 4096;
-// Rows and pairs up to which one workgroup computes a preference loss in one launch.
+// Rows and pairs up to which one workgroup computes a preference loss in one launch: a launch
+// costs the host more than the device (4607 rows in 8 pairs, one launch and two: 16.4 and 21.7 us
+// a call, 13.2 and 9.0 replayed from a graph; 64 rows of one pair, replayed: 7.2 and 8.4; 8192 rows
+// of 16 pairs: 18.1 and 8.9).
 constexpr int64_t PREF_SOLO_ROWS = 8192;
-constexpr int PREF_SOLO_PAIRS = 16;
+constexpr int PREF_SOLO_PAIRS = 8;
 struct PrefArgs {
   int64_t T;
   const float* logp;

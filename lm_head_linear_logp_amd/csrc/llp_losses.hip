@@ -73,7 +73,11 @@ __device__ __forceinline__ bool cu_bad(const int32_t* cu, int S, int64_t T, int 
 // or per sequence (SEQ_MEAN); the loss kernel, one pass over the rows; one workgroup that adds
 // up its partial sums. With more than POLICY_SEQS sequences one more workgroup, after the count,
 // finds the number of sequences with scored rows; up to that many every block of the loss kernel
-// looks through the counts itself.
+// looks through the counts itself (2^20 rows, us of a replayed call, with the workgroup and
+// without: 1024 sequences 21.2 and 20.1, 4096 24.7 and 25.9, 16384 36 and 46).
+// The loss kernel reads 21 bytes a row and writes 8: 13.4 us for 2^20 rows that the caches hold,
+// 2.3 TB/s, on which the sequence search, the transcendentals and the fp64 sums weigh as much as
+// the memory; count and sum 5.9 and 3.9 us, little more than a launch each.
 // ------------------------------------------------------------------------------------
 constexpr int POLICY_COUNT_ROWS = 16384, POLICY_SEQS = 2048;
 constexpr int SOLO_THREADS = 1024;
@@ -484,14 +488,18 @@ hipError_t launch_policy(const PolicyArgs& a, hipStream_t s) {
 }
 
 // ------------------------------------------------------------------------------------
-// Preference loss. Few rows in few pairs: one workgroup, one launch. Else, first launch: the sum of logp - ref_logp over each sequence's scored rows;
-// PREF_SPLIT workgroups share a sequence, workgroup y taking its chunks y, y + PREF_SPLIT, ... of
+// Preference loss. Few rows in few pairs: one workgroup, one launch. Else, first launch: the sum
+// of logp - ref_logp over each sequence's scored rows; PREF_SPLIT workgroups share a sequence, workgroup y taking its chunks y, y + PREF_SPLIT, ... of
 // PREF_CHUNK rows, so that a sum's order depends on its sequence alone. Second: the sums become each
 // pair's loss and gradient coefficient, and the losses are added up. Third (with few pairs, in
-// one launch with the second): the coefficients are spread over the scored rows.
+// one launch with the second): the coefficients are spread over the scored rows. Bound by memory
+// and launches: 512 pairs of 4128769 rows take 12.5 + 4.7 + 8.2 us (3.0 and 2.5 TB/s in the first
+// and the third).
 // ------------------------------------------------------------------------------------
 // Sum of the scored rows' log ratios of the sequence [from, to), part y of PREF_SPLIT, by thread
 // `tid` of LOSS_THREADS; n rows, `bad` when one of them is not finite.
+// HELD: the rows are in LDS, and one at a time they cost least.
+template <bool HELD>
 __device__ __forceinline__ void pref_partial(const PrefArgs& a, int64_t from, int64_t to, int y, int tid,
                                              double& sum, int& n, int& bad) {
   const int64_t b = from > 0 ? from : 0;
@@ -500,6 +508,17 @@ __device__ __forceinline__ void pref_partial(const PrefArgs& a, int64_t from, in
   n = bad = 0;
   for (int64_t c = b + (int64_t)y * PREF_CHUNK; c < e; c += PREF_SPLIT * PREF_CHUNK) {
     const int64_t ce = c + PREF_CHUNK < e ? c + PREF_CHUNK : e;
+    if constexpr (HELD) {
+#pragma unroll 1
+      for (int t = (int)c + tid; t < (int)ce; t += LOSS_THREADS) {
+        if (a.mask[t] == 0) continue;
+        const float lp = a.logp[t], rf = a.ref != nullptr ? a.ref[t] : 0.f;
+        if (fabsf(lp) < INFINITY && fabsf(rf) < INFINITY) sum += (double)lp - (double)rf;
+        else bad = 1;
+        ++n;
+      }
+      continue;
+    }
     constexpr int N = PREF_CHUNK / LOSS_THREADS;
     // A chunk's loads all in flight; the rows' order does not depend on their alignment.
     float lp[N], rf[N];
@@ -527,7 +546,7 @@ __global__ __launch_bounds__(LOSS_THREADS) void k_pref_sum(PrefArgs a) {
   __shared__ int shi[LOSS_THREADS / 64];
   double sum;
   int n, bad;
-  pref_partial(a, a.cu[blockIdx.x], a.cu[blockIdx.x + 1], blockIdx.y, threadIdx.x, sum, n, bad);
+  pref_partial<false>(a, a.cu[blockIdx.x], a.cu[blockIdx.x + 1], blockIdx.y, threadIdx.x, sum, n, bad);
   sum = block_sum<LOSS_THREADS / 64>(sum, shd);
   n = block_sum<LOSS_THREADS / 64>(n, shi);
   bad = block_sum<LOSS_THREADS / 64>(bad, shi);
@@ -663,7 +682,8 @@ __device__ __forceinline__ void pref_spread(const PrefArgs& a, int64_t t, const 
 }
 
 // FEW (at most PREF_FEW pairs): every workgroup works the pairs out for itself, the first one
-// writes them out, and the launch in between is saved.
+// writes them out, and the launch in between is saved (4000 rows a pair, us of a replayed call,
+// with that launch and without: 128 pairs 11.3 and 10.2, 256 12.7 and 12.7, 512 18.0 and 27.1).
 constexpr int PREF_FEW = 128;
 
 template <bool VEC, bool FEW>
@@ -702,16 +722,46 @@ __global__ __launch_bounds__(PAIR_THREADS) void k_pref_solo(PrefArgs a) {
   __shared__ int wcnt[PREF_SOLO_SEQS][PREF_SPLIT][GW], cnts[PREF_SOLO_SEQS][PREF_SPLIT], shi[NW];
   __shared__ float coef[PREF_SOLO_SEQS];
   __shared__ int cu[PREF_SOLO_SEQS + 1];
+  // All rows, read at once: a group's sequences follow one another without waiting for memory.
+  __shared__ float lp[PREF_SOLO_ROWS], rf[PREF_SOLO_ROWS];
+  __shared__ __attribute__((aligned(16))) uint8_t on[PREF_SOLO_ROWS];
   const int group = threadIdx.x / LOSS_THREADS, tid = threadIdx.x % LOSS_THREADS;
   for (int i = threadIdx.x; i <= 2 * a.P; i += PAIR_THREADS) cu[i] = a.cu[i];
+  {
+    constexpr int N = PREF_SOLO_ROWS / PAIR_THREADS;
+    float l[N], r[N];
+    uint8_t m[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int t = i * PAIR_THREADS + threadIdx.x;
+      const bool in = t < a.T;
+      l[i] = in ? a.logp[t] : 0.f;
+      r[i] = in && a.ref != nullptr ? a.ref[t] : 0.f;
+      m[i] = in && (a.mask == nullptr || a.mask[t] != 0);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int t = i * PAIR_THREADS + threadIdx.x;
+      lp[t] = l[i];
+      rf[t] = r[i];
+      on[t] = m[i];
+    }
+  }
   __syncthreads();
+  PrefArgs own = a;
+  own.cu = cu;
+  own.logp = lp;
+  own.ref = rf;
+  own.mask = on;
+  own.sum = &sums[0][0];
+  own.cnt = &cnts[0][0];
   for (int s = group; s < 2 * a.P; s += GROUPS)
     for (int y = 0; y < PREF_SPLIT; ++y) {
       double sum = 0.0;
       int n = 0, bad = 0;
       // Most responses end before their later parts begin.
       if ((int64_t)cu[s + 1] - cu[s] > (int64_t)y * PREF_CHUNK) {
-        pref_partial(a, cu[s], cu[s + 1], y, tid, sum, n, bad);
+        pref_partial<true>(own, cu[s], cu[s + 1], y, tid, sum, n, bad);
         sum = wave_sum(sum);
         static_assert(PREF_SOLO_ROWS < 1 << 16, "count and flags share a word");
         n = wave_sum(n + (bad << 16));
@@ -739,10 +789,6 @@ __global__ __launch_bounds__(PAIR_THREADS) void k_pref_solo(PrefArgs a) {
     cnts[s][y] = bad ? -1 : n;
   }
   __syncthreads();
-  PrefArgs own = a;
-  own.cu = cu;
-  own.sum = &sums[0][0];
-  own.cnt = &cnts[0][0];
   pref_pairs<NW>(own, coef, true, shd, shi);
   __syncthreads();
   if (a.dlogp == nullptr) return;
