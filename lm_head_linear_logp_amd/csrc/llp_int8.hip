@@ -153,9 +153,9 @@ hipError_t launch_quant(const QuantArgs& a, hipStream_t s) {
 // Fused forward on int8 operands. The tile, its walk and its epilogue are the bf16 forward's; the
 // int32 sums (exact) become z * tau = (sum * weight scale) * hidden scale + bias in fp32 before
 // the epilogue: three roundings of 2^-24 and, for sums past 2^24, the conversion's. Bound by the
-// matrix cores: 3686 scored rows of 4096 x 151669 columns take 1994 us, 2.30 PTOP/s, with the MFMA
-// pipes busy 69 % of the time at the clock that such a load is left with; the library's plain int8
-// product of 8192^3 reaches 2.26.
+// matrix cores: 3686 scored rows of 4096 x 151669 columns take 1906 to 1994 us, 2.3 to 2.4e15
+// operations a second, with the MFMA pipes busy 69 % of the time at the 1.56 GHz that such a load
+// is left with; the library's plain int8 product of 8192^3 reaches 2.26e15.
 // ------------------------------------------------------------------------------------
 // The tile's 256 weight scales, 256 biases and 256 hidden scales sit behind the forward's LDS, in
 // the same array; they are written while the accumulators start (every wave has by then passed
