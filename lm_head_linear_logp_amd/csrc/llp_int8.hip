@@ -282,7 +282,7 @@ __device__ __forceinline__ int few_target(const LayoutArgs& la, int t, int& stat
 }
 
 template <int BMODE, int NB, int IB, int KS, int BUFS>
-__global__ __launch_bounds__(1024 / IB * KS) __attribute__((amdgpu_waves_per_eu(KS * 16 / IB == 4 ? 3 : 2))) void k_fwd8_few(Fwd8Args a) {
+__global__ __launch_bounds__(1024 / IB * KS) __attribute__((amdgpu_waves_per_eu(KS * 16 / IB == 4 && NB < 3 ? 3 : 2))) void k_fwd8_few(Fwd8Args a) {
   constexpr int CG = 16 / IB;   // column groups
   constexpr int THREADS = 64 * CG * KS, LDT = BM + 4;   // LDT: ints per row of sums, off the bank stride
   __shared__ __attribute__((aligned(16))) float red[6 * 256];
@@ -522,10 +522,12 @@ hipError_t launch_fwd8_few(const Fwd8Args& a, hipStream_t s) {
   if (a.f.nvt > 0) {
     // Eight blocks of 16 columns per wave and two parts of K, in 4 waves, while the registers hold
     // them (151936 columns of 4096, us of a replayed call: 16 rows 119, with four parts 137; 32 rows
-    // 119, with four parts 137, with four blocks a wave and one part 158); 64 rows with four blocks
-    // 140, in one part 151 (with eight they spill).
+    // 119, with four parts 137, with four blocks a wave and one part 158; 48 rows 121, with the sums
+    // of both parts in LDS, which leaves one workgroup per compute unit, 128, with four blocks a
+    // wave 141); 64 rows with four blocks 140, in one part 151 (with eight they spill).
     if (a.la.T <= 16) launch_few<1, 8, 2, 2>(a, s);
     else if (a.la.T <= 32) launch_few<2, 8, 2, 2>(a, s);
+    else if (a.la.T <= 48) launch_few<3, 8, 2, 1>(a, s);
     else launch_few<4, 4, 2, 2>(a, s);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;

@@ -144,7 +144,7 @@ def test_forward_int8_parity(llp, T, H, real, pad, bias, mask, tau):
             assert not host(out[k])[off].any(), k
 
 
-@pytest.mark.parametrize("T", [3, 16, 17, 30, 32, 33, 64, 70])
+@pytest.mark.parametrize("T", [3, 16, 17, 30, 32, 33, 48, 49, 64, 70])
 def test_forward_int8_many_tiles_and_few_rows(llp, T):
     # 2344 vocabulary tiles: more than a few-row combine holds in LDS; masked rows among them.
     H, real, pad = 128, 600000, 600064
