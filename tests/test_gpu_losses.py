@@ -204,6 +204,68 @@ def test_losses_malformed_layouts(llp, cu):
         assert int(st) == llp.STATUS_BITS["LAYOUT_INVALID"]
 
 
+@pytest.mark.parametrize("S", [4, 40, 600, 5000])
+@pytest.mark.parametrize("kind", ["end", "start", "falls", "past", "below"])
+def test_losses_malformed_layouts_of_many_rows(llp, S, kind):
+    # The forms of several launches: no row is read or written past the ends, everything is 0.
+    T = 9001
+    say(f"malformed layout {kind} S={S}")
+    x = _rows(T, S)
+    cu = _cuts(x["g"], T, S)
+    k = S // 2
+    if kind == "end":
+        cu[S] = T - 1
+    elif kind == "start":
+        cu[0] = 1
+    elif kind == "falls":
+        cu[k] = cu[k + 1] + 1
+    elif kind == "past":
+        cu[k] = 2 ** 31 - 1
+    else:
+        cu[k] = -2 ** 31
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    a = [dev(x[n]) for n in ("logp", "old", "adv")]
+    out = llp.policy_grads(*a, cu_seqlens=dev(cu), reduction="seq_mean", loss_mask=dev(x["mask"]), status=st)
+    for n in ("loss", "dlogp"):
+        assert not host(out[n]).any(), n
+    assert int(st) == llp.STATUS_BITS["LAYOUT_INVALID"]
+    st.zero_()
+    got = llp.policy_grads(*a, cu_seqlens=dev(cu), loss_mask=dev(x["mask"]), status=st)
+    assert int(st) == llp.STATUS_BITS["LAYOUT_INVALID"]
+    assert bytes_equal(got["dlogp"], llp.policy_grads(*a, loss_mask=dev(x["mask"]))["dlogp"])
+    st.zero_()
+    p = llp.preference_grads(a[0], dev(cu), loss_mask=dev(x["mask"]), status=st)
+    for n in p:
+        assert not host(p[n]).any(), n
+    assert int(st) == llp.STATUS_BITS["LAYOUT_INVALID"]
+
+
+@pytest.mark.parametrize("T", [700, 4096, 20001])
+@pytest.mark.parametrize("S", [1024, 1025, 2048, 2049, 5000])
+def test_policy_many_sequences(llp, T, S):
+    say(f"policy T={T} S={S}")
+    x = _rows(T, T + S)
+    cu = _cuts(x["g"], T, S)
+    kw = dict(reduction="seq_mean", kl_coef=0.1, entropy_coef=0.01)
+    out, ref = _run_policy(llp, x, cu=cu, **kw)
+    _close_policy(out, ref)
+    again, _ = _run_policy(llp, x, cu=cu, **kw)
+    assert all(bytes_equal(out[k], again[k]) for k in out)
+
+
+@pytest.mark.parametrize("P,T", [(1, 8192), (8, 8192), (9, 8192), (8, 8193), (8, 16), (128, 5000), (129, 5000)])
+def test_preference_where_the_launches_change(llp, P, T):
+    say(f"preference P={P} T={T}")
+    x = _rows(T, P + T)
+    cu = _cuts(x["g"], T, 2 * P)
+    out = llp.preference_grads(dev(x["logp"]), dev(cu), ref_logp=dev(x["ref"]), loss_mask=dev(x["mask"]), beta=0.2)
+    ref = O.preference(x["logp"], cu, ref=x["ref"], mask=x["mask"], beta=0.2)
+    _close_pref(out, ref, x)
+    x["logp"][x["mask"] == 0] = np.nan             # rows that are not scored are not looked at
+    same = llp.preference_grads(dev(x["logp"]), dev(cu), ref_logp=dev(x["ref"]), loss_mask=dev(x["mask"]), beta=0.2)
+    assert all(bytes_equal(out[k], same[k]) for k in out)
+
+
 @pytest.mark.parametrize("shift", [1, 2, 3])
 def test_losses_on_unaligned_views_match_aligned(llp, shift):
     T = 2051
