@@ -458,7 +458,9 @@ enum { LLP_PREF_SIGMOID = 1, LLP_PREF_HINGE = 2, LLP_PREF_IPO = 3 };
  *   IPO      (h - 1 / (2 beta))^2
  * loss = sum_i pair_weight_i l_i / P, or without the 1 / P for LLP_REDUCE_SUM.
  *   logp         fp32 [T];  ref_logp fp32 [T] or NULL
- *   pair_weight  fp32 [P] or NULL (1). A pair of weight 0 adds nothing whatever its rows hold.
+ *   pair_weight  fp32 [P] or NULL (1). A pair of weight 0 adds nothing whatever its rows hold; its
+ *                own outputs (l_i, beta R) are written as any pair's, or as 0 where a scored row is
+ *                not finite, without a status.
  *   beta > 0, 0 <= label_smoothing < 1 (0 unless SIGMOID), gamma finite (0 for IPO)
  *   reduction    LLP_REDUCE_SUM, or LLP_REDUCE_TOKEN_MEAN for the mean over pairs
  * A pair with a scored row (or a weight) that is not finite sets LLP_STATUS_VALUE_NOT_FINITE,

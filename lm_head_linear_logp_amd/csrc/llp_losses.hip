@@ -597,8 +597,9 @@ __device__ __forceinline__ PairOut pref_pair(const PrefArgs& a, int p, double up
     }
   }
   PairOut o;
-  o.unfit = w != 0.f && (odd || !(fabsf(w) < INFINITY));
-  const bool ok = w != 0.f && !o.unfit;
+  // A pair of weight 0 keeps its own loss and rewards; it adds nothing and is not reported.
+  const bool fit = !odd && fabsf(w) < INFINITY, live = fit && w != 0.f;
+  o.unfit = !fit && w != 0.f;
   const double h = R[0] - R[1], m = a.beta * h - a.gamma;
   double l, g;   // the pair's loss and its derivative by h
   if (a.kind == LLP_PREF_SIGMOID) {
@@ -612,13 +613,13 @@ __device__ __forceinline__ PairOut pref_pair(const PrefArgs& a, int p, double up
     l = x * x;
     g = 2.0 * x;
   }
-  const double c = ok ? up * (double)w * g : 0.0;
+  const double c = live ? up * (double)w * g : 0.0;
   o.coef[0] = (float)(c * per[0]);
   o.coef[1] = (float)(-c * per[1]);
-  o.loss = ok ? (double)w * l : 0.0;
-  o.l = ok ? (float)l : 0.f;
-  o.chosen = ok ? (float)(a.beta * R[0]) : 0.f;
-  o.rejected = ok ? (float)(a.beta * R[1]) : 0.f;
+  o.loss = live ? (double)w * l : 0.0;
+  o.l = fit ? (float)l : 0.f;
+  o.chosen = fit ? (float)(a.beta * R[0]) : 0.f;
+  o.rejected = fit ? (float)(a.beta * R[1]) : 0.f;
   return o;
 }
 

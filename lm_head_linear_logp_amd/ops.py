@@ -280,7 +280,8 @@ def preference_grads(logp: torch.Tensor, cu_seqlens: torch.Tensor, *,
     ``backward``. kind "sigmoid", "hinge" or "ipo"; reduction "mean" (over pairs) or "sum";
     average: mean log ratio per response instead of the sum. Returns loss [1], pair_loss [P],
     chosen [P] and rejected [P] (beta times the responses' log ratios) and dlogp [T] (None
-    unless want_grad)."""
+    unless want_grad). pair_weight weighs the pairs in the loss; a pair of weight 0 still gets its
+    own pair_loss, chosen and rejected."""
     dev, T = _len(logp, "logp", _F32)
     layout = _layout(T, loss_mask, _tensor(cu_seqlens, "cu_seqlens"), dev)
     if layout.num_seqs % 2:

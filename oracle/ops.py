@@ -139,7 +139,7 @@ def preference(logp, cu, ref=None, mask=None, pair_weight=None, beta=0.1, kind="
             rows.append(k)
             per.append(f)
             R.append(x[k].sum() * f)
-        if wt == 0.0 or not np.isfinite(wt) or not np.isfinite(x[np.concatenate(rows)]).all():
+        if not np.isfinite(wt) or not np.isfinite(x[np.concatenate(rows)]).all():
             continue
         h = R[0] - R[1]
         m = beta * h - gamma
