@@ -386,7 +386,6 @@ LLP_API llp_status llp_policy_loss(const llp_policy_request* req, const llp_poli
   a.dual = (float)req->dual_clip;
   a.klc64 = req->kl_coef;
   a.entc64 = req->entropy_coef;
-  a.klc = (float)req->kl_coef;
   a.kl_kind = req->kl_kind;
   a.reduction = req->reduction;
   a.denom = req->denominator;

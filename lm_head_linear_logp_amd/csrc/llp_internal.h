@@ -341,7 +341,6 @@ struct PolicyArgs {
   int32_t S;
   double log_lo, log_hi, log_dual;     // borders of d = logp - old_logp
   float lo, hi, dual;                  // the clipped ratios
-  float klc;
   int32_t kl_kind, reduction;
   const float* denom;
   int32_t nblocks;                     // blocks of the loss kernel; 0: one workgroup does it all

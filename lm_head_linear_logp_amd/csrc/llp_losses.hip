@@ -1,8 +1,8 @@
 // llp_losses.hip -- losses on scored log-probabilities and their gradients: the clipped policy
 // loss with a KL term, and the preference loss of paired responses.
 //
-// Both are bound by memory at many rows and by launches at few. Per-row arithmetic is fp32, sums
-// are fp64, in an order fixed by the sizes alone; there are no float atomics.
+// Both are bound by memory at many rows and by launches at few. A row's exponentials are fp32, its
+// products and all sums fp64, in an order fixed by the sizes alone; there are no float atomics.
 #include "llp_internal.h"
 
 #include <hip/hip_runtime.h>
@@ -145,8 +145,11 @@ __device__ __forceinline__ float exp_minus_linear(float y) {
   return p * y * y;
 }
 
+// Exponentials in fp32, the products after them in fp64: finite values of any size give finite
+// terms, so that a term of weight or coefficient 0 adds 0.
 struct PolicyRow {
-  float pg, kl, ratio, grad;   // policy term, KL value, r, d (policy + kl_coef kl) / d logp
+  double pg, kl, grad;   // policy term, KL value, d (policy + kl_coef kl) / d logp
+  float ratio;           // r
   bool clipped;
 };
 
@@ -171,25 +174,25 @@ __device__ __forceinline__ PolicyRow policy_row(const PolicyArgs& a, float lp, f
     used = a.dual;
     o.clipped = true;
   }
-  o.pg = -adv * used;
-  o.grad = o.clipped || !inside ? 0.f : -adv * o.ratio;
-  o.kl = 0.f;
+  o.pg = -(double)adv * (double)used;
+  o.grad = o.clipped || !inside ? 0.0 : -(double)adv * (double)o.ratio;
+  o.kl = 0.0;
   if (a.ref != nullptr) {
     const double xd = (double)ref - (double)lp;
-    const float x = (float)xd;
-    float g;
+    double g;
     if (a.kl_kind == LLP_KL_K1) {
-      o.kl = -x;
-      g = 1.f;
+      o.kl = -xd;
+      g = 1.0;
     } else if (a.kl_kind == LLP_KL_K2) {
-      o.kl = 0.5f * x * x;
-      g = -x;
+      o.kl = 0.5 * xd * xd;
+      g = -xd;
     } else {
+      const float x = (float)xd;
       const float y = fminf(fmaxf(x, -(float)LLP_LOG_RATIO_MAX), (float)LLP_LOG_RATIO_MAX);
-      o.kl = exp_minus_linear(y);
-      g = fabs(xd) <= (double)LLP_LOG_RATIO_MAX ? -expm1f(x) : 0.f;
+      o.kl = (double)exp_minus_linear(y);
+      g = fabs(xd) <= (double)LLP_LOG_RATIO_MAX ? -(double)expm1f(x) : 0.0;
     }
-    o.grad = fmaf(a.klc, g, o.grad);
+    o.grad = fma(a.klc64, g, o.grad);
   }
   return o;
 }
@@ -283,13 +286,13 @@ __device__ __forceinline__ void policy_rows(const PolicyArgs& a, int64_t t, cons
       continue;
     }
     const PolicyRow r = policy_row(a, x.lp[i], x.old[i], x.adv[i], x.ref[i]);
-    sum[0] += w * (double)r.pg;
-    sum[1] += w * (double)r.kl;
+    sum[0] += w * r.pg;
+    sum[1] += w * r.kl;
     sum[2] += w * (double)x.ent[i];
     sum[3] += r.clipped ? w : 0.0;
     sum[4] += w * (double)r.ratio;
     sum[5] += w * ((double)x.old[i] - (double)x.lp[i]);
-    dl[i] = (float)(up * w * (double)r.grad);
+    dl[i] = (float)(up * w * r.grad);
     de[i] = (float)(up * w * -a.entc64);
   }
   store4<VEC>(a.dlogp, t, a.T, dl);
