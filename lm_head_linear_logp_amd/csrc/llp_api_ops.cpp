@@ -140,7 +140,7 @@ llp_status check_policy(const llp_policy_request* req) {
 }
 
 struct PolicyWs {
-  size_t count, meta, part, total;
+  size_t count, meta, looks, part, total;
   int32_t ncount, nblocks;
 };
 
@@ -159,6 +159,7 @@ PolicyWs policy_ws(const llp_policy_request& r) {
   Regions g;
   w.count = g.take((size_t)w.ncount * 4);
   w.meta = g.take(4);
+  w.looks = g.take(LAYOUT_LOOKS * 4);
   w.part = g.take((size_t)w.nblocks * LLP_POLICY_STATS * 8);
   w.total = g.off;
   return w;
@@ -191,7 +192,7 @@ llp_status check_pref(const llp_pref_request* req) {
 }
 
 struct PrefWs {
-  size_t sum, cnt, coef, total;
+  size_t sum, cnt, coef, looks, total;
 };
 
 PrefWs pref_ws(const llp_pref_request& r) {
@@ -203,6 +204,7 @@ PrefWs pref_ws(const llp_pref_request& r) {
   w.sum = g.take(n * PREF_SPLIT * 8);
   w.cnt = g.take(n * PREF_SPLIT * 4);
   w.coef = g.take(n * 4);
+  w.looks = g.take(LAYOUT_LOOKS * 4);
   w.total = g.off;
   return w;
 }
@@ -393,6 +395,8 @@ LLP_API llp_status llp_policy_loss(const llp_policy_request* req, const llp_poli
   a.ncount = w.ncount;
   a.count = at<int32_t>(workspace, w.count);
   a.meta = at<int32_t>(workspace, w.meta);
+  a.looks = at<int32_t>(workspace, w.looks);
+  a.first = req->reduction == LLP_REDUCE_SEQ_MEAN && layout_first(req->layout);
   a.part = at<double>(workspace, w.part);
   a.loss = out->loss;
   a.stats = out->stats;
@@ -440,6 +444,8 @@ LLP_API llp_status llp_preference_loss(const llp_pref_request* req, const llp_pr
   a.sum = at<double>(workspace, w.sum);
   a.cnt = at<int32_t>(workspace, w.cnt);
   a.coef = at<float>(workspace, w.coef);
+  a.looks = at<int32_t>(workspace, w.looks);
+  a.first = layout_first(req->layout);
   a.loss = out->loss;
   a.pair_loss = out->pair_loss;
   a.chosen = out->chosen;

@@ -324,6 +324,16 @@ struct EmbBwdArgs {
   int32_t* status;
 };
 
+// The losses read each sequence's rows where cu_seqlens says they are: T rows in all, but a malformed
+// one may name all of them again for every other sequence, hours of work at the largest sizes. Where
+// sequences x rows pass this, a launch in front looks the layout over and a malformed one's rows are
+// not read; below, 2^36 rows at most are (about 0.3 s), and that launch is saved.
+constexpr int64_t LAYOUT_FIRST = int64_t(1) << 37;
+constexpr int LAYOUT_LOOKS = 64;   // its workgroups
+inline bool layout_first(const llp_token_layout& l) {
+  return (int64_t)l.num_seqs * l.num_tokens > LAYOUT_FIRST;
+}
+
 // Rows and sequences up to which one workgroup computes a policy loss in one launch (us of a
 // replayed call, one launch and three: 4096 rows 9.9 and 12.5, by sequence 15.0 and 16.5; 8192
 // rows 13.4 and 12.8, by sequence 23.1 and 16.3).
@@ -347,6 +357,8 @@ struct PolicyArgs {
   int32_t ncount;                      // blocks of the count kernel (0: nothing to count)
   int32_t* count;                      // [ncount] scored rows, or [S] for SEQ_MEAN
   int32_t* meta;                       // [1] sequences with scored rows, -1: malformed cu_seqlens
+  int32_t first;                       // the layout is looked over in front (layout_first)
+  int32_t* looks;                      // [LAYOUT_LOOKS] what that found (1: malformed)
   double* part;                        // [nblocks][LLP_POLICY_STATS]
   float* loss;
   float* stats;
@@ -381,6 +393,8 @@ struct PrefArgs {
   double* sum;       // [2 P][PREF_SPLIT]
   int32_t* cnt;      // [2 P][PREF_SPLIT], scored rows; -1 when one of them is not finite
   float* coef;       // [2 P] d loss / d logp of a scored row of the sequence
+  int32_t first;     // the layout is looked over in front (layout_first)
+  int32_t* looks;    // [LAYOUT_LOOKS] what that found (1: malformed)
   float* loss;
   float* pair_loss;
   float* chosen;

@@ -67,6 +67,22 @@ __device__ __forceinline__ bool cu_bad(const int32_t* cu, int S, int64_t T, int 
   return (i == 0 && c != 0) || (i == S && (int64_t)c != T) || (i < S && cu[i + 1] < c);
 }
 
+// Whether the layout is malformed, found before anything reads the rows it names (layout_first), a
+// slice of it per workgroup (us of a replayed call with and without: policy of 2^20 rows in 2^17
+// sequences 149 and 139, preference 898 and 885).
+__global__ __launch_bounds__(1024) void k_layout_first(const int32_t* cu, int S, int64_t T, int32_t* looks) {
+  __shared__ int sh[16];
+  int bad = 0;
+#pragma unroll 4
+  for (int i = blockIdx.x * 1024 + threadIdx.x; i <= S; i += LAYOUT_LOOKS * 1024) bad |= cu_bad(cu, S, T, i) ? 1 : 0;
+  bad = block_sum<16>(bad, sh);
+  if (threadIdx.x == 0) looks[blockIdx.x] = bad != 0 ? 1 : 0;
+}
+static_assert(LAYOUT_LOOKS == 64, "one flag per lane");
+__device__ __forceinline__ bool layout_found_bad(const int32_t* looks) {
+  return __builtin_amdgcn_ballot_w64(looks[threadIdx.x & 63] != 0) != 0;
+}
+
 // ------------------------------------------------------------------------------------
 // Clipped policy loss. Up to POLICY_SOLO_ROWS rows one workgroup does it all in one launch.
 // Beyond, launches: scored rows counted per block of POLICY_COUNT_ROWS (TOKEN_MEAN with a mask)
@@ -87,6 +103,11 @@ __global__ __launch_bounds__(LOSS_THREADS) void k_policy_count(PolicyArgs a) {
   __shared__ int sh[LOSS_THREADS / 64];
   int64_t b, e;
   bool bad = false;
+  if (a.first && layout_found_bad(a.looks)) {
+    if (threadIdx.x == 0) a.count[blockIdx.x] = -1;
+    if (threadIdx.x == 0 && blockIdx.x == 0 && a.status) atomicOr(a.status, LLP_STATUS_LAYOUT_INVALID);
+    return;
+  }
   if (a.reduction == LLP_REDUCE_SEQ_MEAN) {
     bad = cu_bad(a.cu, a.S, a.T, blockIdx.x) || cu_bad(a.cu, a.S, a.T, blockIdx.x + 1);
     b = a.cu[blockIdx.x] > 0 ? a.cu[blockIdx.x] : 0;
@@ -472,6 +493,11 @@ hipError_t launch_policy(const PolicyArgs& a, hipStream_t s) {
     else hipLaunchKernelGGL(k_policy_solo<false>, dim3(1), dim3(SOLO_THREADS), 0, s, a);
     return hipGetLastError();
   }
+  if (a.first) {
+    hipLaunchKernelGGL(k_layout_first, dim3(LAYOUT_LOOKS), dim3(1024), 0, s, a.cu, a.S, a.T, a.looks);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
   if (a.ncount > 0) {
     hipLaunchKernelGGL(k_policy_count, dim3((unsigned)a.ncount), block, 0, s, a);
     const hipError_t e = hipGetLastError();
@@ -549,6 +575,7 @@ __global__ __launch_bounds__(LOSS_THREADS) void k_pref_sum(PrefArgs a) {
   __shared__ int shi[LOSS_THREADS / 64];
   double sum;
   int n, bad;
+  if (a.first && layout_found_bad(a.looks)) return;   // every output is 0, whatever the sums are
   pref_partial<false>(a, a.cu[blockIdx.x], a.cu[blockIdx.x + 1], blockIdx.y, threadIdx.x, sum, n, bad);
   sum = block_sum<LOSS_THREADS / 64>(sum, shd);
   n = block_sum<LOSS_THREADS / 64>(n, shi);
@@ -816,6 +843,11 @@ hipError_t launch_preference(const PrefArgs& a, hipStream_t s) {
     else
       hipLaunchKernelGGL(k_pref_solo<false>, dim3(1), dim3(PAIR_THREADS), 0, s, a);
     return hipGetLastError();
+  }
+  if (a.first) {
+    hipLaunchKernelGGL(k_layout_first, dim3(LAYOUT_LOOKS), dim3(1024), 0, s, a.cu, 2 * a.P, a.T, a.looks);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
   }
   if (a.P > 0) {
     hipLaunchKernelGGL(k_pref_sum, dim3((unsigned)(2 * a.P), PREF_SPLIT), dim3(LOSS_THREADS), 0, s, a);

@@ -1,5 +1,5 @@
 """Losses where a value, a weight or a layout is at its edge: pairs of weight 0, terms past
-fp32's range."""
+fp32's range, layouts that name the same rows for every sequence."""
 import numpy as np
 import pytest
 import torch
@@ -90,3 +90,61 @@ def test_policy_terms_past_fp32_of_finite_rows(llp, T, case):
     with np.errstate(over="ignore"):
         want = r["stats"][2].astype(np.float32)
     assert float(out["stats"][2]) == want or abs(float(out["stats"][2]) - r["stats"][2]) <= 16 * EPS * abs(want)
+
+
+def test_layouts_that_name_all_rows_for_every_sequence_cost_no_more(llp):
+    # 2^19 sequences of 2^22 rows each: read as they stand, 2e12 mask bytes and 2e13 of log-probs.
+    S, T = 1 << 20, 1 << 22
+    cu = torch.zeros(S + 1, dtype=torch.int32, device="cuda")
+    cu[1::2] = T
+    lp = torch.randn(T, device="cuda")
+    mask = torch.ones(T, dtype=torch.uint8, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    calls = (lambda: llp.policy_grads(lp, lp, lp, cu_seqlens=cu, loss_mask=mask, reduction="seq_mean", status=st),
+             lambda: llp.preference_grads(lp, cu, loss_mask=mask, status=st))
+    for name, call in zip(("policy", "preference"), calls):
+        say(f"layout of {S} x {T} rows: {name}")
+        st.zero_()
+        ends = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+        ends[0].record()
+        out = call()
+        ends[1].record()
+        torch.cuda.synchronize()
+        for k in out:
+            assert out[k] is None or not host(out[k]).any(), k
+        assert int(st) == llp.STATUS_BITS["LAYOUT_INVALID"]
+        ms = ends[0].elapsed_time(ends[1])
+        say(f"{name}: {ms:.2f} ms")
+        assert ms < 200     # 2e12 bytes take longer than this at twice the memory's rate
+
+
+def test_losses_of_well_formed_layouts_looked_over_first(llp):
+    # 2^20 sequences, most of them empty, of 2^18 rows: the layout is looked over before it is used.
+    S, T = 1 << 20, 1 << 18
+    g = np.random.default_rng(2)
+    cu = np.concatenate([[0], np.sort(g.integers(0, T + 1, S - 1)), [T]]).astype(np.int32)
+    lp, adv = -g.exponential(1.0, T).astype(np.float32), g.standard_normal(T).astype(np.float32)
+    mask = (g.random(T) < 0.7).astype(np.uint8)
+    on = mask != 0
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    say("policy and preference of 2^20 sequences")
+    out = llp.policy_grads(dev(lp), dev(lp), dev(adv), cu_seqlens=dev(cu), loss_mask=dev(mask),
+                           reduction="seq_mean", status=st)
+    seq = np.searchsorted(cu, np.arange(T), side="right") - 1
+    n = np.bincount(seq[on], minlength=S)
+    w = np.where(on, 1.0 / (np.maximum(n, 1)[seq] * (n > 0).sum()), 0.0)
+    # ratios are 1: each term is its advantage, exact; fp64 sums, rounded once
+    assert np.all(np.abs(host(out["dlogp"]) + w * adv) <= 2 * EPS * w * np.abs(adv))
+    assert abs(float(out["loss"]) + (w * adv).sum()) <= 2 * EPS * (w * np.abs(adv)).sum()
+    assert float(out["stats"][7]) == on.sum() and int(st) == 0
+    p = llp.preference_grads(dev(lp), dev(cu), loss_mask=dev(mask), beta=0.5, status=st)
+    R = np.bincount(seq[on], weights=lp[on].astype(np.float64), minlength=S)
+    h = R[0::2] - R[1::2]
+    lim = 2 * EPS * np.abs(R) + 1e-12
+    assert np.all(np.abs(host(p["chosen"]) - 0.5 * R[0::2]) <= lim[0::2])
+    assert np.all(np.abs(host(p["rejected"]) - 0.5 * R[1::2]) <= lim[1::2])
+    per = np.logaddexp(0, -0.5 * h)
+    assert abs(float(p["loss"]) - per.mean()) <= 2 * EPS * per.mean() + 1e-12 and int(st) == 0
+    gr = -0.5 / (1 + np.exp(0.5 * h)) / (S // 2)
+    want = np.where(on, np.where(seq % 2 == 0, 1, -1) * gr[seq // 2], 0.0)
+    assert np.all(np.abs(host(p["dlogp"]) - want) <= 2 * EPS * np.abs(want) + 1e-18)
