@@ -86,9 +86,6 @@ llp_status check_int8(const llp_int8_request* req) {
 }
 
 // ---- Losses ---------------------------------------------------------------------------------
-constexpr int64_t kPolicyBlockRows = 1024, kPolicyCountRows = 16384;
-constexpr int64_t kPolicyBlocks = 1024;
-
 // One workgroup per sequence: a launch holds fewer than 2^32 threads.
 constexpr int32_t kMaxSeqs = 1 << 23;
 
@@ -152,10 +149,10 @@ PolicyWs policy_ws(const llp_policy_request& r) {
     return w;   // one workgroup, no workspace
   if (by_seq) w.ncount = r.layout.num_seqs;
   else if (r.reduction == LLP_REDUCE_TOKEN_MEAN && r.layout.loss_mask && !r.denominator)
-    w.ncount = (int32_t)((T + kPolicyCountRows - 1) / kPolicyCountRows);
-  int64_t nb = (T + kPolicyBlockRows - 1) / kPolicyBlockRows;
+    w.ncount = (int32_t)((T + POLICY_COUNT_ROWS - 1) / POLICY_COUNT_ROWS);
+  int64_t nb = (T + POLICY_BLOCK_ROWS - 1) / POLICY_BLOCK_ROWS;
   if (nb < 1) nb = 1;   // no rows in many sequences
-  w.nblocks = (int32_t)(nb < kPolicyBlocks ? nb : kPolicyBlocks);
+  w.nblocks = (int32_t)(nb < POLICY_BLOCKS ? nb : POLICY_BLOCKS);
   Regions g;
   w.count = g.take((size_t)w.ncount * 4);
   w.meta = g.take(4);

@@ -339,6 +339,9 @@ inline bool layout_first(const llp_token_layout& l) {
 // rows 13.4 and 12.8, by sequence 23.1 and 16.3).
 constexpr int64_t POLICY_SOLO_ROWS = 4096;
 constexpr int POLICY_SOLO_SEQS = 1024;
+// Beyond: rows per workgroup of the count and per workgroup and pass of the loss kernel, and the
+// latter's most workgroups.
+constexpr int64_t POLICY_COUNT_ROWS = 16384, POLICY_BLOCK_ROWS = 1024, POLICY_BLOCKS = 1024;
 struct PolicyArgs {
   int64_t T;
   const float* logp;

@@ -95,8 +95,10 @@ __device__ __forceinline__ bool layout_found_bad(const int32_t* looks) {
 // 2.3 TB/s, on which the sequence search, the transcendentals and the fp64 sums weigh as much as
 // the memory; count and sum 5.9 and 3.9 us, little more than a launch each.
 // ------------------------------------------------------------------------------------
-constexpr int POLICY_COUNT_ROWS = 16384, POLICY_SEQS = 2048;
+constexpr int POLICY_SEQS = 2048;
 constexpr int SOLO_THREADS = 1024;
+static_assert(POLICY_BLOCK_ROWS == LOSS_THREADS * 4, "four rows per thread of the loss kernel");
+static_assert(POLICY_SOLO_ROWS <= SOLO_THREADS * 4, "four rows per thread of the one workgroup");
 
 // SEQ_MEAN counts carry a malformed cu_seqlens as -1.
 __global__ __launch_bounds__(LOSS_THREADS) void k_policy_count(PolicyArgs a) {
@@ -423,7 +425,8 @@ __global__ __launch_bounds__(SOLO_THREADS) void k_policy_solo(PolicyArgs a) {
   const bool by_seq = a.reduction == LLP_REDUCE_SEQ_MEAN;
   int status = 0, n = 0;
   PolicyRows x;
-  policy_load<VEC>(a, threadIdx.x * 4, x);
+  const int64_t t = threadIdx.x * 4;   // four rows a thread: all of them
+  policy_load<VEC>(a, t, x);
   bool bad = false;
   if (a.cu != nullptr)
     for (int i = threadIdx.x; i <= a.S; i += SOLO_THREADS) bad |= cu_bad(a.cu, a.S, a.T, i);
@@ -434,46 +437,35 @@ __global__ __launch_bounds__(SOLO_THREADS) void k_policy_solo(PolicyArgs a) {
     void_layout = block_sum<NW>(bad ? 1 : 0, shi) != 0;
     if (!void_layout) {
       // Whole numbers: the order of the additions is free. A run of rows of one sequence is one.
-      for (int64_t t0 = 0; t0 < a.T; t0 += SOLO_THREADS * 4) {
-        const int64_t t = t0 + threadIdx.x * 4;
-        if (t0 > 0) mask4<VEC>(a.mask, t, a.T, x.m);
-        int s = -1, s_end = 0, run = 0;
+      int s = -1, s_end = 0, run = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (!x.m[i]) continue;
-          if (s < 0 || t + i >= s_end) {
-            if (run) atomicAdd(count + s, run);
-            s = seq_of(a.cu, t + i, s < 0 ? 0 : s, a.S - 1);
-            s_end = a.cu[s + 1];
-            run = 0;
-          }
-          ++run;
+      for (int i = 0; i < 4; ++i) {
+        if (!x.m[i]) continue;
+        if (s < 0 || t + i >= s_end) {
+          if (run) atomicAdd(count + s, run);
+          s = seq_of(a.cu, t + i, s < 0 ? 0 : s, a.S - 1);
+          s_end = a.cu[s + 1];
+          run = 0;
         }
-        if (run) atomicAdd(count + s, run);
+        ++run;
       }
+      if (run) atomicAdd(count + s, run);
     }
     __syncthreads();
     for (int i = threadIdx.x; i < a.S; i += SOLO_THREADS) n += count[i] > 0 ? 1 : 0;
   } else if (a.reduction == LLP_REDUCE_TOKEN_MEAN && a.denom == nullptr) {
-    for (int64_t t0 = 0; t0 < a.T; t0 += SOLO_THREADS * 4) {
-      if (t0 > 0) mask4<VEC>(a.mask, t0 + threadIdx.x * 4, a.T, x.m);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) n += x.m[i] ? 1 : 0;
-    }
+    for (int i = 0; i < 4; ++i) n += x.m[i] ? 1 : 0;
   }
   n = block_sum<NW>(n, shi);
   const double norm = policy_norm(a, n);
   const double up = a.dloss != nullptr ? (double)a.dloss[0] : 1.0;
   double sum[POLICY_SUMS] = {0.0, 0.0, 0.0, 0.0, 0.0, 0.0, 0.0};
-  for (int64_t t0 = 0; t0 < a.T; t0 += SOLO_THREADS * 4) {
-    const int64_t t = t0 + threadIdx.x * 4;
-    if (a.T > SOLO_THREADS * 4) policy_load<VEC>(a, t, x);
-    if (void_layout) {
+  if (void_layout) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x.m[i] = false;
-    }
-    policy_rows<VEC>(a, t, x, norm, up, by_seq, count, 0, a.S - 1, sum, status);
+    for (int i = 0; i < 4; ++i) x.m[i] = false;
   }
+  policy_rows<VEC>(a, t, x, norm, up, by_seq, count, 0, a.S - 1, sum, status);
   if (status && a.status) atomicOr(a.status, status);
   policy_finish(a, policy_total<NW>(sum, shd), fin);
 }
