@@ -18,11 +18,15 @@ namespace llp {
 // entropy = ln S - ln2 * Q / S. An empty shard gives lse = -inf, entropy 0, target logit 0,
 // in_range 0 and logp -inf ([top-p replay, "Changes" table]: empty vocabulary rows).
 // ------------------------------------------------------------------------------------
-// Q = wa (Q + S da log2 e) + wb (q + s db log2 e) and S = wa S + wb s, each rounding written out, so
-// that every kernel that folds gives the same bits.
+// Each rounding of a combine is written out, here and below, so that every kernel that combines
+// gives the same bits however the compiler would contract its products.
+// q + s d log2 e:
+__device__ __forceinline__ float weighed(float q, float s, float d) { return fmaf(kLog2e, s * d, q); }
+
+// Q = wa (Q + S da log2 e) + wb (q + s db log2 e) and S = wa S + wb s.
 __device__ __forceinline__ void fold_sums(float& S, float& Q, float wa, float wb, float da, float db,
                                           float s, float q) {
-  const float x = fmaf(kLog2e, S * da, Q), y = fmaf(kLog2e, s * db, q);
+  const float x = weighed(Q, S, da), y = weighed(q, s, db);
   Q = fmaf(wb, y, wa * x);
   S = fmaf(wb, s, wa * S);
 }
@@ -59,8 +63,8 @@ __device__ __forceinline__ void combine_chain(int c, int nvt, Max max_of, Get ge
       get(vt, m, s, q);
       const float d = m - mmax;
       const float e = expf(d);
-      S += e * s;
-      Q += e * (q + s * d * kLog2e);
+      S = fmaf(e, s, S);
+      Q = fmaf(e, weighed(q, s, d), Q);
     }
     M = mmax;
   }
@@ -76,7 +80,7 @@ __device__ __forceinline__ void combine_out(const CombineArgs& a, int row, bool 
   } else {
     const float ls = logf(S);
     lse = M + ls;
-    ent = ls - kLn2 * (Q / S);
+    ent = fmaf(-kLn2, Q / S, ls);
   }
   const float tz = hit ? target : 0.f;
   a.out_t[row] = tz;
@@ -122,7 +126,7 @@ __device__ __forceinline__ void combine_few(const CombineArgs& a, int j, Combine
     for (int vt = tid; vt < a.nvt; vt += COMBINE_FEW_THREADS) {
       const float d = l.m[vt] - mmax, s = l.s[vt], q = l.q[vt];
       l.m[vt] = expf(d);
-      l.q[vt] = q + s * d * kLog2e;
+      l.q[vt] = weighed(q, s, d);
     }
   __syncthreads();
   if (tid < COMBINE_CHAINS) {
@@ -133,8 +137,8 @@ __device__ __forceinline__ void combine_few(const CombineArgs& a, int j, Combine
 #pragma unroll 8
       for (int vt = c; vt < a.nvt; vt += COMBINE_CHAINS) {
         const float e = l.m[vt];
-        S += e * l.s[vt];
-        Q += e * l.q[vt];
+        S = fmaf(e, l.s[vt], S);
+        Q = fmaf(e, l.q[vt], Q);
       }
       M = mmax;
     }
