@@ -1,6 +1,5 @@
 """A forward of few rows ends in a combine of its own: its rows have the bits they have in a large
 batch, with entropy and without, and in the library's own scratch."""
-import numpy as np
 import pytest
 import torch
 
