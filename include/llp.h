@@ -22,9 +22,12 @@
  *   - `stream` is a hipStream_t passed as void* (NULL = the null stream).
  *   - Execution calls (every call but llp_open and the workspace sizes) never allocate, never
  *     synchronize and never read device memory on the host, so they can be captured into a
- *     HIP graph. Every row's result is a function of that row's inputs and the fixed kernel
- *     configuration only: results are bitwise reproducible run to run and do not depend on
- *     how rows are batched or ordered (dweight/dbias: reproducible for a fixed batch).
+ *     HIP graph. Results are bitwise reproducible run to run. What is computed per row (scores
+ *     and their partials, dhidden, quantised and embedded rows) is a function of that row's
+ *     inputs and the fixed kernel configuration only and does not depend on how rows are
+ *     batched or ordered; nor do a preference pair's own loss and rewards. Sums over a batch
+ *     (dweight, dbias, the embedding gradient, the losses' totals and statistics) are
+ *     reproducible for a fixed batch.
  *   - Errors are returned as llp_status; no exception crosses the ABI and the library never
  *     aborts. llp_last_error() describes the last non-OK status of the calling thread.
  *   - Host-detectable problems (shapes, strides, alignment, partition, temperature, limits)
@@ -409,7 +412,7 @@ enum { LLP_REDUCE_TOKEN_MEAN = 1, LLP_REDUCE_SEQ_MEAN = 2, LLP_REDUCE_SUM = 3 };
  *   logp, old_logp, advantages   fp32 [T]
  *   ref_logp   fp32 [T], or NULL (then no KL term; kl_coef must be 0)
  *   entropy    fp32 [T], or NULL (then no bonus; entropy_coef must be 0)
- *   layout     T < 2^31, num_seqs <= 2^23 (else LLP_ERR_UNSUPPORTED); cu_seqlens is required
+ *   layout     T < 2^31; num_seqs <= 2^23 (else LLP_ERR_UNSUPPORTED); cu_seqlens is required
  *              for SEQ_MEAN. A malformed cu_seqlens sets
  *              LLP_STATUS_LAYOUT_INVALID, and with SEQ_MEAN every output is 0 then.
  *   0 <= clip_low <= 1, clip_high >= 0, dual_clip 0 (none) or > 1, all coefficients finite.
@@ -463,8 +466,8 @@ enum { LLP_PREF_SIGMOID = 1, LLP_PREF_HINGE = 2, LLP_PREF_IPO = 3 };
  *                not finite, without a status.
  *   beta > 0, 0 <= label_smoothing < 1 (0 unless SIGMOID), gamma finite (0 for IPO)
  *   reduction    LLP_REDUCE_SUM, or LLP_REDUCE_TOKEN_MEAN for the mean over pairs
- * A pair with a scored row (or a weight) that is not finite sets LLP_STATUS_VALUE_NOT_FINITE,
- * adds nothing, and its outputs and gradients are 0. A malformed cu_seqlens sets
+ * Another pair with a scored row (or a weight) that is not finite sets
+ * LLP_STATUS_VALUE_NOT_FINITE, adds nothing, and its outputs and gradients are 0. A malformed cu_seqlens sets
  * LLP_STATUS_LAYOUT_INVALID and every output is 0. */
 typedef struct {
   const float* logp;

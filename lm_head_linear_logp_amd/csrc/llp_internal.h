@@ -377,9 +377,16 @@ struct PolicyArgs {
 constexpr int PREF_SPLIT = 4;
 constexpr int PREF_CHUNK = 4096;
 // Rows and pairs up to which one workgroup computes a preference loss in one launch: a launch
-// costs the host more than the device (4607 rows in 8 pairs, one launch and two: 16.4 and 21.7 us
-// a call, 13.2 and 9.0 replayed from a graph; 64 rows of one pair, replayed: 7.2 and 8.4; 8192 rows
-// of 16 pairs: 18.1 and 8.9).
+// costs the host more than the device. One launch and two, us a call and replayed from a graph:
+//   1 pair of 64 rows       14.7 and 19.2,   7.1 and  8.3
+//   4 pairs of 2300 rows    14.6 and 19.1,   9.4 and  8.9
+//   8 pairs of 4607 rows    14.6 and 19.1,  13.0 and  9.1
+//   9 pairs of 4607 rows    14.6 and 19.0,  13.4 and  9.1
+//   16 pairs of 8192 rows   17.4 and 19.0,  17.9 and  8.7
+//   32 pairs of 8192 rows   27.6 and 19.2,  28.2 and  8.8
+// The border weighs the two: a stream that waits for the host gains 4.5 us by it up to 8 pairs, a
+// graph or a busy stream loses up to 4 from 5 pairs on (and gains 1 at one pair). Past it a call's
+// gain shrinks and a replay's loss grows.
 constexpr int64_t PREF_SOLO_ROWS = 8192;
 constexpr int PREF_SOLO_PAIRS = 8;
 struct PrefArgs {
