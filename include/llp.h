@@ -76,7 +76,9 @@ enum {
   LLP_STATUS_REPLAY_ID_INVALID = 4,   /* a replay id outside [-1, real_vocab) (slot ignored) */
   LLP_STATUS_LAYOUT_INVALID = 8,      /* cu_seqlens not 0 = c0 <= c1 <= ... <= cS = T */
   LLP_STATUS_TOKEN_OUT_OF_RANGE = 16, /* an embedded token id outside [0, real_vocab) */
-  LLP_STATUS_VALUE_NOT_FINITE = 32    /* a scored row of a loss holds an infinity or NaN */
+  LLP_STATUS_VALUE_NOT_FINITE = 32,   /* a scored row of a loss, a beam's logits or its score
+                                         hold a NaN or an infinity that has no meaning there */
+  LLP_STATUS_PARENT_INVALID = 64      /* a parent outside [-1, number of source beams) */
 };
 
 enum { LLP_DTYPE_BF16 = 1, LLP_DTYPE_F32 = 2 };
@@ -521,6 +523,188 @@ typedef struct {
   int32_t* status_word;
 } llp_embedding_request;
 
+/* ---- Products of operands in 8-bit floating point -------------------------------------------
+ * A head (or another projection) held as e4m3 bytes with an fp32 scale for each block of
+ * 128 x 128, multiplied with activations quantised in groups of 128 columns: logits for decoding,
+ * and, with the operands quantised along the other dimension, both gradients. An operand is a
+ * matrix [rows, depth] whose depth is the summed dimension, padded with zero bytes to a multiple
+ * of LLP_FP8_BLOCK. Its scales come in one of two layouts, G = depth / LLP_FP8_BLOCK:
+ *   by group  (block_rows 1): scale[g * scale_stride + r], scale_stride >= rows
+ *   by block  (block_rows 128): scale[(r / 128) * scale_stride + g], scale_stride >= G */
+#define LLP_FP8_BLOCK 128
+
+/* Quantisation of x, or with `transpose` of its transpose: the operand Y [M, K] is x [rows, cols]
+ * or its transpose.
+ *   x      [rows, cols] bf16 or fp32 (x_dtype), row stride x_stride elements (>= cols), any
+ *          alignment of its element type.
+ *   q      e4m3 (finite, no infinities) [M, K rounded up to LLP_FP8_BLOCK], row stride q_stride
+ *          bytes (>= the padded K, multiple of 16), 16-byte aligned base. Columns past K are
+ *          written as 0.
+ *   scale  fp32, as above for `block_rows` (1 or LLP_FP8_BLOCK).
+ * With a = max |Y| over a block: its scale is max(a, 1e-30) * fl32(1/448) and q = Y / scale (fp32,
+ * correctly rounded) to the nearest e4m3 value, ties to even. A block holding an infinity or NaN
+ * gives q = 0 and scale = NaN. rows and cols >= 0, below 2^31; ceil(rows / 128) * ceil(cols / 128)
+ * < 2^23 (else LLP_ERR_UNSUPPORTED). */
+typedef struct {
+  const void* x;
+  int32_t x_dtype;
+  int32_t block_rows;
+  int64_t x_stride;
+  int64_t rows;
+  int64_t cols;
+  int32_t transpose;
+  int32_t reserved;
+  uint8_t* q;
+  int64_t q_stride;
+  float* scale;
+  int64_t scale_stride;
+} llp_fp8_quant_request;
+
+/* A product of two such operands over their common depth:
+ *   p[t][v] = sum_g x_scale[g][t] weight_scale[v / 128][g] sum_{k in g} x[t][k] weight[v][k]
+ *   x       [rows, depth] e4m3, scales by group; weight [cols, depth] e4m3, scales by block. Row
+ *           strides in bytes, >= depth and multiples of 16, below 2^24; 16-byte aligned bases.
+ *   depth   a multiple of LLP_FP8_BLOCK, 0 <= depth <= 2^23 (0: the sums are 0).
+ *   rows, cols  0 .. 2^23 - 256; ceil(rows / 32) * ceil(cols / 128) < 2^23 (else
+ *           LLP_ERR_UNSUPPORTED).
+ * The groups are added in ascending order in fp32, so an element depends on its two rows alone,
+ * whatever the call's other rows. A group's 128 products are summed in fp32 where out is fp32; where it
+ * is bf16 they are summed by the 8-bit matrix instructions, which cut 8 products at a time about 14
+ * bits below the largest: a hundredth of the result's rounding to bf16.
+ * llp_linear_fp8: out[t][v] = p + bias[v], [rows, cols] of out_dtype, row stride out_stride
+ *   elements (>= cols), any alignment of its element type, rounded once. bias [cols] of bias_dtype
+ *   or NULL. flags must be 0.
+ * llp_dweight_fp8: the gradient of a weight, with `weight` the transposed upstream gradient [V, T]
+ *   and `x` the transposed input [H, T]: out[v][t] += p (fp32), [cols, rows], row stride
+ *   out_stride >= rows. With LLP_FLAG_OVERWRITE_GRADS it is written, and out_dtype may be bf16.
+ *   bias must be NULL. */
+typedef struct {
+  const uint8_t* x;
+  int64_t x_stride;
+  const float* x_scale;
+  int64_t x_scale_stride;
+  const uint8_t* weight;
+  int64_t weight_stride;
+  const float* weight_scale;
+  int64_t weight_scale_stride;
+  const void* bias;
+  int32_t bias_dtype;
+  int32_t out_dtype;
+  void* out;
+  int64_t out_stride;
+  int64_t rows;
+  int64_t cols;
+  int64_t depth;
+  uint32_t flags;
+  int32_t reserved;
+} llp_fp8_linear_request;
+
+/* ---- Beam search ----------------------------------------------------------------------------
+ * One step over B sequences of K beams each: every beam's most likely tokens from its logits (per
+ * vocabulary shard), the selection over a sequence's beams, shards and vocabulary, and the
+ * reordering of whatever is kept per beam. */
+#define LLP_MAX_BEAMS 64      /* beams of a sequence, and candidates selected for it */
+
+/* Candidates of each row of logits: the `num` largest real columns (1 <= num <= LLP_MAX_BEAMS), by
+ * logit descending and token ascending, and what normalises the row.
+ *   logits   as in llp_logits_request; num_rows rows, below 2^22.
+ *   vocab    as in llp_request; local_size at most 2^23 - 256 and padded_vocab < 2^40 (else
+ *            LLP_ERR_UNSUPPORTED).
+ *   temperature  z = x * fl32(1/temperature).
+ * -inf logits are no candidates. A row that holds a NaN or +inf among its real columns sets
+ * LLP_STATUS_VALUE_NOT_FINITE and gets no candidates and sum = -1. */
+typedef struct {
+  const void* logits;
+  int32_t logits_dtype;
+  int32_t num;
+  int64_t logits_stride;
+  int64_t num_rows;
+  llp_vocab_partition vocab;
+  float temperature;
+  int32_t reserved;
+  int32_t* status_word;
+} llp_beam_request;
+
+/* What llp_beam_candidates writes and llp_beam_select reads, device arrays:
+ *   value   fp32 [num_rows, num], the logits x in descending order (-inf past the last candidate)
+ *   token   int64 [num_rows, num] global ids (-1 past the last candidate)
+ *   max     fp32 [num_rows], the largest logit (-inf for a row without one)
+ *   sum     fp64 [num_rows], sum exp((x - max) fl32(1/temperature)) over the real columns; 0 for a
+ *           row without a finite logit */
+typedef struct {
+  float* value;
+  int64_t* token;
+  float* max;
+  double* sum;
+} llp_beam_parts;
+
+/* Selection over `world` shards' candidates (rank order) of num_seqs x num_beams rows.
+ *   scores     fp32 [num_seqs, num_beams], a beam's score so far
+ *   finished   uint8 [num_seqs, num_beams] or NULL: a finished beam has one candidate, end_id, with
+ *              its own score
+ *   num        candidates in each row of the parts; num_out chosen, 1 <= num_out <= num <=
+ *              LLP_MAX_BEAMS (so the choice is one over the whole vocabulary); num_seqs < 2^22
+ * A candidate's total is score + ((x - M) c - log(sum_r sum[r] e^{(max[r] - M) c})) with M =
+ * max_r max[r] and c = fl32(1/temperature), in fp64. Chosen are the num_out largest totals above -inf, by total
+ * descending, then beam, then token ascending.
+ * A beam whose score is -inf has no candidates; nor has one whose score is NaN or +inf or whose
+ * row has sum < 0 in a shard, which sets LLP_STATUS_VALUE_NOT_FINITE. */
+typedef struct {
+  int32_t world;
+  int32_t num;
+  const llp_beam_parts* parts; /* HOST array of `world` structs */
+  int64_t num_seqs;
+  int32_t num_beams;
+  int32_t num_out;
+  const float* scores;
+  const uint8_t* finished;
+  int64_t end_id;
+  float temperature;
+  int32_t reserved;
+  int32_t* status_word;
+} llp_beam_select_request;
+
+/*   token   int64 [num_seqs, num_out], -1 where fewer candidates than num_out have a total
+ *   parent  int32 [num_seqs, num_out], the beam it continues (-1 there)
+ *   score   fp32 [num_seqs, num_out], the total (-inf there) */
+typedef struct {
+  int64_t* token;
+  int32_t* parent;
+  float* score;
+} llp_beam_out;
+
+/* Reordering of what is kept per beam: for every sequence b and slot j, row b * num_out + j of dst
+ * takes row b * num_src + parents[b][j] of src. A parent of -1 leaves the slot as it is; one
+ * outside [-1, num_src) does too and sets LLP_STATUS_PARENT_INVALID.
+ * A state is `rows` of `outer` pieces of `inner` contiguous bytes: row r's piece o begins at
+ * base + r * row_stride + o * outer_stride (bytes). Pieces of one state do not overlap.
+ *   src, dst  HOST arrays of num_states device pointers, all of the one shape; dst[i] == src[i] is
+ *             the reordering in place (num_src must equal num_out then, and dst's strides src's),
+ *             otherwise no dst may overlap a src. In place are all
+ *             states of a call or none.
+ *   parents   int32 [num_seqs, num_out]
+ *   0 <= num_seqs < 2^22, 0 <= num_states; 1 <= num_src, num_out <= LLP_MAX_BEAMS. A state whose
+ *   sequences hold 2^32 loads or more together is LLP_ERR_UNSUPPORTED (a load is 16 bytes, or less
+ *   where pieces or their strides are no multiples of 16: 4 or 1).
+ * States must not overlap each other. */
+typedef struct {
+  const void* const* src;
+  void* const* dst;
+  int32_t num_states;
+  int32_t num_src;
+  int32_t num_out;
+  int32_t reserved;
+  int64_t num_seqs;
+  int64_t outer;
+  int64_t inner;
+  int64_t src_row_stride;
+  int64_t src_outer_stride;
+  int64_t dst_row_stride;
+  int64_t dst_outer_stride;
+  const int32_t* parents;
+  int32_t* status_word;
+} llp_beam_reorder_request;
+
 /* Loading phase: checks that `device` is a gfx950 GPU and loads the kernels on it; fills
  * `info` (may be NULL). Returns LLP_ERR_UNAVAILABLE when there is no such device. Must
  * succeed on the current device before any execution call. Idempotent. */
@@ -625,6 +809,22 @@ LLP_API llp_status llp_embedding_backward(const llp_embedding_request* req, cons
                                           int32_t dout_dtype, int64_t dout_stride, float* dweight,
                                           int64_t dweight_stride, void* workspace,
                                           size_t workspace_bytes, void* stream);
+
+/* Quantisation in 8-bit floating point (see llp_fp8_quant_request) and products of such operands
+ * (see llp_fp8_linear_request). No workspace. */
+LLP_API llp_status llp_quantize_blocks(const llp_fp8_quant_request* req, void* stream);
+LLP_API llp_status llp_linear_fp8(const llp_fp8_linear_request* req, void* stream);
+LLP_API llp_status llp_dweight_fp8(const llp_fp8_linear_request* req, void* stream);
+
+/* One step of a beam search (see llp_beam_request, llp_beam_select_request and
+ * llp_beam_reorder_request). llp_beam_candidates takes a workspace (device memory, 256-byte aligned),
+ * the others none. */
+LLP_API llp_status llp_beam_workspace_bytes(const llp_beam_request* req, size_t* bytes);
+LLP_API llp_status llp_beam_candidates(const llp_beam_request* req, const llp_beam_parts* out,
+                                       void* workspace, size_t workspace_bytes, void* stream);
+LLP_API llp_status llp_beam_select(const llp_beam_select_request* req, const llp_beam_out* out,
+                                   void* stream);
+LLP_API llp_status llp_beam_reorder(const llp_beam_reorder_request* req, void* stream);
 
 /* Message for the calling thread's last non-OK status ("" if none). */
 LLP_API const char* llp_last_error(void);

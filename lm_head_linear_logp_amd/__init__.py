@@ -12,6 +12,10 @@ Around it (ops.py): scoring with a head in 8-bit integers (``quantize_rows``,
 ``forward_int8``), the losses on the scored log-probabilities (``policy_grads``,
 ``preference_grads``, as autograd nodes ``policy_loss``, ``preference_loss``) and the token
 embedding (``embedding_forward``, ``embedding_backward``, as an autograd node ``embedding``).
+
+Decoding and training with a head in 8-bit floating point (gen.py): ``quantize_blocks``, the
+products ``linear_fp8`` and ``dweight_fp8`` (as an autograd node ``fp8_linear``), and a beam
+search's step (``beam_candidates``, ``beam_select``, ``beam_reorder``).
 """
 from __future__ import annotations
 
@@ -26,7 +30,8 @@ __all__ = ["LLPError", "open", "workspace_bytes", "forward", "forward_noalloc", 
            "backward", "top_p_replay", "last_error", "STATUS_BITS", "forward_logits",
            "keep_mask_replay", "SCRATCH_BYTES", "linear_logp", "quantize_rows", "forward_int8",
            "policy_grads", "policy_loss", "preference_grads", "preference_loss",
-           "embedding_forward", "embedding_backward", "embedding"]
+           "embedding_forward", "embedding_backward", "embedding", "quantize_blocks", "linear_fp8",
+           "dweight_fp8", "fp8_linear", "beam_candidates", "beam_select", "beam_reorder"]
 
 # Size of the static device scratch llp_forward_noalloc works in (include/llp.h).
 SCRATCH_BYTES = 32 << 20
@@ -36,7 +41,8 @@ STATUS_BITS = {"TARGET_OUT_OF_RANGE": A.LLP_STATUS_TARGET_OUT_OF_RANGE,
                "REPLAY_ID_INVALID": A.LLP_STATUS_REPLAY_ID_INVALID,
                "LAYOUT_INVALID": A.LLP_STATUS_LAYOUT_INVALID,
                "TOKEN_OUT_OF_RANGE": A.LLP_STATUS_TOKEN_OUT_OF_RANGE,
-               "VALUE_NOT_FINITE": A.LLP_STATUS_VALUE_NOT_FINITE}
+               "VALUE_NOT_FINITE": A.LLP_STATUS_VALUE_NOT_FINITE,
+               "PARENT_INVALID": A.LLP_STATUS_PARENT_INVALID}
 
 
 class LLPError(RuntimeError):
@@ -583,3 +589,5 @@ def linear_logp(hidden: torch.Tensor, weight: torch.Tensor, target_ids: torch.Te
 
 from .ops import (embedding, embedding_backward, embedding_forward, forward_int8,  # noqa: E402
                   policy_grads, policy_loss, preference_grads, preference_loss, quantize_rows)
+from .gen import (beam_candidates, beam_reorder, beam_select, dweight_fp8, fp8_linear,  # noqa: E402
+                  linear_fp8, quantize_blocks)

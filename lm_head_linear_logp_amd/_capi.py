@@ -19,6 +19,7 @@ LLP_STATUS_REPLAY_ID_INVALID = 4
 LLP_STATUS_LAYOUT_INVALID = 8
 LLP_STATUS_TOKEN_OUT_OF_RANGE = 16
 LLP_STATUS_VALUE_NOT_FINITE = 32
+LLP_STATUS_PARENT_INVALID = 64
 
 LLP_DTYPE_BF16 = 1
 LLP_DTYPE_F32 = 2
@@ -31,6 +32,8 @@ LLP_G_SLAB_COLUMNS = 32768
 LLP_MAX_REPLAY_IDS = 64
 LLP_MAX_WORLD = 64
 LLP_INT8_COLUMNS = 128
+LLP_FP8_BLOCK = 128
+LLP_MAX_BEAMS = 64
 LLP_KL_K1, LLP_KL_K2, LLP_KL_K3 = 1, 2, 3
 LLP_REDUCE_TOKEN_MEAN, LLP_REDUCE_SEQ_MEAN, LLP_REDUCE_SUM = 1, 2, 3
 LLP_LOG_RATIO_MAX = 20
@@ -154,6 +157,53 @@ class llp_embedding_request(C.Structure):
                 ("scale", C.c_float), ("flags", C.c_uint32), ("status_word", vp)]
 
 
+class llp_fp8_quant_request(C.Structure):
+    _fields_ = [("x", vp), ("x_dtype", C.c_int32), ("block_rows", C.c_int32),
+                ("x_stride", C.c_int64), ("rows", C.c_int64), ("cols", C.c_int64),
+                ("transpose", C.c_int32), ("reserved", C.c_int32), ("q", vp),
+                ("q_stride", C.c_int64), ("scale", vp), ("scale_stride", C.c_int64)]
+
+
+class llp_fp8_linear_request(C.Structure):
+    _fields_ = [("x", vp), ("x_stride", C.c_int64), ("x_scale", vp), ("x_scale_stride", C.c_int64),
+                ("weight", vp), ("weight_stride", C.c_int64), ("weight_scale", vp),
+                ("weight_scale_stride", C.c_int64), ("bias", vp), ("bias_dtype", C.c_int32),
+                ("out_dtype", C.c_int32), ("out", vp), ("out_stride", C.c_int64),
+                ("rows", C.c_int64), ("cols", C.c_int64), ("depth", C.c_int64),
+                ("flags", C.c_uint32), ("reserved", C.c_int32)]
+
+
+class llp_beam_request(C.Structure):
+    _fields_ = [("logits", vp), ("logits_dtype", C.c_int32), ("num", C.c_int32),
+                ("logits_stride", C.c_int64), ("num_rows", C.c_int64),
+                ("vocab", llp_vocab_partition), ("temperature", C.c_float),
+                ("reserved", C.c_int32), ("status_word", vp)]
+
+
+class llp_beam_parts(C.Structure):
+    _fields_ = [("value", vp), ("token", vp), ("max", vp), ("sum", vp)]
+
+
+class llp_beam_select_request(C.Structure):
+    _fields_ = [("world", C.c_int32), ("num", C.c_int32), ("parts", C.POINTER(llp_beam_parts)),
+                ("num_seqs", C.c_int64), ("num_beams", C.c_int32), ("num_out", C.c_int32),
+                ("scores", vp), ("finished", vp), ("end_id", C.c_int64),
+                ("temperature", C.c_float), ("reserved", C.c_int32), ("status_word", vp)]
+
+
+class llp_beam_out(C.Structure):
+    _fields_ = [("token", vp), ("parent", vp), ("score", vp)]
+
+
+class llp_beam_reorder_request(C.Structure):
+    _fields_ = [("src", C.POINTER(vp)), ("dst", C.POINTER(vp)), ("num_states", C.c_int32),
+                ("num_src", C.c_int32), ("num_out", C.c_int32), ("reserved", C.c_int32),
+                ("num_seqs", C.c_int64), ("outer", C.c_int64), ("inner", C.c_int64),
+                ("src_row_stride", C.c_int64), ("src_outer_stride", C.c_int64),
+                ("dst_row_stride", C.c_int64), ("dst_outer_stride", C.c_int64), ("parents", vp),
+                ("status_word", vp)]
+
+
 SIGNATURES = {
     "llp_open": (C.c_int, [C.c_int32, C.POINTER(llp_info)]),
     "llp_workspace_bytes": (C.c_int, [C.POINTER(llp_request), C.c_int32, C.POINTER(C.c_size_t)]),
@@ -185,6 +235,15 @@ SIGNATURES = {
                                                 C.POINTER(C.c_size_t)]),
     "llp_embedding_backward": (C.c_int, [C.POINTER(llp_embedding_request), vp, C.c_int32,
                                          C.c_int64, vp, C.c_int64, vp, C.c_size_t, vp]),
+    "llp_quantize_blocks": (C.c_int, [C.POINTER(llp_fp8_quant_request), vp]),
+    "llp_linear_fp8": (C.c_int, [C.POINTER(llp_fp8_linear_request), vp]),
+    "llp_dweight_fp8": (C.c_int, [C.POINTER(llp_fp8_linear_request), vp]),
+    "llp_beam_workspace_bytes": (C.c_int, [C.POINTER(llp_beam_request), C.POINTER(C.c_size_t)]),
+    "llp_beam_candidates": (C.c_int, [C.POINTER(llp_beam_request), C.POINTER(llp_beam_parts), vp,
+                                      C.c_size_t, vp]),
+    "llp_beam_select": (C.c_int, [C.POINTER(llp_beam_select_request), C.POINTER(llp_beam_out),
+                                  vp]),
+    "llp_beam_reorder": (C.c_int, [C.POINTER(llp_beam_reorder_request), vp]),
     "llp_last_error": (C.c_char_p, []),
 }
 

@@ -15,8 +15,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libllp.so")
-SOURCES = ["llp_api.cpp", "llp_api_ops.cpp", "llp_kernels.hip", "llp_int8.hip", "llp_losses.hip",
-           "llp_embedding.hip"]
+SOURCES = ["llp_api.cpp", "llp_api_ops.cpp", "llp_api_gen.cpp", "llp_kernels.hip", "llp_int8.hip",
+           "llp_losses.hip", "llp_embedding.hip", "llp_fp8.hip", "llp_beam.hip"]
 ARCH = "gfx950"
 
 

@@ -1,0 +1,446 @@
+// llp_beam.hip -- one step of a beam search: the most likely tokens of every row of logits, the
+// selection over a sequence's beams and shards, and the reordering of what is kept per beam.
+#include "llp_internal.h"
+#include "llp_tile.hpp"
+
+#include <math.h>
+
+namespace llp {
+
+// ------------------------------------------------------------------------------------
+// Ordered keys. A value and its place become one number that is larger the better the candidate:
+// the value's bits in an order that compares as unsigned, then the place inverted, so that no two
+// candidates are equal and ties go to the lowest place. 0 is no candidate.
+// ------------------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t ordered(float x) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, x + 0.f);   // -0 is 0
+  return u ^ ((u >> 31) != 0 ? 0xFFFFFFFFu : 0x80000000u);
+}
+__device__ __forceinline__ float unordered(uint32_t k) {
+  return __builtin_bit_cast(float, k ^ ((k >> 31) != 0 ? 0x80000000u : 0xFFFFFFFFu));
+}
+
+struct Key64 {   // logit, column
+  uint64_t k;
+  __device__ __forceinline__ bool above(const Key64& o) const { return k > o.k; }
+  __device__ __forceinline__ Key64 from(int lane) const {
+    const int lo = __shfl((int)(uint32_t)k, lane), hi = __shfl((int)(k >> 32), lane);
+    return {(uint64_t)(uint32_t)hi << 32 | (uint32_t)lo};
+  }
+  __device__ __forceinline__ bool any() const { return k != 0; }
+  static __device__ __forceinline__ Key64 none() { return {0}; }
+};
+
+struct Key128 {   // total, then beam and token
+  uint64_t k, at;
+  __device__ __forceinline__ bool above(const Key128& o) const { return k > o.k || (k == o.k && at > o.at); }
+  __device__ __forceinline__ Key128 from(int lane) const {
+    const Key64 a = Key64{k}.from(lane), b = Key64{at}.from(lane);
+    return {a.k, b.k};
+  }
+  __device__ __forceinline__ bool any() const { return k != 0; }
+  static __device__ __forceinline__ Key128 none() { return {0, 0}; }
+};
+
+// The wave's 64 keys, largest first (bitonic network).
+template <class K>
+__device__ __forceinline__ K sort64(K x) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int size = 2; size <= 64; size *= 2)
+#pragma unroll
+    for (int j = size / 2; j > 0; j /= 2) {
+      const K y = x.from(lane ^ j);
+      // The lower lane of a pair takes the larger key in a descending run.
+      const bool larger = ((lane & j) == 0) == ((lane & size) == 0 || size == 64);
+      if (y.above(x) == larger) x = y;
+    }
+  return x;
+}
+
+// The 64 largest of two runs of 64, each largest first.
+template <class K>
+__device__ __forceinline__ K merge64(K x, K y) {
+  const int lane = threadIdx.x & 63;
+  y = y.from(63 - lane);
+  if (y.above(x)) x = y;
+#pragma unroll
+  for (int j = 32; j > 0; j /= 2) {
+    const K z = x.from(lane ^ j);
+    if (z.above(x) == ((lane & j) == 0)) x = z;
+  }
+  return x;
+}
+
+// A wave's best `num` keys so far: sorted in its lanes, and up to 63 later ones in LDS that are
+// above the worst of them as it was when it was last looked at.
+template <class K>
+struct Best {
+  K list;      // lane i: the i-th largest
+  K bar;       // only larger keys can still enter
+  K* buf;      // [128] of LDS, this wave's
+  int held;    // keys in buf
+
+  __device__ __forceinline__ void init(K* b) {
+    list = bar = K::none();
+    buf = b;
+    held = 0;
+  }
+  __device__ __forceinline__ void fold(int n, int num) {
+    const int lane = threadIdx.x & 63;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    const K x = lane < n ? buf[lane] : K::none();
+    list = merge64(list, sort64(x));
+    const K b = list.from(num - 1);
+    if (b.above(bar)) bar = b;
+  }
+  // Each lane's key, where it is above the bar. Called by the whole wave.
+  __device__ __forceinline__ void add(K x, int num) {
+    const int lane = threadIdx.x & 63;
+    const bool in = x.above(bar);
+    const uint64_t m = __builtin_amdgcn_ballot_w64(in);
+    if (m == 0) return;
+    if (in) buf[held + __popcll(m & ((1ull << lane) - 1))] = x;
+    held += __popcll(m);
+    if (held < 64) return;
+    fold(64, num);
+    held -= 64;
+    K y = K::none();
+    if (lane < held) y = buf[64 + lane];
+    __builtin_amdgcn_wave_barrier();
+    if (lane < held) buf[lane] = y;
+  }
+  __device__ __forceinline__ void finish(int num) {
+    if (held > 0) fold(held, num);
+    held = 0;
+  }
+};
+
+// ------------------------------------------------------------------------------------
+// Candidates. A wave walks blocks of 2048 columns of one row, 32 values a lane in registers: the
+// block's maximum and its sum of exponentials go to the workspace (so the row's normaliser does not
+// depend on how many waves share it), and the values above the wave's bar into its best keys. The
+// first block's bar is the num-th largest of the 64 lanes' maxima, each of which is a value of
+// its own. Bound by memory: one read of the logits.
+//
+// exp((x - max) c) as 2^t, t = (x - max) c log2 e: t's rounding and the low part of c log2 e are
+// made up for to first order, so that a term is off by the exponential's own rounding alone and
+// sums over thousands of columns by about 1e-8: two beams' totals closer than that are rare.
+// ------------------------------------------------------------------------------------
+constexpr int BEAM_WAVES = 4;
+
+template <bool BF16>
+__device__ __forceinline__ void beam_load(const void* row, int64_t c0, int64_t n_real, float (&x)[32]) {
+  constexpr int V = BF16 ? 8 : 4;   // values per 16 bytes
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int i = 0; i < 32 / V; ++i) {
+    const int64_t c = c0 + i * 64 * V + lane * V;
+    if (c + V <= n_real) {
+      if constexpr (BF16) {
+        const u32x4 u = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(row) + c);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          x[i * V + 2 * k] = __builtin_bit_cast(float, u[k] << 16);
+          x[i * V + 2 * k + 1] = __builtin_bit_cast(float, u[k] & 0xFFFF0000u);
+        }
+      } else {
+        const float4 u = *reinterpret_cast<const float4*>(static_cast<const float*>(row) + c);
+        x[i * V] = u.x; x[i * V + 1] = u.y; x[i * V + 2] = u.z; x[i * V + 3] = u.w;
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        x[i * V + k] = -INFINITY;
+        if (c + k < n_real)
+          x[i * V + k] = BF16 ? bf16_to_f32(static_cast<const uint16_t*>(row)[c + k])
+                              : static_cast<const float*>(row)[c + k];
+      }
+    }
+  }
+}
+
+template <bool BF16>
+__global__ __launch_bounds__(64 * BEAM_WAVES) void k_beam_rows(BeamArgs a) {
+  __shared__ Key64 room[BEAM_WAVES][128];
+  constexpr int V = BF16 ? 8 : 4;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t w = (int64_t)blockIdx.x * BEAM_WAVES + wave;
+  const int64_t r = w / a.splits;
+  const int sp = (int)(w % a.splits);
+  if (r >= a.rows) return;
+  const char* const row = static_cast<const char*>(a.logits) + r * a.ld * (BF16 ? 2 : 4);
+  const int b0 = (int)((int64_t)a.blocks * sp / a.splits), b1 = (int)((int64_t)a.blocks * (sp + 1) / a.splits);
+  const double cl = (double)a.c1 * 1.4426950408889634074;
+  const float ch = (float)cl, clo = (float)(cl - (double)ch);
+  Best<Key64> best;
+  best.init(room[wave]);
+  for (int b = b0; b < b1; ++b) {
+    const int64_t c0 = (int64_t)b * BEAM_BLOCK;
+    float x[32];
+    beam_load<BF16>(row, c0, a.n_real, x);
+    float mine = -INFINITY;
+    bool fine = true;
+#pragma unroll
+    for (int e = 0; e < 32; ++e) {
+      fine &= x[e] < INFINITY;
+      mine = fmaxf(mine, x[e]);
+    }
+    float top = mine;
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off));
+    const bool bad = __builtin_amdgcn_ballot_w64(!fine) != 0;
+    float s = 0.f;
+    if (!bad && top > -INFINITY) {
+#pragma unroll
+      for (int e = 0; e < 32; ++e) {
+        const float d = x[e] - top;   // -inf for a column that is none, or far below
+        const float t = d * ch;
+        const float rest = fmaf(d, clo, fmaf(d, ch, -t));
+        const float v = __builtin_amdgcn_exp2f(t);
+        s += t > -150.f ? fmaf(v, rest * kLn2, v) : 0.f;
+      }
+#pragma unroll
+      for (int off = 32; off > 0; off >>= 1) s += __shfl_xor(s, off);
+    }
+    if (lane == 0) {
+      a.pm[r * a.blocks + b] = top;
+      a.ps[r * a.blocks + b] = bad ? -1.f : s;
+    }
+    if (bad) continue;   // the row has no candidates
+    if (b == b0) {
+      const Key64 m = sort64(Key64{mine > -INFINITY ? (uint64_t)ordered(mine) << 32 : 0});
+      const Key64 at = m.from(a.num - 1);
+      if (at.any()) best.bar = Key64{at.k - 1};
+    }
+    const float bar = best.bar.any() ? unordered((uint32_t)(best.bar.k >> 32)) : -INFINITY;
+    // The bar's value may be one below the smallest that counts: >= and the key decide.
+    if (__builtin_amdgcn_ballot_w64(mine >= bar && mine > -INFINITY) == 0) continue;
+#pragma unroll
+    for (int e = 0; e < 32; ++e) {
+      const bool may = x[e] >= bar && x[e] > -INFINITY;
+      if (__builtin_amdgcn_ballot_w64(may) == 0) continue;
+      const uint32_t c = (uint32_t)c0 + (e / V) * 64 * V + lane * V + e % V;
+      best.add(Key64{may ? (uint64_t)ordered(x[e]) << 32 | (uint32_t)~c : 0}, a.num);
+    }
+  }
+  best.finish(a.num);
+  if (lane < a.num) a.keys[w * a.num + lane] = best.list.k;
+}
+
+// A row's outputs from its waves' candidates and its blocks' sums: one wave a row.
+__global__ __launch_bounds__(64) void k_beam_join(BeamArgs a) {
+  __shared__ Key64 room[128];
+  const int lane = threadIdx.x;
+  const int64_t r = blockIdx.x;
+  // The candidates first: their loads are the longer chain.
+  const uint64_t* const keys = a.keys + r * a.splits * a.num;
+  const int total = a.splits * a.num;
+  uint64_t head = 0;
+  for (int i = lane; i < a.splits; i += 64) {
+    const uint64_t k = keys[(int64_t)i * a.num];
+    head = k > head ? k : head;
+  }
+  Best<Key64> best;
+  best.init(room);
+  // The num-th largest of the lanes' heads is a bar that num keys reach.
+  const Key64 at = sort64(Key64{head}).from(a.num - 1);
+  if (at.any()) best.bar = Key64{at.k - 1};
+  for (int i = 0; i < total; i += 64) best.add(Key64{i + lane < total ? keys[i + lane] : 0}, a.num);
+  best.finish(a.num);
+  float M = -INFINITY;
+  bool bad = false;
+  for (int i = lane; i < a.blocks; i += 64) {
+    M = fmaxf(M, a.pm[r * a.blocks + i]);
+    bad |= a.ps[r * a.blocks + i] < 0.f;
+  }
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor(M, off));
+  bad = __builtin_amdgcn_ballot_w64(bad) != 0;
+  double S = 0.0;
+  if (M > -INFINITY && !bad) {
+    for (int i = lane; i < a.blocks; i += 64) {
+      const float m = a.pm[r * a.blocks + i];
+      if (m > -INFINITY) S += (double)a.ps[r * a.blocks + i] * exp(((double)m - (double)M) * (double)a.c1);
+    }
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) S += __shfl_xor(S, off);
+  }
+  if (lane == 0) {
+    a.max[r] = bad ? -INFINITY : M;
+    a.sum[r] = bad ? -1.0 : S;
+    if (bad && a.status) atomicOr(a.status, LLP_STATUS_VALUE_NOT_FINITE);
+  }
+  if (lane < a.num) {
+    const bool in = best.list.any() && !bad;
+    a.value[r * a.num + lane] = in ? unordered((uint32_t)(best.list.k >> 32)) : -INFINITY;
+    a.token[r * a.num + lane] = in ? a.offset + (int64_t)(uint32_t)~(uint32_t)best.list.k : -1;
+  }
+}
+
+hipError_t launch_beam_candidates(const BeamArgs& a, hipStream_t s) {
+  if (a.rows <= 0) return hipSuccess;
+  if (a.blocks > 0) {
+    const dim3 grid((unsigned)((a.rows * a.splits + BEAM_WAVES - 1) / BEAM_WAVES)), block(64 * BEAM_WAVES);
+    if (a.bf16) hipLaunchKernelGGL((k_beam_rows<true>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((k_beam_rows<false>), grid, block, 0, s, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL(k_beam_join, dim3((unsigned)a.rows), dim3(64), 0, s, a);
+  return hipGetLastError();
+}
+
+// ------------------------------------------------------------------------------------
+// Selection: one wave a sequence. Totals and the normalisers' sums over shards in fp64, so that the
+// choice between two beams' candidates is the formula's. Candidates come rank by rank, so the bar
+// rises early. Latency: a few hundred keys.
+// ------------------------------------------------------------------------------------
+__device__ __forceinline__ uint64_t ordered64(double x) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x + 0.0);
+  return u ^ ((u >> 63) != 0 ? ~0ull : 1ull << 63);
+}
+__device__ __forceinline__ double unordered64(uint64_t k) {
+  return __builtin_bit_cast(double, k ^ ((k >> 63) != 0 ? 1ull << 63 : ~0ull));
+}
+constexpr uint64_t BEAM_AT = 40;   // bits of a token in a key; the host keeps ids below 2^40
+
+__global__ __launch_bounds__(64) void k_beam_select(BeamSelectArgs a) {
+  __shared__ Key128 room[128];
+  __shared__ double norm[LLP_MAX_BEAMS], score[LLP_MAX_BEAMS];
+  __shared__ float top[LLP_MAX_BEAMS];
+  __shared__ int kind[LLP_MAX_BEAMS];   // 0: no candidates, 1: its row's, 2: end_id
+  const int lane = threadIdx.x;
+  const int64_t b = blockIdx.x;
+  const double c = (double)a.c1;
+  Best<Key128> best;
+  best.init(room);
+  Key128 end = Key128::none();
+  if (lane < a.K) {
+    const int64_t row = b * a.K + lane;
+    const float sc = a.scores[row];
+    const bool over = a.finished != nullptr && a.finished[row] != 0;
+    bool bad = !(sc < INFINITY);
+    float M = -INFINITY;
+    double S = 0.0;
+    if (!over) {
+      for (int r = 0; r < a.world; ++r) {
+        M = fmaxf(M, a.max[r][row]);
+        bad |= !(a.sum[r][row] >= 0.0);
+      }
+      if (M > -INFINITY && !bad)
+        for (int r = 0; r < a.world; ++r) {
+          const float m = a.max[r][row];
+          if (m > -INFINITY) S += a.sum[r][row] * exp(((double)m - (double)M) * c);
+        }
+    }
+    if (bad && a.status) atomicOr(a.status, LLP_STATUS_VALUE_NOT_FINITE);
+    const bool live = !bad && sc > -INFINITY;
+    kind[lane] = !live ? 0 : over ? 2 : M > -INFINITY ? 1 : 0;
+    norm[lane] = log(S);
+    score[lane] = (double)sc;
+    top[lane] = M;
+    if (live && over) end = Key128{ordered64((double)sc), ~((uint64_t)lane << BEAM_AT)};
+  }
+  __syncthreads();
+  best.add(end, a.num_out);
+  const int per = a.world * a.K, total = per * a.num;
+  for (int i = 0; i < total; i += 64) {
+    Key128 x = Key128::none();
+    if (i + lane < total) {
+      const int rank = (i + lane) / per, k = (i + lane) % per / a.world, r = (i + lane) % per % a.world;
+      if (kind[k] == 1) {
+        const int64_t at = (b * a.K + k) * a.num + rank;
+        const int64_t token = a.token[r][at];
+        const double z = ((double)a.value[r][at] - (double)top[k]) * c;
+        const double t = score[k] + (z - norm[k]);
+        if (token >= 0 && t > -INFINITY) x = Key128{ordered64(t), ~((uint64_t)k << BEAM_AT | (uint64_t)token)};
+      }
+    }
+    best.add(x, a.num_out);
+  }
+  best.finish(a.num_out);
+  if (lane < a.num_out) {
+    const int64_t o = b * a.num_out + lane;
+    const bool in = best.list.any();
+    const uint64_t at = ~best.list.at;
+    const int k = in ? (int)(at >> BEAM_AT) : -1;
+    a.out_parent[o] = k;
+    a.out_token[o] = !in ? -1 : kind[k] == 2 ? a.end_id : (int64_t)(at & ((1ull << BEAM_AT) - 1));
+    a.out_score[o] = in ? (float)unordered64(best.list.k) : -INFINITY;
+  }
+}
+
+hipError_t launch_beam_select(const BeamSelectArgs& a, hipStream_t s) {
+  if (a.seqs <= 0) return hipSuccess;
+  hipLaunchKernelGGL(k_beam_select, dim3((unsigned)a.seqs), dim3(64), 0, s, a);
+  return hipGetLastError();
+}
+
+// ------------------------------------------------------------------------------------
+// Reordering. A thread takes one unit (16 bytes) of every slot of a sequence: all of a slot's loads
+// come before the first store, so the reordering is done in place without a copy, and a slot that
+// keeps its own rows costs nothing. Bound by memory: the moved slots read and written (a beam that
+// several slots take is read from the caches after the first).
+// ------------------------------------------------------------------------------------
+template <int SLOTS, class U>
+__global__ __launch_bounds__(256) void k_beam_reorder(ReorderArgs a, int64_t units, int32_t per) {
+  const int64_t w = blockIdx.x / per;   // state, then sequence
+  const int64_t b = w % a.seqs;
+  const int st = (int)(w / a.seqs);
+  const int64_t u = (int64_t)(blockIdx.x % per) * 256 + threadIdx.x;
+  const bool mine = u < a.outer * units;
+  const int64_t o = mine ? u / units : 0, at = mine ? u % units * (int64_t)sizeof(U) : 0;
+  const char* const src = static_cast<const char*>(a.src[st]) + b * a.K * a.sr + o * a.so + at;
+  char* const dst = static_cast<char*>(a.dst[st]) + b * a.N * a.dr + o * a.dout + at;
+  const bool in_place = a.src[st] == a.dst[st];
+  U v[SLOTS];
+  int from[SLOTS];
+  bool wrong = false;
+#pragma unroll
+  for (int j = 0; j < SLOTS; ++j) {
+    from[j] = -1;
+    if (j < a.N) {
+      int p = __builtin_amdgcn_readfirstlane(a.parents[b * a.N + j]);
+      if (p < -1 || p >= a.K) {
+        wrong = true;
+        p = -1;
+      }
+      if (!(in_place && p == j)) from[j] = p;
+    }
+    if (from[j] >= 0 && mine) v[j] = *reinterpret_cast<const U*>(src + from[j] * a.sr);
+  }
+#pragma unroll
+  for (int j = 0; j < SLOTS; ++j)
+    if (from[j] >= 0 && mine) *reinterpret_cast<U*>(dst + j * a.dr) = v[j];
+  if (wrong && a.status && st == 0 && blockIdx.x % per == 0 && threadIdx.x == 0)
+    atomicOr(a.status, LLP_STATUS_PARENT_INVALID);
+}
+
+template <int SLOTS, class U>
+static hipError_t launch_reorder_as(const ReorderArgs& a, hipStream_t s) {
+  const int64_t units = a.inner / (int64_t)sizeof(U);
+  const int64_t per = (a.outer * units + 255) / 256;
+  hipLaunchKernelGGL((k_beam_reorder<SLOTS, U>), dim3((unsigned)(per * a.seqs * a.states)), dim3(256), 0, s,
+                     a, units, (int32_t)per);
+  return hipGetLastError();
+}
+
+template <class U>
+static hipError_t launch_reorder_of(const ReorderArgs& a, hipStream_t s) {
+  if (a.N <= 4) return launch_reorder_as<4, U>(a, s);
+  if (a.N <= 8) return launch_reorder_as<8, U>(a, s);
+  if (a.N <= 16) return launch_reorder_as<16, U>(a, s);
+  if (a.N <= 32) return launch_reorder_as<32, U>(a, s);
+  return launch_reorder_as<64, U>(a, s);
+}
+
+hipError_t launch_beam_reorder(const ReorderArgs& a, hipStream_t s) {
+  if (a.states <= 0 || a.seqs <= 0 || a.outer <= 0 || a.inner <= 0) return hipSuccess;
+  if (a.unit == 16 && a.N <= 32) return launch_reorder_of<u32x4>(a, s);
+  if (a.unit >= 4) return launch_reorder_of<uint32_t>(a, s);
+  return launch_reorder_of<uint8_t>(a, s);
+}
+
+}  // namespace llp

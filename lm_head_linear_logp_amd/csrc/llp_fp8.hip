@@ -1,0 +1,563 @@
+// llp_fp8.hip -- operands in 8-bit floating point (e4m3) with an fp32 scale for each block of 128:
+// their quantisation, their product (logits, input gradient) and the weight gradient.
+#include "llp_internal.h"
+#include "llp_tile.hpp"
+
+#include <math.h>
+
+namespace llp {
+
+// ------------------------------------------------------------------------------------
+// Quantisation: scale = max(max |x|, 1e-30) * fl32(1/448) over 1 or 128 rows of 128 columns, q =
+// x / scale as e4m3 (ties to even). A workgroup holds a 128 x 128 tile of x in registers, 8 x 8 values a
+// thread, so that either layout, and the transpose (through LDS, whole 128-byte rows out), costs
+// one read and one write. Bound by memory.
+// ------------------------------------------------------------------------------------
+constexpr int Q8_THREADS = 256;
+
+// Columns c .. c + 7 of a row, 0 at and past `cols`. VEC: rows are 16-byte aligned.
+template <bool BF16, bool VEC>
+__device__ __forceinline__ void q8_load(const void* row, int64_t c, int64_t cols, float (&v)[8]) {
+  if (VEC && c + 8 <= cols) {
+    if constexpr (BF16) {
+      const u32x4 u = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(row) + c);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __builtin_bit_cast(float, u[i] << 16);
+        v[2 * i + 1] = __builtin_bit_cast(float, u[i] & 0xFFFF0000u);
+      }
+    } else {
+      const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(row) + c);
+      const float4 b = *reinterpret_cast<const float4*>(static_cast<const float*>(row) + c + 4);
+      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[i] = 0.f;
+      if (c + i < cols)
+        v[i] = BF16 ? bf16_to_f32(static_cast<const uint16_t*>(row)[c + i])
+                    : static_cast<const float*>(row)[c + i];
+    }
+  }
+}
+
+__device__ __forceinline__ uint2 q8_bytes(const float (&v)[8]) {
+  int lo = 0, hi = 0;
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], lo, false);
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], lo, true);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[4], v[5], hi, false);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[6], v[7], hi, true);
+  return make_uint2((uint32_t)lo, (uint32_t)hi);
+}
+
+// Eight values as e4m3 of the correctly rounded quotient x / scale. With inv = fl(1 / scale),
+// x * inv is off from that quotient by at most 3 half steps of fp32; only where 2^-21 to either side
+// gives another byte are the wave's divisions carried out. |quotient| <= 448 (1 + 2^-22), which
+// rounds to 448.
+__device__ __forceinline__ uint2 q8_pack(const float (&v)[8], const float (&scale)[8],
+                                         const float (&inv)[8]) {
+  float lo[8], hi[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float p = v[i] * inv[i];
+    lo[i] = fmaf(p, -0x1p-21f, p);
+    hi[i] = fmaf(p, 0x1p-21f, p);
+  }
+  uint2 w = q8_bytes(lo);
+  const uint2 u = q8_bytes(hi);
+  if (__builtin_amdgcn_ballot_w64(w.x != u.x || w.y != u.y) != 0) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) lo[i] = v[i] / scale[i];
+    w = q8_bytes(lo);
+  }
+  return w;
+}
+
+__device__ __forceinline__ float q8_top(float top, float x) {
+  const float m = fabsf(x);   // an infinity or NaN makes the top infinite
+  return m <= top ? top : m < INFINITY ? m : INFINITY;
+}
+
+// Thread (team, lane): rows team * 8 .. + 7 and columns lane * 8 .. + 7 of the tile.
+template <bool BF16, bool VEC, bool BLOCK, bool TRANS>
+__global__ __launch_bounds__(Q8_THREADS) void k_quant8(Quant8Args a) {
+  __shared__ float tops[4][128];
+  __shared__ __attribute__((aligned(16))) uint8_t turned[TRANS ? 128 * 128 : 16];
+  const int64_t ntc = (a.cols + 127) / 128;
+  const int64_t r0 = blockIdx.x / ntc * 128, c0 = blockIdx.x % ntc * 128;
+  const int lane = threadIdx.x & 15, team = threadIdx.x >> 4, wave = threadIdx.x >> 6;
+  float v[8][8];
+#pragma unroll
+  for (int p = 0; p < 8; ++p) {
+    const int64_t r = r0 + team * 8 + p;
+    if (r < a.rows) {
+      q8_load<BF16, VEC>(static_cast<const char*>(a.x) + r * a.ldx * (BF16 ? 2 : 4), c0 + lane * 8, a.cols, v[p]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[p][i] = 0.f;
+    }
+  }
+  float top[8];   // of this thread's rows, or with TRANS of its columns
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top[i] = 0.f;
+#pragma unroll
+  for (int p = 0; p < 8; ++p)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float& t = top[BLOCK ? 0 : TRANS ? i : p];
+      t = q8_top(t, v[p][i]);
+    }
+  if constexpr (BLOCK) {
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) top[0] = fmaxf(top[0], __shfl_xor(top[0], off));
+    if ((threadIdx.x & 63) == 0) tops[wave][0] = top[0];
+    __syncthreads();
+    top[0] = fmaxf(fmaxf(tops[0][0], tops[1][0]), fmaxf(tops[2][0], tops[3][0]));
+#pragma unroll
+    for (int i = 1; i < 8; ++i) top[i] = top[0];
+  } else if constexpr (TRANS) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      top[i] = fmaxf(top[i], __shfl_xor(top[i], 16));
+      top[i] = fmaxf(top[i], __shfl_xor(top[i], 32));
+      if ((threadIdx.x & 63) < 16) tops[wave][lane * 8 + i] = top[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int c = lane * 8 + i;
+      top[i] = fmaxf(fmaxf(tops[0][c], tops[1][c]), fmaxf(tops[2][c], tops[3][c]));
+    }
+  } else {
+#pragma unroll
+    for (int p = 0; p < 8; ++p)
+#pragma unroll
+      for (int off = 8; off > 0; off >>= 1) top[p] = fmaxf(top[p], __shfl_xor(top[p], off));
+  }
+  float scale[8], inv[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    scale[i] = fmaxf(top[i], 1e-30f) * (1.f / 448.f);
+    inv[i] = 1.f / scale[i];
+  }
+  // The scales: of rows or columns at a thread each, of a block at the first one.
+#pragma unroll
+  for (int i = 0; i < (BLOCK ? 1 : 8); ++i) {
+    const float s = top[i] < INFINITY ? scale[i] : __builtin_nanf("");
+    if constexpr (BLOCK) {
+      const int64_t rb = r0 / 128, cb = c0 / 128;
+      if (threadIdx.x == 0) a.scale[TRANS ? cb * a.lds + rb : rb * a.lds + cb] = s;
+    } else if constexpr (TRANS) {
+      if (team == 0 && c0 + lane * 8 + i < a.cols) a.scale[r0 / 128 * a.lds + c0 + lane * 8 + i] = s;
+    } else {
+      if (lane == 0 && r0 + team * 8 + i < a.rows) a.scale[c0 / 128 * a.lds + r0 + team * 8 + i] = s;
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    // Row k of this thread's 8 x 8 values, or its column k.
+    float x[8], sc[8], iv[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      x[i] = TRANS ? v[i][k] : v[k][i];
+      sc[i] = scale[k];
+      iv[i] = inv[k];
+    }
+    uint2 w = q8_pack(x, sc, iv);
+    if (!(top[k] < INFINITY)) w = make_uint2(0, 0);
+    if constexpr (TRANS) {
+      // 8-byte piece `team` of the tile's column, its place swizzled so that a wave's writes
+      // spread over the banks.
+      *reinterpret_cast<uint2*>(turned + (lane * 8 + k) * 128 + (team ^ lane) * 8) = w;
+    } else {
+      const int64_t r = r0 + team * 8 + k;
+      if (r < a.rows) *reinterpret_cast<uint2*>(a.q + r * a.ldq + c0 + lane * 8) = w;
+    }
+  }
+  if constexpr (TRANS) {
+    __syncthreads();
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      const int c = p * 32 + (threadIdx.x >> 3), h = threadIdx.x & 7;   // column, 16-byte piece
+      const uint2 lo = *reinterpret_cast<const uint2*>(turned + c * 128 + ((2 * h) ^ (c >> 3)) * 8);
+      const uint2 hi = *reinterpret_cast<const uint2*>(turned + c * 128 + ((2 * h + 1) ^ (c >> 3)) * 8);
+      if (c0 + c < a.cols)
+        *reinterpret_cast<uint4*>(a.q + (c0 + c) * a.ldq + r0 + 16 * h) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+    }
+  }
+}
+
+template <bool BF16, bool VEC>
+static void launch_quant8_as(const Quant8Args& a, dim3 grid, hipStream_t s) {
+  if (a.block && a.transpose) hipLaunchKernelGGL((k_quant8<BF16, VEC, true, true>), grid, dim3(Q8_THREADS), 0, s, a);
+  else if (a.block) hipLaunchKernelGGL((k_quant8<BF16, VEC, true, false>), grid, dim3(Q8_THREADS), 0, s, a);
+  else if (a.transpose) hipLaunchKernelGGL((k_quant8<BF16, VEC, false, true>), grid, dim3(Q8_THREADS), 0, s, a);
+  else hipLaunchKernelGGL((k_quant8<BF16, VEC, false, false>), grid, dim3(Q8_THREADS), 0, s, a);
+}
+
+hipError_t launch_quant8(const Quant8Args& a, hipStream_t s) {
+  if (a.rows <= 0 || a.cols <= 0) return hipSuccess;
+  const dim3 grid((unsigned)((a.rows + 127) / 128 * ((a.cols + 127) / 128)));
+  const bool vec = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && a.ldx * (a.bf16 ? 2 : 4) % 16 == 0;
+  if (a.bf16) vec ? launch_quant8_as<true, true>(a, grid, s) : launch_quant8_as<true, false>(a, grid, s);
+  else vec ? launch_quant8_as<false, true>(a, grid, s) : launch_quant8_as<false, false>(a, grid, s);
+  return hipGetLastError();
+}
+
+// ------------------------------------------------------------------------------------
+// The product. A K step is one group of 128: a 128-byte line of every row, two
+// v_mfma_f32_32x32x64_f8f6f4 for a block of 32 x 32 into accumulators that start at 0, and
+//   acc = fma(sum of the group, x_scale * weight_scale, acc).
+// MFMA operand A = weight rows (M), B = rows of x (N): a lane then holds one row of x, whose scale
+// is one register per block, and the weight's scale is the same for all of a wave's rows (they
+// lie in one block of 128), so a group costs one fma per element and one product per lane beside
+// the matrix cores.
+//
+// v_mfma_f32_32x32x64_f8f6f4: lane l supplies 32 bytes of A[l % 32] and of B[l % 32]; D as the bf16
+// 32x32 MFMA (llp_tile.hpp). Which 32 of the 64 bytes a lane holds does not matter while A and B
+// agree: the first 16 are chunk 4 kk + l / 32 of the line, the others chunk 4 kk + 2 + l / 32.
+//
+// Precision. The e4m3 MFMAs (every form of them) add 8 products at a time as if cut about 14 bits
+// below the largest: measured on values drawn as activations are, a sum of 64 is 1.7e-5 of its norm
+// off. That is a hundredth of bf16's rounding, so results that are written in bf16 take it; results
+// in fp32 (FULL) do not: their bytes become bf16 (exact) in front of the bf16 MFMA, whose sums
+// keep fp32's bits, at half the matrix rate.
+//
+// Either way every tile runs the same chain for each element, so an element has the same bits
+// whatever the tile and however many rows the call has.
+// ------------------------------------------------------------------------------------
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+__device__ __forceinline__ f32x16 mfma8(const i32x8& a, const i32x8& b, const f32x16& c) {
+  // Scales of 0: the form without block scales; formats 0: e4m3.
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
+}
+
+// 16 e4m3 values as bf16, which holds them exactly: two MFMA operands of 8.
+__device__ __forceinline__ void widen8(const i32x4& x, bf16x8 (&y)[2]) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const bf16x2 lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)x[2 * k + i], 1.f, false);
+      const bf16x2 hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)x[2 * k + i], 1.f, true);
+      y[k][4 * i] = lo[0]; y[k][4 * i + 1] = lo[1];
+      y[k][4 * i + 2] = hi[0]; y[k][4 * i + 3] = hi[1];
+    }
+}
+
+// 16 bytes (or 4) per lane from byte offset voff + soff into the LDS window at `lds`, lane order.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc8(const void* base, uint64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc((void*)base, (short)0,
+                                           (int)(uint32_t)(bytes < 0xFFFFFFFFull ? bytes : 0xFFFFFFFFull), 0x00020000);
+}
+__device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, uint8_t* lds, uint32_t voff, int soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16, voff, soff, 0, 0);
+}
+__device__ __forceinline__ void dma4(__amdgpu_buffer_rsrc_t r, uint8_t* lds, uint32_t voff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 4, voff, 0, 0, 0);
+}
+
+// A workgroup's tile: TM weight rows x TN rows of x by WM x WN waves, NST stages in flight.
+template <int TM, int TN, int WM, int WN, int NST>
+struct Tile8 {
+  static constexpr int NW = WM * WN, ROWS = TM + TN;
+  static constexpr int MB = TM / WM / 32, NB = TN / WN / 32;   // blocks per wave
+  static constexpr int NIA = TM / 8 / NW, NIB = TN / 8 / NW;   // loads per wave and step
+  static constexpr int LOADS = NIA + NIB + 1;                  // and the scales'
+  static constexpr int STAGE = ROWS * 128 + NW * 256;          // bytes
+  static constexpr int OUT_LD = MB * 32 + 4;                   // floats per row of x of the output's staging
+  static constexpr int OUT = NW * 32 * OUT_LD * 4;
+  static constexpr int LDS = NST * STAGE > OUT ? NST * STAGE : OUT;
+  static_assert(TM % (8 * NW) == 0 && TN % (8 * NW) == 0, "whole loads");
+  static_assert(TM / WM <= 128 && 128 % (TM / WM) == 0, "a wave's rows lie in one block");
+  static_assert(NB * 32 <= 64 && LDS <= 160 * 1024, "scales by lane, LDS");
+  static_assert((NST - 2) * LOADS < 64, "loads in flight");
+};
+
+// A wave's accumulators as rows of `out`: 32 rows of x at a time through the wave's own part of
+// the LDS, from where each row's columns are stored together.
+template <class T>
+__device__ __forceinline__ void store_rows8(const f32x16 (&acc)[T::MB][T::NB], const Linear8Args& a,
+                                            int64_t v0, int64_t t0, float* st) {
+  constexpr int COLS = T::MB * 32;
+  const int lane = threadIdx.x & 63;
+  const int64_t nv = a.V - v0;
+#pragma unroll
+  for (int ni = 0; ni < T::NB; ++ni) {
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int mi = 0; mi < T::MB; ++mi)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        float4 y;
+        y.x = acc[mi][ni][4 * g]; y.y = acc[mi][ni][4 * g + 1];
+        y.z = acc[mi][ni][4 * g + 2]; y.w = acc[mi][ni][4 * g + 3];
+        *reinterpret_cast<float4*>(st + (lane & 31) * T::OUT_LD + mi * 32 + 8 * g + 4 * (lane >> 5)) = y;
+      }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    // 8 columns per lane.
+    constexpr int LANES = COLS / 8, STEP = 64 / LANES;
+    const int c = lane % LANES * 8;
+    float b[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      b[i] = 0.f;
+      if (a.bias != nullptr && c + i < nv)
+        b[i] = a.bias_f32 ? static_cast<const float*>(a.bias)[v0 + c + i]
+                          : bf16_to_f32(static_cast<const uint16_t*>(a.bias)[v0 + c + i]);
+    }
+#pragma unroll
+    for (int j = 0; j < 32; j += STEP) {
+      const int64_t t = t0 + ni * 32 + j + lane / LANES;
+      const float* p = st + (j + lane / LANES) * T::OUT_LD + c;
+      const float4 lo = *reinterpret_cast<const float4*>(p), hi = *reinterpret_cast<const float4*>(p + 4);
+      float y[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+      if (a.bias != nullptr) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] += b[i];
+      }
+      if (t >= a.T) continue;
+      if (a.out_bf16) {
+        uint16_t* o = static_cast<uint16_t*>(a.out) + t * a.ldo + v0 + c;
+        const uint4 w = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
+                                   pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+        if (a.vec && c + 8 <= nv) {
+          *reinterpret_cast<uint4*>(o) = w;
+        } else {
+          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (c + i < nv) o[i] = (uint16_t)(u[i / 2] >> (16 * (i & 1)));
+        }
+      } else {
+        float* o = static_cast<float*>(a.out) + t * a.ldo + v0 + c;
+        if (a.vec && c + 8 <= nv) {
+          *reinterpret_cast<float4*>(o) = make_float4(y[0], y[1], y[2], y[3]);
+          *reinterpret_cast<float4*>(o + 4) = make_float4(y[4], y[5], y[6], y[7]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (c + i < nv) o[i] = y[i];
+        }
+      }
+    }
+  }
+}
+
+// The weight gradient's layout: a register holds 32 neighbouring columns of one row per half wave.
+template <class T>
+__device__ __forceinline__ void store_cols8(const f32x16 (&acc)[T::MB][T::NB], const Linear8Args& a,
+                                            int64_t v0, int64_t t0) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int ni = 0; ni < T::NB; ++ni) {
+    const int64_t h = t0 + ni * 32 + (lane & 31);
+#pragma unroll
+    for (int mi = 0; mi < T::MB; ++mi) {
+      const int64_t v = v0 + mi * 32;
+      if (a.out_bf16) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int64_t row = v + mfma_row(r, lane);
+          if (h < a.T && row < a.V)
+            static_cast<uint16_t*>(a.out)[row * a.ldo + h] = (uint16_t)pack_bf16x2(acc[mi][ni][r], 0.f);
+        }
+      } else {
+        float old[16];
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int64_t row = v + mfma_row(r, lane);
+          old[r] = 0.f;
+          if (a.accumulate && h < a.T && row < a.V) old[r] = static_cast<const float*>(a.out)[row * a.ldo + h];
+        }
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int64_t row = v + mfma_row(r, lane);
+          if (h < a.T && row < a.V)
+            static_cast<float*>(a.out)[row * a.ldo + h] = a.accumulate ? old[r] + acc[mi][ni][r] : acc[mi][ni][r];
+        }
+      }
+    }
+  }
+}
+
+template <int TM, int TN, int WM, int WN, int NST, bool GRAD, bool FULL, int EU>
+__global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(EU, EU))) void k_linear8(Linear8Args a) {
+  using T = Tile8<TM, TN, WM, WN, NST>;
+  __shared__ __attribute__((aligned(16))) uint8_t smem[T::LDS];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave % WM, wn = wave / WM;
+  int vt, tb;
+  vocab_token_tile(xcd_remap(blockIdx.x, gridDim.x), a.nvt, a.ntb, vt, tb);
+  const int64_t v0 = (int64_t)vt * TM, t0 = (int64_t)tb * TN;
+  const int nv = a.V - v0 < TM ? (int)(a.V - v0) : TM;
+  const int nt = a.T - t0 < TN ? (int)(a.T - t0) : TN;
+  const int n = a.steps;
+  // The wave's loads: instruction i moves rows 8 q .. 8 q + 7, q = i NW + wave, lane l the 16-byte
+  // chunk (l % 8) ^ swz8(row) of row 8 q + l / 8. Rows past the last are read as the last.
+  const __amdgpu_buffer_rsrc_t ra = rsrc8(a.W + v0 * a.ldw, (uint64_t)(nv - 1) * a.ldw + n * 128);
+  const __amdgpu_buffer_rsrc_t rb = rsrc8(a.x + t0 * a.ldx, (uint64_t)(nt - 1) * a.ldx + n * 128);
+  uint32_t va[T::NIA], vb[T::NIB];
+#pragma unroll
+  for (int i = 0; i < T::NIA; ++i) {
+    const int r = 8 * (i * T::NW + wave) + (lane >> 3);
+    va[i] = (uint32_t)((r < nv ? r : nv - 1) * a.ldw) + (((lane & 7) ^ dma::swz8(r)) << 4);
+  }
+#pragma unroll
+  for (int i = 0; i < T::NIB; ++i) {
+    const int r = 8 * (i * T::NW + wave) + (lane >> 3);
+    vb[i] = (uint32_t)((r < nt ? r : nt - 1) * a.ldx) + (((lane & 7) ^ dma::swz8(r)) << 4);
+  }
+  const int ts = wn * T::NB * 32 + lane % (T::NB * 32);   // the row whose scale this lane loads
+  const uint32_t vs = 4 * (ts < nt ? ts : nt - 1);
+  const float* const xs = a.xs + t0;
+  auto issue = [&](int s, int stage) {
+    uint8_t* const st = smem + stage * T::STAGE;
+#pragma unroll
+    for (int i = 0; i < T::NIA; ++i) dma16(ra, st + (i * T::NW + wave) * 1024, va[i], s * 128);
+#pragma unroll
+    for (int i = 0; i < T::NIB; ++i) dma16(rb, st + TM * 128 + (i * T::NW + wave) * 1024, vb[i], s * 128);
+    dma4(rsrc8(xs + s * a.ldxs, (uint64_t)nt * 4), st + T::ROWS * 128 + wave * 256, vs);
+  };
+  const float* const ws = a.ws + (v0 + wm * (TM / WM)) / 128 * a.ldws;
+  const bool live = wm * (TM / WM) < nv;   // else the wave's block of weight scales may not exist
+  auto weight_scales = [&](int s) { return live && s + lane < n ? ws[s + lane] : 0.f; };
+  // Fragment addresses within a stage.
+  int fa[T::MB], fb[T::NB], xa[T::MB], xb[T::NB];
+#pragma unroll
+  for (int i = 0; i < T::MB; ++i) {
+    const int r = (wm * T::MB + i) * 32 + (lane & 31);
+    fa[i] = r * 128;
+    xa[i] = dma::swz8(r) ^ (lane >> 5);
+  }
+#pragma unroll
+  for (int i = 0; i < T::NB; ++i) {
+    const int r = (wn * T::NB + i) * 32 + (lane & 31);
+    fb[i] = TM * 128 + r * 128;
+    xb[i] = dma::swz8(r) ^ (lane >> 5);
+  }
+  auto chunk = [&](const uint8_t* st, int row, int x, int q) {
+    return *reinterpret_cast<const i32x4*>(st + row + (((2 * q) ^ x) << 4));
+  };
+  auto fragment = [&](const uint8_t* st, int row, int x, int kk) {
+    return __builtin_shufflevector(chunk(st, row, x, 2 * kk), chunk(st, row, x, 2 * kk + 1), 0, 1, 2, 3, 4, 5, 6, 7);
+  };
+  f32x16 acc[T::MB][T::NB];
+#pragma unroll
+  for (int mi = 0; mi < T::MB; ++mi)
+#pragma unroll
+    for (int ni = 0; ni < T::NB; ++ni)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[mi][ni][r] = 0.f;
+  if (n > 0) {
+    float wsr = weight_scales(0);
+#pragma unroll
+    for (int s = 0; s < NST - 1; ++s) issue(s < n ? s : n - 1, s);
+    int stage = 0, fill = NST - 1;
+    for (int s = 0; s < n; ++s) {
+      // Step s has landed, and every wave is past its reads of the stage that is filled next.
+      dma::wait_vmem_le<(NST - 2) * T::LOADS>();
+      dma::lds_barrier();
+      issue(s + NST - 1 < n ? s + NST - 1 : n - 1, fill);
+      if ((s & 63) == 0 && s > 0) wsr = weight_scales(s);
+      const uint8_t* const st = smem + stage * T::STAGE;
+      const float* const sc = reinterpret_cast<const float*>(st + T::ROWS * 128 + wave * 256);
+      const float w = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, wsr), s & 63));
+      float scale[T::NB];
+#pragma unroll
+      for (int ni = 0; ni < T::NB; ++ni) scale[ni] = sc[ni * 32 + (lane & 31)] * w;
+      if constexpr (FULL) {
+        f32x16 p[T::MB][T::NB];
+#pragma unroll
+        for (int mi = 0; mi < T::MB; ++mi)
+#pragma unroll
+          for (int ni = 0; ni < T::NB; ++ni)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) p[mi][ni][r] = 0.f;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          bf16x8 b[T::NB][2];
+#pragma unroll
+          for (int ni = 0; ni < T::NB; ++ni) widen8(chunk(st, fb[ni], xb[ni], q), b[ni]);
+#pragma unroll
+          for (int mi = 0; mi < T::MB; ++mi) {
+            bf16x8 x[2];
+            widen8(chunk(st, fa[mi], xa[mi], q), x);
+#pragma unroll
+            for (int ni = 0; ni < T::NB; ++ni) {
+              dma::mfma1(x[0], b[ni][0], p[mi][ni]);
+              dma::mfma1(x[1], b[ni][1], p[mi][ni]);
+            }
+          }
+        }
+#pragma unroll
+        for (int mi = 0; mi < T::MB; ++mi)
+#pragma unroll
+          for (int ni = 0; ni < T::NB; ++ni)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[mi][ni][r] = fmaf(p[mi][ni][r], scale[ni], acc[mi][ni][r]);
+      } else {
+        i32x8 b[T::NB][2];
+#pragma unroll
+        for (int ni = 0; ni < T::NB; ++ni) {
+          b[ni][0] = fragment(st, fb[ni], xb[ni], 0);
+          b[ni][1] = fragment(st, fb[ni], xb[ni], 1);
+        }
+#pragma unroll
+        for (int mi = 0; mi < T::MB; ++mi) {
+          const i32x8 a0 = fragment(st, fa[mi], xa[mi], 0), a1 = fragment(st, fa[mi], xa[mi], 1);
+#pragma unroll
+          for (int ni = 0; ni < T::NB; ++ni) {
+            f32x16 p;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) p[r] = 0.f;
+            p = mfma8(a0, b[ni][0], p);
+            p = mfma8(a1, b[ni][1], p);
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[mi][ni][r] = fmaf(p[r], scale[ni], acc[mi][ni][r]);
+          }
+        }
+      }
+      stage = stage + 1 < NST ? stage + 1 : 0;
+      fill = fill + 1 < NST ? fill + 1 : 0;
+    }
+    dma::wait_vmem_le<0>();
+    __syncthreads();   // the output's staging takes the stages' place
+  }
+  const int64_t vw = v0 + wm * (TM / WM), tw = t0 + wn * (TN / WN);
+  if constexpr (GRAD) store_cols8<T>(acc, a, vw, tw);
+  else store_rows8<T>(acc, a, vw, tw, reinterpret_cast<float*>(smem) + wave * 32 * T::OUT_LD);
+}
+
+template <int TM, int TN, int WM, int WN, int NST, bool GRAD, bool FULL, int EU>
+static hipError_t launch_linear8_as(Linear8Args a, hipStream_t s) {
+  a.nvt = (int32_t)((a.V + TM - 1) / TM);
+  a.ntb = (int32_t)((a.T + TN - 1) / TN);
+  hipLaunchKernelGGL((k_linear8<TM, TN, WM, WN, NST, GRAD, FULL, EU>), dim3((unsigned)(a.nvt * a.ntb)),
+                     dim3(64 * WM * WN), 0, s, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_linear8(const Linear8Args& a, hipStream_t s) {
+  if (a.T <= 0 || a.V <= 0) return hipSuccess;
+  if (a.grad) {
+    if (a.out_bf16) return launch_linear8_as<256, 256, 2, 4, 2, true, false, 2>(a, s);
+    return launch_linear8_as<128, 128, 2, 2, 2, true, true, 2>(a, s);
+  }
+  if (a.out_bf16) {
+    if (a.T <= 32) return launch_linear8_as<128, 32, 4, 1, 3, false, false, 2>(a, s);
+    if (a.T <= 64) return launch_linear8_as<128, 64, 4, 1, 3, false, false, 2>(a, s);
+    if (a.T <= 512) return launch_linear8_as<128, 128, 2, 2, 2, false, false, 2>(a, s);
+    return launch_linear8_as<256, 256, 2, 4, 2, false, false, 2>(a, s);
+  }
+  if (a.T <= 32) return launch_linear8_as<128, 32, 4, 1, 3, false, true, 2>(a, s);
+  if (a.T <= 64) return launch_linear8_as<128, 64, 4, 1, 3, false, true, 2>(a, s);
+  return launch_linear8_as<128, 128, 2, 2, 2, false, true, 2>(a, s);
+}
+
+}  // namespace llp

@@ -414,6 +414,98 @@ struct PrefArgs {
   int32_t* status;
 };
 
+// Quantisation in blocks of 128 (llp_fp8.hip).
+struct Quant8Args {
+  const void* x;
+  int32_t bf16;
+  int64_t ldx;
+  int64_t rows, cols;
+  int32_t block, transpose;
+  uint8_t* q;
+  int64_t ldq;
+  float* scale;
+  int64_t lds;
+};
+
+// A product of operands in e4m3 (llp_fp8.hip): out[t][v], or with `grad` out[v][t].
+struct Linear8Args {
+  const uint8_t* x;      // [T] rows, scales by group: xs[g * ldxs + t]
+  int64_t ldx;
+  const float* xs;
+  int64_t ldxs;
+  const uint8_t* W;      // [V] rows, scales by block: ws[(v / 128) * ldws + g]
+  int64_t ldw;
+  const float* ws;
+  int64_t ldws;
+  const void* bias;
+  int32_t bias_f32;
+  int32_t out_bf16;
+  void* out;
+  int64_t ldo;
+  int64_t T, V;
+  int32_t steps;         // groups of 128
+  int32_t grad;          // the weight gradient's layout of out
+  int32_t accumulate;    // grad: out += the product
+  int32_t vec;           // rows of out are 16-byte aligned
+  int32_t nvt, ntb;      // tiles of the launch
+};
+
+// Beam search (llp_beam.hip). A wave takes BEAM_BLOCK columns of a row at a time.
+constexpr int BEAM_BLOCK = 2048;
+// Waves per row: enough for four on every SIMD of 256 compute units, at most one per block.
+inline int beam_splits(int64_t rows, int32_t blocks) {
+  int64_t n = rows > 0 ? 4096 / rows : 1;
+  if (n > blocks) n = blocks;
+  return n < 1 ? 1 : (int)n;
+}
+struct BeamArgs {
+  const void* logits;
+  int32_t bf16;
+  int64_t ld;
+  int64_t rows, n_real, offset;
+  int32_t num;
+  int32_t splits;        // waves per row
+  int32_t blocks;        // blocks of BEAM_BLOCK columns per row
+  float c1;
+  uint64_t* keys;        // [rows][splits][num] sorted candidates of each wave
+  float* pm;             // [rows][blocks] largest logit and sum of each block
+  float* ps;
+  float* value;
+  int64_t* token;
+  float* max;
+  double* sum;
+  int32_t* status;
+};
+
+struct BeamSelectArgs {
+  int32_t world, num, K, num_out;
+  int64_t seqs;
+  const float* value[LLP_MAX_WORLD];
+  const int64_t* token[LLP_MAX_WORLD];
+  const float* max[LLP_MAX_WORLD];
+  const double* sum[LLP_MAX_WORLD];
+  const float* scores;
+  const uint8_t* finished;
+  int64_t end_id;
+  float c1;
+  int64_t* out_token;
+  int32_t* out_parent;
+  float* out_score;
+  int32_t* status;
+};
+
+constexpr int REORDER_STATES = 64;   // states per launch
+struct ReorderArgs {
+  const void* src[REORDER_STATES];
+  void* dst[REORDER_STATES];
+  int32_t states, K, N;              // K source beams, N slots per sequence
+  int32_t unit;                      // bytes per load: 16, 8, 4, 2 or 1
+  int64_t seqs, outer, inner;
+  int64_t sr, so, dr, dout;          // row and outer strides of src and dst, bytes
+  const int32_t* parents;
+  int32_t* status;
+};
+
 hipError_t launch_layout(const LayoutArgs& a, hipStream_t s);
 hipError_t launch_fwd(const FwdArgs& a, hipStream_t s);
 hipError_t launch_combine(const CombineArgs& a, int64_t T_cap, hipStream_t s);
@@ -436,6 +528,11 @@ hipError_t launch_embedding_sort(const EmbBwdArgs& a, hipStream_t s);
 hipError_t launch_embedding_sum(const EmbBwdArgs& a, hipStream_t s);
 hipError_t launch_policy(const PolicyArgs& a, hipStream_t s);
 hipError_t launch_preference(const PrefArgs& a, hipStream_t s);
+hipError_t launch_quant8(const Quant8Args& a, hipStream_t s);
+hipError_t launch_linear8(const Linear8Args& a, hipStream_t s);
+hipError_t launch_beam_candidates(const BeamArgs& a, hipStream_t s);
+hipError_t launch_beam_select(const BeamSelectArgs& a, hipStream_t s);
+hipError_t launch_beam_reorder(const ReorderArgs& a, hipStream_t s);
 hipError_t probe_kernels();
 // Looks up this device's copy of the static scratch (the current device must be `device`);
 // idempotent. Called under the library's open lock.
