@@ -383,39 +383,41 @@ hipError_t launch_beam_select(const BeamSelectArgs& a, hipStream_t s) {
 // come before the first store, so the reordering is done in place without a copy, and a slot that
 // keeps its own rows costs nothing. Bound by memory: the moved slots read and written (a beam that
 // several slots take is read from the caches after the first).
+// No load is conditional (a slot that is not moved reads the state's first unit): behind a branch each
+// would be waited for before the next.
 // ------------------------------------------------------------------------------------
 template <int SLOTS, class U>
-__global__ __launch_bounds__(256) void k_beam_reorder(ReorderArgs a, int64_t units, int32_t per) {
-  const int64_t w = blockIdx.x / per;   // state, then sequence
-  const int64_t b = w % a.seqs;
-  const int st = (int)(w / a.seqs);
-  const int64_t u = (int64_t)(blockIdx.x % per) * 256 + threadIdx.x;
-  const bool mine = u < a.outer * units;
-  const int64_t o = mine ? u / units : 0, at = mine ? u % units * (int64_t)sizeof(U) : 0;
-  const char* const src = static_cast<const char*>(a.src[st]) + b * a.K * a.sr + o * a.so + at;
-  char* const dst = static_cast<char*>(a.dst[st]) + b * a.N * a.dr + o * a.dout + at;
-  const bool in_place = a.src[st] == a.dst[st];
-  U v[SLOTS];
-  int from[SLOTS];
+__global__ __launch_bounds__(256) void k_beam_reorder(ReorderArgs a, uint32_t units, uint32_t per) {
+  const uint32_t w = blockIdx.x / per;   // state, then sequence
+  const uint32_t st = w / (uint32_t)a.seqs;
+  const int64_t b = w - st * (uint32_t)a.seqs;
+  const int lane = threadIdx.x & 63;
+  int p = -1;
   bool wrong = false;
+  const char* const src = static_cast<const char*>(a.src[st]);
+  char* const dst = static_cast<char*>(a.dst[st]);
+  if (lane < a.N) {
+    p = a.parents[b * a.N + lane];
+    wrong = p < -1 || p >= a.K;
+    if (wrong || (src == dst && p == lane)) p = -1;
+  }
+  if (wrong && a.status && st == 0 && blockIdx.x % per == 0 && threadIdx.x < 64)
+    atomicOr(a.status, LLP_STATUS_PARENT_INVALID);
+  const uint32_t u = (blockIdx.x % per) * 256 + threadIdx.x;   // below 2^32: the host's limit
+  const uint32_t o = u / units;
+  const bool mine = o < a.outer;
+  const int64_t at = (int64_t)(u - o * units) * sizeof(U);
+  const char* const from = src + b * a.K * a.sr + o * a.so + at;
+  char* const to = dst + b * a.N * a.dr + o * a.dout + at;
+  U v[SLOTS];
 #pragma unroll
   for (int j = 0; j < SLOTS; ++j) {
-    from[j] = -1;
-    if (j < a.N) {
-      int p = __builtin_amdgcn_readfirstlane(a.parents[b * a.N + j]);
-      if (p < -1 || p >= a.K) {
-        wrong = true;
-        p = -1;
-      }
-      if (!(in_place && p == j)) from[j] = p;
-    }
-    if (from[j] >= 0 && mine) v[j] = *reinterpret_cast<const U*>(src + from[j] * a.sr);
+    const int q = __builtin_amdgcn_readlane(p, j);
+    v[j] = *reinterpret_cast<const U*>(q >= 0 && mine ? from + q * a.sr : src);
   }
 #pragma unroll
   for (int j = 0; j < SLOTS; ++j)
-    if (from[j] >= 0 && mine) *reinterpret_cast<U*>(dst + j * a.dr) = v[j];
-  if (wrong && a.status && st == 0 && blockIdx.x % per == 0 && threadIdx.x == 0)
-    atomicOr(a.status, LLP_STATUS_PARENT_INVALID);
+    if (__builtin_amdgcn_readlane(p, j) >= 0 && mine) *reinterpret_cast<U*>(to + j * a.dr) = v[j];
 }
 
 template <int SLOTS, class U>
@@ -423,7 +425,7 @@ static hipError_t launch_reorder_as(const ReorderArgs& a, hipStream_t s) {
   const int64_t units = a.inner / (int64_t)sizeof(U);
   const int64_t per = (a.outer * units + 255) / 256;
   hipLaunchKernelGGL((k_beam_reorder<SLOTS, U>), dim3((unsigned)(per * a.seqs * a.states)), dim3(256), 0, s,
-                     a, units, (int32_t)per);
+                     a, (uint32_t)units, (uint32_t)per);
   return hipGetLastError();
 }
 
@@ -432,13 +434,15 @@ static hipError_t launch_reorder_of(const ReorderArgs& a, hipStream_t s) {
   if (a.N <= 4) return launch_reorder_as<4, U>(a, s);
   if (a.N <= 8) return launch_reorder_as<8, U>(a, s);
   if (a.N <= 16) return launch_reorder_as<16, U>(a, s);
-  if (a.N <= 32) return launch_reorder_as<32, U>(a, s);
-  return launch_reorder_as<64, U>(a, s);
+  if constexpr (sizeof(U) < 16) {   // the host takes smaller units for more slots
+    if (a.N > 32) return launch_reorder_as<64, U>(a, s);
+  }
+  return launch_reorder_as<32, U>(a, s);
 }
 
 hipError_t launch_beam_reorder(const ReorderArgs& a, hipStream_t s) {
   if (a.states <= 0 || a.seqs <= 0 || a.outer <= 0 || a.inner <= 0) return hipSuccess;
-  if (a.unit == 16 && a.N <= 32) return launch_reorder_of<u32x4>(a, s);
+  if (a.unit == 16) return launch_reorder_of<u32x4>(a, s);
   if (a.unit >= 4) return launch_reorder_of<uint32_t>(a, s);
   return launch_reorder_of<uint8_t>(a, s);
 }

@@ -207,32 +207,35 @@ hipError_t launch_quant8(const Quant8Args& a, hipStream_t s) {
 }
 
 // ------------------------------------------------------------------------------------
-// The product. A K step is one group of 128: a 128-byte line of every row, two
-// v_mfma_f32_32x32x64_f8f6f4 for a block of 32 x 32 into accumulators that start at 0, and
+// The product. A K step is one group of 128, a 128-byte line of every row: for a block of 16 x 16 one
+// v_mfma_f32_16x16x128_f8f6f4 into accumulators that start at 0, then
 //   acc = fma(sum of the group, x_scale * weight_scale, acc).
-// MFMA operand A = weight rows (M), B = rows of x (N): a lane then holds one row of x, whose scale
-// is one register per block, and the weight's scale is the same for all of a wave's rows (they
-// lie in one block of 128), so a group costs one fma per element and one product per lane beside
-// the matrix cores.
+// MFMA operand A = weight rows (M), B = rows of x (N): a lane then holds one row of x per block, whose
+// scale is one register, and the weight's scale is the same for all of a wave's rows (they lie in
+// one block of 128), so a group costs one fma per element and one product per lane beside the
+// matrix cores. The MFMA over the whole group leaves 4 sums per block to scale, where the 32 x 32
+// form would hold 16 over two of them: that is what lets 128 x 64 outputs per wave fit 256 registers.
 //
-// v_mfma_f32_32x32x64_f8f6f4: lane l supplies 32 bytes of A[l % 32] and of B[l % 32]; D as the bf16
-// 32x32 MFMA (llp_tile.hpp). Which 32 of the 64 bytes a lane holds does not matter while A and B
-// agree: the first 16 are chunk 4 kk + l / 32 of the line, the others chunk 4 kk + 2 + l / 32.
+// v_mfma_f32_16x16x128_f8f6f4: lane l supplies 32 bytes of A[l % 16] and of B[l % 16] and holds
+// D[4 (l / 16) + r][l % 16]. Which 32 of the 128 bytes a lane holds does not matter while A and B
+// agree: 16-byte chunks l / 16 and 4 + l / 16 of the line.
 //
-// Precision. The e4m3 MFMAs (every form of them) add 8 products at a time as if cut about 14 bits
-// below the largest: measured on values drawn as activations are, a sum of 64 is 1.7e-5 of its norm
-// off. That is a hundredth of bf16's rounding, so results that are written in bf16 take it; results
-// in fp32 (FULL) do not: their bytes become bf16 (exact) in front of the bf16 MFMA, whose sums
-// keep fp32's bits, at half the matrix rate.
+// Precision. The e4m3 MFMAs (every form of them) add 8 products at a time cut towards zero at 2^-13
+// of the largest one's power of two: measured on values drawn as activations are, a sum of 64 is
+// 1.7e-5 of its norm off. That is a hundredth of bf16's rounding, so results that are written in
+// bf16 take it; results in fp32 (FULL) do not: their bytes become bf16 (exact) in front of the bf16
+// MFMA, whose sums keep fp32's bits, at half the matrix rate.
 //
 // Either way every tile runs the same chain for each element, so an element has the same bits
 // whatever the tile and however many rows the call has.
 // ------------------------------------------------------------------------------------
 typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-__device__ __forceinline__ f32x16 mfma8(const i32x8& a, const i32x8& b, const f32x16& c) {
+__device__ __forceinline__ f32x4 mfma8(const i32x8& a, const i32x8& b) {
   // Scales of 0: the form without block scales; formats 0: e4m3.
-  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
+  const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, zero, 0, 0, 0, 0, 0, 0);
 }
 
 // 16 e4m3 values as bf16, which holds them exactly: two MFMA operands of 8.
@@ -260,69 +263,83 @@ __device__ __forceinline__ void dma4(__amdgpu_buffer_rsrc_t r, uint8_t* lds, uin
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 4, voff, 0, 0, 0);
 }
 
-// A workgroup's tile: TM weight rows x TN rows of x by WM x WN waves, NST stages in flight.
-template <int TM, int TN, int WM, int WN, int NST>
+// One value that a whole wave reads, as a scalar load: a vector load's wait would drain the loads in
+// flight behind it.
+__device__ __forceinline__ float scalar8(const float* p) {
+  return *(const __attribute__((address_space(4))) float*)(uintptr_t)p;
+}
+
+// A workgroup's tile: TM weight rows x TN rows of x by WM x WN waves, NST stages in flight. A wave's
+// accumulators are MB x NB blocks of S x S: 16 in bf16 results, 32 in fp32 ones.
+template <int TM, int TN, int WM, int WN, int NST, bool FULL>
 struct Tile8 {
+  static constexpr int S = FULL ? 32 : 16, REGS = S * S / 64;
   static constexpr int NW = WM * WN, ROWS = TM + TN;
-  static constexpr int MB = TM / WM / 32, NB = TN / WN / 32;   // blocks per wave
+  static constexpr int MW = TM / WM, NWV = TN / WN;            // a wave's rows of the weight and of x
+  static constexpr int MB = MW / S, NB = NWV / S;
   static constexpr int NIA = TM / 8 / NW, NIB = TN / 8 / NW;   // loads per wave and step
   static constexpr int LOADS = NIA + NIB + 1;                  // and the scales'
   static constexpr int STAGE = ROWS * 128 + NW * 256;          // bytes
-  static constexpr int OUT_LD = MB * 32 + 4;                   // floats per row of x of the output's staging
-  static constexpr int OUT = NW * 32 * OUT_LD * 4;
+  static constexpr int OUT_LD = MW + 4;                        // floats per row of x of the output's staging
+  static constexpr int OUT = NW * S * OUT_LD * 4;
   static constexpr int LDS = NST * STAGE > OUT ? NST * STAGE : OUT;
+  typedef float Acc[MB][NB][REGS];
   static_assert(TM % (8 * NW) == 0 && TN % (8 * NW) == 0, "whole loads");
-  static_assert(TM / WM <= 128 && 128 % (TM / WM) == 0, "a wave's rows lie in one block");
-  static_assert(NB * 32 <= 64 && LDS <= 160 * 1024, "scales by lane, LDS");
+  static_assert(MW <= 128 && 128 % MW == 0, "a wave's rows lie in one block");
+  static_assert(NWV <= 64 && LDS <= 160 * 1024, "scales by lane, LDS");
   static_assert((NST - 2) * LOADS < 64, "loads in flight");
 };
 
-// A wave's accumulators as rows of `out`: 32 rows of x at a time through the wave's own part of
-// the LDS, from where each row's columns are stored together.
+// A wave's own LDS, written by some lanes and read by others.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// A wave's accumulators as rows of `out`: S rows of x at a time through the wave's own part of the
+// LDS, from where each row's columns are stored together.
 template <class T>
-__device__ __forceinline__ void store_rows8(const f32x16 (&acc)[T::MB][T::NB], const Linear8Args& a,
-                                            int64_t v0, int64_t t0, float* st) {
-  constexpr int COLS = T::MB * 32;
+__device__ __forceinline__ void store_rows8(const typename T::Acc& acc, const Linear8Args& a, int64_t v0,
+                                            int64_t t0, float* st) {
   const int lane = threadIdx.x & 63;
   const int64_t nv = a.V - v0;
+  // 8 columns per lane.
+  constexpr int LANES = T::MW / 8, STEP = 64 / LANES;
+  const int c = lane % LANES * 8;
+  float b[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    b[i] = 0.f;
+    if (a.bias != nullptr && c + i < nv)
+      b[i] = a.bias_f32 ? static_cast<const float*>(a.bias)[v0 + c + i]
+                        : bf16_to_f32(static_cast<const uint16_t*>(a.bias)[v0 + c + i]);
+  }
 #pragma unroll
   for (int ni = 0; ni < T::NB; ++ni) {
-    __builtin_amdgcn_wave_barrier();
+    wave_sync();
 #pragma unroll
     for (int mi = 0; mi < T::MB; ++mi)
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
+      for (int g = 0; g < T::REGS / 4; ++g) {
         float4 y;
         y.x = acc[mi][ni][4 * g]; y.y = acc[mi][ni][4 * g + 1];
         y.z = acc[mi][ni][4 * g + 2]; y.w = acc[mi][ni][4 * g + 3];
-        *reinterpret_cast<float4*>(st + (lane & 31) * T::OUT_LD + mi * 32 + 8 * g + 4 * (lane >> 5)) = y;
+        *reinterpret_cast<float4*>(st + lane % T::S * T::OUT_LD + mi * T::S + 8 * g + 4 * (lane / T::S)) = y;
       }
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-    // 8 columns per lane.
-    constexpr int LANES = COLS / 8, STEP = 64 / LANES;
-    const int c = lane % LANES * 8;
-    float b[8];
+    wave_sync();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      b[i] = 0.f;
-      if (a.bias != nullptr && c + i < nv)
-        b[i] = a.bias_f32 ? static_cast<const float*>(a.bias)[v0 + c + i]
-                          : bf16_to_f32(static_cast<const uint16_t*>(a.bias)[v0 + c + i]);
-    }
-#pragma unroll
-    for (int j = 0; j < 32; j += STEP) {
-      const int64_t t = t0 + ni * 32 + j + lane / LANES;
-      const float* p = st + (j + lane / LANES) * T::OUT_LD + c;
+    for (int j = 0; j < T::S; j += STEP) {
+      const int row = j + lane / LANES;
+      const int64_t t = t0 + ni * T::S + row;
+      if (row >= T::S || t >= a.T) continue;
+      const float* p = st + row * T::OUT_LD + c;
       const float4 lo = *reinterpret_cast<const float4*>(p), hi = *reinterpret_cast<const float4*>(p + 4);
       float y[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
       if (a.bias != nullptr) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) y[i] += b[i];
       }
-      if (t >= a.T) continue;
-      if (a.out_bf16) {
+      if constexpr (T::S == 16) {
         uint16_t* o = static_cast<uint16_t*>(a.out) + t * a.ldo + v0 + c;
         const uint4 w = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
                                    pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
@@ -349,46 +366,102 @@ __device__ __forceinline__ void store_rows8(const f32x16 (&acc)[T::MB][T::NB], c
   }
 }
 
-// The weight gradient's layout: a register holds 32 neighbouring columns of one row per half wave.
+// The weight gradient's layout, out[weight row][row of x]. In fp32 a register holds 32 neighbouring
+// columns of one row per half wave, two whole lines: stored (and the old values added) from there. A
+// buffer resource over each 32 rows (the host keeps a row's stride below 2^24 elements) drops what
+// lies past the last row, and lanes past the last column point past it.
 template <class T>
-__device__ __forceinline__ void store_cols8(const f32x16 (&acc)[T::MB][T::NB], const Linear8Args& a,
-                                            int64_t v0, int64_t t0) {
+__device__ __forceinline__ void store_cols_f32(const typename T::Acc& acc, const Linear8Args& a, int64_t v0,
+                                               int64_t t0) {
+  static_assert(T::S == 32, "fp32 results");
   const int lane = threadIdx.x & 63;
+  const uint32_t ld = (uint32_t)(a.ldo * 4);
 #pragma unroll
-  for (int ni = 0; ni < T::NB; ++ni) {
-    const int64_t h = t0 + ni * 32 + (lane & 31);
+  for (int mi = 0; mi < T::MB; ++mi) {
+    const int64_t v = v0 + mi * 32;
+    const int64_t left = a.V - v;
+    if (left <= 0) break;
+    const __amdgpu_buffer_rsrc_t r = rsrc8(static_cast<float*>(a.out) + v * a.ldo,
+                                           (uint64_t)((left < 32 ? left : 32) - 1) * ld + (uint64_t)a.T * 4);
 #pragma unroll
-    for (int mi = 0; mi < T::MB; ++mi) {
-      const int64_t v = v0 + mi * 32;
-      if (a.out_bf16) {
+    for (int ni = 0; ni < T::NB; ++ni) {
+      const int64_t h = t0 + ni * 32 + (lane & 31);
+      const bool in = h < a.T;
+      const uint32_t at = (uint32_t)h * 4 + (lane >> 5) * 4 * ld;
+      auto place = [&](int k) { return (int)(in ? at + ((k >> 2) * 8 + (k & 3)) * ld : 0xFFFFFFFFu); };
+      float old[16];
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const int64_t row = v + mfma_row(r, lane);
-          if (h < a.T && row < a.V)
-            static_cast<uint16_t*>(a.out)[row * a.ldo + h] = (uint16_t)pack_bf16x2(acc[mi][ni][r], 0.f);
-        }
+      for (int k = 0; k < 16; ++k)
+        old[k] = a.accumulate ? __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, place(k), 0, 0)) : 0.f;
+#pragma unroll
+      for (int k = 0; k < 16; ++k)
+        __builtin_amdgcn_raw_buffer_store_b32(
+            __builtin_bit_cast(uint32_t, a.accumulate ? old[k] + acc[mi][ni][k] : acc[mi][ni][k]), r, place(k), 0, 0);
+    }
+  }
+}
+
+// In bf16 a block's rows are 32 bytes long: 16 rows of the wave at a time go through its part of the
+// LDS and are stored as rows of all the wave's columns.
+template <class T>
+__device__ __forceinline__ void store_cols_bf16(const typename T::Acc& acc, const Linear8Args& a, int64_t v0,
+                                                int64_t t0, float* st) {
+  static_assert(T::S == 16, "bf16 results");
+  constexpr int LD = T::NWV + 4, LANES = T::NWV / 8, STEP = 64 / LANES;
+  static_assert(16 * LD <= T::S * T::OUT_LD, "within the wave's part");
+  const int lane = threadIdx.x & 63;
+  const int c = lane % LANES * 8;
+  const int64_t nt = a.T - t0;
+#pragma unroll
+  for (int mi = 0; mi < T::MB; ++mi) {
+    wave_sync();
+#pragma unroll
+    for (int ni = 0; ni < T::NB; ++ni)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) st[(4 * (lane >> 4) + r) * LD + ni * 16 + (lane & 15)] = acc[mi][ni][r];
+    wave_sync();
+#pragma unroll
+    for (int j = 0; j < 16; j += STEP) {
+      const int64_t v = v0 + mi * 16 + j + lane / LANES;
+      if (v >= a.V) continue;
+      const float* p = st + (j + lane / LANES) * LD + c;
+      const float4 lo = *reinterpret_cast<const float4*>(p), hi = *reinterpret_cast<const float4*>(p + 4);
+      uint16_t* o = static_cast<uint16_t*>(a.out) + v * a.ldo + t0 + c;
+      const uint32_t u[4] = {pack_bf16x2(lo.x, lo.y), pack_bf16x2(lo.z, lo.w), pack_bf16x2(hi.x, hi.y),
+                             pack_bf16x2(hi.z, hi.w)};
+      if (a.vec && c + 8 <= nt) {
+        *reinterpret_cast<uint4*>(o) = make_uint4(u[0], u[1], u[2], u[3]);
       } else {
-        float old[16];
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const int64_t row = v + mfma_row(r, lane);
-          old[r] = 0.f;
-          if (a.accumulate && h < a.T && row < a.V) old[r] = static_cast<const float*>(a.out)[row * a.ldo + h];
-        }
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const int64_t row = v + mfma_row(r, lane);
-          if (h < a.T && row < a.V)
-            static_cast<float*>(a.out)[row * a.ldo + h] = a.accumulate ? old[r] + acc[mi][ni][r] : acc[mi][ni][r];
-        }
+        for (int i = 0; i < 8; ++i)
+          if (c + i < nt) o[i] = (uint16_t)(u[i / 2] >> (16 * (i & 1)));
       }
     }
   }
 }
 
+template <class T, bool GRAD>
+__device__ __forceinline__ void store8(const typename T::Acc& acc, const Linear8Args& a, int64_t v0, int64_t t0,
+                                       uint8_t* smem, int wave) {
+  float* const st = reinterpret_cast<float*>(smem) + wave * T::S * T::OUT_LD;
+  if constexpr (!GRAD) store_rows8<T>(acc, a, v0, t0, st);
+  else if constexpr (T::S == 32) store_cols_f32<T>(acc, a, v0, t0);
+  else store_cols_bf16<T>(acc, a, v0, t0, st);
+}
+
+template <class T>
+__device__ __forceinline__ void zero8(typename T::Acc& acc) {
+#pragma unroll
+  for (int mi = 0; mi < T::MB; ++mi)
+#pragma unroll
+    for (int ni = 0; ni < T::NB; ++ni)
+#pragma unroll
+      for (int r = 0; r < T::REGS; ++r) acc[mi][ni][r] = 0.f;
+}
+
 template <int TM, int TN, int WM, int WN, int NST, bool GRAD, bool FULL, int EU>
 __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(EU, EU))) void k_linear8(Linear8Args a) {
-  using T = Tile8<TM, TN, WM, WN, NST>;
+  using T = Tile8<TM, TN, WM, WN, NST, FULL>;
   __shared__ __attribute__((aligned(16))) uint8_t smem[T::LDS];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave % WM, wn = wave / WM;
@@ -413,7 +486,7 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(EU
     const int r = 8 * (i * T::NW + wave) + (lane >> 3);
     vb[i] = (uint32_t)((r < nt ? r : nt - 1) * a.ldx) + (((lane & 7) ^ dma::swz8(r)) << 4);
   }
-  const int ts = wn * T::NB * 32 + lane % (T::NB * 32);   // the row whose scale this lane loads
+  const int ts = wn * T::NWV + lane % T::NWV;   // the row whose scale this lane loads
   const uint32_t vs = 4 * (ts < nt ? ts : nt - 1);
   const float* const xs = a.xs + t0;
   auto issue = [&](int s, int stage) {
@@ -424,38 +497,16 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(EU
     for (int i = 0; i < T::NIB; ++i) dma16(rb, st + TM * 128 + (i * T::NW + wave) * 1024, vb[i], s * 128);
     dma4(rsrc8(xs + s * a.ldxs, (uint64_t)nt * 4), st + T::ROWS * 128 + wave * 256, vs);
   };
-  const float* const ws = a.ws + (v0 + wm * (TM / WM)) / 128 * a.ldws;
-  const bool live = wm * (TM / WM) < nv;   // else the wave's block of weight scales may not exist
-  auto weight_scales = [&](int s) { return live && s + lane < n ? ws[s + lane] : 0.f; };
-  // Fragment addresses within a stage.
-  int fa[T::MB], fb[T::NB], xa[T::MB], xb[T::NB];
-#pragma unroll
-  for (int i = 0; i < T::MB; ++i) {
-    const int r = (wm * T::MB + i) * 32 + (lane & 31);
-    fa[i] = r * 128;
-    xa[i] = dma::swz8(r) ^ (lane >> 5);
-  }
-#pragma unroll
-  for (int i = 0; i < T::NB; ++i) {
-    const int r = (wn * T::NB + i) * 32 + (lane & 31);
-    fb[i] = TM * 128 + r * 128;
-    xb[i] = dma::swz8(r) ^ (lane >> 5);
-  }
-  auto chunk = [&](const uint8_t* st, int row, int x, int q) {
-    return *reinterpret_cast<const i32x4*>(st + row + (((2 * q) ^ x) << 4));
+  // A wave past the last row reads the last block's.
+  const float* const ws = a.ws + (v0 + (wm * T::MW < nv ? wm * T::MW : nv - 1)) / 128 * a.ldws;
+  // Chunk q of this lane's row of a block: 16 rows in 4 chunks, or 32 in 2, per read.
+  auto chunk = [&](const uint8_t* st, int r0, int q) {
+    const int r = r0 + lane % T::S;
+    return *reinterpret_cast<const i32x4*>(st + r * 128 + (((q * (64 / T::S) + lane / T::S) ^ dma::swz8(r)) << 4));
   };
-  auto fragment = [&](const uint8_t* st, int row, int x, int kk) {
-    return __builtin_shufflevector(chunk(st, row, x, 2 * kk), chunk(st, row, x, 2 * kk + 1), 0, 1, 2, 3, 4, 5, 6, 7);
-  };
-  f32x16 acc[T::MB][T::NB];
-#pragma unroll
-  for (int mi = 0; mi < T::MB; ++mi)
-#pragma unroll
-    for (int ni = 0; ni < T::NB; ++ni)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) acc[mi][ni][r] = 0.f;
+  typename T::Acc acc;
+  zero8<T>(acc);
   if (n > 0) {
-    float wsr = weight_scales(0);
 #pragma unroll
     for (int s = 0; s < NST - 1; ++s) issue(s < n ? s : n - 1, s);
     int stage = 0, fill = NST - 1;
@@ -464,13 +515,13 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(EU
       dma::wait_vmem_le<(NST - 2) * T::LOADS>();
       dma::lds_barrier();
       issue(s + NST - 1 < n ? s + NST - 1 : n - 1, fill);
-      if ((s & 63) == 0 && s > 0) wsr = weight_scales(s);
-      const uint8_t* const st = smem + stage * T::STAGE;
-      const float* const sc = reinterpret_cast<const float*>(st + T::ROWS * 128 + wave * 256);
-      const float w = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, wsr), s & 63));
+      const uint8_t* const sa = smem + stage * T::STAGE;
+      const uint8_t* const sb = sa + TM * 128;
+      const float* const sc = reinterpret_cast<const float*>(sa + T::ROWS * 128 + wave * 256);
+      const float w = scalar8(ws + s);
       float scale[T::NB];
 #pragma unroll
-      for (int ni = 0; ni < T::NB; ++ni) scale[ni] = sc[ni * 32 + (lane & 31)] * w;
+      for (int ni = 0; ni < T::NB; ++ni) scale[ni] = sc[ni * T::S + lane % T::S] * w;
       if constexpr (FULL) {
         f32x16 p[T::MB][T::NB];
 #pragma unroll
@@ -483,11 +534,11 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(EU
         for (int q = 0; q < 4; ++q) {
           bf16x8 b[T::NB][2];
 #pragma unroll
-          for (int ni = 0; ni < T::NB; ++ni) widen8(chunk(st, fb[ni], xb[ni], q), b[ni]);
+          for (int ni = 0; ni < T::NB; ++ni) widen8(chunk(sb, wn * T::NWV + ni * 32, q), b[ni]);
 #pragma unroll
           for (int mi = 0; mi < T::MB; ++mi) {
             bf16x8 x[2];
-            widen8(chunk(st, fa[mi], xa[mi], q), x);
+            widen8(chunk(sa, wm * T::MW + mi * 32, q), x);
 #pragma unroll
             for (int ni = 0; ni < T::NB; ++ni) {
               dma::mfma1(x[0], b[ni][0], p[mi][ni]);
@@ -502,24 +553,20 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(EU
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[mi][ni][r] = fmaf(p[mi][ni][r], scale[ni], acc[mi][ni][r]);
       } else {
-        i32x8 b[T::NB][2];
+        i32x8 b[T::NB];
 #pragma unroll
-        for (int ni = 0; ni < T::NB; ++ni) {
-          b[ni][0] = fragment(st, fb[ni], xb[ni], 0);
-          b[ni][1] = fragment(st, fb[ni], xb[ni], 1);
-        }
+        for (int ni = 0; ni < T::NB; ++ni)
+          b[ni] = __builtin_shufflevector(chunk(sb, wn * T::NWV + ni * 16, 0), chunk(sb, wn * T::NWV + ni * 16, 1),
+                                          0, 1, 2, 3, 4, 5, 6, 7);
 #pragma unroll
         for (int mi = 0; mi < T::MB; ++mi) {
-          const i32x8 a0 = fragment(st, fa[mi], xa[mi], 0), a1 = fragment(st, fa[mi], xa[mi], 1);
+          const i32x8 x = __builtin_shufflevector(chunk(sa, wm * T::MW + mi * 16, 0), chunk(sa, wm * T::MW + mi * 16, 1),
+                                                  0, 1, 2, 3, 4, 5, 6, 7);
 #pragma unroll
           for (int ni = 0; ni < T::NB; ++ni) {
-            f32x16 p;
+            const f32x4 p = mfma8(x, b[ni]);
 #pragma unroll
-            for (int r = 0; r < 16; ++r) p[r] = 0.f;
-            p = mfma8(a0, b[ni][0], p);
-            p = mfma8(a1, b[ni][1], p);
-#pragma unroll
-            for (int r = 0; r < 16; ++r) acc[mi][ni][r] = fmaf(p[r], scale[ni], acc[mi][ni][r]);
+            for (int r = 0; r < 4; ++r) acc[mi][ni][r] = fmaf(p[r], scale[ni], acc[mi][ni][r]);
           }
         }
       }
@@ -529,9 +576,147 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(EU
     dma::wait_vmem_le<0>();
     __syncthreads();   // the output's staging takes the stages' place
   }
-  const int64_t vw = v0 + wm * (TM / WM), tw = t0 + wn * (TN / WN);
-  if constexpr (GRAD) store_cols8<T>(acc, a, vw, tw);
-  else store_rows8<T>(acc, a, vw, tw, reinterpret_cast<float*>(smem) + wave * 32 * T::OUT_LD);
+  store8<T, GRAD>(acc, a, v0 + wm * T::MW, t0 + wn * T::NWV, smem, wave);
+}
+
+// The wide form of the bf16 results: 256 x 256 by 8 waves of 128 x 64, two per SIMD. The same chain
+// with every read ahead of its use: 16 weight rows' four MFMAs run while the next 16 are read and the
+// four sums before them are scaled; the next step's first fragments are read under the last rows' MFMAs,
+// and the step after next is loaded from there on, into the stage that the barrier in front of them has
+// freed. LDS: the weight rows' two stages, those of x, the scales'.
+struct Wide8 {
+  using T = Tile8<256, 256, 2, 4, 2, false>;
+  static constexpr int B0 = 2 * 256 * 128, S0 = 2 * B0;   // where x's stages and the scales' begin
+};
+
+template <bool GRAD>
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_linear8_wide(Linear8Args a) {
+  using T = Wide8::T;
+  __shared__ __attribute__((aligned(16))) uint8_t smem[T::LDS];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave & 1, wn = wave >> 1;
+  int vt, tb;
+  vocab_token_tile(xcd_remap(blockIdx.x, gridDim.x), a.nvt, a.ntb, vt, tb);
+  const int64_t v0 = (int64_t)vt * 256, t0 = (int64_t)tb * 256;
+  const int nv = a.V - v0 < 256 ? (int)(a.V - v0) : 256;
+  const int nt = a.T - t0 < 256 ? (int)(a.T - t0) : 256;
+  const int n = a.steps;
+  const __amdgpu_buffer_rsrc_t ra = rsrc8(a.W + v0 * a.ldw, (uint64_t)(nv - 1) * a.ldw + n * 128);
+  const __amdgpu_buffer_rsrc_t rb = rsrc8(a.x + t0 * a.ldx, (uint64_t)(nt - 1) * a.ldx + n * 128);
+  uint32_t va[4], vb[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 8 * (i * 8 + wave) + (lane >> 3);
+    const uint32_t c = ((lane & 7) ^ dma::swz8(r)) << 4;
+    va[i] = (uint32_t)((r < nv ? r : nv - 1) * a.ldw) + c;
+    vb[i] = (uint32_t)((r < nt ? r : nt - 1) * a.ldx) + c;
+  }
+  const int ts = wn * 64 + lane;
+  const uint32_t vs = 4 * (ts < nt ? ts : nt - 1);
+  const float* const xs = a.xs + t0;
+  auto issue_a = [&](int s, int stage) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) dma16(ra, smem + stage * 32768 + (i * 8 + wave) * 1024, va[i], s * 128);
+  };
+  auto issue_b = [&](int s, int stage) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) dma16(rb, smem + Wide8::B0 + stage * 32768 + (i * 8 + wave) * 1024, vb[i], s * 128);
+    dma4(rsrc8(xs + s * a.ldxs, (uint64_t)nt * 4), smem + Wide8::S0 + stage * 2048 + wave * 256, vs);
+  };
+  const float* const ws = a.ws + (v0 + (wm * 128 < nv ? wm * 128 : 0)) / 128 * a.ldws;
+  // Chunks l / 16 and 4 + l / 16 of this lane's row of 16-row block i: its swizzle is the first block's
+  // with 2 i exclusive-or'd in, so four addresses serve them all, ad[i % 4] and ad[i % 4 ^ 2] + 2048 i of
+  // the weight's, bd of x's.
+  int ad[4], bd[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int r = lane & 15, at = r * 128 + (((lane >> 4) ^ dma::swz8(r) ^ (2 * j)) << 4);
+    ad[j] = wm * 128 * 128 + at;
+    bd[j] = Wide8::B0 + wn * 64 * 128 + at;
+  }
+  auto read = [&](const int (&at)[4], int i) {
+    const i32x4 lo = *reinterpret_cast<const i32x4*>(smem + at[i & 3] + 2048 * i);
+    const i32x4 hi = *reinterpret_cast<const i32x4*>(smem + at[(i & 3) ^ 2] + 2048 * i);
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  };
+  typename T::Acc acc;
+  zero8<T>(acc);
+  if (n > 0) {
+    f32x4 p[4];
+    float sc[4], last[4];
+#pragma unroll
+    for (int ni = 0; ni < 4; ++ni) {
+      p[ni] = f32x4{0.f, 0.f, 0.f, 0.f};
+      last[ni] = 0.f;
+    }
+    issue_a(0, 0);
+    issue_b(0, 0);
+    issue_a(1 < n ? 1 : 0, 1);
+    issue_b(1 < n ? 1 : 0, 1);
+    dma::wait_vmem_le<T::LOADS>();
+    dma::lds_barrier();
+    i32x8 A[2], B[4];
+    const int sa = Wide8::S0 + wave * 256 + (lane & 15) * 4;
+    A[0] = read(ad, 0);
+    {
+      const float w = scalar8(ws);
+#pragma unroll
+      for (int ni = 0; ni < 4; ++ni) {
+        B[ni] = read(bd, ni);
+        sc[ni] = *reinterpret_cast<const float*>(smem + sa + ni * 64) * w;
+      }
+    }
+    auto promote = [&](float (&c)[4], const f32x4& q, float f) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) c[r] = fmaf(q[r], f, c[r]);
+      // The sums are taken here: without this the compiler puts all of a step's fmas at its end, and
+      // every block's sums into registers until then (184 spilled).
+      asm volatile("" : "+v"(c[0]), "+v"(c[1]), "+v"(c[2]), "+v"(c[3]));
+    };
+    for (int s = 0; s < n; ++s) {
+      const int kd = s + 2 < n ? s + 2 : n - 1;
+      const float w = scalar8(ws + (s + 1 < n ? s + 1 : s));   // of the next step
+#pragma unroll
+      for (int mi = 0; mi < 7; ++mi) {
+        A[(mi + 1) & 1] = read(ad, mi + 1);
+#pragma unroll
+        for (int ni = 0; ni < 4; ++ni) {
+          if (mi == 0) promote(acc[7][ni], p[ni], last[ni]);
+          else promote(acc[mi - 1][ni], p[ni], sc[ni]);
+          p[ni] = mfma8(A[mi & 1], B[ni]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      // Step s + 1 has landed, and every wave holds the last of step s.
+      dma::wait_vmem_le<0>();
+      dma::lds_barrier();
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        ad[q] ^= 32768;
+        bd[q] ^= 32768;
+      }
+      A[0] = read(ad, 0);
+#pragma unroll
+      for (int ni = 0; ni < 4; ++ni) {
+        promote(acc[6][ni], p[ni], sc[ni]);
+        p[ni] = mfma8(A[1], B[ni]);
+        B[ni] = read(bd, ni);
+      }
+      issue_a(kd, s & 1);
+      issue_b(kd, s & 1);
+#pragma unroll
+      for (int ni = 0; ni < 4; ++ni) {
+        last[ni] = sc[ni];
+        sc[ni] = *reinterpret_cast<const float*>(smem + sa + ((s + 1) & 1) * 2048 + ni * 64) * w;
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int ni = 0; ni < 4; ++ni) promote(acc[7][ni], p[ni], last[ni]);
+    dma::wait_vmem_le<0>();
+    __syncthreads();   // the output's staging takes the stages' place
+  }
+  store8<T, GRAD>(acc, a, v0 + wm * 128, t0 + wn * 64, smem, wave);
 }
 
 template <int TM, int TN, int WM, int WN, int NST, bool GRAD, bool FULL, int EU>
@@ -543,17 +728,25 @@ static hipError_t launch_linear8_as(Linear8Args a, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <bool GRAD>
+static hipError_t launch_linear8_wide(Linear8Args a, hipStream_t s) {
+  a.nvt = (int32_t)((a.V + 255) / 256);
+  a.ntb = (int32_t)((a.T + 255) / 256);
+  hipLaunchKernelGGL((k_linear8_wide<GRAD>), dim3((unsigned)(a.nvt * a.ntb)), dim3(512), 0, s, a);
+  return hipGetLastError();
+}
+
 hipError_t launch_linear8(const Linear8Args& a, hipStream_t s) {
   if (a.T <= 0 || a.V <= 0) return hipSuccess;
   if (a.grad) {
-    if (a.out_bf16) return launch_linear8_as<256, 256, 2, 4, 2, true, false, 2>(a, s);
+    if (a.out_bf16) return launch_linear8_wide<true>(a, s);
     return launch_linear8_as<128, 128, 2, 2, 2, true, true, 2>(a, s);
   }
   if (a.out_bf16) {
     if (a.T <= 32) return launch_linear8_as<128, 32, 4, 1, 3, false, false, 2>(a, s);
     if (a.T <= 64) return launch_linear8_as<128, 64, 4, 1, 3, false, false, 2>(a, s);
     if (a.T <= 512) return launch_linear8_as<128, 128, 2, 2, 2, false, false, 2>(a, s);
-    return launch_linear8_as<256, 256, 2, 4, 2, false, false, 2>(a, s);
+    return launch_linear8_wide<false>(a, s);
   }
   if (a.T <= 32) return launch_linear8_as<128, 32, 4, 1, 3, false, true, 2>(a, s);
   if (a.T <= 64) return launch_linear8_as<128, 64, 4, 1, 3, false, true, 2>(a, s);
