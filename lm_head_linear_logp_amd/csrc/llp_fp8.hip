@@ -218,7 +218,10 @@ hipError_t launch_quant8(const Quant8Args& a, hipStream_t s) {
 //
 // v_mfma_f32_16x16x128_f8f6f4: lane l supplies 32 bytes of A[l % 16] and of B[l % 16] and holds
 // D[4 (l / 16) + r][l % 16]. Which 32 of the 128 bytes a lane holds does not matter while A and B
-// agree: 16-byte chunks l / 16 and 4 + l / 16 of the line.
+// agree: 16-byte chunks 2 (l / 16) and the next of the line. Chunk c of row r sits at c ^ swz16(r) of its
+// line: a ds_read_b128 serves 16 lanes at a time, of which half may be of the next 16-lane group, and
+// with neighbouring groups two chunks apart those 16 fall on all banks once (chunks one apart, as a first
+// form had them, conflicted in 45 % of the LDS's cycles).
 //
 // Precision. The e4m3 MFMAs (every form of them) add 8 products at a time cut towards zero at 2^-13
 // of the largest one's power of two: measured on values drawn as activations are, a sum of 64 is
@@ -269,6 +272,8 @@ __device__ __forceinline__ float scalar8(const float* p) {
   return *(const __attribute__((address_space(4))) float*)(uintptr_t)p;
 }
 
+__device__ __forceinline__ int swz16(int row) { return (row ^ ((row >> 3) & 1)) & 7; }
+
 // A workgroup's tile: TM weight rows x TN rows of x by WM x WN waves, NST stages in flight. A wave's
 // accumulators are MB x NB blocks of S x S: 16 in bf16 results, 32 in fp32 ones.
 template <int TM, int TN, int WM, int WN, int NST, bool FULL>
@@ -283,6 +288,8 @@ struct Tile8 {
   static constexpr int OUT_LD = MW + 4;                        // floats per row of x of the output's staging
   static constexpr int OUT = NW * S * OUT_LD * 4;
   static constexpr int LDS = NST * STAGE > OUT ? NST * STAGE : OUT;
+  // Where 16-byte chunk 0 of a row sits in its line; the others are exclusive-or'd with it.
+  static __device__ __forceinline__ int swz(int row) { return FULL ? dma::swz8(row) : swz16(row); }
   typedef float Acc[MB][NB][REGS];
   static_assert(TM % (8 * NW) == 0 && TN % (8 * NW) == 0, "whole loads");
   static_assert(MW <= 128 && 128 % MW == 0, "a wave's rows lie in one block");
@@ -472,19 +479,19 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(EU
   const int nt = a.T - t0 < TN ? (int)(a.T - t0) : TN;
   const int n = a.steps;
   // The wave's loads: instruction i moves rows 8 q .. 8 q + 7, q = i NW + wave, lane l the 16-byte
-  // chunk (l % 8) ^ swz8(row) of row 8 q + l / 8. Rows past the last are read as the last.
+  // chunk (l % 8) ^ swz(row) of row 8 q + l / 8. Rows past the last are read as the last.
   const __amdgpu_buffer_rsrc_t ra = rsrc8(a.W + v0 * a.ldw, (uint64_t)(nv - 1) * a.ldw + n * 128);
   const __amdgpu_buffer_rsrc_t rb = rsrc8(a.x + t0 * a.ldx, (uint64_t)(nt - 1) * a.ldx + n * 128);
   uint32_t va[T::NIA], vb[T::NIB];
 #pragma unroll
   for (int i = 0; i < T::NIA; ++i) {
     const int r = 8 * (i * T::NW + wave) + (lane >> 3);
-    va[i] = (uint32_t)((r < nv ? r : nv - 1) * a.ldw) + (((lane & 7) ^ dma::swz8(r)) << 4);
+    va[i] = (uint32_t)((r < nv ? r : nv - 1) * a.ldw) + (((lane & 7) ^ T::swz(r)) << 4);
   }
 #pragma unroll
   for (int i = 0; i < T::NIB; ++i) {
     const int r = 8 * (i * T::NW + wave) + (lane >> 3);
-    vb[i] = (uint32_t)((r < nt ? r : nt - 1) * a.ldx) + (((lane & 7) ^ dma::swz8(r)) << 4);
+    vb[i] = (uint32_t)((r < nt ? r : nt - 1) * a.ldx) + (((lane & 7) ^ T::swz(r)) << 4);
   }
   const int ts = wn * T::NWV + lane % T::NWV;   // the row whose scale this lane loads
   const uint32_t vs = 4 * (ts < nt ? ts : nt - 1);
@@ -499,10 +506,11 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(EU
   };
   // A wave past the last row reads the last block's.
   const float* const ws = a.ws + (v0 + (wm * T::MW < nv ? wm * T::MW : nv - 1)) / 128 * a.ldws;
-  // Chunk q of this lane's row of a block: 16 rows in 4 chunks, or 32 in 2, per read.
+  // The lane's q-th chunk of its row of a block.
   auto chunk = [&](const uint8_t* st, int r0, int q) {
     const int r = r0 + lane % T::S;
-    return *reinterpret_cast<const i32x4*>(st + r * 128 + (((q * (64 / T::S) + lane / T::S) ^ dma::swz8(r)) << 4));
+    const int c = FULL ? 2 * q + lane / 32 : 2 * (lane / 16) + q;
+    return *reinterpret_cast<const i32x4*>(st + r * 128 + ((c ^ T::swz(r)) << 4));
   };
   typename T::Acc acc;
   zero8<T>(acc);
@@ -607,7 +615,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = 8 * (i * 8 + wave) + (lane >> 3);
-    const uint32_t c = ((lane & 7) ^ dma::swz8(r)) << 4;
+    const uint32_t c = ((lane & 7) ^ swz16(r)) << 4;
     va[i] = (uint32_t)((r < nv ? r : nv - 1) * a.ldw) + c;
     vb[i] = (uint32_t)((r < nt ? r : nt - 1) * a.ldx) + c;
   }
@@ -624,19 +632,18 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     dma4(rsrc8(xs + s * a.ldxs, (uint64_t)nt * 4), smem + Wide8::S0 + stage * 2048 + wave * 256, vs);
   };
   const float* const ws = a.ws + (v0 + (wm * 128 < nv ? wm * 128 : 0)) / 128 * a.ldws;
-  // Chunks l / 16 and 4 + l / 16 of this lane's row of 16-row block i: its swizzle is the first block's
-  // with 2 i exclusive-or'd in, so four addresses serve them all, ad[i % 4] and ad[i % 4 ^ 2] + 2048 i of
-  // the weight's, bd of x's.
-  int ad[4], bd[4];
+  // The lane's two chunks of its row of 16-row block i: at ad[0] and ad[1] + 2048 i of the weight's, bd of
+  // x's.
+  int ad[2], bd[2];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int r = lane & 15, at = r * 128 + (((lane >> 4) ^ dma::swz8(r) ^ (2 * j)) << 4);
-    ad[j] = wm * 128 * 128 + at;
-    bd[j] = Wide8::B0 + wn * 64 * 128 + at;
+  for (int q = 0; q < 2; ++q) {
+    const int r = lane & 15, at = r * 128 + (((2 * (lane >> 4) + q) ^ swz16(r)) << 4);
+    ad[q] = wm * 128 * 128 + at;
+    bd[q] = Wide8::B0 + wn * 64 * 128 + at;
   }
-  auto read = [&](const int (&at)[4], int i) {
-    const i32x4 lo = *reinterpret_cast<const i32x4*>(smem + at[i & 3] + 2048 * i);
-    const i32x4 hi = *reinterpret_cast<const i32x4*>(smem + at[(i & 3) ^ 2] + 2048 * i);
+  auto read = [&](const int (&at)[2], int i) {
+    const i32x4 lo = *reinterpret_cast<const i32x4*>(smem + at[0] + 2048 * i);
+    const i32x4 hi = *reinterpret_cast<const i32x4*>(smem + at[1] + 2048 * i);
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
   };
   typename T::Acc acc;
@@ -691,7 +698,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
       dma::wait_vmem_le<0>();
       dma::lds_barrier();
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
+      for (int q = 0; q < 2; ++q) {
         ad[q] ^= 32768;
         bd[q] ^= 32768;
       }
