@@ -691,8 +691,8 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
           if (mi == 0) promote(acc[7][ni], p[ni], last[ni]);
           else promote(acc[mi - 1][ni], p[ni], sc[ni]);
           p[ni] = mfma8(A[mi & 1], B[ni]);
+          __builtin_amdgcn_sched_barrier(0);
         }
-        __builtin_amdgcn_sched_barrier(0);
       }
       // Step s + 1 has landed, and every wave holds the last of step s.
       dma::wait_vmem_le<0>();
@@ -708,6 +708,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
         promote(acc[6][ni], p[ni], sc[ni]);
         p[ni] = mfma8(A[1], B[ni]);
         B[ni] = read(bd, ni);
+        __builtin_amdgcn_sched_barrier(0);
       }
       issue_a(kd, s & 1);
       issue_b(kd, s & 1);
