@@ -589,9 +589,9 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(EU
 
 // The wide form of the bf16 results: 256 x 256 by 8 waves of 128 x 64, two per SIMD. The same chain
 // with every read ahead of its use: 16 weight rows' four MFMAs run while the next 16 are read and the
-// four sums before them are scaled; the next step's first fragments are read under the last rows' MFMAs,
-// and the step after next is loaded from there on, into the stage that the barrier in front of them has
-// freed. LDS: the weight rows' two stages, those of x, the scales'.
+// four sums before them are scaled; the next step's first fragments are read under the last rows' MFMAs.
+// From there on the step after next is loaded into the stage that the barrier in front has freed, one load
+// after an MFMA (nine in a row hold up the wave's MFMAs: 5 % slower). LDS: the weight rows' two stages, those of x, the scales'.
 struct Wide8 {
   using T = Tile8<256, 256, 2, 4, 2, false>;
   static constexpr int B0 = 2 * 256 * 128, S0 = 2 * B0;   // where x's stages and the scales' begin
@@ -622,14 +622,11 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   const int ts = wn * 64 + lane;
   const uint32_t vs = 4 * (ts < nt ? ts : nt - 1);
   const float* const xs = a.xs + t0;
-  auto issue_a = [&](int s, int stage) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) dma16(ra, smem + stage * 32768 + (i * 8 + wave) * 1024, va[i], s * 128);
-  };
-  auto issue_b = [&](int s, int stage) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) dma16(rb, smem + Wide8::B0 + stage * 32768 + (i * 8 + wave) * 1024, vb[i], s * 128);
-    dma4(rsrc8(xs + s * a.ldxs, (uint64_t)nt * 4), smem + Wide8::S0 + stage * 2048 + wave * 256, vs);
+  // Load k of a step's nine: the weight rows', those of x, their scales.
+  auto load = [&](int k, int s, int stage) {
+    if (k < 4) dma16(ra, smem + stage * 32768 + (k * 8 + wave) * 1024, va[k], s * 128);
+    else if (k < 8) dma16(rb, smem + Wide8::B0 + stage * 32768 + ((k - 4) * 8 + wave) * 1024, vb[k - 4], s * 128);
+    else dma4(rsrc8(xs + s * a.ldxs, (uint64_t)nt * 4), smem + Wide8::S0 + stage * 2048 + wave * 256, vs);
   };
   const float* const ws = a.ws + (v0 + (wm * 128 < nv ? wm * 128 : 0)) / 128 * a.ldws;
   // The lane's two chunks of its row of 16-row block i: at ad[0] and ad[1] + 2048 i of the weight's, bd of
@@ -656,11 +653,11 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
       p[ni] = f32x4{0.f, 0.f, 0.f, 0.f};
       last[ni] = 0.f;
     }
-    issue_a(0, 0);
-    issue_b(0, 0);
-    issue_a(1 < n ? 1 : 0, 1);
-    issue_b(1 < n ? 1 : 0, 1);
-    dma::wait_vmem_le<T::LOADS>();
+#pragma unroll
+    for (int k = 0; k < 9; ++k) load(k, 0, 0);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) load(k, 1 < n ? 1 : 0, 1);
+    dma::wait_vmem_le<3>();
     dma::lds_barrier();
     i32x8 A[2], B[4];
     const int sa = Wide8::S0 + wave * 256 + (lane & 15) * 4;
@@ -681,8 +678,8 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
       asm volatile("" : "+v"(c[0]), "+v"(c[1]), "+v"(c[2]), "+v"(c[3]));
     };
     for (int s = 0; s < n; ++s) {
-      const int kd = s + 2 < n ? s + 2 : n - 1;
-      const float w = scalar8(ws + (s + 1 < n ? s + 1 : s));   // of the next step
+      const int k1 = s + 1 < n ? s + 1 : s, k2 = s + 2 < n ? s + 2 : n - 1;
+      const float w = scalar8(ws + k1);   // of the next step
 #pragma unroll
       for (int mi = 0; mi < 7; ++mi) {
         A[(mi + 1) & 1] = read(ad, mi + 1);
@@ -691,6 +688,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
           if (mi == 0) promote(acc[7][ni], p[ni], last[ni]);
           else promote(acc[mi - 1][ni], p[ni], sc[ni]);
           p[ni] = mfma8(A[mi & 1], B[ni]);
+          if (mi < 2 && ni < 3) load(3 + mi * 3 + ni, k1, (s + 1) & 1);
           __builtin_amdgcn_sched_barrier(0);
         }
       }
@@ -708,10 +706,9 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
         promote(acc[6][ni], p[ni], sc[ni]);
         p[ni] = mfma8(A[1], B[ni]);
         B[ni] = read(bd, ni);
+        if (ni < 3) load(ni, k2, s & 1);
         __builtin_amdgcn_sched_barrier(0);
       }
-      issue_a(kd, s & 1);
-      issue_b(kd, s & 1);
 #pragma unroll
       for (int ni = 0; ni < 4; ++ni) {
         last[ni] = sc[ni];
