@@ -303,9 +303,18 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_wave_barrier();
 }
 
+// 16 bytes of a result; PAST: past the caches, for results far larger than they are, whose lines would
+// push out operands that other tiles read (weight gradient of a shard: 538 -> 512 us).
+template <bool PAST>
+__device__ __forceinline__ void store16(uint16_t* p, const uint4& w) {
+  const u32x4 v = {w.x, w.y, w.z, w.w};
+  if constexpr (PAST) __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(p));
+  else *reinterpret_cast<u32x4*>(p) = v;
+}
+
 // A wave's accumulators as rows of `out`: S rows of x at a time through the wave's own part of the
 // LDS, from where each row's columns are stored together.
-template <class T>
+template <class T, bool PAST>
 __device__ __forceinline__ void store_rows8(const typename T::Acc& acc, const Linear8Args& a, int64_t v0,
                                             int64_t t0, float* st) {
   const int lane = threadIdx.x & 63;
@@ -351,7 +360,7 @@ __device__ __forceinline__ void store_rows8(const typename T::Acc& acc, const Li
         const uint4 w = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
                                    pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
         if (a.vec && c + 8 <= nv) {
-          *reinterpret_cast<uint4*>(o) = w;
+          store16<PAST>(o, w);
         } else {
           const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -410,7 +419,7 @@ __device__ __forceinline__ void store_cols_f32(const typename T::Acc& acc, const
 
 // In bf16 a block's rows are 32 bytes long: 16 rows of the wave at a time go through its part of the
 // LDS and are stored as rows of all the wave's columns.
-template <class T>
+template <class T, bool PAST>
 __device__ __forceinline__ void store_cols_bf16(const typename T::Acc& acc, const Linear8Args& a, int64_t v0,
                                                 int64_t t0, float* st) {
   static_assert(T::S == 16, "bf16 results");
@@ -437,7 +446,7 @@ __device__ __forceinline__ void store_cols_bf16(const typename T::Acc& acc, cons
       const uint32_t u[4] = {pack_bf16x2(lo.x, lo.y), pack_bf16x2(lo.z, lo.w), pack_bf16x2(hi.x, hi.y),
                              pack_bf16x2(hi.z, hi.w)};
       if (a.vec && c + 8 <= nt) {
-        *reinterpret_cast<uint4*>(o) = make_uint4(u[0], u[1], u[2], u[3]);
+        store16<PAST>(o, make_uint4(u[0], u[1], u[2], u[3]));
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -447,13 +456,13 @@ __device__ __forceinline__ void store_cols_bf16(const typename T::Acc& acc, cons
   }
 }
 
-template <class T, bool GRAD>
+template <class T, bool GRAD, bool PAST>
 __device__ __forceinline__ void store8(const typename T::Acc& acc, const Linear8Args& a, int64_t v0, int64_t t0,
                                        uint8_t* smem, int wave) {
   float* const st = reinterpret_cast<float*>(smem) + wave * T::S * T::OUT_LD;
-  if constexpr (!GRAD) store_rows8<T>(acc, a, v0, t0, st);
+  if constexpr (!GRAD) store_rows8<T, PAST>(acc, a, v0, t0, st);
   else if constexpr (T::S == 32) store_cols_f32<T>(acc, a, v0, t0);
-  else store_cols_bf16<T>(acc, a, v0, t0, st);
+  else store_cols_bf16<T, PAST>(acc, a, v0, t0, st);
 }
 
 template <class T>
@@ -584,7 +593,7 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(EU
     dma::wait_vmem_le<0>();
     __syncthreads();   // the output's staging takes the stages' place
   }
-  store8<T, GRAD>(acc, a, v0 + wm * T::MW, t0 + wn * T::NWV, smem, wave);
+  store8<T, GRAD, false>(acc, a, v0 + wm * T::MW, t0 + wn * T::NWV, smem, wave);
 }
 
 // The wide form of the bf16 results: 256 x 256 by 8 waves of 128 x 64, two per SIMD. The same chain
@@ -721,7 +730,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     dma::wait_vmem_le<0>();
     __syncthreads();   // the output's staging takes the stages' place
   }
-  store8<T, GRAD>(acc, a, v0 + wm * 128, t0 + wn * 64, smem, wave);
+  store8<T, GRAD, true>(acc, a, v0 + wm * 128, t0 + wn * 64, smem, wave);
 }
 
 template <int TM, int TN, int WM, int WN, int NST, bool GRAD, bool FULL, int EU>
