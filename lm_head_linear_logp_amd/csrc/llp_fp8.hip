@@ -9,11 +9,16 @@ namespace llp {
 
 // ------------------------------------------------------------------------------------
 // Quantisation: scale = max(max |x|, 1e-30) * fl32(1/448) over 1 or 128 rows of 128 columns, q =
-// x / scale as e4m3 (ties to even). A workgroup holds a 128 x 128 tile of x in registers, 8 x 8 values a
-// thread, so that either layout, and the transpose (through LDS, whole 128-byte rows out), costs
-// one read and one write. Bound by memory.
+// x / scale as e4m3 (ties to even). By blocks, or transposed, a workgroup holds a 128 x 128 tile of x in
+// registers, 8 x 8 values a thread, so that either costs one read and one write; the transpose goes
+// through LDS and out in whole 128-byte rows. Bound by memory: 37984 x 4096 bf16 (467 MB) in blocks 100 us,
+// transposed 98, 4.7 TB/s, a copy's rate; by group 109; 4096 x 37984 by group and transposed 120. (With
+// IEEE reciprocals, shuffles through LDS and floating point maxima 106, 104, 121 and 137.)
 // ------------------------------------------------------------------------------------
 constexpr int Q8_THREADS = 256;
+// Groups from which a team takes four rows instead of one (us: 4096 x 4096 bf16 17.4 and 14.3, 4096 x 37984
+// 125 and 130, 37984 x 4096 109 and 123).
+constexpr int64_t Q8_MANY_GROUPS = 1 << 19;
 
 // Columns c .. c + 7 of a row, 0 at and past `cols`. VEC: rows are 16-byte aligned.
 template <bool BF16, bool VEC>
@@ -52,16 +57,15 @@ __device__ __forceinline__ uint2 q8_bytes(const float (&v)[8]) {
   return make_uint2((uint32_t)lo, (uint32_t)hi);
 }
 
-// Eight values as e4m3 of the correctly rounded quotient x / scale. With inv = fl(1 / scale),
-// x * inv is off from that quotient by at most 3 half steps of fp32; only where 2^-21 to either side
-// gives another byte are the wave's divisions carried out. |quotient| <= 448 (1 + 2^-22), which
+// Eight values as e4m3 of the correctly rounded quotient x / scale. With inv the reciprocal to 2^-23,
+// x * inv is off from that quotient by at most 2^-22 of it; only where 2^-21 to either side gives
+// another byte are the wave's divisions carried out. |quotient| <= 448 (1 + 2^-22), which
 // rounds to 448.
-__device__ __forceinline__ uint2 q8_pack(const float (&v)[8], const float (&scale)[8],
-                                         const float (&inv)[8]) {
+__device__ __forceinline__ uint2 q8_pack(const float (&v)[8], float scale, float inv) {
   float lo[8], hi[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float p = v[i] * inv[i];
+    const float p = v[i] * inv;
     lo[i] = fmaf(p, -0x1p-21f, p);
     hi[i] = fmaf(p, 0x1p-21f, p);
   }
@@ -69,21 +73,53 @@ __device__ __forceinline__ uint2 q8_pack(const float (&v)[8], const float (&scal
   const uint2 u = q8_bytes(hi);
   if (__builtin_amdgcn_ballot_w64(w.x != u.x || w.y != u.y) != 0) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) lo[i] = v[i] / scale[i];
+    for (int i = 0; i < 8; ++i) lo[i] = v[i] / scale;
     w = q8_bytes(lo);
   }
   return w;
 }
 
-__device__ __forceinline__ float q8_top(float top, float x) {
-  const float m = fabsf(x);   // an infinity or NaN makes the top infinite
-  return m <= top ? top : m < INFINITY ? m : INFINITY;
+// The largest size of values, as its bits: they order as whole numbers, an infinity above all finite
+// values and a NaN above it.
+__device__ __forceinline__ uint32_t q8_top(uint32_t top, float x) {
+  const uint32_t m = __builtin_bit_cast(uint32_t, x) & 0x7FFFFFFFu;
+  return m > top ? m : top;
 }
+__device__ __forceinline__ uint32_t q8_max(uint32_t a, uint32_t b) { return a > b ? a : b; }
+
+// Over the 16 lanes of a team: rotations within rows of 16 lanes.
+__device__ __forceinline__ uint32_t q8_team_top(uint32_t x) {
+  x = q8_max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x128, 0xf, 0xf, false));
+  x = q8_max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x124, 0xf, 0xf, false));
+  x = q8_max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x122, 0xf, 0xf, false));
+  return q8_max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x121, 0xf, 0xf, false));
+}
+
+// Over the lanes l, l ^ 16, l ^ 32 and l ^ 48.
+__device__ __forceinline__ uint32_t q8_teams_top(uint32_t x) {
+  const auto h = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+  x = q8_max(h[0], h[1]);
+  const auto q = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+  return q8_max(q[0], q[1]);
+}
+
+// A block's scale, its reciprocal to 2^-23, and whether all of it is finite.
+struct Q8Scale {
+  float scale, inv;
+  bool fine;
+  __device__ __forceinline__ void of(uint32_t top) {
+    fine = top < 0x7F800000u;
+    scale = fmaxf(__builtin_bit_cast(float, top), 1e-30f) * (1.f / 448.f);
+    inv = __builtin_amdgcn_rcpf(scale);
+  }
+  __device__ __forceinline__ float out() const { return fine ? scale : __builtin_nanf(""); }
+};
 
 // Thread (team, lane): rows team * 8 .. + 7 and columns lane * 8 .. + 7 of the tile.
 template <bool BF16, bool VEC, bool BLOCK, bool TRANS>
 __global__ __launch_bounds__(Q8_THREADS) void k_quant8(Quant8Args a) {
-  __shared__ float tops[4][128];
+  static_assert(BLOCK || TRANS, "k_quant8_rows");
+  __shared__ uint32_t tops[4][128];
   __shared__ __attribute__((aligned(16))) uint8_t turned[TRANS ? 128 * 128 : 16];
   const int64_t ntc = (a.cols + 127) / 128;
   const int64_t r0 = blockIdx.x / ntc * 128, c0 = blockIdx.x % ntc * 128;
@@ -99,74 +135,47 @@ __global__ __launch_bounds__(Q8_THREADS) void k_quant8(Quant8Args a) {
       for (int i = 0; i < 8; ++i) v[p][i] = 0.f;
     }
   }
-  float top[8];   // of this thread's rows, or with TRANS of its columns
+  uint32_t top[8];   // of this thread's columns, or of all in the first
 #pragma unroll
-  for (int i = 0; i < 8; ++i) top[i] = 0.f;
+  for (int i = 0; i < 8; ++i) top[i] = 0;
 #pragma unroll
   for (int p = 0; p < 8; ++p)
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      float& t = top[BLOCK ? 0 : TRANS ? i : p];
+      uint32_t& t = top[BLOCK ? 0 : i];
       t = q8_top(t, v[p][i]);
     }
+  Q8Scale sc[BLOCK ? 1 : 8];
   if constexpr (BLOCK) {
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) top[0] = fmaxf(top[0], __shfl_xor(top[0], off));
+    top[0] = q8_teams_top(q8_team_top(top[0]));
     if ((threadIdx.x & 63) == 0) tops[wave][0] = top[0];
     __syncthreads();
-    top[0] = fmaxf(fmaxf(tops[0][0], tops[1][0]), fmaxf(tops[2][0], tops[3][0]));
-#pragma unroll
-    for (int i = 1; i < 8; ++i) top[i] = top[0];
-  } else if constexpr (TRANS) {
+    sc[0].of(q8_max(q8_max(tops[0][0], tops[1][0]), q8_max(tops[2][0], tops[3][0])));
+    const int64_t rb = r0 / 128, cb = c0 / 128;
+    if (threadIdx.x == 0) a.scale[TRANS ? cb * a.lds + rb : rb * a.lds + cb] = sc[0].out();
+  } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      top[i] = fmaxf(top[i], __shfl_xor(top[i], 16));
-      top[i] = fmaxf(top[i], __shfl_xor(top[i], 32));
+      top[i] = q8_teams_top(top[i]);
       if ((threadIdx.x & 63) < 16) tops[wave][lane * 8 + i] = top[i];
     }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int c = lane * 8 + i;
-      top[i] = fmaxf(fmaxf(tops[0][c], tops[1][c]), fmaxf(tops[2][c], tops[3][c]));
-    }
-  } else {
-#pragma unroll
-    for (int p = 0; p < 8; ++p)
-#pragma unroll
-      for (int off = 8; off > 0; off >>= 1) top[p] = fmaxf(top[p], __shfl_xor(top[p], off));
-  }
-  float scale[8], inv[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    scale[i] = fmaxf(top[i], 1e-30f) * (1.f / 448.f);
-    inv[i] = 1.f / scale[i];
-  }
-  // The scales: of rows or columns at a thread each, of a block at the first one.
-#pragma unroll
-  for (int i = 0; i < (BLOCK ? 1 : 8); ++i) {
-    const float s = top[i] < INFINITY ? scale[i] : __builtin_nanf("");
-    if constexpr (BLOCK) {
-      const int64_t rb = r0 / 128, cb = c0 / 128;
-      if (threadIdx.x == 0) a.scale[TRANS ? cb * a.lds + rb : rb * a.lds + cb] = s;
-    } else if constexpr (TRANS) {
-      if (team == 0 && c0 + lane * 8 + i < a.cols) a.scale[r0 / 128 * a.lds + c0 + lane * 8 + i] = s;
-    } else {
-      if (lane == 0 && r0 + team * 8 + i < a.rows) a.scale[c0 / 128 * a.lds + r0 + team * 8 + i] = s;
+      sc[i].of(q8_max(q8_max(tops[0][c], tops[1][c]), q8_max(tops[2][c], tops[3][c])));
+      if (team == 0 && c0 + c < a.cols) a.scale[r0 / 128 * a.lds + c0 + c] = sc[i].out();
     }
   }
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     // Row k of this thread's 8 x 8 values, or its column k.
-    float x[8], sc[8], iv[8];
+    float x[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      x[i] = TRANS ? v[i][k] : v[k][i];
-      sc[i] = scale[k];
-      iv[i] = inv[k];
-    }
-    uint2 w = q8_pack(x, sc, iv);
-    if (!(top[k] < INFINITY)) w = make_uint2(0, 0);
+    for (int i = 0; i < 8; ++i) x[i] = TRANS ? v[i][k] : v[k][i];
+    const Q8Scale& own = sc[BLOCK ? 0 : k];
+    uint2 w = q8_pack(x, own.scale, own.inv);
+    if (!own.fine) w = make_uint2(0, 0);
     if constexpr (TRANS) {
       // 8-byte piece `team` of the tile's column, its place swizzled so that a wave's writes
       // spread over the banks.
@@ -189,20 +198,61 @@ __global__ __launch_bounds__(Q8_THREADS) void k_quant8(Quant8Args a) {
   }
 }
 
+// By group and not transposed: 16 lanes a group and nothing shared; a team takes the same group of ROWS
+// rows, whose scales are neighbours.
+template <bool BF16, bool VEC, int ROWS>
+__global__ __launch_bounds__(Q8_THREADS) void k_quant8_rows(Quant8Args a) {
+  const int64_t groups = (a.cols + 127) / 128;
+  const int64_t w = (int64_t)blockIdx.x * (Q8_THREADS / 16) + (threadIdx.x >> 4);
+  const int lane = threadIdx.x & 15;
+  const int64_t r0 = w / groups * ROWS, g = w % groups;
+  float v[ROWS][8];
+#pragma unroll
+  for (int p = 0; p < ROWS; ++p) {
+    if (r0 + p < a.rows) {
+      q8_load<BF16, VEC>(static_cast<const char*>(a.x) + (r0 + p) * a.ldx * (BF16 ? 2 : 4), g * 128 + lane * 8, a.cols, v[p]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[p][i] = 0.f;
+    }
+  }
+#pragma unroll
+  for (int p = 0; p < ROWS; ++p) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = q8_top(top, v[p][i]);
+    Q8Scale sc;
+    sc.of(q8_team_top(top));
+    uint2 q = q8_pack(v[p], sc.scale, sc.inv);
+    if (!sc.fine) q = make_uint2(0, 0);
+    if (r0 + p < a.rows) {
+      *reinterpret_cast<uint2*>(a.q + (r0 + p) * a.ldq + g * 128 + lane * 8) = q;
+      if (lane == 0) a.scale[g * a.lds + r0 + p] = sc.out();
+    }
+  }
+}
+
+template <bool BF16, bool VEC, int ROWS>
+static void launch_quant8_rows(const Quant8Args& a, hipStream_t s) {
+  const int64_t teams = (a.rows + ROWS - 1) / ROWS * ((a.cols + 127) / 128);
+  hipLaunchKernelGGL((k_quant8_rows<BF16, VEC, ROWS>), dim3((unsigned)((teams + 15) / 16)), dim3(Q8_THREADS), 0, s, a);
+}
+
 template <bool BF16, bool VEC>
-static void launch_quant8_as(const Quant8Args& a, dim3 grid, hipStream_t s) {
+static void launch_quant8_as(const Quant8Args& a, hipStream_t s) {
+  const dim3 grid((unsigned)((a.rows + 127) / 128 * ((a.cols + 127) / 128)));
   if (a.block && a.transpose) hipLaunchKernelGGL((k_quant8<BF16, VEC, true, true>), grid, dim3(Q8_THREADS), 0, s, a);
   else if (a.block) hipLaunchKernelGGL((k_quant8<BF16, VEC, true, false>), grid, dim3(Q8_THREADS), 0, s, a);
   else if (a.transpose) hipLaunchKernelGGL((k_quant8<BF16, VEC, false, true>), grid, dim3(Q8_THREADS), 0, s, a);
-  else hipLaunchKernelGGL((k_quant8<BF16, VEC, false, false>), grid, dim3(Q8_THREADS), 0, s, a);
+  else if (a.rows * ((a.cols + 127) / 128) < Q8_MANY_GROUPS) launch_quant8_rows<BF16, VEC, 1>(a, s);
+  else launch_quant8_rows<BF16, VEC, 4>(a, s);
 }
 
 hipError_t launch_quant8(const Quant8Args& a, hipStream_t s) {
   if (a.rows <= 0 || a.cols <= 0) return hipSuccess;
-  const dim3 grid((unsigned)((a.rows + 127) / 128 * ((a.cols + 127) / 128)));
   const bool vec = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && a.ldx * (a.bf16 ? 2 : 4) % 16 == 0;
-  if (a.bf16) vec ? launch_quant8_as<true, true>(a, grid, s) : launch_quant8_as<true, false>(a, grid, s);
-  else vec ? launch_quant8_as<false, true>(a, grid, s) : launch_quant8_as<false, false>(a, grid, s);
+  if (a.bf16) vec ? launch_quant8_as<true, true>(a, s) : launch_quant8_as<true, false>(a, s);
+  else vec ? launch_quant8_as<false, true>(a, s) : launch_quant8_as<false, false>(a, s);
   return hipGetLastError();
 }
 
@@ -756,14 +806,22 @@ hipError_t launch_linear8(const Linear8Args& a, hipStream_t s) {
     if (a.out_bf16) return launch_linear8_wide<true>(a, s);
     return launch_linear8_as<128, 128, 2, 2, 2, true, true, 2>(a, s);
   }
+  // Few rows, the weight's bytes bound them: where 128 columns a workgroup would leave compute units
+  // with one, and so with two steps in flight, 64 columns each (us, 128 and 64 columns: 1 row of 37984 44.5 and
+  // 40.8, of 151936 121 and 126; 37 rows 52.2 and 45.8; 64 rows of 151936 149 and 159).
+  const bool narrow = a.V < 65536;
   if (a.out_bf16) {
-    if (a.T <= 32) return launch_linear8_as<128, 32, 4, 1, 3, false, false, 2>(a, s);
-    if (a.T <= 64) return launch_linear8_as<128, 64, 4, 1, 3, false, false, 2>(a, s);
+    if (a.T <= 32) return narrow ? launch_linear8_as<64, 32, 2, 1, 3, false, false, 2>(a, s)
+                                 : launch_linear8_as<128, 32, 4, 1, 3, false, false, 2>(a, s);
+    if (a.T <= 64) return narrow ? launch_linear8_as<64, 64, 2, 1, 3, false, false, 2>(a, s)
+                                 : launch_linear8_as<128, 64, 4, 1, 3, false, false, 2>(a, s);
     if (a.T <= 512) return launch_linear8_as<128, 128, 2, 2, 2, false, false, 2>(a, s);
     return launch_linear8_wide<false>(a, s);
   }
-  if (a.T <= 32) return launch_linear8_as<128, 32, 4, 1, 3, false, true, 2>(a, s);
-  if (a.T <= 64) return launch_linear8_as<128, 64, 4, 1, 3, false, true, 2>(a, s);
+  if (a.T <= 32) return narrow ? launch_linear8_as<64, 32, 2, 1, 3, false, true, 2>(a, s)
+                               : launch_linear8_as<128, 32, 4, 1, 3, false, true, 2>(a, s);
+  if (a.T <= 64) return narrow ? launch_linear8_as<64, 64, 2, 1, 3, false, true, 2>(a, s)
+                               : launch_linear8_as<128, 64, 4, 1, 3, false, true, 2>(a, s);
   return launch_linear8_as<128, 128, 2, 2, 2, false, true, 2>(a, s);
 }
 
