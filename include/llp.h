@@ -610,7 +610,7 @@ typedef struct {
  *   logits   as in llp_logits_request; num_rows rows, below 2^22.
  *   vocab    as in llp_request; local_size at most 2^23 - 256 and padded_vocab < 2^40 (else
  *            LLP_ERR_UNSUPPORTED).
- *   temperature  z = x * fl32(1/temperature).
+ *   temperature  in [2^-64, 2^64]; z = x * fl32(1/temperature).
  * -inf logits are no candidates. A row that holds a NaN or +inf among its real columns sets
  * LLP_STATUS_VALUE_NOT_FINITE and gets no candidates and sum = -1. */
 typedef struct {

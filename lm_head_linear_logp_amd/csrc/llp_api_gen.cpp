@@ -105,6 +105,14 @@ llp_status run_linear(const llp_fp8_linear_request* req, bool grad, void* stream
 }
 
 // ---- Beam search ----------------------------------------------------------------------------
+// c1 = 1 / temperature within what the kernels' exponents hold.
+llp_status check_beam_temperature(float temperature, float* c1) {
+  *c1 = (float)(1.0 / (double)temperature);
+  LLP_CHECK(temperature > 0.f && *c1 >= 0x1p-64f && *c1 <= 0x1p64f, LLP_ERR_INVALID_ARGUMENT,
+            "temperature must be in [2^-64, 2^64]");
+  return LLP_OK;
+}
+
 llp_status check_beam(const llp_beam_request* req, float* c1) {
   LLP_CHECK(req != nullptr, LLP_ERR_INVALID_ARGUMENT, "request is NULL");
   llp_status st = check_partition(req->vocab);
@@ -127,11 +135,7 @@ llp_status check_beam(const llp_beam_request* req, float* c1) {
     LLP_CHECK(req->num_rows == 1 || req->logits_stride * es % 16 == 0, LLP_ERR_INVALID_ARGUMENT,
               "rows of logits must be 16-byte aligned");
   }
-  LLP_CHECK(isfinite(req->temperature) && req->temperature > 0.f, LLP_ERR_INVALID_ARGUMENT,
-            "temperature must be finite and > 0");
-  *c1 = (float)(1.0 / (double)req->temperature);
-  LLP_CHECK(isfinite(*c1), LLP_ERR_INVALID_ARGUMENT, "1 / temperature must be finite in fp32");
-  return LLP_OK;
+  return check_beam_temperature(req->temperature, c1);
 }
 
 struct BeamWs {
@@ -277,9 +281,9 @@ LLP_API llp_status llp_beam_select(const llp_beam_select_request* req, const llp
             req->num_out);
   LLP_CHECK(req->num_seqs >= 0 && req->num_seqs < (int64_t(1) << 22), LLP_ERR_INVALID_ARGUMENT,
             "num_seqs %lld outside [0, 2^22)", (long long)req->num_seqs);
-  LLP_CHECK(isfinite(req->temperature) && req->temperature > 0.f &&
-                isfinite((float)(1.0 / (double)req->temperature)),
-            LLP_ERR_INVALID_ARGUMENT, "temperature must be finite and > 0 (and its reciprocal finite)");
+  float c1;
+  llp_status st = check_beam_temperature(req->temperature, &c1);
+  if (st != LLP_OK) return st;
   LLP_CHECK(req->parts != nullptr && out != nullptr, LLP_ERR_INVALID_ARGUMENT, "parts and out are required");
   BeamSelectArgs a{};
   if (req->num_seqs > 0) {
@@ -296,7 +300,7 @@ LLP_API llp_status llp_beam_select(const llp_beam_select_request* req, const llp
       a.sum[r] = p.sum;
     }
   }
-  llp_status st = check_device();
+  st = check_device();
   if (st != LLP_OK) return st;
   a.world = req->world;
   a.num = req->num;
@@ -306,7 +310,7 @@ LLP_API llp_status llp_beam_select(const llp_beam_select_request* req, const llp
   a.scores = req->scores;
   a.finished = req->finished;
   a.end_id = req->end_id;
-  a.c1 = (float)(1.0 / (double)req->temperature);
+  a.c1 = c1;
   a.out_token = out->token;
   a.out_parent = out->parent;
   a.out_score = out->score;

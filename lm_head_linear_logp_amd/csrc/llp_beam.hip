@@ -5,6 +5,8 @@
 
 #include <math.h>
 
+#include <type_traits>
+
 namespace llp {
 
 // ------------------------------------------------------------------------------------
@@ -20,12 +22,70 @@ __device__ __forceinline__ float unordered(uint32_t k) {
   return __builtin_bit_cast(float, k ^ ((k >> 31) != 0 ? 0x80000000u : 0xFFFFFFFFu));
 }
 
+// The value of lane l ^ J, without the LDS's latency: moves within rows of 16 lanes, swaps of rows
+// and of halves. (A sort of 64 keys through ds_bpermute took about 2700 cycles, so about 1000.)
+template <int J>
+__device__ __forceinline__ uint32_t across(uint32_t x) {
+  if constexpr (J == 1) return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0xB1, 0xf, 0xf, false);       // quad 1 0 3 2
+  else if constexpr (J == 2) return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x4E, 0xf, 0xf, false);  // quad 2 3 0 1
+  else if constexpr (J == 4) {
+    const int up = __builtin_amdgcn_update_dpp(0, (int)x, 0x104, 0xf, 0x5, false);                             // row_shl:4
+    return (uint32_t)__builtin_amdgcn_update_dpp(up, (int)x, 0x114, 0xf, 0xA, false);                          // row_shr:4
+  } else if constexpr (J == 8) return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x128, 0xf, 0xf, false);  // row_ror:8
+  else if constexpr (J == 16) {
+    const auto y = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    return (threadIdx.x & 16) != 0 ? y[0] : y[1];
+  } else {
+    const auto y = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+    return (threadIdx.x & 32) != 0 ? y[0] : y[1];
+  }
+}
+template <int J>
+__device__ __forceinline__ float across(float x) {
+  return __builtin_bit_cast(float, across<J>(__builtin_bit_cast(uint32_t, x)));
+}
+
+__device__ __forceinline__ float wave_max(float x) {
+  x = fmaxf(x, across<1>(x));
+  x = fmaxf(x, across<2>(x));
+  x = fmaxf(x, across<4>(x));
+  x = fmaxf(x, across<8>(x));
+  x = fmaxf(x, across<16>(x));
+  return fmaxf(x, across<32>(x));
+}
+__device__ __forceinline__ float wave_sum(float x) {
+  x += across<1>(x);
+  x += across<2>(x);
+  x += across<4>(x);
+  x += across<8>(x);
+  x += across<16>(x);
+  return x + across<32>(x);
+}
+__device__ __forceinline__ double wave_sum(double x) {
+  auto add = [&](auto j) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = across<decltype(j)::value>((uint32_t)u), hi = across<decltype(j)::value>((uint32_t)(u >> 32));
+    x += __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+  };
+  add(std::integral_constant<int, 1>());
+  add(std::integral_constant<int, 2>());
+  add(std::integral_constant<int, 4>());
+  add(std::integral_constant<int, 8>());
+  add(std::integral_constant<int, 16>());
+  add(std::integral_constant<int, 32>());
+  return x;
+}
+
 struct Key64 {   // logit, column
   uint64_t k;
   __device__ __forceinline__ bool above(const Key64& o) const { return k > o.k; }
   __device__ __forceinline__ Key64 from(int lane) const {
     const int lo = __shfl((int)(uint32_t)k, lane), hi = __shfl((int)(k >> 32), lane);
     return {(uint64_t)(uint32_t)hi << 32 | (uint32_t)lo};
+  }
+  template <int J>
+  __device__ __forceinline__ Key64 other() const {
+    return {(uint64_t)across<J>((uint32_t)(k >> 32)) << 32 | across<J>((uint32_t)k)};
   }
   __device__ __forceinline__ bool any() const { return k != 0; }
   static __device__ __forceinline__ Key64 none() { return {0}; }
@@ -38,37 +98,55 @@ struct Key128 {   // total, then beam and token
     const Key64 a = Key64{k}.from(lane), b = Key64{at}.from(lane);
     return {a.k, b.k};
   }
+  template <int J>
+  __device__ __forceinline__ Key128 other() const {
+    const Key64 a = Key64{k}.other<J>(), b = Key64{at}.other<J>();
+    return {a.k, b.k};
+  }
   __device__ __forceinline__ bool any() const { return k != 0; }
   static __device__ __forceinline__ Key128 none() { return {0, 0}; }
 };
 
-// The wave's 64 keys, largest first (bitonic network).
+struct Key32 {   // a logit alone
+  uint32_t k;
+  __device__ __forceinline__ bool above(const Key32& o) const { return k > o.k; }
+  template <int J>
+  __device__ __forceinline__ Key32 other() const { return {across<J>(k)}; }
+};
+
+// One step of a bitonic network: runs of SIZE lanes are left largest first, every other one last.
+template <int SIZE, int J, class K>
+__device__ __forceinline__ void exchange(K& x) {
+  const int lane = threadIdx.x & 63;
+  const K y = x.template other<J>();
+  // The lower lane of a pair takes the larger key in a descending run.
+  const bool larger = ((lane & J) == 0) == ((lane & SIZE) == 0 || SIZE == 64);
+  if (y.above(x) == larger) x = y;
+}
+template <int SIZE, int J, class K>
+__device__ __forceinline__ void exchanges(K& x) {
+  exchange<SIZE, J>(x);
+  if constexpr (J > 1) exchanges<SIZE, J / 2>(x);
+}
+
+// The wave's 64 keys, largest first.
 template <class K>
 __device__ __forceinline__ K sort64(K x) {
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int size = 2; size <= 64; size *= 2)
-#pragma unroll
-    for (int j = size / 2; j > 0; j /= 2) {
-      const K y = x.from(lane ^ j);
-      // The lower lane of a pair takes the larger key in a descending run.
-      const bool larger = ((lane & j) == 0) == ((lane & size) == 0 || size == 64);
-      if (y.above(x) == larger) x = y;
-    }
+  exchanges<2, 1>(x);
+  exchanges<4, 2>(x);
+  exchanges<8, 4>(x);
+  exchanges<16, 8>(x);
+  exchanges<32, 16>(x);
+  exchanges<64, 32>(x);
   return x;
 }
 
 // The 64 largest of two runs of 64, each largest first.
 template <class K>
 __device__ __forceinline__ K merge64(K x, K y) {
-  const int lane = threadIdx.x & 63;
-  y = y.from(63 - lane);
+  y = y.from(63 - (threadIdx.x & 63));
   if (y.above(x)) x = y;
-#pragma unroll
-  for (int j = 32; j > 0; j /= 2) {
-    const K z = x.from(lane ^ j);
-    if (z.above(x) == ((lane & j) == 0)) x = z;
-  }
+  exchanges<64, 32>(x);
   return x;
 }
 
@@ -122,41 +200,59 @@ struct Best {
 // block's maximum and its sum of exponentials go to the workspace (so the row's normaliser does not
 // depend on how many waves share it), and the values above the wave's bar into its best keys. The
 // first block's bar is the num-th largest of the 64 lanes' maxima, each of which is a value of
-// its own. Bound by memory: one read of the logits.
+// its own. Bound by memory: one read of the logits, past the caches (512 rows of 151669 fp32 columns, 311 MB:
+// 62 us, 5.0 TB/s; 69 through them; twice or four times the waves, or the next block loaded under the
+// present one's work, no faster).
 //
-// exp((x - max) c) as 2^t, t = (x - max) c log2 e: t's rounding and the low part of c log2 e are
-// made up for to first order, so that a term is off by the exponential's own rounding alone and
-// sums over thousands of columns by about 1e-8: two beams' totals closer than that are rare.
+// exp((x - max) c) as 2^t, t = (x - max) c log2 e with the constant in two parts: its rounding would shift
+// every term alike, by 2e-7 for the bulk of a row; t's own roundings, and the exponential's, differ in
+// sign from term to term, so that a sum over thousands of columns is off by about 1e-8 and two beams'
+// totals closer than that are rare.
 // ------------------------------------------------------------------------------------
 constexpr int BEAM_WAVES = 4;
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 
+// The lane's 32 values of the block at c0, -inf past the last column. No load is conditional per lane (each
+// would be waited for by itself: 32 in a row, 20 us): past the last whole 16 bytes the last are
+// loaded again, and the columns behind them, fewer than 16 bytes, come one by one for all lanes.
+template <bool BF16>
+__device__ __forceinline__ float beam_value(const void* row, int64_t c) {
+  return BF16 ? bf16_to_f32(static_cast<const uint16_t*>(row)[c]) : static_cast<const float*>(row)[c];
+}
 template <bool BF16>
 __device__ __forceinline__ void beam_load(const void* row, int64_t c0, int64_t n_real, float (&x)[32]) {
   constexpr int V = BF16 ? 8 : 4;   // values per 16 bytes
   const int lane = threadIdx.x & 63;
+  const int64_t whole = n_real / V * V;
+  if (whole > 0) {
 #pragma unroll
-  for (int i = 0; i < 32 / V; ++i) {
-    const int64_t c = c0 + i * 64 * V + lane * V;
-    if (c + V <= n_real) {
+    for (int i = 0; i < 32 / V; ++i) {
+      const int64_t c = c0 + i * 64 * V + lane * V;
+      const int64_t at = c < whole ? c : whole - V;
       if constexpr (BF16) {
-        const u32x4 u = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(row) + c);
+        const u32x4 u = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(row) + at));
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           x[i * V + 2 * k] = __builtin_bit_cast(float, u[k] << 16);
           x[i * V + 2 * k + 1] = __builtin_bit_cast(float, u[k] & 0xFFFF0000u);
         }
       } else {
-        const float4 u = *reinterpret_cast<const float4*>(static_cast<const float*>(row) + c);
-        x[i * V] = u.x; x[i * V + 1] = u.y; x[i * V + 2] = u.z; x[i * V + 3] = u.w;
-      }
-    } else {
+        const f32x4 u = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(static_cast<const float*>(row) + at));
 #pragma unroll
-      for (int k = 0; k < V; ++k) {
-        x[i * V + k] = -INFINITY;
-        if (c + k < n_real)
-          x[i * V + k] = BF16 ? bf16_to_f32(static_cast<const uint16_t*>(row)[c + k])
-                              : static_cast<const float*>(row)[c + k];
+        for (int k = 0; k < 4; ++k) x[i * V + k] = u[k];
       }
+    }
+  }
+  if (c0 + BEAM_BLOCK > whole) {
+    float rest[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) rest[k] = beam_value<BF16>(row, whole + k < n_real ? whole + k : n_real - 1);
+#pragma unroll
+    for (int i = 0; i < 32 / V; ++i) {
+      const int64_t c = c0 + i * 64 * V + lane * V;
+#pragma unroll
+      for (int k = 0; k < V; ++k)
+        if (c >= whole) x[i * V + k] = c + k < n_real ? rest[k] : -INFINITY;
     }
   }
 }
@@ -173,36 +269,35 @@ __global__ __launch_bounds__(64 * BEAM_WAVES) void k_beam_rows(BeamArgs a) {
   const char* const row = static_cast<const char*>(a.logits) + r * a.ld * (BF16 ? 2 : 4);
   const int b0 = (int)((int64_t)a.blocks * sp / a.splits), b1 = (int)((int64_t)a.blocks * (sp + 1) / a.splits);
   const double cl = (double)a.c1 * 1.4426950408889634074;
-  const float ch = (float)cl, clo = (float)(cl - (double)ch);
+  const float ch = (float)cl, clo = (float)(cl - (double)ch), low = -200.f / ch;
   Best<Key64> best;
   best.init(room[wave]);
   for (int b = b0; b < b1; ++b) {
     const int64_t c0 = (int64_t)b * BEAM_BLOCK;
     float x[32];
     beam_load<BF16>(row, c0, a.n_real, x);
-    float mine = -INFINITY;
-    bool fine = true;
+    float part[4];      // the largest of each 8 values
+    bool fine = true;   // no NaN
 #pragma unroll
-    for (int e = 0; e < 32; ++e) {
-      fine &= x[e] < INFINITY;
-      mine = fmaxf(mine, x[e]);
+    for (int q = 0; q < 4; ++q) {
+      part[q] = -INFINITY;
+#pragma unroll
+      for (int e = 8 * q; e < 8 * q + 8; e += 2) {
+        fine &= !__builtin_isunordered(x[e], x[e + 1]);
+        part[q] = fmaxf(part[q], fmaxf(x[e], x[e + 1]));
+      }
     }
-    float top = mine;
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off));
-    const bool bad = __builtin_amdgcn_ballot_w64(!fine) != 0;
+    const float mine = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
+    const float top = wave_max(mine);
+    const bool bad = __builtin_amdgcn_ballot_w64(!fine) != 0 || top == INFINITY;
     float s = 0.f;
     if (!bad && top > -INFINITY) {
 #pragma unroll
       for (int e = 0; e < 32; ++e) {
-        const float d = x[e] - top;   // -inf for a column that is none, or far below
-        const float t = d * ch;
-        const float rest = fmaf(d, clo, fmaf(d, ch, -t));
-        const float v = __builtin_amdgcn_exp2f(t);
-        s += t > -150.f ? fmaf(v, rest * kLn2, v) : 0.f;
+        const float d = fmaxf(x[e] - top, low);   // 2^-200 for a column that is none, or far below
+        s += __builtin_amdgcn_exp2f(fmaf(d, ch, d * clo));
       }
-#pragma unroll
-      for (int off = 32; off > 0; off >>= 1) s += __shfl_xor(s, off);
+      s = wave_sum(s);
     }
     if (lane == 0) {
       a.pm[r * a.blocks + b] = top;
@@ -210,19 +305,22 @@ __global__ __launch_bounds__(64 * BEAM_WAVES) void k_beam_rows(BeamArgs a) {
     }
     if (bad) continue;   // the row has no candidates
     if (b == b0) {
-      const Key64 m = sort64(Key64{mine > -INFINITY ? (uint64_t)ordered(mine) << 32 : 0});
-      const Key64 at = m.from(a.num - 1);
-      if (at.any()) best.bar = Key64{at.k - 1};
+      const Key32 m = sort64(Key32{mine > -INFINITY ? ordered(mine) : 0});
+      const uint32_t at = __shfl((int)m.k, a.num - 1);
+      if (at != 0) best.bar = Key64{((uint64_t)at << 32) - 1};
     }
     const float bar = best.bar.any() ? unordered((uint32_t)(best.bar.k >> 32)) : -INFINITY;
     // The bar's value may be one below the smallest that counts: >= and the key decide.
-    if (__builtin_amdgcn_ballot_w64(mine >= bar && mine > -INFINITY) == 0) continue;
 #pragma unroll
-    for (int e = 0; e < 32; ++e) {
-      const bool may = x[e] >= bar && x[e] > -INFINITY;
-      if (__builtin_amdgcn_ballot_w64(may) == 0) continue;
-      const uint32_t c = (uint32_t)c0 + (e / V) * 64 * V + lane * V + e % V;
-      best.add(Key64{may ? (uint64_t)ordered(x[e]) << 32 | (uint32_t)~c : 0}, a.num);
+    for (int q = 0; q < 4; ++q) {
+      if (__builtin_amdgcn_ballot_w64(part[q] >= bar && part[q] > -INFINITY) == 0) continue;
+#pragma unroll
+      for (int e = 8 * q; e < 8 * q + 8; ++e) {
+        const bool may = x[e] >= bar && x[e] > -INFINITY;
+        if (__builtin_amdgcn_ballot_w64(may) == 0) continue;
+        const uint32_t c = (uint32_t)c0 + (e / V) * 64 * V + lane * V + e % V;
+        best.add(Key64{may ? (uint64_t)ordered(x[e]) << 32 | (uint32_t)~c : 0}, a.num);
+      }
     }
   }
   best.finish(a.num);
@@ -255,8 +353,7 @@ __global__ __launch_bounds__(64) void k_beam_join(BeamArgs a) {
     M = fmaxf(M, a.pm[r * a.blocks + i]);
     bad |= a.ps[r * a.blocks + i] < 0.f;
   }
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor(M, off));
+  M = wave_max(M);
   bad = __builtin_amdgcn_ballot_w64(bad) != 0;
   double S = 0.0;
   if (M > -INFINITY && !bad) {
@@ -264,8 +361,7 @@ __global__ __launch_bounds__(64) void k_beam_join(BeamArgs a) {
       const float m = a.pm[r * a.blocks + i];
       if (m > -INFINITY) S += (double)a.ps[r * a.blocks + i] * exp(((double)m - (double)M) * (double)a.c1);
     }
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) S += __shfl_xor(S, off);
+    S = wave_sum(S);
   }
   if (lane == 0) {
     a.max[r] = bad ? -INFINITY : M;
@@ -316,6 +412,25 @@ __global__ __launch_bounds__(64) void k_beam_select(BeamSelectArgs a) {
   const double c = (double)a.c1;
   Best<Key128> best;
   best.init(room);
+  const int per = a.world * a.K, total = per * a.num;
+  // The first candidates of each lane are loaded in front of all else.
+  struct Item {
+    int k, r;
+    int64_t at;
+  };
+  auto item = [&](int i) {
+    const int rank = i / per, in = i - rank * per, k = in / a.world;
+    return Item{k, in - k * a.world, (b * a.K + k) * a.num + rank};
+  };
+  constexpr int AHEAD = 4;
+  float value[AHEAD];
+  int64_t token[AHEAD];
+#pragma unroll
+  for (int q = 0; q < AHEAD; ++q) {
+    const Item t = item(q * 64 + lane < total ? q * 64 + lane : 0);
+    value[q] = a.value[t.r][t.at];
+    token[q] = a.token[t.r][t.at];
+  }
   Key128 end = Key128::none();
   if (lane < a.K) {
     const int64_t row = b * a.K + lane;
@@ -332,7 +447,8 @@ __global__ __launch_bounds__(64) void k_beam_select(BeamSelectArgs a) {
       if (M > -INFINITY && !bad)
         for (int r = 0; r < a.world; ++r) {
           const float m = a.max[r][row];
-          if (m > -INFINITY) S += a.sum[r][row] * exp(((double)m - (double)M) * c);
+          if (m == M) S += a.sum[r][row];
+          else if (m > -INFINITY) S += a.sum[r][row] * exp(((double)m - (double)M) * c);
         }
     }
     if (bad && a.status) atomicOr(a.status, LLP_STATUS_VALUE_NOT_FINITE);
@@ -345,20 +461,21 @@ __global__ __launch_bounds__(64) void k_beam_select(BeamSelectArgs a) {
   }
   __syncthreads();
   best.add(end, a.num_out);
-  const int per = a.world * a.K, total = per * a.num;
-  for (int i = 0; i < total; i += 64) {
+  auto take = [&](int i, float v, int64_t id) {
     Key128 x = Key128::none();
-    if (i + lane < total) {
-      const int rank = (i + lane) / per, k = (i + lane) % per / a.world, r = (i + lane) % per % a.world;
-      if (kind[k] == 1) {
-        const int64_t at = (b * a.K + k) * a.num + rank;
-        const int64_t token = a.token[r][at];
-        const double z = ((double)a.value[r][at] - (double)top[k]) * c;
-        const double t = score[k] + (z - norm[k]);
-        if (token >= 0 && t > -INFINITY) x = Key128{ordered64(t), ~((uint64_t)k << BEAM_AT | (uint64_t)token)};
-      }
+    const int k = item(i < total ? i : 0).k;
+    if (i < total && kind[k] == 1) {
+      const double t = score[k] + (((double)v - (double)top[k]) * c - norm[k]);
+      if (id >= 0 && t > -INFINITY) x = Key128{ordered64(t), ~((uint64_t)k << BEAM_AT | (uint64_t)id)};
     }
     best.add(x, a.num_out);
+  };
+#pragma unroll
+  for (int q = 0; q < AHEAD; ++q)
+    if (q * 64 < total) take(q * 64 + lane, value[q], token[q]);
+  for (int i = AHEAD * 64; i < total; i += 64) {
+    const Item t = item(i + lane < total ? i + lane : 0);
+    take(i + lane, a.value[t.r][t.at], a.token[t.r][t.at]);
   }
   best.finish(a.num_out);
   if (lane < a.num_out) {
