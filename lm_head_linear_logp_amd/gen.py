@@ -344,6 +344,46 @@ def _pieces(shape, *strides):
     return (dims[0][0], inner, dims[0][1]) if dims else (1, inner, (0,) * len(strides))
 
 
+class _Layout:
+    """What states of one layout share: beams K of a sequence, pieces and strides in bytes, and where
+    they are."""
+    __slots__ = ("K", "rows", "outer", "inner", "sr", "so", "dr", "do", "extent", "src_extent", "src", "dst")
+
+
+def _reorder_layout(s, d, i, B, N, dev):
+    """The checked layout of states[i] = s and what it goes to (inner 0: nothing to move)."""
+    if s.dim() < 1 or s.device != dev or d.device != dev or s.dtype != d.dtype or s.shape[1:] != d.shape[1:]:
+        raise ValueError(f"states[{i}] and what it goes to must be tensors [rows, ...] on {dev}, "
+                         "alike but for their rows")
+    if d.shape[0] != B * N or (s.shape[0] % B if B else s.shape[0]):
+        raise ValueError(f"states[{i}] has {s.shape[0]} rows, to be written {d.shape[0]}: {B} sequences "
+                         f"of {N} are expected")
+    c = _Layout()
+    c.src, c.dst, c.inner = [], [], 0
+    if s.numel() == 0 or d.numel() == 0:
+        if d.numel():
+            raise ValueError(f"states[{i}] holds no rows")
+        return c
+    p = _pieces(s.shape[1:], s.stride()[1:], d.stride()[1:])
+    if p is None:
+        raise ValueError(f"states[{i}] of strides {s.stride()} is not rows of pieces at one stride")
+    size = s.element_size()
+    c.outer, c.inner, c.rows = p[0], p[1] * size, d.shape[0]
+    c.so, c.do = (st * size for st in p[2])
+    c.K = _num(s.shape[0] // B, "beams per sequence")
+    c.dr = d.stride(0) * size if c.rows > 1 else 0
+    c.sr = c.dr if d is s else s.stride(0) * size if s.shape[0] > 1 else 0
+    steps = sorted((st, n) for st, n in ((c.dr, c.rows), (c.do, c.outer)) if n > 1)
+    reach = c.inner
+    for st, n in steps:
+        if st < reach:
+            raise ValueError(f"rows of {'out' if d is not s else 'states'}[{i}] overlap")
+        reach += (n - 1) * st
+    c.extent = (c.rows - 1) * c.dr + (c.outer - 1) * c.do + c.inner
+    c.src_extent = (s.shape[0] - 1) * c.sr + (c.outer - 1) * c.so + c.inner
+    return c
+
+
 def beam_reorder(states, parents: torch.Tensor, *, out=None, status: Optional[torch.Tensor] = None):
     """llp_beam_reorder: what is kept per beam follows the beams that were chosen. states: a tensor
     or a sequence of them, of any dtype, [B * K, ...] with the beams of a sequence in consecutive
@@ -365,59 +405,40 @@ def beam_reorder(states, parents: torch.Tensor, *, out=None, status: Optional[to
     if not parents.is_contiguous():
         raise ValueError("parents must be contiguous")
     _status(status, dev)
-    calls, seen = {}, []
+    calls, seen = {}, []   # states of one layout go together
     for i, (s, d) in enumerate(zip(src, dst)):
-        _tensor(s, f"states[{i}]")
-        _tensor(d, f"out[{i}]")
-        if s.dim() < 1 or s.device != dev or d.device != dev or s.dtype != d.dtype or s.shape[1:] != d.shape[1:]:
-            raise ValueError(f"states[{i}] and what it goes to must be tensors [rows, ...] on {dev}, "
-                             "alike but for their rows")
-        if d.shape[0] != B * N or (s.shape[0] % B if B else s.shape[0]):
-            raise ValueError(f"states[{i}] has {s.shape[0]} rows, to be written {d.shape[0]}: {B} sequences "
-                             f"of {N} are expected")
-        if s.numel() == 0 or d.numel() == 0:
-            if d.numel():
-                raise ValueError(f"states[{i}] holds no rows")
+        if not (isinstance(s, torch.Tensor) and isinstance(d, torch.Tensor)):
+            raise TypeError(f"states[{i}] and what it goes to must be tensors")
+        key = (s.shape, s.stride(), s.dtype, s.device) if d is s else (
+            s.shape, s.stride(), s.dtype, s.device, d.shape, d.stride(), d.dtype, d.device)
+        call = calls.get(key)
+        if call is None:
+            call = calls[key] = _reorder_layout(s, d, i, B, N, dev)
+        if call.inner == 0:
             continue
-        p = _pieces(s.shape[1:], s.stride()[1:], d.stride()[1:])
-        if p is None:
-            raise ValueError(f"states[{i}] of strides {s.stride()} is not rows of pieces at one stride")
-        size = s.element_size()
-        outer, inner, (so, do) = p
-        K = _num(s.shape[0] // B, "beams per sequence")
-        sr, dr = s.stride(0), d.stride(0)
-        if s.shape[0] == 1:
-            sr = 0
-        if d.shape[0] == 1:
-            dr = 0
-        if d is s:
-            sr = dr
-        steps = sorted((st, n) for st, n in ((dr, d.shape[0]), (do, outer)) if n > 1)
-        if any(st < reach for (st, _), reach in zip(steps, (inner, *((n - 1) * st + inner for st, n in steps)))):
-            raise ValueError(f"rows of {'out' if d is not s else 'states'}[{i}] overlap")
-        first, last = d.data_ptr(), d.data_ptr() + size * ((d.shape[0] - 1) * dr + (outer - 1) * do + inner)
-        seen.append((first, last, i, d.shape[0], dr * size, outer, do * size, inner * size))
-        if d is not s:
-            end = s.data_ptr() + size * ((s.shape[0] - 1) * sr + (outer - 1) * so + inner)
-            if s.data_ptr() < last and first < end:
-                raise ValueError(f"out[{i}] overlaps states[{i}]")
-        key = (K, outer, inner * size, sr * size, so * size, dr * size, do * size)
-        calls.setdefault(key, []).append((s.data_ptr(), first))
+        first = d.data_ptr()
+        seen.append((first, first + call.extent, i, call))
+        if d is not s and s.data_ptr() < first + call.extent and first < s.data_ptr() + call.src_extent:
+            raise ValueError(f"out[{i}] overlaps states[{i}]")
+        call.src.append(s.data_ptr())
+        call.dst.append(first)
     _apart(seen, [(s.data_ptr(), s) for s in src] if out is not None else [])
     if seen:
         _ready(dev)
-    for (K, outer, inner, sr, so, dr, do), ptrs in calls.items():
-        n = len(ptrs)
+    for c in calls.values():
+        n = len(c.src)
+        if n == 0:
+            continue
         r = A.llp_beam_reorder_request(
-            (C.c_void_p * n)(*(p[0] for p in ptrs)), (C.c_void_p * n)(*(p[1] for p in ptrs)), n, K, N, 0,
-            B, outer, inner, sr, so, dr, do, parents.data_ptr(), _ptr(status))
+            (C.c_void_p * n)(*c.src), (C.c_void_p * n)(*c.dst), n, c.K, N, 0, B, c.outer, c.inner, c.sr,
+            c.so, c.dr, c.do, parents.data_ptr(), _ptr(status))
         _call(dev, "llp_beam_reorder", C.byref(r))
     return states if out is None else out
 
 
 def _apart(seen, sources):
     """Refuses states that share bytes: a call moves them all at once."""
-    seen = sorted(seen)
+    seen.sort(key=lambda t: t[:2])
     for i, a in enumerate(seen):
         for b in seen[i + 1:]:
             if b[0] >= a[1]:
@@ -432,14 +453,14 @@ def _apart(seen, sources):
 
 
 def _interleaved(a, b):
-    """Whether two states of one shape, the second no lower in memory, lie between each other's pieces,
+    """Whether two states of one layout, the second no lower in memory, lie between each other's pieces,
     as the keys and values of a cache [rows, 2, ...] do."""
-    rows, rs, outer, os, inner = a[3:]
-    if b[3:] != a[3:]:
+    c = a[3]
+    if b[3] is not c:
         return False
     shift = b[0] - a[0]
-    levels, extent = [], inner   # stride, steps, and the bytes of what lies within one step
-    for s, n in sorted((s, n) for s, n in ((rs, rows), (os, outer)) if n > 1):
+    levels, extent = [], c.inner   # stride, steps, and the bytes of what lies within one step
+    for s, n in sorted((s, n) for s, n in ((c.dr, c.rows), (c.do, c.outer)) if n > 1):
         levels.append((s, n, extent))
         extent += (n - 1) * s
     if shift >= extent:
