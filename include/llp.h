@@ -608,7 +608,7 @@ typedef struct {
 /* Candidates of each row of logits: the `num` largest real columns (1 <= num <= LLP_MAX_BEAMS), by
  * logit descending and token ascending, and what normalises the row.
  *   logits   as in llp_logits_request; num_rows rows, below 2^22.
- *   vocab    as in llp_request; local_size at most 2^23 - 256 and padded_vocab < 2^40 (else
+ *   vocab    as in llp_request; local_size at most 2^21 and padded_vocab < 2^40 (else
  *            LLP_ERR_UNSUPPORTED).
  *   temperature  in [2^-64, 2^64]; z = x * fl32(1/temperature).
  * -inf logits are no candidates. A row that holds a NaN or +inf among its real columns sets
@@ -817,11 +817,8 @@ LLP_API llp_status llp_linear_fp8(const llp_fp8_linear_request* req, void* strea
 LLP_API llp_status llp_dweight_fp8(const llp_fp8_linear_request* req, void* stream);
 
 /* One step of a beam search (see llp_beam_request, llp_beam_select_request and
- * llp_beam_reorder_request). llp_beam_candidates takes a workspace (device memory, 256-byte aligned),
- * the others none. */
-LLP_API llp_status llp_beam_workspace_bytes(const llp_beam_request* req, size_t* bytes);
-LLP_API llp_status llp_beam_candidates(const llp_beam_request* req, const llp_beam_parts* out,
-                                       void* workspace, size_t workspace_bytes, void* stream);
+ * llp_beam_reorder_request). No workspace. */
+LLP_API llp_status llp_beam_candidates(const llp_beam_request* req, const llp_beam_parts* out, void* stream);
 LLP_API llp_status llp_beam_select(const llp_beam_select_request* req, const llp_beam_out* out,
                                    void* stream);
 LLP_API llp_status llp_beam_reorder(const llp_beam_reorder_request* req, void* stream);

@@ -238,9 +238,7 @@ SIGNATURES = {
     "llp_quantize_blocks": (C.c_int, [C.POINTER(llp_fp8_quant_request), vp]),
     "llp_linear_fp8": (C.c_int, [C.POINTER(llp_fp8_linear_request), vp]),
     "llp_dweight_fp8": (C.c_int, [C.POINTER(llp_fp8_linear_request), vp]),
-    "llp_beam_workspace_bytes": (C.c_int, [C.POINTER(llp_beam_request), C.POINTER(C.c_size_t)]),
-    "llp_beam_candidates": (C.c_int, [C.POINTER(llp_beam_request), C.POINTER(llp_beam_parts), vp,
-                                      C.c_size_t, vp]),
+    "llp_beam_candidates": (C.c_int, [C.POINTER(llp_beam_request), C.POINTER(llp_beam_parts), vp]),
     "llp_beam_select": (C.c_int, [C.POINTER(llp_beam_select_request), C.POINTER(llp_beam_out),
                                   vp]),
     "llp_beam_reorder": (C.c_int, [C.POINTER(llp_beam_reorder_request), vp]),

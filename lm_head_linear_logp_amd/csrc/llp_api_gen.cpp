@@ -73,6 +73,9 @@ llp_status run_linear(const llp_fp8_linear_request* req, bool grad, void* stream
   const size_t es = size_of(p.out_dtype);
   LLP_CHECK(p.out_stride >= ocols && p.out_stride < kMaxStride, LLP_ERR_INVALID_ARGUMENT,
             "out_stride %lld must be >= %lld", (long long)p.out_stride, (long long)ocols);
+  // 32 rows of an fp32 gradient are addressed with 32-bit byte offsets.
+  LLP_CHECK(!grad || p.out_dtype != LLP_DTYPE_F32 || p.out_stride < (int64_t(1) << 24), LLP_ERR_UNSUPPORTED,
+            "an fp32 gradient's out_stride must be < 2^24");
   if (orows > 0 && ocols > 0) {
     LLP_CHECK(p.out != nullptr, LLP_ERR_INVALID_ARGUMENT, "out is NULL");
     LLP_CHECK(aligned(p.out, es), LLP_ERR_INVALID_ARGUMENT, "out not aligned to its element type");
@@ -119,8 +122,9 @@ llp_status check_beam(const llp_beam_request* req, float* c1) {
   if (st != LLP_OK) return st;
   LLP_CHECK(req->num_rows >= 0 && req->num_rows < (int64_t(1) << 22), LLP_ERR_INVALID_ARGUMENT,
             "num_rows %lld outside [0, 2^22)", (long long)req->num_rows);
-  LLP_CHECK(req->vocab.local_size <= kMaxRows, LLP_ERR_UNSUPPORTED,
-            "local_size %lld exceeds 2^23 - 256", (long long)req->vocab.local_size);
+  // A workgroup keeps 36 bytes for every 2048 columns.
+  LLP_CHECK(req->vocab.local_size <= (int64_t(1) << 21), LLP_ERR_UNSUPPORTED,
+            "local_size %lld exceeds 2^21", (long long)req->vocab.local_size);
   LLP_CHECK(req->vocab.padded_vocab < kMaxStride, LLP_ERR_UNSUPPORTED, "padded_vocab must be < 2^40");
   LLP_CHECK(req->num >= 1 && req->num <= LLP_MAX_BEAMS, LLP_ERR_INVALID_ARGUMENT,
             "num %d outside [1, %d]", req->num, LLP_MAX_BEAMS);
@@ -136,23 +140,6 @@ llp_status check_beam(const llp_beam_request* req, float* c1) {
               "rows of logits must be 16-byte aligned");
   }
   return check_beam_temperature(req->temperature, c1);
-}
-
-struct BeamWs {
-  size_t keys, pm, ps, total;
-  int32_t splits, blocks;
-};
-
-BeamWs beam_ws(const llp_beam_request& r) {
-  BeamWs w{};
-  w.blocks = (int32_t)(round_up(local_real(r.vocab), BEAM_BLOCK) / BEAM_BLOCK);
-  w.splits = w.blocks > 0 ? beam_splits(r.num_rows, w.blocks) : 0;
-  Regions g;
-  w.keys = g.take((size_t)r.num_rows * w.splits * r.num * 8);
-  w.pm = g.take((size_t)r.num_rows * w.blocks * 4);
-  w.ps = g.take((size_t)r.num_rows * w.blocks * 4);
-  w.total = g.off;
-  return w;
 }
 
 // Whether `rows` x `outer` pieces of `inner` bytes at these strides are apart: the smaller stride
@@ -219,17 +206,7 @@ LLP_API llp_status llp_dweight_fp8(const llp_fp8_linear_request* req, void* stre
   return run_linear(req, true, stream);
 }
 
-LLP_API llp_status llp_beam_workspace_bytes(const llp_beam_request* req, size_t* bytes) {
-  float c1;
-  llp_status st = check_beam(req, &c1);
-  if (st != LLP_OK) return st;
-  LLP_CHECK(bytes != nullptr, LLP_ERR_INVALID_ARGUMENT, "bytes is NULL");
-  *bytes = beam_ws(*req).total;
-  return LLP_OK;
-}
-
-LLP_API llp_status llp_beam_candidates(const llp_beam_request* req, const llp_beam_parts* out,
-                                       void* workspace, size_t workspace_bytes, void* stream) {
+LLP_API llp_status llp_beam_candidates(const llp_beam_request* req, const llp_beam_parts* out, void* stream) {
   float c1;
   llp_status st = check_beam(req, &c1);
   if (st != LLP_OK) return st;
@@ -237,11 +214,6 @@ LLP_API llp_status llp_beam_candidates(const llp_beam_request* req, const llp_be
   if (req->num_rows > 0)
     LLP_CHECK(out->value && out->token && out->max && out->sum, LLP_ERR_INVALID_ARGUMENT,
               "out.value, out.token, out.max and out.sum are required");
-  const BeamWs w = beam_ws(*req);
-  LLP_CHECK(workspace_bytes >= w.total, LLP_ERR_INVALID_ARGUMENT,
-            "workspace of %zu bytes is smaller than the %zu required", workspace_bytes, w.total);
-  LLP_CHECK(workspace != nullptr && aligned(workspace, 256), LLP_ERR_INVALID_ARGUMENT,
-            "workspace must be non-NULL and 256-byte aligned");
   st = check_device();
   if (st != LLP_OK) return st;
   BeamArgs a{};
@@ -252,12 +224,8 @@ LLP_API llp_status llp_beam_candidates(const llp_beam_request* req, const llp_be
   a.n_real = local_real(req->vocab);
   a.offset = req->vocab.offset;
   a.num = req->num;
-  a.splits = w.splits;
-  a.blocks = w.blocks;
+  a.blocks = (int32_t)(round_up(a.n_real, BEAM_BLOCK) / BEAM_BLOCK);
   a.c1 = c1;
-  a.keys = at<uint64_t>(workspace, w.keys);
-  a.pm = at<float>(workspace, w.pm);
-  a.ps = at<float>(workspace, w.ps);
   a.value = out->value;
   a.token = out->token;
   a.max = out->max;

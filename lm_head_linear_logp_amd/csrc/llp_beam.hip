@@ -196,38 +196,40 @@ struct Best {
 };
 
 // ------------------------------------------------------------------------------------
-// Candidates. A wave walks blocks of 2048 columns of one row, 32 values a lane in registers: the
-// block's maximum and its sum of exponentials go to the workspace (so the row's normaliser does not
-// depend on how many waves share it), and the values above the wave's bar into its best keys. The
-// first block's bar is the num-th largest of the 64 lanes' maxima, each of which is a value of
-// its own. Bound by memory: one read of the logits, past the caches (512 rows of 151669 fp32 columns, 311 MB:
-// 62 us, 5.0 TB/s; 69 through them; twice or four times the waves, or the next block loaded under the
-// present one's work, no faster).
+// Candidates: a workgroup a row. Each wave takes blocks of 2048 columns, 32 values a lane in registers,
+// and leaves the sum of the block's exponentials and the largest value of each 16 lanes' 512, a piece, in
+// LDS (so the row's normaliser does not depend on how many waves share it). The num-th largest of some
+// pieces' maxima is a bar that num values reach: only the pieces whose maximum reaches it, few more
+// than num, are read again for the values that do, and sorted.
+//
+// Bound by memory with many rows: one read of the logits, past the caches. With few, a row is one compute
+// unit's, and its exponentials bound it; several workgroups a row would need a second launch to join
+// them, whose cost on the host is more than they gain.
 //
 // exp((x - max) c) as 2^t, t = (x - max) c log2 e with the constant in two parts: its rounding would shift
 // every term alike, by 2e-7 for the bulk of a row; t's own roundings, and the exponential's, differ in
 // sign from term to term, so that a sum over thousands of columns is off by about 1e-8 and two beams'
 // totals closer than that are rare.
 // ------------------------------------------------------------------------------------
-constexpr int BEAM_WAVES = 4;
+constexpr int BEAM_WAVES = 16;   // of a workgroup, at most
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-// The lane's 32 values of the block at c0, -inf past the last column. No load is conditional per lane (each
-// would be waited for by itself: 32 in a row, 20 us): past the last whole 16 bytes the last are
-// loaded again, and the columns behind them, fewer than 16 bytes, come one by one for all lanes.
 template <bool BF16>
 __device__ __forceinline__ float beam_value(const void* row, int64_t c) {
   return BF16 ? bf16_to_f32(static_cast<const uint16_t*>(row)[c]) : static_cast<const float*>(row)[c];
 }
+// 32 values of a lane, a block's 16 bytes at c0, c0 + 1024, ..: -inf past the last column. No load is
+// conditional per lane (each would be waited for by itself: 32 in a row, 20 us): past the last whole 16
+// bytes the last are loaded again, and the columns behind them, fewer than 16 bytes, come one by
+// one for all lanes.
 template <bool BF16>
 __device__ __forceinline__ void beam_load(const void* row, int64_t c0, int64_t n_real, float (&x)[32]) {
   constexpr int V = BF16 ? 8 : 4;   // values per 16 bytes
-  const int lane = threadIdx.x & 63;
   const int64_t whole = n_real / V * V;
   if (whole > 0) {
 #pragma unroll
     for (int i = 0; i < 32 / V; ++i) {
-      const int64_t c = c0 + i * 64 * V + lane * V;
+      const int64_t c = c0 + i * 64 * V;
       const int64_t at = c < whole ? c : whole - V;
       if constexpr (BF16) {
         const u32x4 u = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(row) + at));
@@ -243,13 +245,13 @@ __device__ __forceinline__ void beam_load(const void* row, int64_t c0, int64_t n
       }
     }
   }
-  if (c0 + BEAM_BLOCK > whole) {
+  if (__builtin_amdgcn_ballot_w64(c0 + (32 / V - 1) * 64 * V >= whole) != 0) {
     float rest[V];
 #pragma unroll
     for (int k = 0; k < V; ++k) rest[k] = beam_value<BF16>(row, whole + k < n_real ? whole + k : n_real - 1);
 #pragma unroll
     for (int i = 0; i < 32 / V; ++i) {
-      const int64_t c = c0 + i * 64 * V + lane * V;
+      const int64_t c = c0 + i * 64 * V;
 #pragma unroll
       for (int k = 0; k < V; ++k)
         if (c >= whole) x[i * V + k] = c + k < n_real ? rest[k] : -INFINITY;
@@ -257,119 +259,133 @@ __device__ __forceinline__ void beam_load(const void* row, int64_t c0, int64_t n
   }
 }
 
+// LDS of a row: keys that wait for each wave, each wave's best, the pieces' largest values, the blocks' sums
+// and the pieces to read again.
+static size_t beam_lds(int waves, int blocks) { return (size_t)waves * 192 * sizeof(Key64) + (size_t)blocks * 36; }
+
 template <bool BF16>
 __global__ __launch_bounds__(64 * BEAM_WAVES) void k_beam_rows(BeamArgs a) {
-  __shared__ Key64 room[BEAM_WAVES][128];
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  __shared__ float shared_bar;
+  __shared__ int shared_bad, shared_count;
   constexpr int V = BF16 ? 8 : 4;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t w = (int64_t)blockIdx.x * BEAM_WAVES + wave;
-  const int64_t r = w / a.splits;
-  const int sp = (int)(w % a.splits);
-  if (r >= a.rows) return;
+  const int waves = blockDim.x >> 6, pieces = 4 * a.blocks;
+  Key64* const room = reinterpret_cast<Key64*>(smem);
+  Key64* const lists = room + waves * 128;
+  float* const tops = reinterpret_cast<float*>(lists + waves * 64);
+  float* const sums = tops + pieces;
+  int* const reread = reinterpret_cast<int*>(sums + a.blocks);
+  const int64_t r = blockIdx.x;
   const char* const row = static_cast<const char*>(a.logits) + r * a.ld * (BF16 ? 2 : 4);
-  const int b0 = (int)((int64_t)a.blocks * sp / a.splits), b1 = (int)((int64_t)a.blocks * (sp + 1) / a.splits);
   const double cl = (double)a.c1 * 1.4426950408889634074;
-  const float ch = (float)cl, clo = (float)(cl - (double)ch), low = -200.f / ch;
-  Best<Key64> best;
-  best.init(room[wave]);
-  for (int b = b0; b < b1; ++b) {
-    const int64_t c0 = (int64_t)b * BEAM_BLOCK;
+  // The high part is the smaller one, so that the low part is above 0 and -inf times it is -inf.
+  const float near = (float)cl;
+  const float ch = (double)near < cl ? near : __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, near) - 1);
+  const float clo = (float)(cl - (double)ch);
+  for (int b = wave; b < a.blocks; b += waves) {
     float x[32];
-    beam_load<BF16>(row, c0, a.n_real, x);
-    float part[4];      // the largest of each 8 values
-    bool fine = true;   // no NaN
+    beam_load<BF16>(row, (int64_t)b * BEAM_BLOCK + lane * V, a.n_real, x);
+    float top = -INFINITY;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      part[q] = -INFINITY;
+    for (int e = 0; e < 32; ++e) top = fmaxf(top, x[e]);
+    top = fmaxf(top, across<1>(top));
+    top = fmaxf(top, across<2>(top));
+    top = fmaxf(top, across<4>(top));
+    top = fmaxf(top, across<8>(top));
+    if ((lane & 15) == 0) tops[4 * b + (lane >> 4)] = top;
+    top = fmaxf(top, across<16>(top));
+    top = fmaxf(top, across<32>(top));
+    // A NaN, which the maxima pass over, or +inf makes the sum NaN.
+    const float base = top > -INFINITY ? top : 0.f;
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int e = 8 * q; e < 8 * q + 8; e += 2) {
-        fine &= !__builtin_isunordered(x[e], x[e + 1]);
-        part[q] = fmaxf(part[q], fmaxf(x[e], x[e + 1]));
-      }
+    for (int e = 0; e < 32; ++e) {
+      const float d = x[e] - base;
+      s[e & 3] += __builtin_amdgcn_exp2f(fmaf(d, ch, d * clo));
     }
-    const float mine = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
-    const float top = wave_max(mine);
-    const bool bad = __builtin_amdgcn_ballot_w64(!fine) != 0 || top == INFINITY;
-    float s = 0.f;
-    if (!bad && top > -INFINITY) {
-#pragma unroll
-      for (int e = 0; e < 32; ++e) {
-        const float d = fmaxf(x[e] - top, low);   // 2^-200 for a column that is none, or far below
-        s += __builtin_amdgcn_exp2f(fmaf(d, ch, d * clo));
-      }
-      s = wave_sum(s);
+    const float sum = wave_sum((s[0] + s[1]) + (s[2] + s[3]));
+    if (lane == 0) sums[b] = sum;
+  }
+  __syncthreads();
+  if (wave == 0) {
+    float most = -INFINITY;
+    for (int i = lane; i < pieces; i += 64) most = fmaxf(most, tops[i]);
+    const Key32 m = sort64(Key32{most > -INFINITY ? ordered(most) : 0});
+    const uint32_t at = (uint32_t)__shfl((int)m.k, a.num - 1);
+    const float bar = at != 0 ? unordered(at) : -INFINITY;
+    int n = 0;
+    for (int i = 0; i < pieces; i += 64) {
+      const float top = i + lane < pieces ? tops[i + lane] : -INFINITY;
+      const bool in = top >= bar && top > -INFINITY;
+      const uint64_t all = __builtin_amdgcn_ballot_w64(in);
+      if (in) reread[n + __popcll(all & ((1ull << lane) - 1))] = i + lane;
+      n += __popcll(all);
     }
     if (lane == 0) {
-      a.pm[r * a.blocks + b] = top;
-      a.ps[r * a.blocks + b] = bad ? -1.f : s;
+      shared_bar = bar;
+      shared_count = n;
     }
-    if (bad) continue;   // the row has no candidates
-    if (b == b0) {
-      const Key32 m = sort64(Key32{mine > -INFINITY ? ordered(mine) : 0});
-      const uint32_t at = __shfl((int)m.k, a.num - 1);
-      if (at != 0) best.bar = Key64{((uint64_t)at << 32) - 1};
-    }
-    const float bar = best.bar.any() ? unordered((uint32_t)(best.bar.k >> 32)) : -INFINITY;
-    // The bar's value may be one below the smallest that counts: >= and the key decide.
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      if (__builtin_amdgcn_ballot_w64(part[q] >= bar && part[q] > -INFINITY) == 0) continue;
-#pragma unroll
-      for (int e = 8 * q; e < 8 * q + 8; ++e) {
-        const bool may = x[e] >= bar && x[e] > -INFINITY;
-        if (__builtin_amdgcn_ballot_w64(may) == 0) continue;
-        const uint32_t c = (uint32_t)c0 + (e / V) * 64 * V + lane * V + e % V;
-        best.add(Key64{may ? (uint64_t)ordered(x[e]) << 32 | (uint32_t)~c : 0}, a.num);
+  }
+  if (wave == waves - 1) {
+    float M = -INFINITY;
+    bool bad = false;
+    for (int i = lane; i < pieces; i += 64) M = fmaxf(M, tops[i]);
+    for (int i = lane; i < a.blocks; i += 64) bad |= __builtin_isnan(sums[i]);
+    M = wave_max(M);
+    bad = __builtin_amdgcn_ballot_w64(bad) != 0;
+    double S = 0.0;
+    if (!bad && M > -INFINITY) {
+      for (int i = lane; i < a.blocks; i += 64) {
+        const float m = fmaxf(fmaxf(tops[4 * i], tops[4 * i + 1]), fmaxf(tops[4 * i + 2], tops[4 * i + 3]));
+        if (m > -INFINITY) S += (double)sums[i] * exp(((double)m - (double)M) * (double)a.c1);
       }
+      S = wave_sum(S);
+    }
+    if (lane == 0) {
+      shared_bad = bad;
+      a.max[r] = bad ? -INFINITY : M;
+      a.sum[r] = bad ? -1.0 : S;
+      if (bad && a.status) atomicOr(a.status, LLP_STATUS_VALUE_NOT_FINITE);
     }
   }
-  best.finish(a.num);
-  if (lane < a.num) a.keys[w * a.num + lane] = best.list.k;
-}
-
-// A row's outputs from its waves' candidates and its blocks' sums: one wave a row.
-__global__ __launch_bounds__(64) void k_beam_join(BeamArgs a) {
-  __shared__ Key64 room[128];
-  const int lane = threadIdx.x;
-  const int64_t r = blockIdx.x;
-  // The candidates first: their loads are the longer chain.
-  const uint64_t* const keys = a.keys + r * a.splits * a.num;
-  const int total = a.splits * a.num;
-  uint64_t head = 0;
-  for (int i = lane; i < a.splits; i += 64) {
-    const uint64_t k = keys[(int64_t)i * a.num];
-    head = k > head ? k : head;
-  }
+  __syncthreads();
+  const float bar = shared_bar;
+  const bool bad = shared_bad != 0;
   Best<Key64> best;
-  best.init(room);
-  // The num-th largest of the lanes' heads is a bar that num keys reach.
-  const Key64 at = sort64(Key64{head}).from(a.num - 1);
-  if (at.any()) best.bar = Key64{at.k - 1};
-  for (int i = 0; i < total; i += 64) best.add(Key64{i + lane < total ? keys[i + lane] : 0}, a.num);
-  best.finish(a.num);
-  float M = -INFINITY;
-  bool bad = false;
-  for (int i = lane; i < a.blocks; i += 64) {
-    M = fmaxf(M, a.pm[r * a.blocks + i]);
-    bad |= a.ps[r * a.blocks + i] < 0.f;
-  }
-  M = wave_max(M);
-  bad = __builtin_amdgcn_ballot_w64(bad) != 0;
-  double S = 0.0;
-  if (M > -INFINITY && !bad) {
-    for (int i = lane; i < a.blocks; i += 64) {
-      const float m = a.pm[r * a.blocks + i];
-      if (m > -INFINITY) S += (double)a.ps[r * a.blocks + i] * exp(((double)m - (double)M) * (double)a.c1);
+  best.init(room + wave * 128);
+  if (bar > -INFINITY) best.bar = Key64{((uint64_t)ordered(bar) << 32) - 1};
+  // Four pieces at a time, 16 lanes each; lanes without one repeat the first.
+  const int count = bad ? 0 : shared_count;
+  for (int i = wave * 4; i < count; i += waves * 4) {
+    const int mine = i + (lane >> 4);
+    const bool has = mine < count;
+    const int q = reread[has ? mine : i];
+    const int64_t c0 = (int64_t)(q >> 2) * BEAM_BLOCK + ((q & 3) * 16 + (lane & 15)) * V;
+    float x[32];
+    beam_load<BF16>(row, c0, a.n_real, x);
+#pragma unroll
+    for (int e = 0; e < 32; ++e) {
+      const bool may = has && x[e] >= bar && x[e] > -INFINITY;
+      if (__builtin_amdgcn_ballot_w64(may) == 0) continue;
+      const uint32_t c = (uint32_t)c0 + (e / V) * 64 * V + e % V;
+      best.add(Key64{may ? (uint64_t)ordered(x[e]) << 32 | (uint32_t)~c : 0}, a.num);
     }
-    S = wave_sum(S);
   }
-  if (lane == 0) {
-    a.max[r] = bad ? -INFINITY : M;
-    a.sum[r] = bad ? -1.0 : S;
-    if (bad && a.status) atomicOr(a.status, LLP_STATUS_VALUE_NOT_FINITE);
+  best.finish(a.num);
+  // Half of the waves that read pieces hand their best to the others until one wave holds the row's.
+  const int active = (count + 3) / 4 < waves ? (count + 3) / 4 : waves;
+  lists[wave * 64 + lane] = best.list;
+  __syncthreads();
+  for (int step = 1; step < active; step *= 2) {
+    if (wave % (2 * step) == 0 && wave + step < active) {
+      best.list = merge64(best.list, lists[(wave + step) * 64 + lane]);
+      lists[wave * 64 + lane] = best.list;
+    }
+    __syncthreads();
   }
-  if (lane < a.num) {
-    const bool in = best.list.any() && !bad;
+  if (wave == 0 && lane < a.num) {
+    const bool in = best.list.any();
     a.value[r * a.num + lane] = in ? unordered((uint32_t)(best.list.k >> 32)) : -INFINITY;
     a.token[r * a.num + lane] = in ? a.offset + (int64_t)(uint32_t)~(uint32_t)best.list.k : -1;
   }
@@ -377,14 +393,13 @@ __global__ __launch_bounds__(64) void k_beam_join(BeamArgs a) {
 
 hipError_t launch_beam_candidates(const BeamArgs& a, hipStream_t s) {
   if (a.rows <= 0) return hipSuccess;
-  if (a.blocks > 0) {
-    const dim3 grid((unsigned)((a.rows * a.splits + BEAM_WAVES - 1) / BEAM_WAVES)), block(64 * BEAM_WAVES);
-    if (a.bf16) hipLaunchKernelGGL((k_beam_rows<true>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((k_beam_rows<false>), grid, block, 0, s, a);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  hipLaunchKernelGGL(k_beam_join, dim3((unsigned)a.rows), dim3(64), 0, s, a);
+  // As many waves on a row as leave no compute unit a second round of workgroups (a unit holds 20 waves).
+  int waves = a.rows <= 256 ? 16 : a.rows <= 512 ? 8 : 4;
+  if (waves > a.blocks) waves = a.blocks > 0 ? a.blocks : 1;
+  const dim3 grid((unsigned)a.rows), block(64 * waves);
+  const size_t lds = beam_lds(waves, a.blocks);
+  if (a.bf16) hipLaunchKernelGGL((k_beam_rows<true>), grid, block, lds, s, a);
+  else hipLaunchKernelGGL((k_beam_rows<false>), grid, block, lds, s, a);
   return hipGetLastError();
 }
 
@@ -466,7 +481,7 @@ __global__ __launch_bounds__(64) void k_beam_select(BeamSelectArgs a) {
     const int k = item(i < total ? i : 0).k;
     if (i < total && kind[k] == 1) {
       const double t = score[k] + (((double)v - (double)top[k]) * c - norm[k]);
-      if (id >= 0 && t > -INFINITY) x = Key128{ordered64(t), ~((uint64_t)k << BEAM_AT | (uint64_t)id)};
+      if ((uint64_t)id >> BEAM_AT == 0 && t > -INFINITY) x = Key128{ordered64(t), ~((uint64_t)k << BEAM_AT | (uint64_t)id)};
     }
     best.add(x, a.num_out);
   };

@@ -452,24 +452,14 @@ struct Linear8Args {
 
 // Beam search (llp_beam.hip). A wave takes BEAM_BLOCK columns of a row at a time.
 constexpr int BEAM_BLOCK = 2048;
-// Waves per row: enough for four on every SIMD of 256 compute units, at most one per block.
-inline int beam_splits(int64_t rows, int32_t blocks) {
-  int64_t n = rows > 0 ? 4096 / rows : 1;
-  if (n > blocks) n = blocks;
-  return n < 1 ? 1 : (int)n;
-}
 struct BeamArgs {
   const void* logits;
   int32_t bf16;
   int64_t ld;
   int64_t rows, n_real, offset;
   int32_t num;
-  int32_t splits;        // waves per row
   int32_t blocks;        // blocks of BEAM_BLOCK columns per row
   float c1;
-  uint64_t* keys;        // [rows][splits][num] sorted candidates of each wave
-  float* pm;             // [rows][blocks] largest logit and sum of each block
-  float* ps;
   float* value;
   int64_t* token;
   float* max;

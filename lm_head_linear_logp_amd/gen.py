@@ -11,9 +11,8 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _capi as A
-from . import _need, _ptr, _status, _vec, _vocab
-from .ops import (_DTYPE, _F32, _I32, _I64, _U8, _at, _call, _check_space, _opt, _ready, _space,
-                  _tensor)
+from . import _need, _ptr, _status, _vocab
+from .ops import _DTYPE, _F32, _I32, _I64, _U8, _at, _call, _ready, _tensor
 
 _F8, _F64 = torch.float8_e4m3fn, torch.float64
 _BLOCK = A.LLP_FP8_BLOCK
@@ -33,8 +32,10 @@ def _rows(t, name):
     _tensor(t, name)
     if t.dtype not in _DTYPE:
         raise TypeError(f"{name} must be a bf16 or fp32 tensor, got {t.dtype}")
-    _need(t, name, t.dtype, 2, t.device)
-    return t.device
+    dev = t.device
+    if not (t.dim() == 2 and t.is_contiguous()):
+        _need(t, name, t.dtype, 2, dev)
+    return dev
 
 
 # ---- Products in 8-bit floating point ----------------------------------------------------------
@@ -75,11 +76,12 @@ def quantize_blocks(x: torch.Tensor, *, rows: int = 1, transpose: bool = False,
         lds = _scale_stride(scale, "out[1]", M, G * _BLOCK, rows != 1, dev)
     _ready(dev)
     if out is None:
-        q = torch.empty((M, G * _BLOCK), dtype=_F8, device=dev)
+        q = torch.empty(M, G * _BLOCK, dtype=_F8, device=dev)
         if rows == 1:
-            scale, lds = torch.empty((G, M), dtype=_F32, device=dev).t(), max(M, 1)
+            lds = max(M, 1)
+            scale = torch.empty_strided((M, G), (1, lds), dtype=_F32, device=dev)
         else:
-            scale, lds = torch.empty((_blocks(M), G), dtype=_F32, device=dev), max(G, 1)
+            scale, lds = torch.empty(_blocks(M), G, dtype=_F32, device=dev), max(G, 1)
     req = A.llp_fp8_quant_request(x.data_ptr(), _DTYPE[x.dtype], rows, _stride(x, R, Cc), R, Cc,
                                   1 if transpose else 0, 0, q.data_ptr(), _stride(q, M, G * _BLOCK),
                                   scale.data_ptr(), lds)
@@ -129,9 +131,7 @@ def linear_fp8(x: torch.Tensor, x_scale: torch.Tensor, weight: torch.Tensor,
     _ready(dev)
     if out is None:
         width = V + -V % (4 if out_dtype == _F32 else 8)
-        out = torch.empty((T, width), dtype=out_dtype, device=dev)
-        if width != V:
-            out = out[:, :V]
+        out = torch.empty_strided((T, V), (width, 1), dtype=out_dtype, device=dev)
     r.out, r.out_dtype, r.out_stride = out.data_ptr(), _DTYPE[out_dtype], _stride(out, T, V)
     _call(dev, "llp_linear_fp8", C.byref(r))
     return out
@@ -157,7 +157,7 @@ def dweight_fp8(dout_t: torch.Tensor, dout_scale: torch.Tensor, x_t: torch.Tenso
     r.flags = A.LLP_FLAG_OVERWRITE_GRADS if overwrite else 0
     _ready(dev)
     if dweight is None:
-        dweight = torch.empty((V, H), dtype=out_dtype, device=dev)
+        dweight = torch.empty(V, H, dtype=out_dtype, device=dev)
     r.out, r.out_dtype, r.out_stride = dweight.data_ptr(), _DTYPE[out_dtype], _stride(dweight, V, H)
     _call(dev, "llp_dweight_fp8", C.byref(r))
     return dweight
@@ -215,13 +215,23 @@ _PARTS = (("value", _F32), ("token", _I64), ("max", _F32), ("sum", _F64))
 
 
 def _check_parts(p, name, rows, num, dev):
+    v, i, m, s = p["value"], p["token"], p["max"], p["sum"]
+    if (type(v) is type(i) is type(m) is type(s) is torch.Tensor
+            and v.dtype is _F32 and i.dtype is _I64 and m.dtype is _F32 and s.dtype is _F64
+            and v.shape == i.shape == (rows, num) and m.shape == s.shape == (rows,)
+            and v.device == i.device == m.device == s.device == dev and v.is_contiguous()
+            and i.is_contiguous() and m.is_contiguous() and s.is_contiguous()):
+        return
     for k, dt in _PARTS:
-        t = p[k]
         shape = (rows, num) if k in ("value", "token") else (rows,)
-        if not (type(t) is torch.Tensor and t.dtype is dt and t.shape == shape and t.device == dev
-                and t.is_contiguous()):
-            _need(t, f"{name}['{k}']", dt, len(shape), dev, shape)
+        _need(p[k], f"{name}['{k}']", dt, len(shape), dev, shape)
+        if not p[k].is_contiguous():
             raise ValueError(f"{name}['{k}'] must be contiguous")
+
+
+def _part_pointers(p):
+    return A.llp_beam_parts(p["value"].data_ptr(), p["token"].data_ptr(), p["max"].data_ptr(),
+                            p["sum"].data_ptr())
 
 
 def _num(n, name):
@@ -233,7 +243,7 @@ def _num(n, name):
 def beam_candidates(logits: torch.Tensor, num: int, *, temperature: float = 1.0, offset: int = 0,
                     real_vocab: Optional[int] = None, padded_vocab: Optional[int] = None,
                     rank: int = 0, world: int = 1, status: Optional[torch.Tensor] = None,
-                    workspace: Optional[torch.Tensor] = None, out: Optional[dict] = None) -> dict:
+                    out: Optional[dict] = None) -> dict:
     """llp_beam_candidates on one vocabulary shard: the `num` most likely tokens of each row of
     logits [rows, local_size] (bf16 or fp32, rows 16-byte aligned) and what normalises the row.
     Returns value (logits) and token (global ids) [rows, num], most likely first, ties to the lowest
@@ -251,16 +261,13 @@ def beam_candidates(logits: torch.Tensor, num: int, *, temperature: float = 1.0,
     r.status_word = _ptr(status)
     if out is not None:
         _check_parts(out, "out", R, num, dev)
-    _check_space(workspace, dev)
     _ready(dev)
     if out is None:
-        out = dict(value=torch.empty((R, num), dtype=_F32, device=dev),
-                   token=torch.empty((R, num), dtype=_I64, device=dev),
+        out = dict(value=torch.empty(R, num, dtype=_F32, device=dev),
+                   token=torch.empty(R, num, dtype=_I64, device=dev),
                    max=torch.empty(R, dtype=_F32, device=dev),
                    sum=torch.empty(R, dtype=_F64, device=dev))
-    o = A.llp_beam_parts(*(out[k].data_ptr() for k, _ in _PARTS))
-    ws, size, _keep = _space("llp_beam_workspace_bytes", r, dev, workspace)
-    _call(dev, "llp_beam_candidates", C.byref(r), C.byref(o), ws, size)
+    _call(dev, "llp_beam_candidates", C.byref(r), C.byref(_part_pointers(out)))
     return out
 
 
@@ -292,7 +299,7 @@ def beam_select(parts: Sequence[dict], scores: torch.Tensor, num: Optional[int] 
     arr = (A.llp_beam_parts * world)()
     for i, p in enumerate(parts):
         _check_parts(p, f"parts[{i}]", B * K, each[1], dev)
-        arr[i] = A.llp_beam_parts(*(p[k].data_ptr() for k, _ in _PARTS))
+        arr[i] = _part_pointers(p)
     r = A.llp_beam_select_request()
     r.world, r.num, r.parts = world, _num(int(each[1]), "candidates a row"), arr
     r.num_seqs, r.num_beams, r.num_out = B, K, num
@@ -314,9 +321,9 @@ def beam_select(parts: Sequence[dict], scores: torch.Tensor, num: Optional[int] 
                 raise ValueError(f"out['{k}'] must be contiguous")
     _ready(dev)
     if out is None:
-        out = dict(token=torch.empty((B, num), dtype=_I64, device=dev),
-                   parent=torch.empty((B, num), dtype=_I32, device=dev),
-                   score=torch.empty((B, num), dtype=_F32, device=dev))
+        out = dict(token=torch.empty(B, num, dtype=_I64, device=dev),
+                   parent=torch.empty(B, num, dtype=_I32, device=dev),
+                   score=torch.empty(B, num, dtype=_F32, device=dev))
     o = A.llp_beam_out(out["token"].data_ptr(), out["parent"].data_ptr(), out["score"].data_ptr())
     _call(dev, "llp_beam_select", C.byref(r), C.byref(o))
     return out

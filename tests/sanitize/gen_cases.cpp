@@ -73,11 +73,9 @@ void candidates(int64_t R, int64_t local, int64_t real, int num, int32_t dt) {
   r.logits = n > 0 ? mem(span(R, r.logits_stride, n) * (dt == LLP_DTYPE_F32 ? 4 : 2)) : nullptr;
   r.status_word = arr<int32_t>(1);
   llp_beam_parts o = {arr<float>(R * num), arr<int64_t>(R * num), arr<float>(R), arr<double>(R)};
-  size_t need = 0;
-  check("beam workspace", llp_beam_workspace_bytes(&r, &need), LLP_OK);
-  void* ws = mem((int64_t)need);
-  check("candidates", llp_beam_candidates(&r, &o, ws, need, nullptr), LLP_OK);
-  check("candidates small", llp_beam_candidates(&r, &o, ws, need - 1, nullptr), LLP_ERR_INVALID_ARGUMENT);
+  check("candidates", llp_beam_candidates(&r, &o, nullptr), LLP_OK);
+  r.num = LLP_MAX_BEAMS + 1;
+  check("candidates num", llp_beam_candidates(&r, &o, nullptr), LLP_ERR_INVALID_ARGUMENT);
   done();
 }
 

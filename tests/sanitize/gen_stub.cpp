@@ -55,9 +55,6 @@ hipError_t launch_linear8(const Linear8Args& a, hipStream_t) {
 hipError_t launch_beam_candidates(const BeamArgs& a, hipStream_t) {
   ++g_gen;
   if (a.blocks > 0) rows(a.logits, a.rows, a.ld, a.n_real, a.bf16 ? 2 : 4);
-  extent(a.keys, a.rows * a.splits * a.num);
-  extent(a.pm, a.rows * a.blocks);
-  extent(a.ps, a.rows * a.blocks);
   extent(a.value, a.rows * a.num);
   extent(a.token, a.rows * a.num);
   extent(a.max, a.rows);

@@ -55,7 +55,7 @@ def linear(grad=False, **over):
     return getattr(A.load(), "llp_dweight_fp8" if grad else "llp_linear_fp8")(C.byref(r), None)
 
 
-def candidates(ws=1 << 30, wsp=FAKE, out=None, **over):
+def candidates(out=None, **over):
     r = A.llp_beam_request()
     r.logits, r.logits_dtype, r.num, r.logits_stride, r.num_rows, r.temperature = FAKE, A.LLP_DTYPE_F32, 8, 1000, 12, 0.7
     r.vocab.local_size = r.vocab.real_vocab = r.vocab.padded_vocab = 1000
@@ -66,7 +66,7 @@ def candidates(ws=1 << 30, wsp=FAKE, out=None, **over):
         else:
             setattr(r, k, v)
     o = A.llp_beam_parts(FAKE, FAKE, FAKE, FAKE) if out is None else out
-    return A.load().llp_beam_candidates(C.byref(r), C.byref(o), wsp, ws, None)
+    return A.load().llp_beam_candidates(C.byref(r), C.byref(o), None)
 
 
 def select(parts=None, out=None, **over):
@@ -117,7 +117,7 @@ def test_linear_refusals(over, want):
 @needs_lib
 @pytest.mark.parametrize("over,want", [
     (dict(bias=FAKE, bias_dtype=A.LLP_DTYPE_F32), INV), (dict(flags=4), INV), (dict(out_stride=299), INV),
-    (dict(out_dtype=A.LLP_DTYPE_BF16), INV), (dict(depth=64), INV)])
+    (dict(out_dtype=A.LLP_DTYPE_BF16), INV), (dict(depth=64), INV), (dict(out_stride=1 << 24), UNS)])
 def test_dweight_refusals(over, want):
     assert linear(True, **over) == want, llp.last_error()
 
@@ -129,8 +129,10 @@ def test_dweight_refusals(over, want):
     (dict(logits=FAKE + 8), INV), (dict(temperature=0.0), INV), (dict(temperature=float("nan")), INV),
     (dict(temperature=1e-39), INV), (dict(offset=-1), INV), (dict(world=0), INV), (dict(real_vocab=0), INV),
     (dict(local_size=1 << 23, padded_vocab=1 << 23, real_vocab=1 << 23, logits_stride=1 << 23), UNS),
-    (dict(local_size=1000, padded_vocab=1 << 41, world=2), UNS), (dict(ws=100), INV), (dict(wsp=None), INV),
-    (dict(wsp=FAKE + 64), INV), (dict(out=A.llp_beam_parts(FAKE, FAKE, FAKE, None)), INV)])
+    (dict(local_size=(1 << 21) + 8, padded_vocab=(1 << 21) + 8, real_vocab=1 << 21, logits_stride=1 << 22), UNS),
+    (dict(local_size=1000, padded_vocab=1 << 41, world=2), UNS),
+    (dict(temperature=2.0 ** -65), INV), (dict(temperature=2.0 ** 65), INV),
+    (dict(out=A.llp_beam_parts(FAKE, FAKE, FAKE, None)), INV)])
 def test_candidates_refusals(over, want):
     assert candidates(**over) == want, llp.last_error()
 
@@ -164,11 +166,9 @@ def test_null_requests():
     lib = A.load()
     assert lib.llp_quantize_blocks(None, None) == INV
     assert lib.llp_linear_fp8(None, None) == INV and lib.llp_dweight_fp8(None, None) == INV
-    assert lib.llp_beam_candidates(None, None, None, 0, None) == INV
+    assert lib.llp_beam_candidates(None, None, None) == INV
     assert lib.llp_beam_select(None, None, None) == INV
     assert lib.llp_beam_reorder(None, None) == INV
-    n = C.c_size_t(0)
-    assert lib.llp_beam_workspace_bytes(None, C.byref(n)) == INV
 
 
 @needs_lib
@@ -270,7 +270,7 @@ def test_candidates_binding():
     reaches_library(lambda: llp.beam_candidates(z, 8, out=part()))
     for bad in (dict(num=0), dict(num=65), dict(num=2.0), dict(out=part(11)), dict(out=part(12, 9)),
                 dict(out=dict(part(), sum=torch.zeros(12))), dict(out=dict(part(), value=torch.zeros(8, 12).t())),
-                dict(status=torch.zeros(1)), dict(workspace=torch.zeros(5)), dict(world=2)):
+                dict(status=torch.zeros(1)), dict(world=2)):
         with pytest.raises(BAD):
             llp.beam_candidates(z, **{"num": 8, **bad})
     for t in (z.half(), z[0], z.t()):
