@@ -279,8 +279,8 @@ hipError_t launch_quant8(const Quant8Args& a, hipStream_t s) {
 // bf16 take it; results in fp32 (FULL) do not: their bytes become bf16 (exact) in front of the bf16
 // MFMA, whose sums keep fp32's bits, at half the matrix rate.
 //
-// Either way every tile runs the same chain for each element, so an element has the same bits
-// whatever the tile and however many rows the call has.
+// Either way every tile runs the same chain for each element, its groups in the same order, so an element
+// has the same bits whatever the tile and however many rows the call has.
 // ------------------------------------------------------------------------------------
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
@@ -326,6 +326,13 @@ __device__ __forceinline__ int swz16(int row) { return (row ^ ((row >> 3) & 1)) 
 
 // A workgroup's tile: TM weight rows x TN rows of x by WM x WN waves, NST stages in flight. A wave's
 // accumulators are MB x NB blocks of S x S: 16 in bf16 results, 32 in fp32 ones.
+// Groups of 128 are taken in turn from group (weight row / 1280) % groups on: workgroups that all read the
+// same columns of rows 4096 bytes apart crowd a few of the memory's channels (1 row of 37984 x 4096 fp8: 40.6
+// us from column 0 on, 33.0 so; of 151936: 121 and 111; 64 rows 133 and 123). 1280: whole tiles of every
+// form, so that a column's order of groups is the same in all of them.
+constexpr int64_t TURN8 = 1280;
+__device__ __forceinline__ int first_group8(int64_t v0, int n) { return n > 0 ? (int)(v0 / TURN8 % n) : 0; }
+
 template <int TM, int TN, int WM, int WN, int NST, bool FULL>
 struct Tile8 {
   static constexpr int S = FULL ? 32 : 16, REGS = S * S / 64;
@@ -397,7 +404,7 @@ __device__ __forceinline__ void store_rows8(const typename T::Acc& acc, const Li
     for (int j = 0; j < T::S; j += STEP) {
       const int row = j + lane / LANES;
       const int64_t t = t0 + ni * T::S + row;
-      if (row >= T::S || t >= a.T) continue;
+      if (lane >= STEP * LANES || row >= T::S || t >= a.T) continue;
       const float* p = st + row * T::OUT_LD + c;
       const float4 lo = *reinterpret_cast<const float4*>(p), hi = *reinterpret_cast<const float4*>(p + 4);
       float y[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
@@ -489,7 +496,7 @@ __device__ __forceinline__ void store_cols_bf16(const typename T::Acc& acc, cons
 #pragma unroll
     for (int j = 0; j < 16; j += STEP) {
       const int64_t v = v0 + mi * 16 + j + lane / LANES;
-      if (v >= a.V) continue;
+      if (lane >= STEP * LANES || j + lane / LANES >= 16 || v >= a.V) continue;
       const float* p = st + (j + lane / LANES) * LD + c;
       const float4 lo = *reinterpret_cast<const float4*>(p), hi = *reinterpret_cast<const float4*>(p + 4);
       uint16_t* o = static_cast<uint16_t*>(a.out) + v * a.ldo + t0 + c;
@@ -555,7 +562,10 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(EU
   const int ts = wn * T::NWV + lane % T::NWV;   // the row whose scale this lane loads
   const uint32_t vs = 4 * (ts < nt ? ts : nt - 1);
   const float* const xs = a.xs + t0;
-  auto issue = [&](int s, int stage) {
+  const int turn = first_group8(v0, n);
+  auto group = [&](int s) { return s + turn < n ? s + turn : s + turn - n; };
+  auto issue = [&](int step, int stage) {
+    const int s = group(step);
     uint8_t* const st = smem + stage * T::STAGE;
 #pragma unroll
     for (int i = 0; i < T::NIA; ++i) dma16(ra, st + (i * T::NW + wave) * 1024, va[i], s * 128);
@@ -585,7 +595,7 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(EU
       const uint8_t* const sa = smem + stage * T::STAGE;
       const uint8_t* const sb = sa + TM * 128;
       const float* const sc = reinterpret_cast<const float*>(sa + T::ROWS * 128 + wave * 256);
-      const float w = scalar8(ws + s);
+      const float w = scalar8(ws + group(s));
       float scale[T::NB];
 #pragma unroll
       for (int ni = 0; ni < T::NB; ++ni) scale[ni] = sc[ni * T::S + lane % T::S] * w;
@@ -646,88 +656,123 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(EU
   store8<T, GRAD, false>(acc, a, v0 + wm * T::MW, t0 + wn * T::NWV, smem, wave);
 }
 
-// The wide form of the bf16 results: 256 x 256 by 8 waves of 128 x 64, two per SIMD. The same chain
-// with every read ahead of its use: 16 weight rows' four MFMAs run while the next 16 are read and the
-// four sums before them are scaled; the next step's first fragments are read under the last rows' MFMAs.
-// From there on the step after next is loaded into the stage that the barrier in front has freed, one load
-// after an MFMA (nine in a row hold up the wave's MFMAs: 5 % slower). LDS: the weight rows' two stages, those of x, the scales'.
+// The wide form of the bf16 results: 32 MB x 64 NB outputs by 8 waves of 16 MB x 16 NB, two per SIMD. The
+// same chain with every read ahead of its use: 16 weight rows' NB MFMAs run while the next 16 are read and
+// the sums before them are scaled; the next step's first fragments are read under the last rows'
+// MFMAs. The barrier in front of those frees the step's stage, into which from there on a later step is
+// loaded, one load after an MFMA (nine in a row hold up the wave's MFMAs: 5 % slower).
+template <int MB_, int NB_>
 struct Wide8 {
-  using T = Tile8<256, 256, 2, 4, 2, false>;
-  static constexpr int B0 = 2 * 256 * 128, S0 = 2 * B0;   // where x's stages and the scales' begin
+  static constexpr int S = 16, REGS = 4, MB = MB_, NB = NB_;
+  static constexpr int MW = 16 * MB, NWV = 16 * NB, TM = 2 * MW, TN = 4 * NWV;
+  static constexpr int STAGE = (TM + TN) * 128, SCALES = TN * 4;
+  static constexpr int FIT = 160 * 1024 / (STAGE + SCALES), NST = FIT < 4 ? FIT : 4;
+  static constexpr int S0 = NST * STAGE;                       // where the scales' stages begin
+  static constexpr int GROUPS = (TM + TN) / 8;                 // of 8 rows, one load each
+  static constexpr int ROWS = (GROUPS + 7) / 8;                // loads of a wave and step,
+  static constexpr int LOADS = ROWS + 1;                       // and the scales'
+  static constexpr int OUT_LD = (MW > NWV ? MW : NWV) + 4;
+  static constexpr int OUT = 8 * S * OUT_LD * 4;
+  static constexpr int LDS = NST * (STAGE + SCALES) > OUT ? NST * (STAGE + SCALES) : OUT;
+  static constexpr bool SPLIT = 128 % MW != 0;                 // a wave's rows may lie in two blocks of 128
+  typedef float Acc[MB][NB][REGS];
+  // Loads behind a row's MFMAs; the first three of a step come behind the last row's.
+  static constexpr int EACH = NB < 3 ? NB : 3;
+  static_assert(NST >= 2 && LDS <= 160 * 1024 && MW <= 128 && LOADS - 3 <= (MB - 1) * EACH && NB >= 2, "shape");
+  static_assert(TURN8 % TM == 0, "one order of groups");
 };
 
-template <bool GRAD>
+template <int MB, int NB, bool GRAD>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_linear8_wide(Linear8Args a) {
-  using T = Wide8::T;
+  using T = Wide8<MB, NB>;
   __shared__ __attribute__((aligned(16))) uint8_t smem[T::LDS];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave & 1, wn = wave >> 1;
   int vt, tb;
   vocab_token_tile(xcd_remap(blockIdx.x, gridDim.x), a.nvt, a.ntb, vt, tb);
-  const int64_t v0 = (int64_t)vt * 256, t0 = (int64_t)tb * 256;
-  const int nv = a.V - v0 < 256 ? (int)(a.V - v0) : 256;
-  const int nt = a.T - t0 < 256 ? (int)(a.T - t0) : 256;
+  const int64_t v0 = (int64_t)vt * T::TM, t0 = (int64_t)tb * T::TN;
+  const int nv = a.V - v0 < T::TM ? (int)(a.V - v0) : T::TM;
+  const int nt = a.T - t0 < T::TN ? (int)(a.T - t0) : T::TN;
   const int n = a.steps;
   const __amdgpu_buffer_rsrc_t ra = rsrc8(a.W + v0 * a.ldw, (uint64_t)(nv - 1) * a.ldw + n * 128);
   const __amdgpu_buffer_rsrc_t rb = rsrc8(a.x + t0 * a.ldx, (uint64_t)(nt - 1) * a.ldx + n * 128);
-  uint32_t va[4], vb[4];
+  // Load k of a step moves 8 rows, the weight's in front of those of x; past the last the last again.
+  // A step's last load is the scales' of 64 rows of x.
+  uint32_t at[T::ROWS];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = 8 * (i * 8 + wave) + (lane >> 3);
-    const uint32_t c = ((lane & 7) ^ swz16(r)) << 4;
-    va[i] = (uint32_t)((r < nv ? r : nv - 1) * a.ldw) + c;
-    vb[i] = (uint32_t)((r < nt ? r : nt - 1) * a.ldx) + c;
+  for (int k = 0; k < T::ROWS; ++k) {
+    const int g = k * 8 + wave < T::GROUPS ? k * 8 + wave : T::GROUPS - 1;
+    const bool is_x = g >= T::TM / 8;
+    const int r = 8 * g + (lane >> 3) - (is_x ? T::TM : 0), last = (is_x ? nt : nv) - 1;
+    at[k] = (uint32_t)((r < last ? r : last) * (is_x ? a.ldx : a.ldw)) + (((lane & 7) ^ swz16(r)) << 4);
   }
-  const int ts = wn * 64 + lane;
+  const int part = wave < NB ? wave : NB - 1;
+  const int ts = part * 64 + lane;
   const uint32_t vs = 4 * (ts < nt ? ts : nt - 1);
   const float* const xs = a.xs + t0;
-  // Load k of a step's nine: the weight rows', those of x, their scales.
+  const int turn = first_group8(v0, n);
   auto load = [&](int k, int s, int stage) {
-    if (k < 4) dma16(ra, smem + stage * 32768 + (k * 8 + wave) * 1024, va[k], s * 128);
-    else if (k < 8) dma16(rb, smem + Wide8::B0 + stage * 32768 + ((k - 4) * 8 + wave) * 1024, vb[k - 4], s * 128);
-    else dma4(rsrc8(xs + s * a.ldxs, (uint64_t)nt * 4), smem + Wide8::S0 + stage * 2048 + wave * 256, vs);
+    if (k < T::ROWS) {
+      const int g = k * 8 + wave < T::GROUPS ? k * 8 + wave : T::GROUPS - 1;
+      uint8_t* const to = smem + stage * T::STAGE + g * 1024;
+      if (8 * (k + 1) <= T::TM / 8 || (8 * k < T::TM / 8 && g < T::TM / 8)) dma16(ra, to, at[k], s * 128);
+      else dma16(rb, to, at[k], s * 128);
+    } else {
+      dma4(rsrc8(xs + s * a.ldxs, (uint64_t)nt * 4), smem + T::S0 + stage * T::SCALES + part * 256, vs);
+    }
   };
-  const float* const ws = a.ws + (v0 + (wm * 128 < nv ? wm * 128 : 0)) / 128 * a.ldws;
+  // Scales of the weight: those of the block of the wave's first row, and of the next (past the last row,
+  // the last block's) from 16-row block `split` on.
+  const int64_t r0 = v0 + wm * T::MW;
+  const int64_t blk = r0 / 128, end = (a.V - 1) / 128;
+  const int split = T::SPLIT ? (int)(128 - r0 % 128) / 16 : MB;
+  const float* const ws = a.ws + (blk < end ? blk : end) * a.ldws;
+  const float* const ws2 = a.ws + (blk + 1 < end ? blk + 1 : end) * a.ldws;
   // The lane's two chunks of its row of 16-row block i: at ad[0] and ad[1] + 2048 i of the weight's, bd of
   // x's.
   int ad[2], bd[2];
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
-    const int r = lane & 15, at = r * 128 + (((2 * (lane >> 4) + q) ^ swz16(r)) << 4);
-    ad[q] = wm * 128 * 128 + at;
-    bd[q] = Wide8::B0 + wn * 64 * 128 + at;
+    const int r = lane & 15, c = r * 128 + (((2 * (lane >> 4) + q) ^ swz16(r)) << 4);
+    ad[q] = wm * T::MW * 128 + c;
+    bd[q] = (T::TM + wn * T::NWV) * 128 + c;
   }
-  auto read = [&](const int (&at)[2], int i) {
-    const i32x4 lo = *reinterpret_cast<const i32x4*>(smem + at[0] + 2048 * i);
-    const i32x4 hi = *reinterpret_cast<const i32x4*>(smem + at[1] + 2048 * i);
+  auto read = [&](const int (&p)[2], int so, int i) {
+    const i32x4 lo = *reinterpret_cast<const i32x4*>(smem + (p[0] + so) + 2048 * i);
+    const i32x4 hi = *reinterpret_cast<const i32x4*>(smem + (p[1] + so) + 2048 * i);
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
   };
   typename T::Acc acc;
   zero8<T>(acc);
   if (n > 0) {
-    f32x4 p[4];
-    float sc[4], last[4];
+    f32x4 p[NB];
+    float sc[NB], last[NB];   // the rows' scales (times the weight's where there is one), and a block's before
 #pragma unroll
-    for (int ni = 0; ni < 4; ++ni) {
+    for (int ni = 0; ni < NB; ++ni) {
       p[ni] = f32x4{0.f, 0.f, 0.f, 0.f};
       last[ni] = 0.f;
     }
+    auto upto = [&](int s) {   // the group of step s; past the last step the last again
+      s = (s < n ? s : n - 1) + turn;
+      return s < n ? s : s - n;
+    };
 #pragma unroll
-    for (int k = 0; k < 9; ++k) load(k, 0, 0);
+    for (int s = 0; s < T::NST - 1; ++s)
 #pragma unroll
-    for (int k = 0; k < 3; ++k) load(k, 1 < n ? 1 : 0, 1);
-    dma::wait_vmem_le<3>();
+      for (int k = 0; k < T::LOADS; ++k) load(k, upto(s), s);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) load(k, upto(T::NST - 1), T::NST - 1);
+    dma::wait_vmem_le<(T::NST - 2) * T::LOADS + 3>();
     dma::lds_barrier();
-    i32x8 A[2], B[4];
-    const int sa = Wide8::S0 + wave * 256 + (lane & 15) * 4;
-    A[0] = read(ad, 0);
-    {
-      const float w = scalar8(ws);
+    i32x8 A[2], B[NB];
+    const int sa = T::S0 + wn * T::NWV * 4 + (lane & 15) * 4;
+    A[0] = read(ad, 0, 0);
+    float w = scalar8(ws + turn), w2 = T::SPLIT ? scalar8(ws2 + turn) : 0.f;
 #pragma unroll
-      for (int ni = 0; ni < 4; ++ni) {
-        B[ni] = read(bd, ni);
-        sc[ni] = *reinterpret_cast<const float*>(smem + sa + ni * 64) * w;
-      }
+    for (int ni = 0; ni < NB; ++ni) {
+      B[ni] = read(bd, 0, ni);
+      sc[ni] = *reinterpret_cast<const float*>(smem + sa + ni * 64);
+      if (!T::SPLIT) sc[ni] *= w;
     }
     auto promote = [&](float (&c)[4], const f32x4& q, float f) {
 #pragma unroll
@@ -736,51 +781,57 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
       // every block's sums into registers until then (184 spilled).
       asm volatile("" : "+v"(c[0]), "+v"(c[1]), "+v"(c[2]), "+v"(c[3]));
     };
+    auto scale = [&](int mi, int ni) { return T::SPLIT ? sc[ni] * (mi < split ? w : w2) : sc[ni]; };
+    int stage = 0, fill = T::NST - 1;
     for (int s = 0; s < n; ++s) {
-      const int k1 = s + 1 < n ? s + 1 : s, k2 = s + 2 < n ? s + 2 : n - 1;
-      const float w = scalar8(ws + k1);   // of the next step
+      const int next = stage + 1 < T::NST ? stage + 1 : 0, so = stage * T::STAGE, sn = next * T::STAGE;
+      const float wn1 = scalar8(ws + upto(s + 1)), wn2 = T::SPLIT ? scalar8(ws2 + upto(s + 1)) : 0.f;
+      const int k1 = upto(s + T::NST - 1), k2 = upto(s + T::NST);
 #pragma unroll
-      for (int mi = 0; mi < 7; ++mi) {
-        A[(mi + 1) & 1] = read(ad, mi + 1);
+      for (int mi = 0; mi < MB - 1; ++mi) {
+        A[(mi + 1) & 1] = read(ad, so, mi + 1);
 #pragma unroll
-        for (int ni = 0; ni < 4; ++ni) {
-          if (mi == 0) promote(acc[7][ni], p[ni], last[ni]);
-          else promote(acc[mi - 1][ni], p[ni], sc[ni]);
+        for (int ni = 0; ni < NB; ++ni) {
+          if (mi == 0) promote(acc[MB - 1][ni], p[ni], last[ni]);
+          else promote(acc[mi - 1][ni], p[ni], scale(mi - 1, ni));
           p[ni] = mfma8(A[mi & 1], B[ni]);
-          if (mi < 2 && ni < 3) load(3 + mi * 3 + ni, k1, (s + 1) & 1);
+          const int k = 3 + mi * T::EACH + ni;
+          if (ni < T::EACH && k < T::LOADS) load(k, k1, fill);
           __builtin_amdgcn_sched_barrier(0);
         }
       }
       // Step s + 1 has landed, and every wave holds the last of step s.
-      dma::wait_vmem_le<0>();
+      dma::wait_vmem_le<(T::NST - 2) * T::LOADS>();
       dma::lds_barrier();
+      i32x8 first = read(ad, sn, 0);
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        ad[q] ^= 32768;
-        bd[q] ^= 32768;
-      }
-      A[0] = read(ad, 0);
-#pragma unroll
-      for (int ni = 0; ni < 4; ++ni) {
-        promote(acc[6][ni], p[ni], sc[ni]);
-        p[ni] = mfma8(A[1], B[ni]);
-        B[ni] = read(bd, ni);
-        if (ni < 3) load(ni, k2, s & 1);
+      for (int ni = 0; ni < NB; ++ni) {
+        promote(acc[MB - 2][ni], p[ni], scale(MB - 2, ni));
+        p[ni] = mfma8(A[(MB - 1) & 1], B[ni]);
+        B[ni] = read(bd, sn, ni);
+        if (ni < 3) load(ni, k2, stage);
+        if (NB == 2 && ni == 1) load(2, k2, stage);
         __builtin_amdgcn_sched_barrier(0);
       }
+      A[0] = first;
 #pragma unroll
-      for (int ni = 0; ni < 4; ++ni) {
-        last[ni] = sc[ni];
-        sc[ni] = *reinterpret_cast<const float*>(smem + sa + ((s + 1) & 1) * 2048 + ni * 64) * w;
+      for (int ni = 0; ni < NB; ++ni) {
+        last[ni] = scale(MB - 1, ni);
+        sc[ni] = *reinterpret_cast<const float*>(smem + sa + next * T::SCALES + ni * 64);
+        if (!T::SPLIT) sc[ni] *= wn1;
       }
+      w = wn1;
+      w2 = wn2;
+      fill = stage;
+      stage = next;
       __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
-    for (int ni = 0; ni < 4; ++ni) promote(acc[7][ni], p[ni], last[ni]);
+    for (int ni = 0; ni < NB; ++ni) promote(acc[MB - 1][ni], p[ni], last[ni]);
     dma::wait_vmem_le<0>();
     __syncthreads();   // the output's staging takes the stages' place
   }
-  store8<T, GRAD, true>(acc, a, v0 + wm * 128, t0 + wn * 64, smem, wave);
+  store8<T, GRAD, true>(acc, a, r0, t0 + wn * T::NWV, smem, wave);
 }
 
 template <int TM, int TN, int WM, int WN, int NST, bool GRAD, bool FULL, int EU>
@@ -792,18 +843,55 @@ static hipError_t launch_linear8_as(Linear8Args a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <bool GRAD>
+template <int MB, int NB, bool GRAD>
 static hipError_t launch_linear8_wide(Linear8Args a, hipStream_t s) {
-  a.nvt = (int32_t)((a.V + 255) / 256);
-  a.ntb = (int32_t)((a.T + 255) / 256);
-  hipLaunchKernelGGL((k_linear8_wide<GRAD>), dim3((unsigned)(a.nvt * a.ntb)), dim3(512), 0, s, a);
+  using T = Wide8<MB, NB>;
+  a.nvt = (int32_t)((a.V + T::TM - 1) / T::TM);
+  a.ntb = (int32_t)((a.T + T::TN - 1) / T::TN);
+  hipLaunchKernelGGL((k_linear8_wide<MB, NB, GRAD>), dim3((unsigned)(a.nvt * a.ntb)), dim3(512), 0, s, a);
   return hipGetLastError();
+}
+
+// The wide form's shape. A compute unit holds one workgroup, so a call takes as long as its rounds of 256
+// workgroups times what one takes: in units of a block's MFMA its MB NB, 10 for a step's other work and 2
+// where a wave's rows lie in two of the weight's blocks (fitted to every shape at 37 sizes; the shape that the
+// rule takes is 0.4 % slower than the best of them on average). us of a shard, 37984 x 4096, with the shape it
+// takes and with 8 x 4: 128 rows 37 and 59, 180 rows 42 and 60, 300 rows 56 and 102, 512 rows 91 and 108, 600
+// rows 104 and 114.
+template <bool GRAD>
+static hipError_t launch_linear8_bf16(const Linear8Args& a, hipStream_t s) {
+  int64_t least = 0;
+  int mb = 8, nb = 4;
+  for (int m : {8, 5, 4})
+    for (int n : {5, 4, 3, 2}) {
+      if (m * n > 32) continue;   // accumulators past the registers
+      const int64_t tiles = (a.V + 32 * m - 1) / (32 * m) * ((a.T + 64 * n - 1) / (64 * n));
+      const int64_t cost = (tiles + 255) / 256 * (m * n + 10 + (m == 5 ? 2 : 0));
+      if (least == 0 || cost < least) {
+        least = cost;
+        mb = m;
+        nb = n;
+      }
+    }
+  switch (mb * 10 + nb) {
+    case 42: return launch_linear8_wide<4, 2, GRAD>(a, s);
+    case 43: return launch_linear8_wide<4, 3, GRAD>(a, s);
+    case 44: return launch_linear8_wide<4, 4, GRAD>(a, s);
+    case 45: return launch_linear8_wide<4, 5, GRAD>(a, s);
+    case 52: return launch_linear8_wide<5, 2, GRAD>(a, s);
+    case 53: return launch_linear8_wide<5, 3, GRAD>(a, s);
+    case 54: return launch_linear8_wide<5, 4, GRAD>(a, s);
+    case 55: return launch_linear8_wide<5, 5, GRAD>(a, s);
+    case 82: return launch_linear8_wide<8, 2, GRAD>(a, s);
+    case 83: return launch_linear8_wide<8, 3, GRAD>(a, s);
+    default: return launch_linear8_wide<8, 4, GRAD>(a, s);
+  }
 }
 
 hipError_t launch_linear8(const Linear8Args& a, hipStream_t s) {
   if (a.T <= 0 || a.V <= 0) return hipSuccess;
   if (a.grad) {
-    if (a.out_bf16) return launch_linear8_wide<true>(a, s);
+    if (a.out_bf16) return launch_linear8_bf16<true>(a, s);
     return launch_linear8_as<128, 128, 2, 2, 2, true, true, 2>(a, s);
   }
   // Few rows, the weight's bytes bound them: where 128 columns a workgroup would leave compute units
@@ -815,8 +903,7 @@ hipError_t launch_linear8(const Linear8Args& a, hipStream_t s) {
                                  : launch_linear8_as<128, 32, 4, 1, 3, false, false, 2>(a, s);
     if (a.T <= 64) return narrow ? launch_linear8_as<64, 64, 2, 1, 3, false, false, 2>(a, s)
                                  : launch_linear8_as<128, 64, 4, 1, 3, false, false, 2>(a, s);
-    if (a.T <= 512) return launch_linear8_as<128, 128, 2, 2, 2, false, false, 2>(a, s);
-    return launch_linear8_wide<false>(a, s);
+    return launch_linear8_bf16<false>(a, s);
   }
   if (a.T <= 32) return narrow ? launch_linear8_as<64, 32, 2, 1, 3, false, true, 2>(a, s)
                                : launch_linear8_as<128, 32, 4, 1, 3, false, true, 2>(a, s);

@@ -290,3 +290,42 @@ def test_fp8_linear_gradient_against_differences(llp):
             hi[i, j] += 1
             diff = (f(hi, w) - f(lo, w)) / 2 if m is x else (f(x, hi) - f(x, lo)) / 2
             assert float(grad[i, j]) == diff   # whole numbers below 2^24
+
+
+def quantised(llp, R, K, rows, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.randn(R, K, generator=g, device="cuda") * torch.exp(torch.randn(R, 1, generator=g, device="cuda"))
+    return llp.quantize_blocks(x, rows=rows)
+
+
+# Each reaches another shape of workgroup; columns past several turns of the groups' order, ragged ends.
+@pytest.mark.parametrize("T,V", [(65, 203), (130, 16389), (644, 10802), (258, 21804), (65, 32830), (130, 32900), (193, 33012),
+                                 (259, 32795), (196, 20535), (386, 16432), (387, 21949), (130, 20681), (321, 21856),
+                                 (1, 70003), (33, 66001)])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_products_have_the_same_bits_in_every_form(llp, T, V, out):
+    K = 384
+    say(f"forms T={T} V={V} K={K} {out}")
+    x, w = quantised(llp, T, K, 1, T), quantised(llp, V, K, 128, V)
+    d = torch.bfloat16 if out == "bf16" else torch.float32
+    y = llp.linear_fp8(*x, *w, out_dtype=d)
+    # Few rows, few columns: the groups' order repeats after 1280 * 3 columns.
+    for v in range(0, V, 3840 * 4):
+        part = w[0][v:v + 15360], w[1][v // 128:(min(v + 15360, V) + 127) // 128]
+        few = torch.cat([llp.linear_fp8(x[0][t:t + 32], x[1][t:t + 32], *part, out_dtype=d) for t in range(0, T, 32)])
+        assert bytes_equal(y[:, v:v + 15360].contiguous(), few.contiguous())
+    dw = llp.dweight_fp8(*w, *x, out_dtype=d)
+    assert torch.equal(dw, y.t())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_quantize_blocks_of_many_groups(llp, dtype):
+    # From 2^19 groups on four rows go together: the same bytes as a few rows at a time.
+    R, C = 131075, 500
+    g = torch.Generator(device="cuda").manual_seed(7)
+    x = torch.randn(R, C, generator=g, device="cuda").to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+    q, s = llp.quantize_blocks(x)
+    for r in (0, 65530, R - 1001):
+        rq, rs = llp.quantize_blocks(x[r:r + 1001])
+        assert bytes_equal(q[r:r + 1001].view(torch.uint8), rq.view(torch.uint8))
+        assert bytes_equal(s[r:r + 1001].contiguous(), rs.contiguous())
