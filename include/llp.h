@@ -563,12 +563,13 @@ typedef struct {
 /* A product of two such operands over their common depth:
  *   p[t][v] = sum_g x_scale[g][t] weight_scale[v / 128][g] sum_{k in g} x[t][k] weight[v][k]
  *   x       [rows, depth] e4m3, scales by group; weight [cols, depth] e4m3, scales by block. Row
- *           strides in bytes, >= depth and multiples of 16, below 2^24; 16-byte aligned bases.
+ *           strides in bytes, >= depth and multiples of 16, at most 2^23; 16-byte aligned bases.
  *   depth   a multiple of LLP_FP8_BLOCK, 0 <= depth <= 2^23 (0: the sums are 0).
  *   rows, cols  0 .. 2^23 - 256; ceil(rows / 32) * ceil(cols / 128) < 2^23 (else
  *           LLP_ERR_UNSUPPORTED).
- * The groups are added in ascending order in fp32, so an element depends on its two rows alone,
- * whatever the call's other rows. A group's 128 products are summed in fp32 where out is fp32; where it
+ * The groups are added in fp32 in ascending order from group (v / 1280) mod the number of groups on, then
+ * from 0, so an element depends on its two rows and v alone, whatever the call's other rows. A
+ * group's 128 products are summed in fp32 where out is fp32; where it
  * is bf16 they are summed by the 8-bit matrix instructions, which cut 8 products at a time about 14
  * bits below the largest: a hundredth of the result's rounding to bf16.
  * llp_linear_fp8: out[t][v] = p + bias[v], [rows, cols] of out_dtype, row stride out_stride
@@ -576,7 +577,8 @@ typedef struct {
  *   or NULL. flags must be 0.
  * llp_dweight_fp8: the gradient of a weight, with `weight` the transposed upstream gradient [V, T]
  *   and `x` the transposed input [H, T]: out[v][t] += p (fp32), [cols, rows], row stride
- *   out_stride >= rows. With LLP_FLAG_OVERWRITE_GRADS it is written, and out_dtype may be bf16.
+ *   out_stride >= rows, below 2^24 in fp32 (else LLP_ERR_UNSUPPORTED). With LLP_FLAG_OVERWRITE_GRADS
+ *   it is written, and out_dtype may be bf16.
  *   bias must be NULL. */
 typedef struct {
   const uint8_t* x;

@@ -29,8 +29,8 @@ llp_status check_operand(const char* name, const uint8_t* p, int64_t stride, con
   LLP_CHECK(rows <= kMaxRows, LLP_ERR_UNSUPPORTED, "%s: %lld rows exceed 2^23 - 256", name, (long long)rows);
   LLP_CHECK(stride >= depth && stride % 16 == 0, LLP_ERR_INVALID_ARGUMENT,
             "%s stride %lld must be >= depth and a multiple of 16", name, (long long)stride);
-  // Tile rows are addressed with 32-bit byte offsets: 255 rows and the depth.
-  LLP_CHECK(stride < (int64_t(1) << 24), LLP_ERR_UNSUPPORTED, "%s stride must be < 2^24", name);
+  // Tile rows are addressed with 32-bit byte offsets: 319 rows and the depth.
+  LLP_CHECK(stride <= (int64_t(1) << 23), LLP_ERR_UNSUPPORTED, "%s stride must be <= 2^23", name);
   LLP_CHECK(aligned(scale, 4), LLP_ERR_INVALID_ARGUMENT, "%s scale not aligned to fp32", name);
   if (rows > 0 && depth > 0) {
     LLP_CHECK(p && scale, LLP_ERR_INVALID_ARGUMENT, "%s and its scale are required", name);

@@ -47,7 +47,8 @@ def _scale_stride(t, name, rows, depth, by_block, dev):
         _tensor(t, name)
         if t.dtype != _F32 or t.device != dev:
             raise TypeError(f"{name} must be an fp32 tensor on {dev}, got {t.dtype} on {t.device}")
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+        if t.shape != shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
     n, groups = shape
     inner, outer = (1, 0) if by_block else (0, 1)
     if shape[inner] > 1 and t.stride(inner) != 1:

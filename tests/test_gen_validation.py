@@ -104,7 +104,7 @@ def test_quantize_refusals(over, want):
     (dict(depth=100), INV), (dict(depth=-128), INV), (dict(depth=(1 << 23) + 128), UNS), (dict(rows=-1), INV),
     (dict(cols=-1), INV), (dict(rows=1 << 23, x_scale_stride=1 << 23), UNS), (dict(cols=1 << 23, out_stride=1 << 23), UNS),
     (dict(x_stride=128), INV), (dict(x_stride=264), INV), (dict(weight_stride=240), INV), (dict(x_stride=1 << 24), UNS),
-    (dict(weight_stride=1 << 24), UNS), (dict(x_scale_stride=299), INV), (dict(weight_scale_stride=1), INV),
+    (dict(weight_stride=1 << 24), UNS), (dict(x_stride=(1 << 23) + 16), UNS), (dict(weight_stride=(1 << 23) + 16), UNS), (dict(x_scale_stride=299), INV), (dict(weight_scale_stride=1), INV),
     (dict(x=None), INV), (dict(x_scale=None), INV), (dict(weight=None), INV), (dict(weight_scale=None), INV),
     (dict(x=FAKE + 8), INV), (dict(weight=FAKE + 4), INV), (dict(x_scale=FAKE + 1), INV), (dict(out=None), INV),
     (dict(out=FAKE + 2), INV), (dict(out_stride=399), INV), (dict(out_dtype=0), INV), (dict(flags=1), INV),
@@ -249,6 +249,12 @@ def test_dweight_binding(over):
     reaches_library(dw, dweight=torch.zeros(V, T, dtype=torch.bfloat16), overwrite=True)
     with pytest.raises(BAD):
         dw(**over)
+
+
+def test_scales_may_be_parameters():
+    p = torch.nn.Parameter
+    reaches_library(lin, x_scale=p(torch.zeros(2, T).t(), requires_grad=False),
+                    weight_scale=p(torch.zeros(-(-V // 128), 2), requires_grad=False))
 
 
 def test_fp8_linear_binding():
