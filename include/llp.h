@@ -815,6 +815,10 @@ LLP_API llp_status llp_embedding_backward(const llp_embedding_request* req, cons
 /* Quantisation in 8-bit floating point (see llp_fp8_quant_request) and products of such operands
  * (see llp_fp8_linear_request). No workspace. */
 LLP_API llp_status llp_quantize_blocks(const llp_fp8_quant_request* req, void* stream);
+/* Two of them in one pass over their common x: `groups` with block_rows 1 and not transposed, `blocks`
+ * with block_rows 128 and transposed, as the two gradients of a product take an upstream gradient. */
+LLP_API llp_status llp_quantize_both(const llp_fp8_quant_request* groups,
+                                     const llp_fp8_quant_request* blocks, void* stream);
 LLP_API llp_status llp_linear_fp8(const llp_fp8_linear_request* req, void* stream);
 LLP_API llp_status llp_dweight_fp8(const llp_fp8_linear_request* req, void* stream);
 

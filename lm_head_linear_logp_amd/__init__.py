@@ -30,7 +30,7 @@ __all__ = ["LLPError", "open", "workspace_bytes", "forward", "forward_noalloc", 
            "backward", "top_p_replay", "last_error", "STATUS_BITS", "forward_logits",
            "keep_mask_replay", "SCRATCH_BYTES", "linear_logp", "quantize_rows", "forward_int8",
            "policy_grads", "policy_loss", "preference_grads", "preference_loss",
-           "embedding_forward", "embedding_backward", "embedding", "quantize_blocks", "linear_fp8",
+           "embedding_forward", "embedding_backward", "embedding", "quantize_blocks", "quantize_both", "linear_fp8",
            "dweight_fp8", "fp8_linear", "beam_candidates", "beam_select", "beam_reorder"]
 
 # Size of the static device scratch llp_forward_noalloc works in (include/llp.h).
@@ -590,4 +590,4 @@ def linear_logp(hidden: torch.Tensor, weight: torch.Tensor, target_ids: torch.Te
 from .ops import (embedding, embedding_backward, embedding_forward, forward_int8,  # noqa: E402
                   policy_grads, policy_loss, preference_grads, preference_loss, quantize_rows)
 from .gen import (beam_candidates, beam_reorder, beam_select, dweight_fp8, fp8_linear,  # noqa: E402
-                  linear_fp8, quantize_blocks)
+                  linear_fp8, quantize_blocks, quantize_both)

@@ -236,6 +236,7 @@ SIGNATURES = {
     "llp_embedding_backward": (C.c_int, [C.POINTER(llp_embedding_request), vp, C.c_int32,
                                          C.c_int64, vp, C.c_int64, vp, C.c_size_t, vp]),
     "llp_quantize_blocks": (C.c_int, [C.POINTER(llp_fp8_quant_request), vp]),
+    "llp_quantize_both": (C.c_int, [C.POINTER(llp_fp8_quant_request), C.POINTER(llp_fp8_quant_request), vp]),
     "llp_linear_fp8": (C.c_int, [C.POINTER(llp_fp8_linear_request), vp]),
     "llp_dweight_fp8": (C.c_int, [C.POINTER(llp_fp8_linear_request), vp]),
     "llp_beam_candidates": (C.c_int, [C.POINTER(llp_beam_request), C.POINTER(llp_beam_parts), vp]),

@@ -39,6 +39,46 @@ llp_status check_operand(const char* name, const uint8_t* p, int64_t stride, con
   return LLP_OK;
 }
 
+// A quantisation's checks and what its kernel takes.
+llp_status check_quant(const llp_fp8_quant_request* req, Quant8Args* args) {
+  LLP_CHECK(req != nullptr, LLP_ERR_INVALID_ARGUMENT, "request is NULL");
+  const llp_fp8_quant_request& p = *req;
+  LLP_CHECK(p.rows >= 0 && p.rows < (int64_t(1) << 31) && p.cols >= 0 && p.cols < (int64_t(1) << 31),
+            LLP_ERR_INVALID_ARGUMENT, "x of %lld x %lld is out of range", (long long)p.rows, (long long)p.cols);
+  LLP_CHECK(dtype_ok(p.x_dtype), LLP_ERR_INVALID_ARGUMENT, "x_dtype %d is not BF16 or F32", p.x_dtype);
+  LLP_CHECK(p.block_rows == 1 || p.block_rows == LLP_FP8_BLOCK, LLP_ERR_INVALID_ARGUMENT,
+            "block_rows %d is not 1 or %d", p.block_rows, LLP_FP8_BLOCK);
+  LLP_CHECK(p.x_stride >= p.cols && p.x_stride < kMaxStride, LLP_ERR_INVALID_ARGUMENT,
+            "x_stride %lld must be >= cols", (long long)p.x_stride);
+  const int64_t M = p.transpose ? p.cols : p.rows, K = p.transpose ? p.rows : p.cols;
+  LLP_CHECK(p.q_stride >= round_up(K, LLP_FP8_BLOCK) && p.q_stride % 16 == 0 && p.q_stride < kMaxStride,
+            LLP_ERR_INVALID_ARGUMENT, "q_stride %lld must be >= %lld and a multiple of 16", (long long)p.q_stride,
+            (long long)round_up(K, LLP_FP8_BLOCK));
+  LLP_CHECK(p.scale_stride >= (p.block_rows == 1 ? M : blocks_of(K)) && p.scale_stride < kMaxStride,
+            LLP_ERR_INVALID_ARGUMENT, "scale_stride %lld is too small", (long long)p.scale_stride);
+  LLP_CHECK(blocks_of(p.rows) * blocks_of(p.cols) < kMaxTiles, LLP_ERR_UNSUPPORTED,
+            "x of %lld x %lld holds too many blocks", (long long)p.rows, (long long)p.cols);
+  if (M > 0 && K > 0) {
+    LLP_CHECK(p.x && p.q && p.scale, LLP_ERR_INVALID_ARGUMENT, "x, q and scale are required");
+    LLP_CHECK(aligned(p.x, size_of(p.x_dtype)), LLP_ERR_INVALID_ARGUMENT, "x not aligned to its element type");
+    LLP_CHECK(aligned(p.q, 16) && aligned(p.scale, 4), LLP_ERR_INVALID_ARGUMENT,
+              "q must be 16-byte aligned, scale aligned to fp32");
+  }
+  Quant8Args& a = *args;
+  a.x = p.x;
+  a.bf16 = p.x_dtype == LLP_DTYPE_BF16;
+  a.ldx = p.x_stride;
+  a.rows = p.rows;
+  a.cols = p.cols;
+  a.block = p.block_rows != 1;
+  a.transpose = p.transpose != 0;
+  a.q = p.q;
+  a.ldq = p.q_stride;
+  a.scale = p.scale;
+  a.lds = p.scale_stride;
+  return LLP_OK;
+}
+
 llp_status run_linear(const llp_fp8_linear_request* req, bool grad, void* stream) {
   LLP_CHECK(req != nullptr, LLP_ERR_INVALID_ARGUMENT, "request is NULL");
   const llp_fp8_linear_request& p = *req;
@@ -157,44 +197,29 @@ bool apart(int64_t rows, int64_t outer, int64_t inner, int64_t rs, int64_t os) {
 extern "C" {
 
 LLP_API llp_status llp_quantize_blocks(const llp_fp8_quant_request* req, void* stream) {
-  LLP_CHECK(req != nullptr, LLP_ERR_INVALID_ARGUMENT, "request is NULL");
-  const llp_fp8_quant_request& p = *req;
-  LLP_CHECK(p.rows >= 0 && p.rows < (int64_t(1) << 31) && p.cols >= 0 && p.cols < (int64_t(1) << 31),
-            LLP_ERR_INVALID_ARGUMENT, "x of %lld x %lld is out of range", (long long)p.rows, (long long)p.cols);
-  LLP_CHECK(dtype_ok(p.x_dtype), LLP_ERR_INVALID_ARGUMENT, "x_dtype %d is not BF16 or F32", p.x_dtype);
-  LLP_CHECK(p.block_rows == 1 || p.block_rows == LLP_FP8_BLOCK, LLP_ERR_INVALID_ARGUMENT,
-            "block_rows %d is not 1 or %d", p.block_rows, LLP_FP8_BLOCK);
-  LLP_CHECK(p.x_stride >= p.cols && p.x_stride < kMaxStride, LLP_ERR_INVALID_ARGUMENT,
-            "x_stride %lld must be >= cols", (long long)p.x_stride);
-  const int64_t M = p.transpose ? p.cols : p.rows, K = p.transpose ? p.rows : p.cols;
-  LLP_CHECK(p.q_stride >= round_up(K, LLP_FP8_BLOCK) && p.q_stride % 16 == 0 && p.q_stride < kMaxStride,
-            LLP_ERR_INVALID_ARGUMENT, "q_stride %lld must be >= %lld and a multiple of 16", (long long)p.q_stride,
-            (long long)round_up(K, LLP_FP8_BLOCK));
-  LLP_CHECK(p.scale_stride >= (p.block_rows == 1 ? M : blocks_of(K)) && p.scale_stride < kMaxStride,
-            LLP_ERR_INVALID_ARGUMENT, "scale_stride %lld is too small", (long long)p.scale_stride);
-  LLP_CHECK(blocks_of(p.rows) * blocks_of(p.cols) < kMaxTiles, LLP_ERR_UNSUPPORTED,
-            "x of %lld x %lld holds too many blocks", (long long)p.rows, (long long)p.cols);
-  if (M > 0 && K > 0) {
-    LLP_CHECK(p.x && p.q && p.scale, LLP_ERR_INVALID_ARGUMENT, "x, q and scale are required");
-    LLP_CHECK(aligned(p.x, size_of(p.x_dtype)), LLP_ERR_INVALID_ARGUMENT, "x not aligned to its element type");
-    LLP_CHECK(aligned(p.q, 16) && aligned(p.scale, 4), LLP_ERR_INVALID_ARGUMENT,
-              "q must be 16-byte aligned, scale aligned to fp32");
-  }
-  llp_status st = check_device();
-  if (st != LLP_OK) return st;
   Quant8Args a{};
-  a.x = p.x;
-  a.bf16 = p.x_dtype == LLP_DTYPE_BF16;
-  a.ldx = p.x_stride;
-  a.rows = p.rows;
-  a.cols = p.cols;
-  a.block = p.block_rows != 1;
-  a.transpose = p.transpose != 0;
-  a.q = p.q;
-  a.ldq = p.q_stride;
-  a.scale = p.scale;
-  a.lds = p.scale_stride;
+  llp_status st = check_quant(req, &a);
+  if (st != LLP_OK) return st;
+  st = check_device();
+  if (st != LLP_OK) return st;
   LLP_HIP(launch_quant8(a, static_cast<hipStream_t>(stream)), "fp8 quantise kernel launch");
+  return LLP_OK;
+}
+
+LLP_API llp_status llp_quantize_both(const llp_fp8_quant_request* groups, const llp_fp8_quant_request* blocks,
+                                     void* stream) {
+  Quant8Args a{}, t{};
+  llp_status st = check_quant(groups, &a);
+  if (st != LLP_OK) return st;
+  st = check_quant(blocks, &t);
+  if (st != LLP_OK) return st;
+  LLP_CHECK(a.x == t.x && a.bf16 == t.bf16 && a.ldx == t.ldx && a.rows == t.rows && a.cols == t.cols,
+            LLP_ERR_INVALID_ARGUMENT, "the two requests name different x");
+  LLP_CHECK(!a.block && !a.transpose && t.block && t.transpose, LLP_ERR_INVALID_ARGUMENT,
+            "the first request is by group, the second in blocks and transposed");
+  st = check_device();
+  if (st != LLP_OK) return st;
+  LLP_HIP(launch_quant8_both(a, t, static_cast<hipStream_t>(stream)), "fp8 quantise kernel launch");
   return LLP_OK;
 }
 

@@ -11,9 +11,10 @@ namespace llp {
 // Quantisation: scale = max(max |x|, 1e-30) * fl32(1/448) over 1 or 128 rows of 128 columns, q =
 // x / scale as e4m3 (ties to even). By blocks, or transposed, a workgroup holds a 128 x 128 tile of x in
 // registers, 8 x 8 values a thread, so that either costs one read and one write; the transpose goes
-// through LDS and out in whole 128-byte rows. Bound by memory: 37984 x 4096 bf16 (467 MB) in blocks 100 us,
-// transposed 98, 4.7 TB/s, a copy's rate; by group 109; 4096 x 37984 by group and transposed 120. (With
-// IEEE reciprocals, shuffles through LDS and floating point maxima 106, 104, 121 and 137.)
+// through LDS and out in whole 128-byte rows. Bound by memory: 37984 x 4096 bf16 (467 MB) in blocks 90 us,
+// 5.2 TB/s, a copy's rate; transposed 100; by group 108; 4096 x 37984 transposed, in blocks 103, by group 107.
+// (Maxima on the values' bits, moves between lanes instead of LDS shuffles, the hardware's reciprocal and bf16
+// kept as it is loaded: together 15 % off.)
 // ------------------------------------------------------------------------------------
 constexpr int Q8_THREADS = 256;
 // Groups from which a team takes four rows instead of one (us: 4096 x 4096 bf16 17.4 and 14.3, 4096 x 37984
@@ -115,26 +116,118 @@ struct Q8Scale {
   __device__ __forceinline__ float out() const { return fine ? scale : __builtin_nanf(""); }
 };
 
-// Thread (team, lane): rows team * 8 .. + 7 and columns lane * 8 .. + 7 of the tile.
+// Eight values of a row as they were loaded: in bf16 two to a register, so that a thread's 64 leave room for
+// twice the waves.
+template <bool BF16>
+struct __attribute__((aligned(16))) Q8Row {
+  uint32_t u[BF16 ? 4 : 8];
+  __device__ __forceinline__ float at(int i) const {
+    if (!BF16) return __builtin_bit_cast(float, u[i]);
+    return __builtin_bit_cast(float, (i & 1) != 0 ? u[i / 2] & 0xFFFF0000u : u[i / 2] << 16);
+  }
+};
+
+// A workgroup's tile. Transposed, neighbours go along the side with fewer tiles, so that one of the two walks, x's
+// rows or q's, is whole pages of memory (us along columns and along rows, blocks: 4096 x 37984 111 and 103, 4096 x
+// 151936 471 and 378, 37984 x 4096 100 and 113).
+template <bool TRANS>
+__device__ __forceinline__ void q8_place(const Quant8Args& a, int64_t& rb, int64_t& cb) {
+  const int64_t ntr = (a.rows + 127) / 128, ntc = (a.cols + 127) / 128;
+  const bool by_row = TRANS && ntr < ntc;
+  rb = by_row ? blockIdx.x % ntr : blockIdx.x / ntc;
+  cb = by_row ? blockIdx.x / ntr : blockIdx.x % ntc;
+}
+
+// Thread (team, lane): rows team * 8 .. + 7 and columns lane * 8 .. + 7 of a tile, 0 past x.
+template <bool BF16, bool VEC>
+__device__ __forceinline__ void q8_tile(const Quant8Args& a, int64_t r0, int64_t c0, Q8Row<BF16> (&v)[8]) {
+  const int lane = threadIdx.x & 15, team = threadIdx.x >> 4;
+  const int64_t first = r0 + team * 8, c = c0 + lane * 8;
+  const char* const x = static_cast<const char*>(a.x);
+  constexpr int SIZE = BF16 ? 2 : 4, N = BF16 ? 4 : 8;
+  if constexpr (VEC) {
+    // No load is behind a lane's branch: rows past the last are read as the last, 8 columns past the last whole
+    // ones as those, and the columns behind them, fewer than 8, one by one where the tile holds them.
+    const int64_t whole = a.cols & ~(int64_t)7;
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      const char* const row = x + (first + p < a.rows ? first + p : a.rows - 1) * a.ldx * SIZE;
+      if (whole > 0) {
+#pragma unroll
+        for (int i = 0; i < N; i += 4)
+          *reinterpret_cast<u32x4*>(&v[p].u[i]) = *reinterpret_cast<const u32x4*>(row + (c < whole ? c : whole - 8) * SIZE + 4 * i);
+      }
+    }
+    if (c0 + 128 > whole) {
+#pragma unroll
+      for (int p = 0; p < 8; ++p) {
+        const char* const row = x + (first + p < a.rows ? first + p : a.rows - 1) * a.ldx * SIZE;
+        uint32_t y[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int64_t at = whole + i < a.cols ? whole + i : a.cols - 1;
+          y[i] = BF16 ? reinterpret_cast<const uint16_t*>(row)[at] : reinterpret_cast<const uint32_t*>(row)[at];
+          if (c > whole || whole + i >= a.cols) y[i] = 0;
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+          if (c >= whole) v[p].u[i] = BF16 ? y[(2 * i) & 7] | y[(2 * i + 1) & 7] << 16 : y[i];
+      }
+    }
+#pragma unroll
+    for (int p = 0; p < 8; ++p)
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[p].u[i] = first + p < a.rows ? v[p].u[i] : 0;
+  } else {
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (first + p < a.rows) q8_load<BF16, false>(x + (first + p) * a.ldx * SIZE, c, a.cols, y);
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        v[p].u[i] = BF16 ? __builtin_bit_cast(uint32_t, y[(2 * i) & 7]) >> 16 | __builtin_bit_cast(uint32_t, y[(2 * i + 1) & 7])
+                         : __builtin_bit_cast(uint32_t, y[i]);
+    }
+  }
+}
+
+// Keeps the tile as it was loaded across what follows, not the fp32 values made of it.
+template <bool BF16>
+__device__ __forceinline__ void q8_keep(Q8Row<BF16> (&v)[8]) {
+  if constexpr (BF16) {
+#pragma unroll
+    for (int p = 0; p < 8; ++p) asm volatile("" : "+v"(v[p].u[0]), "+v"(v[p].u[1]), "+v"(v[p].u[2]), "+v"(v[p].u[3]));
+  }
+}
+
+// The tile's columns as rows of q, from LDS: 8-byte piece `team` of column c is at (team ^ (c / 8)) * 8 of its 128
+// bytes, so that a wave's writes spread over the banks.
+__device__ __forceinline__ void q8_turned_put(uint8_t* turned, int k, const uint2& w) {
+  const int lane = threadIdx.x & 15, team = threadIdx.x >> 4;
+  *reinterpret_cast<uint2*>(turned + (lane * 8 + k) * 128 + (team ^ lane) * 8) = w;
+}
+__device__ __forceinline__ void q8_turned_store(const uint8_t* turned, const Quant8Args& a, int64_t r0, int64_t c0) {
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    const int c = p * 32 + (threadIdx.x >> 3), h = threadIdx.x & 7;   // column, 16-byte piece
+    const uint2 lo = *reinterpret_cast<const uint2*>(turned + c * 128 + ((2 * h) ^ (c >> 3)) * 8);
+    const uint2 hi = *reinterpret_cast<const uint2*>(turned + c * 128 + ((2 * h + 1) ^ (c >> 3)) * 8);
+    if (c0 + c < a.cols)
+      *reinterpret_cast<uint4*>(a.q + (c0 + c) * a.ldq + r0 + 16 * h) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+  }
+}
+
 template <bool BF16, bool VEC, bool BLOCK, bool TRANS>
 __global__ __launch_bounds__(Q8_THREADS) void k_quant8(Quant8Args a) {
   static_assert(BLOCK || TRANS, "k_quant8_rows");
   __shared__ uint32_t tops[4][128];
   __shared__ __attribute__((aligned(16))) uint8_t turned[TRANS ? 128 * 128 : 16];
-  const int64_t ntc = (a.cols + 127) / 128;
-  const int64_t r0 = blockIdx.x / ntc * 128, c0 = blockIdx.x % ntc * 128;
+  int64_t rb, cb;
+  q8_place<TRANS>(a, rb, cb);
+  const int64_t r0 = rb * 128, c0 = cb * 128;
   const int lane = threadIdx.x & 15, team = threadIdx.x >> 4, wave = threadIdx.x >> 6;
-  float v[8][8];
-#pragma unroll
-  for (int p = 0; p < 8; ++p) {
-    const int64_t r = r0 + team * 8 + p;
-    if (r < a.rows) {
-      q8_load<BF16, VEC>(static_cast<const char*>(a.x) + r * a.ldx * (BF16 ? 2 : 4), c0 + lane * 8, a.cols, v[p]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[p][i] = 0.f;
-    }
-  }
+  Q8Row<BF16> v[8];
+  q8_tile<BF16, VEC>(a, r0, c0, v);
   uint32_t top[8];   // of this thread's columns, or of all in the first
 #pragma unroll
   for (int i = 0; i < 8; ++i) top[i] = 0;
@@ -143,15 +236,15 @@ __global__ __launch_bounds__(Q8_THREADS) void k_quant8(Quant8Args a) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       uint32_t& t = top[BLOCK ? 0 : i];
-      t = q8_top(t, v[p][i]);
+      t = q8_top(t, v[p].at(i));
     }
+  q8_keep(v);
   Q8Scale sc[BLOCK ? 1 : 8];
   if constexpr (BLOCK) {
     top[0] = q8_teams_top(q8_team_top(top[0]));
     if ((threadIdx.x & 63) == 0) tops[wave][0] = top[0];
     __syncthreads();
     sc[0].of(q8_max(q8_max(tops[0][0], tops[1][0]), q8_max(tops[2][0], tops[3][0])));
-    const int64_t rb = r0 / 128, cb = c0 / 128;
     if (threadIdx.x == 0) a.scale[TRANS ? cb * a.lds + rb : rb * a.lds + cb] = sc[0].out();
   } else {
 #pragma unroll
@@ -164,7 +257,7 @@ __global__ __launch_bounds__(Q8_THREADS) void k_quant8(Quant8Args a) {
     for (int i = 0; i < 8; ++i) {
       const int c = lane * 8 + i;
       sc[i].of(q8_max(q8_max(tops[0][c], tops[1][c]), q8_max(tops[2][c], tops[3][c])));
-      if (team == 0 && c0 + c < a.cols) a.scale[r0 / 128 * a.lds + c0 + c] = sc[i].out();
+      if (team == 0 && c0 + c < a.cols) a.scale[rb * a.lds + c0 + c] = sc[i].out();
     }
   }
 #pragma unroll
@@ -172,14 +265,12 @@ __global__ __launch_bounds__(Q8_THREADS) void k_quant8(Quant8Args a) {
     // Row k of this thread's 8 x 8 values, or its column k.
     float x[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = TRANS ? v[i][k] : v[k][i];
+    for (int i = 0; i < 8; ++i) x[i] = TRANS ? v[i].at(k) : v[k].at(i);
     const Q8Scale& own = sc[BLOCK ? 0 : k];
     uint2 w = q8_pack(x, own.scale, own.inv);
     if (!own.fine) w = make_uint2(0, 0);
     if constexpr (TRANS) {
-      // 8-byte piece `team` of the tile's column, its place swizzled so that a wave's writes
-      // spread over the banks.
-      *reinterpret_cast<uint2*>(turned + (lane * 8 + k) * 128 + (team ^ lane) * 8) = w;
+      q8_turned_put(turned, k, w);
     } else {
       const int64_t r = r0 + team * 8 + k;
       if (r < a.rows) *reinterpret_cast<uint2*>(a.q + r * a.ldq + c0 + lane * 8) = w;
@@ -187,15 +278,63 @@ __global__ __launch_bounds__(Q8_THREADS) void k_quant8(Quant8Args a) {
   }
   if constexpr (TRANS) {
     __syncthreads();
+    q8_turned_store(turned, a, r0, c0);
+  }
+}
+
+// Both that a weight's gradient step takes of one x: a by group, t in blocks and transposed. One read instead of
+// two (4096 x 37984 bf16: 108 and 103 us apart, 181
+// together; 4096 x 151936: 424 and 378, 590).
+template <bool BF16, bool VEC>
+__global__ __launch_bounds__(Q8_THREADS) void k_quant8_both(Quant8Args a, Quant8Args t) {
+  __shared__ uint32_t tops[4];
+  __shared__ __attribute__((aligned(16))) uint8_t turned[128 * 128];
+  int64_t rb, cb;
+  q8_place<true>(a, rb, cb);
+  const int64_t r0 = rb * 128, c0 = cb * 128;
+  const int lane = threadIdx.x & 15, team = threadIdx.x >> 4;
+  Q8Row<BF16> v[8];
+  q8_tile<BF16, VEC>(a, r0, c0, v);
+  uint32_t all = 0;
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      const int c = p * 32 + (threadIdx.x >> 3), h = threadIdx.x & 7;   // column, 16-byte piece
-      const uint2 lo = *reinterpret_cast<const uint2*>(turned + c * 128 + ((2 * h) ^ (c >> 3)) * 8);
-      const uint2 hi = *reinterpret_cast<const uint2*>(turned + c * 128 + ((2 * h + 1) ^ (c >> 3)) * 8);
-      if (c0 + c < a.cols)
-        *reinterpret_cast<uint4*>(a.q + (c0 + c) * a.ldq + r0 + 16 * h) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+  for (int p = 0; p < 8; ++p) {
+    uint32_t top = 0;
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      x[i] = v[p].at(i);
+      top = q8_top(top, x[i]);
+    }
+    top = q8_team_top(top);
+    all = q8_max(all, top);
+    Q8Scale sc;
+    sc.of(top);
+    uint2 q = q8_pack(x, sc.scale, sc.inv);
+    if (!sc.fine) q = make_uint2(0, 0);
+    const int64_t r = r0 + team * 8 + p;
+    if (r < a.rows) {
+      *reinterpret_cast<uint2*>(a.q + r * a.ldq + c0 + lane * 8) = q;
+      if (lane == 0) a.scale[cb * a.lds + r] = sc.out();
     }
   }
+  q8_keep(v);
+  all = q8_teams_top(all);
+  if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = all;
+  __syncthreads();
+  Q8Scale sc;
+  sc.of(q8_max(q8_max(tops[0], tops[1]), q8_max(tops[2], tops[3])));
+  if (threadIdx.x == 0) t.scale[cb * t.lds + rb] = sc.out();
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = v[i].at(k);
+    uint2 q = q8_pack(x, sc.scale, sc.inv);
+    if (!sc.fine) q = make_uint2(0, 0);
+    q8_turned_put(turned, k, q);
+  }
+  __syncthreads();
+  q8_turned_store(turned, t, r0, c0);
 }
 
 // By group and not transposed: 16 lanes a group and nothing shared; a team takes the same group of ROWS
@@ -253,6 +392,17 @@ hipError_t launch_quant8(const Quant8Args& a, hipStream_t s) {
   const bool vec = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && a.ldx * (a.bf16 ? 2 : 4) % 16 == 0;
   if (a.bf16) vec ? launch_quant8_as<true, true>(a, s) : launch_quant8_as<true, false>(a, s);
   else vec ? launch_quant8_as<false, true>(a, s) : launch_quant8_as<false, false>(a, s);
+  return hipGetLastError();
+}
+
+hipError_t launch_quant8_both(const Quant8Args& a, const Quant8Args& t, hipStream_t s) {
+  if (a.rows <= 0 || a.cols <= 0) return hipSuccess;
+  const bool vec = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && a.ldx * (a.bf16 ? 2 : 4) % 16 == 0;
+  const dim3 grid((unsigned)((a.rows + 127) / 128 * ((a.cols + 127) / 128)));
+  if (a.bf16 && vec) hipLaunchKernelGGL((k_quant8_both<true, true>), grid, dim3(Q8_THREADS), 0, s, a, t);
+  else if (a.bf16) hipLaunchKernelGGL((k_quant8_both<true, false>), grid, dim3(Q8_THREADS), 0, s, a, t);
+  else if (vec) hipLaunchKernelGGL((k_quant8_both<false, true>), grid, dim3(Q8_THREADS), 0, s, a, t);
+  else hipLaunchKernelGGL((k_quant8_both<false, false>), grid, dim3(Q8_THREADS), 0, s, a, t);
   return hipGetLastError();
 }
 

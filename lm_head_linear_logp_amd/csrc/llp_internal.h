@@ -519,6 +519,7 @@ hipError_t launch_embedding_sum(const EmbBwdArgs& a, hipStream_t s);
 hipError_t launch_policy(const PolicyArgs& a, hipStream_t s);
 hipError_t launch_preference(const PrefArgs& a, hipStream_t s);
 hipError_t launch_quant8(const Quant8Args& a, hipStream_t s);
+hipError_t launch_quant8_both(const Quant8Args& a, const Quant8Args& t, hipStream_t s);   // one x
 hipError_t launch_linear8(const Linear8Args& a, hipStream_t s);
 hipError_t launch_beam_candidates(const BeamArgs& a, hipStream_t s);
 hipError_t launch_beam_select(const BeamSelectArgs& a, hipStream_t s);

@@ -90,6 +90,27 @@ def quantize_blocks(x: torch.Tensor, *, rows: int = 1, transpose: bool = False,
     return q, scale
 
 
+def quantize_both(x: torch.Tensor) -> tuple:
+    """llp_quantize_both: ``quantize_blocks(x)`` and ``quantize_blocks(x, rows=128, transpose=True)`` in one
+    pass over x: what the input's and the weight's gradient take of an upstream gradient. Returns
+    (q, scale, q_t, scale_t)."""
+    dev = _rows(x, "x")
+    R, Cc = x.shape
+    _ready(dev)
+    G, Gt = _blocks(Cc), _blocks(R)
+    q = torch.empty(R, G * _BLOCK, dtype=_F8, device=dev)
+    scale = torch.empty_strided((R, G), (1, max(R, 1)), dtype=_F32, device=dev)
+    q_t = torch.empty(Cc, Gt * _BLOCK, dtype=_F8, device=dev)
+    scale_t = torch.empty(G, Gt, dtype=_F32, device=dev)
+    at, dt, ld = x.data_ptr(), _DTYPE[x.dtype], _stride(x, R, Cc)
+    groups = A.llp_fp8_quant_request(at, dt, 1, ld, R, Cc, 0, 0, q.data_ptr(), G * _BLOCK,
+                                     scale.data_ptr(), max(R, 1))
+    blocks = A.llp_fp8_quant_request(at, dt, _BLOCK, ld, R, Cc, 1, 0, q_t.data_ptr(), Gt * _BLOCK,
+                                     scale_t.data_ptr(), Gt)
+    _call(dev, "llp_quantize_both", C.byref(groups), C.byref(blocks))
+    return q, scale, q_t, scale_t
+
+
 def _product(x, x_scale, weight, weight_scale, names):
     """The request of a product of two e4m3 operands."""
     dev = _tensor(x, names[0]).device
@@ -179,12 +200,17 @@ class _Fp8Linear(torch.autograd.Function):
         if dy.stride(1) != 1 or dy.stride(0) < dy.shape[1]:
             dy = dy.contiguous()
         dx = dw = None
-        if ctx.needs_input_grad[0]:
-            dx = linear_fp8(*quantize_blocks(dy), *quantize_blocks(weight, rows=_BLOCK, transpose=True),
-                            out_dtype=x.dtype)
-        if ctx.needs_input_grad[1]:
-            dw = dweight_fp8(*quantize_blocks(dy, rows=_BLOCK, transpose=True),
-                             *quantize_blocks(x, transpose=True), out_dtype=weight.dtype)
+        want_x, want_w = ctx.needs_input_grad[:2]
+        if want_x and want_w:
+            q, scale, q_t, scale_t = quantize_both(dy)
+        elif want_x:
+            q, scale = quantize_blocks(dy)
+        else:
+            q_t, scale_t = quantize_blocks(dy, rows=_BLOCK, transpose=True)
+        if want_x:
+            dx = linear_fp8(q, scale, *quantize_blocks(weight, rows=_BLOCK, transpose=True), out_dtype=x.dtype)
+        if want_w:
+            dw = dweight_fp8(q_t, scale_t, *quantize_blocks(x, transpose=True), out_dtype=weight.dtype)
         return dx, dw, None
 
 

@@ -43,6 +43,16 @@ void quant(int64_t R, int64_t K, int32_t dt, int block, int tr) {
   const int64_t n = block == 1 ? G : (M + 127) / 128, w = block == 1 ? M : G;
   r.scale_stride = w + 1; r.scale = arr<float>(span(n, w + 1, w));
   check("quant", llp_quantize_blocks(&r, nullptr), LLP_OK);
+  if (block == 1 && !tr) {
+    llp_fp8_quant_request t = r;
+    const int64_t Gr = (R + 127) / 128;
+    t.block_rows = 128; t.transpose = 1; t.q_stride = Gr * 128; t.q = arr<uint8_t>(span(K, Gr * 128, Gr * 128));
+    t.scale_stride = Gr; t.scale = arr<float>(span(G, Gr, Gr));
+    check("both", llp_quantize_both(&r, &t, nullptr), LLP_OK);
+    check("both swapped", llp_quantize_both(&t, &r, nullptr), LLP_ERR_INVALID_ARGUMENT);
+    t.x_stride += 1;
+    check("both apart", llp_quantize_both(&r, &t, nullptr), LLP_ERR_INVALID_ARGUMENT);
+  }
   done();
 }
 

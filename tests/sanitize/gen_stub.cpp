@@ -39,6 +39,12 @@ hipError_t launch_quant8(const Quant8Args& a, hipStream_t) {
   return hipSuccess;
 }
 
+hipError_t launch_quant8_both(const Quant8Args& a, const Quant8Args& t, hipStream_t s) {
+  const hipError_t e = launch_quant8(a, s);
+  --g_gen;
+  return e != hipSuccess ? e : launch_quant8(t, s);
+}
+
 hipError_t launch_linear8(const Linear8Args& a, hipStream_t) {
   ++g_gen;
   const int64_t K = (int64_t)a.steps * 128;

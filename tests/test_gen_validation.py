@@ -165,6 +165,7 @@ def test_reorder_refusals(over, want):
 def test_null_requests():
     lib = A.load()
     assert lib.llp_quantize_blocks(None, None) == INV
+    assert lib.llp_quantize_both(None, None, None) == INV
     assert lib.llp_linear_fp8(None, None) == INV and lib.llp_dweight_fp8(None, None) == INV
     assert lib.llp_beam_candidates(None, None, None) == INV
     assert lib.llp_beam_select(None, None, None) == INV
@@ -223,9 +224,12 @@ def test_quantize_binding():
                 dict(out=(torch.zeros(5, 256, dtype=torch.uint8), torch.zeros(2, 5).t()))):
         with pytest.raises(BAD):
             llp.quantize_blocks(x, **bad)
+    reaches_library(lambda: llp.quantize_both(x))
     for t in (x.half(), x[0], x.t(), x.to(torch.float64), None):
         with pytest.raises(BAD):
             llp.quantize_blocks(t)
+        with pytest.raises(BAD):
+            llp.quantize_both(t)
 
 
 @pytest.mark.parametrize("over", [

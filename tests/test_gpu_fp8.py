@@ -52,6 +52,25 @@ def test_quantize_blocks_exactly(llp, R, C, dtype, ld, transpose, rows):
     assert np.array_equal(codes(q), rq)
 
 
+@pytest.mark.parametrize("R,C,dtype,ld", [
+    (1, 1, "f32", 1), (3, 7, "bf16", 7), (129, 130, "f32", 131), (257, 320, "bf16", 320), (130, 1001, "bf16", 1003),
+    (33, 264, "f32", 268), (300, 384, "bf16", 384), (0, 5, "f32", 5), (5, 0, "bf16", 0)])
+def test_quantize_both_is_the_two_quantisations(llp, R, C, dtype, ld):
+    say(f"quantize_both R={R} C={C} {dtype} ld={ld}")
+    g = np.random.default_rng(R * 10007 + C)
+    x = torch.from_numpy(wild(g, R, ld))
+    x = (x.to(torch.bfloat16) if dtype == "bf16" else x).cuda()[:, :C]
+    if R > 200:
+        x[150, 140], x[3, 5], x[200] = float("nan"), float("inf"), 0
+    q, s, qt, st = llp.quantize_both(x)
+    want = (*llp.quantize_blocks(x), *llp.quantize_blocks(x, rows=128, transpose=True))
+    for a, b in zip((q, s, qt, st), want):
+        assert a.shape == b.shape and a.dtype == b.dtype
+        assert a.numel() == 0 or np.array_equal(host(a.contiguous().view(torch.uint8)) if a.dtype == torch.float8_e4m3fn else host(a),
+                                                host(b.contiguous().view(torch.uint8)) if a.dtype == torch.float8_e4m3fn else host(b),
+                                                equal_nan=a.dtype == torch.float32)
+
+
 def test_quantize_blocks_ties_and_odd_values(llp):
     # With 448 in a block its scale is fl(448 fl(1/448)) = 1: every midpoint of two e4m3 values, and its neighbours.
     mids = ((O.VALUES[1:] + O.VALUES[:-1]) / 2).astype(np.float32)
