@@ -5,7 +5,8 @@ tensors' own device and that device's current stream."""
 from __future__ import annotations
 
 import ctypes as C
-from typing import Optional, Sequence
+import functools
+from typing import NamedTuple, Optional, Sequence
 
 import torch
 from torch.autograd.function import once_differentiable
@@ -114,9 +115,12 @@ def quantize_both(x: torch.Tensor) -> tuple:
 def _product(x, x_scale, weight, weight_scale, names):
     """The request of a product of two e4m3 operands."""
     dev = _tensor(x, names[0]).device
-    _need(x, names[0], _F8, 2, dev)
+    if not (x.dtype is _F8 and x.dim() == 2 and x.is_contiguous()):
+        _need(x, names[0], _F8, 2, dev)
     T, K = x.shape
-    _need(weight, names[1], _F8, 2, dev, (None, K))
+    if not (type(weight) is torch.Tensor and weight.dtype is _F8 and weight.dim() == 2 and weight.device == dev
+            and weight.shape[1] == K and weight.is_contiguous()):
+        _need(weight, names[1], _F8, 2, dev, (None, K))
     V = weight.shape[0]
     if K % _BLOCK:
         raise ValueError(f"{names[0]} has {K} columns, not a multiple of {_BLOCK}")
@@ -314,12 +318,12 @@ def beam_select(parts: Sequence[dict], scores: torch.Tensor, num: Optional[int] 
     if not 1 <= world <= A.LLP_MAX_WORLD:
         raise ValueError(f"beam_select takes 1 to {A.LLP_MAX_WORLD} shards, got {world}")
     dev = _tensor(scores, "scores").device
-    _need(scores, "scores", _F32, 2, dev)
+    if not (scores.dtype is _F32 and scores.dim() == 2 and scores.is_contiguous()):
+        _need(scores, "scores", _F32, 2, dev)
+        raise ValueError("scores must be contiguous")
     B, K = scores.shape
     _num(K, "the number of beams")
     num = _num(K if num is None else num, "num")
-    if not scores.is_contiguous():
-        raise ValueError("scores must be contiguous")
     each = _tensor(parts[0]["value"], "parts[0]['value']").shape
     if len(each) != 2 or each[1] < num:
         raise ValueError(f"parts[0]['value'] has shape {tuple(each)}: {num} candidates a row are needed")
@@ -378,44 +382,47 @@ def _pieces(shape, *strides):
     return (dims[0][0], inner, dims[0][1]) if dims else (1, inner, (0,) * len(strides))
 
 
-class _Layout:
-    """What states of one layout share: beams K of a sequence, pieces and strides in bytes, and where
-    they are."""
-    __slots__ = ("K", "rows", "outer", "inner", "sr", "so", "dr", "do", "extent", "src_extent", "src", "dst")
+class _Layout(NamedTuple):
+    """States' pieces: beams K of a sequence read, rows written, strides and lengths in bytes."""
+    K: int
+    rows: int
+    outer: int
+    inner: int
+    sr: int
+    so: int
+    dr: int
+    do: int
+    extent: int
+    src_extent: int
 
 
-def _reorder_layout(s, d, i, B, N, dev):
-    """The checked layout of states[i] = s and what it goes to (inner 0: nothing to move)."""
-    if s.dim() < 1 or s.device != dev or d.device != dev or s.dtype != d.dtype or s.shape[1:] != d.shape[1:]:
-        raise ValueError(f"states[{i}] and what it goes to must be tensors [rows, ...] on {dev}, "
-                         "alike but for their rows")
-    if d.shape[0] != B * N or (s.shape[0] % B if B else s.shape[0]):
-        raise ValueError(f"states[{i}] has {s.shape[0]} rows, to be written {d.shape[0]}: {B} sequences "
-                         f"of {N} are expected")
-    c = _Layout()
-    c.src, c.dst, c.inner = [], [], 0
-    if s.numel() == 0 or d.numel() == 0:
-        if d.numel():
-            raise ValueError(f"states[{i}] holds no rows")
-        return c
-    p = _pieces(s.shape[1:], s.stride()[1:], d.stride()[1:])
+@functools.lru_cache(maxsize=1024)
+def _reorder_layout(shape, stride, to_shape, to_stride, size, B, N, in_place):
+    """The layout of a state and what it goes to, or None where there is nothing to move."""
+    if len(shape) < 1 or shape[1:] != to_shape[1:]:
+        raise ValueError("and what it goes to must be alike but for their rows")
+    if to_shape[0] != B * N or (shape[0] % B if B else shape[0]):
+        raise ValueError(f"has {shape[0]} rows, to be written {to_shape[0]}: {B} sequences of {N} "
+                         "are expected")
+    if 0 in to_shape:
+        return None
+    if shape[0] == 0:
+        raise ValueError("holds no rows")
+    p = _pieces(shape[1:], stride[1:], to_stride[1:])
     if p is None:
-        raise ValueError(f"states[{i}] of strides {s.stride()} is not rows of pieces at one stride")
-    size = s.element_size()
-    c.outer, c.inner, c.rows = p[0], p[1] * size, d.shape[0]
-    c.so, c.do = (st * size for st in p[2])
-    c.K = _num(s.shape[0] // B, "beams per sequence")
-    c.dr = d.stride(0) * size if c.rows > 1 else 0
-    c.sr = c.dr if d is s else s.stride(0) * size if s.shape[0] > 1 else 0
-    steps = sorted((st, n) for st, n in ((c.dr, c.rows), (c.do, c.outer)) if n > 1)
-    reach = c.inner
-    for st, n in steps:
+        raise ValueError(f"of strides {stride} is not rows of pieces at one stride")
+    outer, inner, rows = p[0], p[1] * size, to_shape[0]
+    so, do = (st * size for st in p[2])
+    K = _num(shape[0] // B, "beams per sequence")
+    dr = to_stride[0] * size if rows > 1 else 0
+    sr = dr if in_place else stride[0] * size if shape[0] > 1 else 0
+    reach = inner
+    for st, n in sorted((st, n) for st, n in ((dr, rows), (do, outer)) if n > 1):
         if st < reach:
-            raise ValueError(f"rows of {'out' if d is not s else 'states'}[{i}] overlap")
+            raise ValueError("has rows to be written that overlap")
         reach += (n - 1) * st
-    c.extent = (c.rows - 1) * c.dr + (c.outer - 1) * c.do + c.inner
-    c.src_extent = (s.shape[0] - 1) * c.sr + (c.outer - 1) * c.so + c.inner
-    return c
+    return _Layout(K, rows, outer, inner, sr, so, dr, do, (rows - 1) * dr + (outer - 1) * do + inner,
+                   (shape[0] - 1) * sr + (outer - 1) * so + inner)
 
 
 def beam_reorder(states, parents: torch.Tensor, *, out=None, status: Optional[torch.Tensor] = None):
@@ -439,32 +446,38 @@ def beam_reorder(states, parents: torch.Tensor, *, out=None, status: Optional[to
     if not parents.is_contiguous():
         raise ValueError("parents must be contiguous")
     _status(status, dev)
-    calls, seen = {}, []   # states of one layout go together
+    calls, seen, last = {}, [], None   # states of one layout go together
     for i, (s, d) in enumerate(zip(src, dst)):
         if not (isinstance(s, torch.Tensor) and isinstance(d, torch.Tensor)):
             raise TypeError(f"states[{i}] and what it goes to must be tensors")
-        key = (s.shape, s.stride(), s.dtype, s.device) if d is s else (
-            s.shape, s.stride(), s.dtype, s.device, d.shape, d.stride(), d.dtype, d.device)
-        call = calls.get(key)
-        if call is None:
-            call = calls[key] = _reorder_layout(s, d, i, B, N, dev)
-        if call.inner == 0:
+        if s.device != dev or d.device != dev or s.dtype != d.dtype:
+            raise ValueError(f"states[{i}] and what it goes to must be on {dev} and of one dtype")
+        key = (s.shape, s.stride(), s.dtype, d.shape, d.stride(), d is s)
+        if key != last:   # most are alike
+            try:
+                c = _reorder_layout(s.shape, s.stride(), d.shape, d.stride(), s.element_size(), B, N, d is s)
+            except ValueError as e:
+                raise ValueError(f"states[{i}] {e}") from None
+            # In place or not is a call's own.
+            src_at, dst_at = calls.setdefault((c, d is s), ([], []))
+            last = key
+        if c is None:
             continue
-        first = d.data_ptr()
-        seen.append((first, first + call.extent, i, call))
-        if d is not s and s.data_ptr() < first + call.extent and first < s.data_ptr() + call.src_extent:
+        at, to = s.data_ptr(), d.data_ptr()
+        seen.append((to, to + c.extent, i, c))
+        if d is not s and at < to + c.extent and to < at + c.src_extent:
             raise ValueError(f"out[{i}] overlaps states[{i}]")
-        call.src.append(s.data_ptr())
-        call.dst.append(first)
-    _apart(seen, [(s.data_ptr(), s) for s in src] if out is not None else [])
+        src_at.append(at)
+        dst_at.append(to)
+    _apart(seen, src if out is not None else [])
     if seen:
         _ready(dev)
-    for c in calls.values():
-        n = len(c.src)
+    for (c, _), (src_at, dst_at) in calls.items():
+        n = len(src_at)
         if n == 0:
             continue
         r = A.llp_beam_reorder_request(
-            (C.c_void_p * n)(*c.src), (C.c_void_p * n)(*c.dst), n, c.K, N, 0, B, c.outer, c.inner, c.sr,
+            (C.c_void_p * n)(*src_at), (C.c_void_p * n)(*dst_at), n, c.K, N, 0, B, c.outer, c.inner, c.sr,
             c.so, c.dr, c.do, parents.data_ptr(), _ptr(status))
         _call(dev, "llp_beam_reorder", C.byref(r))
     return states if out is None else out
@@ -479,7 +492,8 @@ def _apart(seen, sources):
                 break
             if not _interleaved(a, b):
                 raise ValueError(f"states {a[2]} and {b[2]} overlap")
-    for p, s in sources:
+    for s in sources:
+        p = s.data_ptr()
         end = p + s.element_size() * (1 + sum((n - 1) * st for n, st in zip(s.shape, s.stride())))
         for d in seen:
             if s.numel() and p < d[1] and d[0] < end:
@@ -490,7 +504,7 @@ def _interleaved(a, b):
     """Whether two states of one layout, the second no lower in memory, lie between each other's pieces,
     as the keys and values of a cache [rows, 2, ...] do."""
     c = a[3]
-    if b[3] is not c:
+    if b[3] != c:
         return False
     shift = b[0] - a[0]
     levels, extent = [], c.inner   # stride, steps, and the bytes of what lies within one step
