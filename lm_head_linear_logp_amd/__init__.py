@@ -14,8 +14,9 @@ Around it (ops.py): scoring with a head in 8-bit integers (``quantize_rows``,
 embedding (``embedding_forward``, ``embedding_backward``, as an autograd node ``embedding``).
 
 Decoding and training with a head in 8-bit floating point (gen.py): ``quantize_blocks``,
-``quantize_both``, the products ``linear_fp8`` and ``dweight_fp8`` (as an autograd node ``fp8_linear``), and a beam
-search's step (``beam_candidates``, ``beam_select``, ``beam_reorder``).
+``quantize_both``, the products ``linear_fp8`` and ``dweight_fp8`` (as an autograd node
+``fp8_linear``), and a beam search's step (``beam_candidates``, ``beam_select``,
+``beam_reorder``).
 """
 from __future__ import annotations
 
@@ -31,7 +32,8 @@ __all__ = ["LLPError", "open", "workspace_bytes", "forward", "forward_noalloc", 
            "keep_mask_replay", "SCRATCH_BYTES", "linear_logp", "quantize_rows", "forward_int8",
            "policy_grads", "policy_loss", "preference_grads", "preference_loss",
            "embedding_forward", "embedding_backward", "embedding", "quantize_blocks",
-           "quantize_both", "linear_fp8", "dweight_fp8", "fp8_linear", "beam_candidates", "beam_select", "beam_reorder"]
+           "quantize_both", "linear_fp8", "dweight_fp8", "fp8_linear", "beam_candidates",
+           "beam_select", "beam_reorder"]
 
 # Size of the static device scratch llp_forward_noalloc works in (include/llp.h).
 SCRATCH_BYTES = 32 << 20

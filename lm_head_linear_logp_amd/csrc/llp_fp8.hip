@@ -682,6 +682,10 @@ __device__ __forceinline__ void zero8(typename T::Acc& acc) {
       for (int r = 0; r < T::REGS; ++r) acc[mi][ni][r] = 0.f;
 }
 
+// The plain form, NST steps in flight: few rows, which the weight's bytes bound (fp32, 1 row of 151936 x 4096:
+// 106 us, 5.9 TB/s; 37 rows of 37984: 38, 4.1 TB/s, where x's lines take as much of the loads as the weight's),
+// and fp32 results of many (4096 x 37984 x 4096: 1170 us, 1.09e15/s of 1.54e15 that the library's bf16
+// product reaches).
 template <int TM, int TN, int WM, int WN, int NST, bool GRAD, bool FULL, int EU>
 __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(EU, EU))) void k_linear8(Linear8Args a) {
   using T = Tile8<TM, TN, WM, WN, NST, FULL>;
@@ -811,6 +815,11 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(EU
 // the sums before them are scaled; the next step's first fragments are read under the last rows'
 // MFMAs. The barrier in front of those frees the step's stage, into which from there on a later step is
 // loaded, one load after an MFMA (nine in a row hold up the wave's MFMAs: 5 % slower).
+//
+// 4096 x 37984 x 4096: 561 us, 2.27e15/s; 4096 x 151936: 2.13 ms, 2.39e15/s; its gradients 490 (x) and 507 (weight);
+// the library's product of the same bytes with one scale a matrix 517, 1769 and 384 (x). Bound by LDS and matrix
+// cores alike: a step's operands are 196 KB of reads and 64 KB of writes, 2030 cycles at 128 bytes each, and its MFMAs
+// 2048; eight waves of 128 x 64 are what the registers hold with sums that vector instructions scale.
 template <int MB_, int NB_>
 struct Wide8 {
   static constexpr int S = 16, REGS = 4, MB = MB_, NB = NB_;
@@ -1045,8 +1054,9 @@ hipError_t launch_linear8(const Linear8Args& a, hipStream_t s) {
     return launch_linear8_as<128, 128, 2, 2, 2, true, true, 2>(a, s);
   }
   // Few rows, the weight's bytes bound them: where 128 columns a workgroup would leave compute units
-  // with one, and so with two steps in flight, 64 columns each (us, 128 and 64 columns: 1 row of 37984 44.5 and
-  // 40.8, of 151936 121 and 126; 37 rows 52.2 and 45.8; 64 rows of 151936 149 and 159).
+  // with one, and so with two steps in flight, 64 columns each (us in fp32, 128 and 64 columns: 1 row of 37984 36.7
+  // and 33.2, of 151936 108 and 112; 37 rows 43.5 and 38.5, of 151936 129 and 140). More steps in flight (4 to 6)
+  // or 256 columns are no faster.
   const bool narrow = a.V < 65536;
   if (a.out_bf16) {
     if (a.T <= 32) return narrow ? launch_linear8_as<64, 32, 2, 1, 3, false, false, 2>(a, s)
