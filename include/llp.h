@@ -647,7 +647,7 @@ typedef struct {
  *   num        candidates in each row of the parts; num_out chosen, 1 <= num_out <= num <=
  *              LLP_MAX_BEAMS (so the choice is one over the whole vocabulary); num_seqs < 2^22
  * A candidate's total is score + ((x - M) c - log(sum_r sum[r] e^{(max[r] - M) c})) with M =
- * max_r max[r] and c = fl32(1/temperature), in fp64. Chosen are the num_out largest totals above -inf, by total
+ * max_r max[r] and c = fl32(1/temperature), in fp64; one whose token is outside [0, 2^40) is none. Chosen are the num_out largest totals above -inf, by total
  * descending, then beam, then token ascending.
  * A beam whose score is -inf has no candidates; nor has one whose score is NaN or +inf or whose
  * row has sum < 0 in a shard, which sets LLP_STATUS_VALUE_NOT_FINITE. */

@@ -120,6 +120,53 @@ def test_beam_candidates_of_masked_and_broken_rows(llp):
     assert llp.beam_candidates(z[:0], 3, real_vocab=4000)["token"].shape == (0, 3)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_beam_candidates_find_what_is_not_finite_anywhere(llp, dtype):
+    # 2 whole blocks of 2048 and 13 columns, of which the last few are no whole 16 bytes.
+    V = 4109
+    g = np.random.default_rng(11)
+    good = g.standard_normal((1, V)).astype(np.float32)
+    bad = []
+    for at, what in ((0, np.nan), (2047, np.nan), (2048, np.inf), (4095, np.nan), (4096, np.nan), (4103, np.inf), (V - 1, np.nan),
+                     (V - 1, np.inf), (slice(0, 2048), np.nan), (slice(2048, 4096), np.inf), (slice(4096, V), np.nan),
+                     (slice(0, V), np.nan), (slice(0, V), np.inf)):
+        x = good.copy()
+        x[0, at] = what
+        bad.append(x)
+        y = np.full((1, V), -np.inf, np.float32)   # the only value that is no mask
+        y[0, at] = what
+        bad.append(y)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = llp.beam_candidates(rows16(np.concatenate([good, *bad, good]), dtype), 5, status=st)
+    assert int(st) == llp.STATUS_BITS["VALUE_NOT_FINITE"]
+    s = host(got["sum"])
+    assert (s[1:-1] == -1).all() and s[0] > 0 and s[-1] == s[0]
+    assert (host(got["token"])[1:-1] == -1).all() and (host(got["value"])[1:-1] == -np.inf).all()
+    assert (host(got["token"])[[0, -1]] >= 0).all() and (host(got["max"])[1:-1] == -np.inf).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_beam_candidates_of_the_widest_shard(llp, dtype):
+    V = 1 << 21
+    say(f"beam_candidates V={V} {dtype}")
+    x = np.random.default_rng(12).standard_normal((1, V)) * 2
+    z = torch.from_numpy(x.astype(np.float32)).to(dtype).cuda()
+    got = llp.beam_candidates(z, 64)
+    check_candidates(got, host(z.float()), 64, 1.0)
+    # Equal values everywhere: every piece reaches the bar, the first columns win.
+    z.fill_(1.5)
+    check_candidates(llp.beam_candidates(z, 64), host(z.float()), 64, 1.0)
+
+
+def test_beam_select_takes_no_token_that_is_none(llp):
+    # Ids that no vocabulary holds, as a caller's own candidates might have them.
+    part = dict(value=torch.tensor([[3.0, 2.0, 1.0, 0.0]], device="cuda"),
+                token=torch.tensor([[1 << 40, 5, -7, 1 << 62]], device="cuda"),
+                max=torch.tensor([3.0], device="cuda"), sum=torch.tensor([2.0], dtype=torch.float64, device="cuda"))
+    got = llp.beam_select([part], torch.zeros(1, 1, device="cuda"), 4)
+    assert host(got["token"]).tolist() == [[5, -1, -1, -1]] and host(got["parent"]).tolist() == [[0, -1, -1, -1]]
+
+
 def step(llp, z, B, K, num, tau, scores, shards, real, finished=None, end=None, status=None):
     pad = z.shape[1]
     cuts = [min(pad, i * (-(-pad // shards) + 8) // 8 * 8) for i in range(shards)] + [pad]
