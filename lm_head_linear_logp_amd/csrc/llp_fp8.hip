@@ -1049,6 +1049,15 @@ static hipError_t launch_linear8_bf16(const Linear8Args& a, hipStream_t s) {
 
 hipError_t launch_linear8(const Linear8Args& a, hipStream_t s) {
   if (a.T <= 0 || a.V <= 0) return hipSuccess;
+  // Results that two tiles of 64 x 64 a compute unit hold: latency, so the smallest tiles (us, these and the forms
+  // below, 4096 deep unless noted: 64 rows of 4096 fp32 20 and 24, bf16 15 and 17; 200 rows of 4096 fp32 23 and 39,
+  // bf16 16 and 23, 37984 deep 114 and 162; with 600 tiles and more they are slower, 200 rows of 9000 bf16 29 and 23).
+  if ((a.grad || a.T > 32) && (a.V + 63) / 64 * ((a.T + 63) / 64) <= 512) {
+    if (a.grad) return a.out_bf16 ? launch_linear8_as<64, 64, 2, 2, 3, true, false, 2>(a, s)
+                                  : launch_linear8_as<64, 64, 2, 2, 3, true, true, 2>(a, s);
+    return a.out_bf16 ? launch_linear8_as<64, 64, 2, 2, 3, false, false, 2>(a, s)
+                      : launch_linear8_as<64, 64, 2, 2, 3, false, true, 2>(a, s);
+  }
   if (a.grad) {
     if (a.out_bf16) return launch_linear8_bf16<true>(a, s);
     return launch_linear8_as<128, 128, 2, 2, 2, true, true, 2>(a, s);

@@ -319,7 +319,7 @@ def quantised(llp, R, K, rows, seed):
 
 # Each reaches another shape of workgroup; columns past several turns of the groups' order, ragged ends.
 @pytest.mark.parametrize("T,V", [(65, 203), (130, 16389), (644, 10802), (258, 21804), (65, 32830), (130, 32900), (193, 33012),
-                                 (259, 32795), (196, 20535), (386, 16432), (387, 21949), (130, 20681), (321, 21856),
+                                 (259, 32795), (196, 20535), (386, 16432), (387, 21949), (130, 20681), (321, 21856), (65, 16411),
                                  (1, 70003), (33, 66001)])
 @pytest.mark.parametrize("out", ["bf16", "f32"])
 def test_products_have_the_same_bits_in_every_form(llp, T, V, out):
