@@ -7,12 +7,15 @@
 
 namespace llp {
 
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
 // ------------------------------------------------------------------------------------
 // Quantisation: scale = max(max |x|, 1e-30) * fl32(1/448) over 1 or 128 rows of 128 columns, q =
 // x / scale as e4m3 (ties to even). By blocks, or transposed, a workgroup holds a 128 x 128 tile of x in
 // registers, 8 x 8 values a thread, so that either costs one read and one write; the transpose goes
-// through LDS and out in whole 128-byte rows. Bound by memory: 37984 x 4096 bf16 (467 MB) in blocks 90 us,
-// 5.2 TB/s, a copy's rate; transposed 100; by group 108; 4096 x 37984 transposed, in blocks 103, by group 107.
+// through LDS and out in whole 128-byte rows. x, and a transposed q, go past the caches, which hold neither (90 ->
+// 79 us in blocks, 376 -> 345 transposed in blocks, 107 -> 103 by group). Bound by memory: 37984 x 4096 bf16 (467 MB)
+// in blocks 79 us, 5.9 TB/s; transposed 95; 4096 x 37984 by group 103, transposed in blocks 102, by group 107.
 // (Maxima on the values' bits, moves between lanes instead of LDS shuffles, the hardware's reciprocal and bf16
 // kept as it is loaded: together 15 % off.)
 // ------------------------------------------------------------------------------------
@@ -26,17 +29,20 @@ template <bool BF16, bool VEC>
 __device__ __forceinline__ void q8_load(const void* row, int64_t c, int64_t cols, float (&v)[8]) {
   if (VEC && c + 8 <= cols) {
     if constexpr (BF16) {
-      const u32x4 u = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(row) + c);
+      const u32x4 u = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(row) + c));
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         v[2 * i] = __builtin_bit_cast(float, u[i] << 16);
         v[2 * i + 1] = __builtin_bit_cast(float, u[i] & 0xFFFF0000u);
       }
     } else {
-      const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(row) + c);
-      const float4 b = *reinterpret_cast<const float4*>(static_cast<const float*>(row) + c + 4);
-      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+      const f32x4* const p = reinterpret_cast<const f32x4*>(static_cast<const float*>(row) + c);
+      const f32x4 lo = __builtin_nontemporal_load(p), hi = __builtin_nontemporal_load(p + 1);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[i] = lo[i];
+        v[4 + i] = hi[i];
+      }
     }
   } else {
 #pragma unroll
@@ -155,7 +161,8 @@ __device__ __forceinline__ void q8_tile(const Quant8Args& a, int64_t r0, int64_t
       if (whole > 0) {
 #pragma unroll
         for (int i = 0; i < N; i += 4)
-          *reinterpret_cast<u32x4*>(&v[p].u[i]) = *reinterpret_cast<const u32x4*>(row + (c < whole ? c : whole - 8) * SIZE + 4 * i);
+        *reinterpret_cast<u32x4*>(&v[p].u[i]) =
+            __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(row + (c < whole ? c : whole - 8) * SIZE + 4 * i));
       }
     }
     if (c0 + 128 > whole) {
@@ -213,7 +220,7 @@ __device__ __forceinline__ void q8_turned_store(const uint8_t* turned, const Qua
     const uint2 lo = *reinterpret_cast<const uint2*>(turned + c * 128 + ((2 * h) ^ (c >> 3)) * 8);
     const uint2 hi = *reinterpret_cast<const uint2*>(turned + c * 128 + ((2 * h + 1) ^ (c >> 3)) * 8);
     if (c0 + c < a.cols)
-      *reinterpret_cast<uint4*>(a.q + (c0 + c) * a.ldq + r0 + 16 * h) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+      __builtin_nontemporal_store(u32x4{lo.x, lo.y, hi.x, hi.y}, reinterpret_cast<u32x4*>(a.q + (c0 + c) * a.ldq + r0 + 16 * h));
   }
 }
 
@@ -433,7 +440,6 @@ hipError_t launch_quant8_both(const Quant8Args& a, const Quant8Args& t, hipStrea
 // has the same bits whatever the tile and however many rows the call has.
 // ------------------------------------------------------------------------------------
 typedef int i32x8 __attribute__((ext_vector_type(8)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ f32x4 mfma8(const i32x8& a, const i32x8& b) {
   // Scales of 0: the form without block scales; formats 0: e4m3.
