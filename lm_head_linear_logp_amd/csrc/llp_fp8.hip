@@ -20,8 +20,8 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 // kept as it is loaded: together 15 % off.)
 // ------------------------------------------------------------------------------------
 constexpr int Q8_THREADS = 256;
-// Groups from which a team takes four rows instead of one (us: 4096 x 4096 bf16 17.4 and 14.3, 4096 x 37984
-// 125 and 130, 37984 x 4096 109 and 123).
+// Groups from which a team takes four rows instead of one (us: 4096 x 4096 bf16 20.6 and 18.0, 16384 x 4096 51
+// and 51, 37984 x 4096 110 and 119).
 constexpr int64_t Q8_MANY_GROUPS = 1 << 19;
 
 // Columns c .. c + 7 of a row, 0 at and past `cols`. VEC: rows are 16-byte aligned.
