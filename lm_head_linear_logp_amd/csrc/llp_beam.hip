@@ -395,8 +395,9 @@ __global__ __launch_bounds__(64 * BEAM_WAVES) void k_beam_rows(BeamArgs a) {
 
 hipError_t launch_beam_candidates(const BeamArgs& a, hipStream_t s) {
   if (a.rows <= 0) return hipSuccess;
-  // As many waves on a row as leave no compute unit a second round of workgroups (a unit holds 20 waves).
-  int waves = a.rows <= 256 ? 16 : a.rows <= 512 ? 8 : 4;
+  // Waves on a row: a compute unit holds 20 (us a call for 4, 8 and 16 waves: 4 rows of 151669 fp32 26, 21 and 20;
+  // 512 rows 59, 60 and 64; 1000 rows 111, 107 and 120; of 37917 bf16 512 rows 23, 19 and 26, 2000 rows 50, 61 and 91).
+  int waves = a.rows <= 256 ? 16 : a.rows <= 1024 ? 8 : 4;
   if (waves > a.blocks) waves = a.blocks > 0 ? a.blocks : 1;
   const dim3 grid((unsigned)a.rows), block(64 * waves);
   const size_t lds = beam_lds(waves, a.blocks);

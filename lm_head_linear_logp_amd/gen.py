@@ -314,6 +314,8 @@ def beam_select(parts: Sequence[dict], scores: torch.Tensor, num: Optional[int] 
     its own score. Returns token int64, parent int32 (the beam continued) and score fp32, [B, num],
     best first, ties to the lowest beam and token; where too few candidates are there token and
     parent are -1 and the score is -inf."""
+    if isinstance(parts, dict):
+        raise TypeError("parts is a sequence: the shards' results of beam_candidates in rank order")
     world = len(parts)
     if not 1 <= world <= A.LLP_MAX_WORLD:
         raise ValueError(f"beam_select takes 1 to {A.LLP_MAX_WORLD} shards, got {world}")

@@ -298,7 +298,7 @@ def test_select_binding():
                       ([part()], dict(finished=torch.zeros(3, 4), end_id=1)),
                       ([part()], dict(finished=torch.zeros(4, 3, dtype=torch.uint8).t(), end_id=1)),
                       ([part()], dict(out=dict(token=torch.zeros(3, 4), parent=torch.zeros(3, 4), score=torch.zeros(3, 4)))),
-                      ([part()] * 65, {})):
+                      ([part()] * 65, {}), (part(), {})):
         with pytest.raises(BAD):
             llp.beam_select(parts, s, **kw)
     for t in (s.double(), s[0], torch.zeros(4, 3).t(), torch.zeros(3, 0), torch.zeros(1, 65)):
