@@ -210,3 +210,39 @@ def test_the_smallest_and_odd_decoding(llp):
     assert host(got["parent"]).tolist() == [[0, 1, -1, -1]] and host(got["token"]).tolist() == [[0, 0, -1, -1]]
     x = torch.arange(8.0, device="cuda").reshape(4, 2)
     assert torch.equal(llp.beam_reorder(x.clone(), got["parent"]), x)
+
+
+def test_a_captured_autograd_step_replays_as_the_eager_one(llp):
+    # Forward and backward of the autograd node recorded together, its leaves' gradients taken, not accumulated.
+    T, H2, V2 = 150, 256, 400
+    x = torch.zeros(T, H2, dtype=torch.bfloat16, device="cuda", requires_grad=True)
+    w = torch.zeros(V2, H2, dtype=torch.bfloat16, device="cuda", requires_grad=True)
+    dy = torch.zeros(T, V2, dtype=torch.bfloat16, device="cuda")
+
+    def step():
+        y = llp.fp8_linear(x, w)
+        return (y.detach(), *torch.autograd.grad(y, (x, w), dy))
+
+    def fill(seed):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        with torch.no_grad():
+            for t in (x, w, dy):
+                t.copy_(torch.randn(t.shape, generator=g, device="cuda"))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        fill(0)
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for seed in (1, 2, 3):
+        fill(seed)
+        want = [t.clone() for t in step()]
+        torch.cuda.synchronize()
+        graph.replay()
+        assert all(bytes_equal(a, b) for a, b in zip(out, want)), seed
+        torch.cuda.synchronize()
