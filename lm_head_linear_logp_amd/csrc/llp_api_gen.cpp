@@ -361,9 +361,8 @@ LLP_API llp_status llp_beam_reorder(const llp_beam_reorder_request* req, void* s
   if (st != LLP_OK) return st;
   if (!work) return LLP_OK;
   const int64_t per = (p.outer * (p.inner / unit) + 255) / 256 * p.num_seqs;
-  int64_t most = (int64_t(1) << 24) / per;   // states of one launch
+  int64_t most = ((int64_t(1) << 24) - 1) / per;   // states of one launch, within that limit
   if (most > REORDER_STATES) most = REORDER_STATES;
-  if (most < 1) most = 1;
   for (int32_t i = 0; i < p.num_states; i += (int32_t)most) {
     ReorderArgs a{};
     a.states = (int32_t)(p.num_states - i < most ? p.num_states - i : most);
