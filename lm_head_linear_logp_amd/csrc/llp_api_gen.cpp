@@ -162,7 +162,7 @@ llp_status check_beam(const llp_beam_request* req, float* c1) {
   if (st != LLP_OK) return st;
   LLP_CHECK(req->num_rows >= 0 && req->num_rows < (int64_t(1) << 22), LLP_ERR_INVALID_ARGUMENT,
             "num_rows %lld outside [0, 2^22)", (long long)req->num_rows);
-  // A workgroup keeps 36 bytes for every 2048 columns.
+  // A workgroup keeps 32 bytes of LDS for every 2048 columns.
   LLP_CHECK(req->vocab.local_size <= (int64_t(1) << 21), LLP_ERR_UNSUPPORTED,
             "local_size %lld exceeds 2^21", (long long)req->vocab.local_size);
   LLP_CHECK(req->vocab.padded_vocab < kMaxStride, LLP_ERR_UNSUPPORTED, "padded_vocab must be < 2^40");

@@ -53,14 +53,6 @@ __device__ __forceinline__ float wave_max(float x) {
   x = fmaxf(x, across<16>(x));
   return fmaxf(x, across<32>(x));
 }
-__device__ __forceinline__ float wave_sum(float x) {
-  x += across<1>(x);
-  x += across<2>(x);
-  x += across<4>(x);
-  x += across<8>(x);
-  x += across<16>(x);
-  return x + across<32>(x);
-}
 __device__ __forceinline__ double wave_sum(double x) {
   auto add = [&](auto j) {
     const uint64_t u = __builtin_bit_cast(uint64_t, x);
@@ -203,15 +195,18 @@ struct Best {
 // than num, are read again for the values that do, and sorted.
 //
 // Bound by memory with many rows: one read of the logits, past the caches (512 rows of 151669 fp32 columns, 311
-// MB: 56 us, 5.6 TB/s). With few, a row is one compute unit's, and its exponentials bound it (4 rows: 17 us; 80
-// bf16 rows of a shard of 37984: 12). Several workgroups a row and a second launch that joins them took 7.3 + 6
-// us on the device for the 4 rows (62 + 6 for the 512, 10 + 4.6 for the 80), but 17.8 instead of 10.9 us a call on
-// the host, which bounds a beam search's step.
+// MB: 58 us, 5.4 TB/s). With few, a row is one compute unit's, and its exponentials and their sums bound it (4
+// rows: 19 us; 80 bf16 rows of a shard of 37984: 11). Several workgroups a row and a second launch that joins them
+// took 7.3 + 6 us on the device for 4 rows (where this form, with sums in fp32, took 17; 62 + 6 for the 512, 10 +
+// 4.6 for the 80), but 17.8 instead of 10.9 us a call on the host, which bounds a beam search's step.
 //
 // exp((x - max) c) as 2^t, t = (x - max) c log2 e with the constant in two parts: its rounding would shift
-// every term alike, by 2e-7 for the bulk of a row; t's own roundings, and the exponential's, differ in
-// sign from term to term, so that a sum over thousands of columns is off by about 1e-8 and two beams'
-// totals closer than that are rare.
+// every term alike, by 2e-7 for the bulk of a row. A term e in fp32 is off by an ulp of the exponential and by t's
+// two roundings, 2^-23 e (1 + (max - x) c) together at most; a block's largest is 1 exactly. Sums are in fp64:
+// in fp32 a token with most of a row's mass takes the last bits of all that is added to it (measured up to 2.9e-7
+// of the sum; fp64 costs 5 to 11 % of the time with few rows, 1 to 5 % with many). What is left is at most 2^-23
+// of the mass beside the largest token times that factor (measured: flat rows 3e-9 of the sum, 12 likely tokens 2e-9
+// to 7e-9 rms, 5001 columns of one lower value 4e-8).
 // ------------------------------------------------------------------------------------
 constexpr int BEAM_WAVES = 16;   // of a workgroup, at most
 typedef float f32x4 __attribute__((ext_vector_type(4)));
@@ -261,9 +256,9 @@ __device__ __forceinline__ void beam_load(const void* row, int64_t c0, int64_t n
   }
 }
 
-// LDS of a row: keys that wait for each wave, each wave's best, the pieces' largest values, the blocks' sums
-// and the pieces to read again.
-static size_t beam_lds(int waves, int blocks) { return (size_t)waves * 192 * sizeof(Key64) + (size_t)blocks * 36; }
+// LDS of a row: keys that wait for each wave, each wave's best, the blocks' sums, the pieces' largest values
+// and the pieces to read again (64 KB at most).
+static size_t beam_lds(int waves, int blocks) { return (size_t)waves * 192 * sizeof(Key64) + (size_t)blocks * 32; }
 
 template <bool BF16>
 __global__ __launch_bounds__(64 * BEAM_WAVES) void k_beam_rows(BeamArgs a) {
@@ -275,9 +270,9 @@ __global__ __launch_bounds__(64 * BEAM_WAVES) void k_beam_rows(BeamArgs a) {
   const int waves = blockDim.x >> 6, pieces = 4 * a.blocks;
   Key64* const room = reinterpret_cast<Key64*>(smem);
   Key64* const lists = room + waves * 128;
-  float* const tops = reinterpret_cast<float*>(lists + waves * 64);
-  float* const sums = tops + pieces;
-  int* const reread = reinterpret_cast<int*>(sums + a.blocks);
+  double* const sums = reinterpret_cast<double*>(lists + waves * 64);
+  float* const tops = reinterpret_cast<float*>(sums + a.blocks);
+  uint16_t* const reread = reinterpret_cast<uint16_t*>(tops + pieces);   // the host keeps pieces at 4096
   const int64_t r = blockIdx.x;
   const char* const row = static_cast<const char*>(a.logits) + r * a.ld * (BF16 ? 2 : 4);
   const double cl = (double)a.c1 * 1.4426950408889634074;
@@ -300,13 +295,13 @@ __global__ __launch_bounds__(64 * BEAM_WAVES) void k_beam_rows(BeamArgs a) {
     top = fmaxf(top, across<32>(top));
     // A NaN, which the maxima pass over, or +inf makes the sum NaN.
     const float base = top > -INFINITY ? top : 0.f;
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    double s[2] = {0.0, 0.0};
 #pragma unroll
     for (int e = 0; e < 32; ++e) {
       const float d = x[e] - base;
-      s[e & 3] += __builtin_amdgcn_exp2f(fmaf(d, ch, d * clo));
+      s[e & 1] += (double)__builtin_amdgcn_exp2f(fmaf(d, ch, d * clo));
     }
-    const float sum = wave_sum((s[0] + s[1]) + (s[2] + s[3]));
+    const double sum = wave_sum(s[0] + s[1]);
     if (lane == 0) sums[b] = sum;
   }
   __syncthreads();
@@ -321,7 +316,7 @@ __global__ __launch_bounds__(64 * BEAM_WAVES) void k_beam_rows(BeamArgs a) {
       const float top = i + lane < pieces ? tops[i + lane] : -INFINITY;
       const bool in = top >= bar && top > -INFINITY;
       const uint64_t all = __builtin_amdgcn_ballot_w64(in);
-      if (in) reread[n + __popcll(all & ((1ull << lane) - 1))] = i + lane;
+      if (in) reread[n + __popcll(all & ((1ull << lane) - 1))] = (uint16_t)(i + lane);
       n += __popcll(all);
     }
     if (lane == 0) {
@@ -340,7 +335,7 @@ __global__ __launch_bounds__(64 * BEAM_WAVES) void k_beam_rows(BeamArgs a) {
     if (!bad && M > -INFINITY) {
       for (int i = lane; i < a.blocks; i += 64) {
         const float m = fmaxf(fmaxf(tops[4 * i], tops[4 * i + 1]), fmaxf(tops[4 * i + 2], tops[4 * i + 3]));
-        if (m > -INFINITY) S += (double)sums[i] * exp(((double)m - (double)M) * (double)a.c1);
+        if (m > -INFINITY) S += sums[i] * exp(((double)m - (double)M) * (double)a.c1);
       }
       S = wave_sum(S);
     }
