@@ -1,0 +1,199 @@
+"""Products of e4m3 operands in the forms that many results take (the wide tiles, 128 x 128 in fp32): against sums in
+64 bits and, bit for bit, against the forms of few rows, with biases, strides, depths of one to many groups, what
+lies around the output, scales that are not finite, and gradients that are added to."""
+import pytest
+import torch
+
+from tests._gpu import bytes_equal, need_gpu, say
+
+pytestmark = pytest.mark.gpu
+EPS = 2.0 ** -24   # half a step of fp32
+
+
+@pytest.fixture(scope="module")
+def llp():
+    need_gpu()
+    import lm_head_linear_logp_amd as m
+    m.open(0)
+    return m
+
+
+def wide_shape(T, V):
+    """The wide tile that bf16 results of T x V take: 32 m x 64 n, the fewest rounds of 256 workgroups times work."""
+    best = None
+    for m in (8, 5, 4):
+        for n in (5, 4, 3, 2):
+            if m * n <= 32:
+                tiles = -(-V // (32 * m)) * -(-T // (64 * n))
+                cost = -(-tiles // 256) * (m * n + 10 + (2 if m == 5 else 0))
+                if best is None or cost < best[0]:
+                    best = cost, (m, n)
+    return best[1]
+
+
+# Results of more than 512 tiles of 64 x 64, of each wide shape; the depths are 1 to 33 groups.
+SIZES = [(130, 16389, 128), (644, 10802, 256), (258, 21804, 384), (65, 32830, 512), (130, 32900, 640), (193, 33012, 128),
+         (259, 32795, 4224), (196, 20535, 896), (386, 16432, 128), (387, 21949, 256), (130, 20681, 384), (321, 21856, 4096),
+         (65, 16411, 128)]
+
+
+def test_the_sizes_reach_every_wide_shape():
+    shapes = {wide_shape(T, V) for T, V, _ in SIZES}
+    assert shapes == {(4, 2), (4, 3), (4, 4), (4, 5), (5, 2), (5, 3), (5, 4), (5, 5), (8, 2), (8, 3), (8, 4)}
+    assert all(-(-T // 64) * -(-V // 64) > 512 and T > 64 for T, V, _ in SIZES)
+
+
+def normal(g, *shape):
+    return torch.randn(*shape, generator=g, device="cuda")
+
+
+def operands(llp, T, V, K, seed):
+    """Operands quantised, and inside wider ones whose other bytes and scales are NaN."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    xq, xs = llp.quantize_blocks(normal(g, T, K) * torch.exp(normal(g, 1, K)))
+    wq, ws = llp.quantize_blocks(normal(g, V, K) * 0.02, rows=128)
+    x = torch.full((T, K + 32), 0x7F, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    x[:, 16:16 + K] = xq
+    w = torch.full((V, K + 64), 0x7F, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    w[:, 32:32 + K] = wq
+    sx = torch.full((K // 128, T + 7), float("nan"), device="cuda")
+    sx[:, 5:5 + T] = xs.t()
+    sw = torch.full((ws.shape[0], K // 128 + 3), float("nan"), device="cuda")
+    sw[:, 1:1 + K // 128] = ws
+    return (xq, xs, wq, ws), (x[:, 16:16 + K], sx[:, 5:5 + T].t(), w[:, 32:32 + K], sw[:, 1:1 + K // 128])
+
+
+def values(q, s, rows):
+    return q.double() * s.double().repeat_interleave(128, 1).repeat_interleave(rows, 0)[:q.shape[0]]
+
+
+def reference(xq, xs, wq, ws):
+    x, w = values(xq, xs, 1), values(wq, ws, 128).t().contiguous()
+    return x @ w, x.abs() @ w.abs()
+
+
+def within(y, ref, size, K, step):
+    """Into fp32 a group's 128 products are summed with at most one rounding each (2^-23, in case the matrix cores
+    truncate), then scaled and added: 2 more of 2^-24 a group and the scales' product. Into bf16 the 8-bit
+    matrix instructions sum instead, which cut each of 8 products towards zero at 2^-13 of the largest one's
+    power of two: 7 such cuts of at most the sum of 8 products' sizes; over many elements they stay
+    below 2^-13 of the norm. `step` is half a step of the result's type."""
+    slack = size * EPS * (2 * 128 + 2 * -(-K // 128) + 4)
+    if y.dtype == torch.bfloat16:
+        slack = slack + size * 7 * 2.0 ** -13
+    err = (y.double() - ref).abs()
+    over = float((err / (slack + (ref.abs() + slack) * step).clamp_min(1e-300)).max())
+    assert over <= 1, f"{over:.3g} of the bound"
+    if y.dtype == torch.bfloat16:
+        assert float(err.norm()) <= (2.0 ** -8 + 2.0 ** -13) * float(ref.norm())
+
+
+def by_few_rows(llp, x, xs, w, ws, bias, d):
+    """The same product 32 rows at a time and, so that the columns' blocks and order are the call's, whole
+    turns of 1280 times the groups apart."""
+    turn = 1280 * (x.shape[1] // 128) if x.shape[1] < 2048 else w.shape[0]
+    cols = [slice(v, min(v + turn, w.shape[0])) for v in range(0, w.shape[0], turn)]
+    return torch.cat([torch.cat([llp.linear_fp8(x[t:t + 32], xs[t:t + 32], w[c], ws[c.start // 128:-(-c.stop // 128)],
+                                                bias=None if bias is None else bias[c], out_dtype=d)
+                                 for t in range(0, x.shape[0], 32)]) for c in cols], 1)
+
+
+@pytest.mark.parametrize("T,V,K", SIZES)
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_linear_fp8_of_many_results(llp, T, V, K, out):
+    say(f"forms: linear T={T} V={V} K={K} {out} {wide_shape(T, V)}")
+    d = torch.bfloat16 if out == "bf16" else torch.float32
+    plain, inside = operands(llp, T, V, K, T + V)
+    ref, size = reference(*plain)
+    g = torch.Generator(device="cuda").manual_seed(V)
+    for bias, pad in ((None, 0), (torch.float32, 3), (torch.bfloat16, 16)):
+        b = None if bias is None else normal(g, V).to(bias)
+        room = torch.full((T + 2, V + pad), 7.0, dtype=d, device="cuda")
+        y = llp.linear_fp8(*inside, bias=b, out=room[1:T + 1, :V])
+        assert (room[0] == 7).all() and (room[T + 1] == 7).all() and (room[:, V:] == 7).all()
+        r = ref if b is None else ref + b.double()
+        s = size if b is None else size + b.double().abs()
+        within(y, r, s, K, EPS if out == "f32" else 2.0 ** -8)
+        assert bytes_equal(y.contiguous(), by_few_rows(llp, *plain, b, d))
+
+
+@pytest.mark.parametrize("T,V,K", SIZES[::2])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_scales_that_are_not_finite_stay_in_their_rows_and_blocks(llp, T, V, K, out):
+    say(f"forms: NaN scales T={T} V={V} K={K} {out}")
+    d = torch.bfloat16 if out == "bf16" else torch.float32
+    (xq, xs, wq, ws), _ = operands(llp, T, V, K, V)
+    want = llp.linear_fp8(xq, xs, wq, ws, out_dtype=d)
+    xs, ws = xs.t().contiguous().t(), ws.clone()
+    blocks = (1, ws.shape[0] // 2, ws.shape[0] - 1)
+    for t in (0, 63, T - 1):
+        xs[t, K // 128 - 1] = float("nan")
+    for b in blocks:
+        ws[b, 0] = float("nan")
+    bad = torch.zeros((T, V), dtype=torch.bool, device="cuda")
+    bad[[0, 63, T - 1]] = True
+    for b in blocks:
+        bad[:, 128 * b:128 * b + 128] = True
+    y = llp.linear_fp8(xq, xs, wq, ws, out_dtype=d)
+    assert torch.equal(torch.isnan(y), bad) and torch.equal(y[~bad], want[~bad])
+
+
+# The gradient's layout: the same shapes, with the weight's rows as the result's.
+@pytest.mark.parametrize("T,V,K", SIZES)
+def test_dweight_fp8_of_many_results(llp, T, V, K):
+    say(f"forms: dweight H={T} V={V} depth={K}")
+    plain, (x, sx, w, sw) = operands(llp, T, V, K, V - T)
+    ref, size = (m.t().contiguous() for m in reference(*plain))
+    g = torch.Generator(device="cuda").manual_seed(T)
+    for d, pad in ((torch.bfloat16, 5), (torch.bfloat16, 8), (torch.float32, 1)):
+        room = torch.full((V + 2, T + pad), 7.0, dtype=d, device="cuda")
+        y = llp.dweight_fp8(w, sw, x, sx, dweight=room[1:V + 1, :T], overwrite=True)
+        assert (room[0] == 7).all() and (room[V + 1] == 7).all() and (room[:, T:] == 7).all()
+        within(y, ref, size, K, EPS if d == torch.float32 else 2.0 ** -8)
+        assert bytes_equal(y.t().contiguous(), by_few_rows(llp, *plain, None, d))
+        if d == torch.float32:
+            start = normal(g, V, T) * 3
+            room[1:V + 1, :T] = start
+            z = llp.dweight_fp8(w, sw, x, sx, dweight=room[1:V + 1, :T])
+            assert (room[0] == 7).all() and (room[V + 1] == 7).all() and (room[:, T:] == 7).all()
+            assert torch.equal(z, start + llp.dweight_fp8(*plain[2:], *plain[:2]))
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_rows_have_the_same_bits_in_batches_of_every_form(llp, out):
+    # With this many columns 1 to 32 rows, 33 to 64, and from 65 on several shapes of the wide tile.
+    T, V, K = 700, 16517, 640
+    d = torch.bfloat16 if out == "bf16" else torch.float32
+    say(f"forms: batches of {T} x {V} {out}")
+    (xq, xs, wq, ws), _ = operands(llp, T, V, K, 5)
+    counts = (1, 31, 32, 33, 64, 65, 128, 129, 193, 257, 300, 321, 512, 513, 600)
+    assert len({wide_shape(n, V) for n in counts if n > 64}) >= 4
+    whole = llp.linear_fp8(xq, xs, wq, ws, out_dtype=d)
+    for n in counts:
+        for at in (0, T - n):
+            part = llp.linear_fp8(xq[at:at + n], xs[at:at + n], wq, ws, out_dtype=d)
+            assert bytes_equal(part.contiguous(), whole[at:at + n].contiguous()), (n, at)
+
+
+@pytest.mark.parametrize("T,H,V,dtype", [(300, 1100, 2500, "bf16"), (130, 2000, 1300, "f32"), (1000, 700, 3300, "bf16")])
+def test_fp8_linear_of_many_results(llp, T, H, V, dtype):
+    # Forward, input and weight gradient each of more than 512 tiles (or of few rows), the upstream
+    # gradient that of a mean negative log-likelihood: softmax less one where the target is.
+    say(f"forms: node T={T} H={H} V={V} {dtype}")
+    d = torch.bfloat16 if dtype == "bf16" else torch.float32
+    step = 2.0 ** -8 if dtype == "bf16" else EPS
+    g = torch.Generator(device="cuda").manual_seed(T)
+    x = normal(g, T, H).to(d).requires_grad_()
+    w = (normal(g, V, H) * 0.05).to(d).requires_grad_()
+    y = llp.fp8_linear(x, w)
+    dy = torch.softmax(y.detach().float(), 1)
+    dy[torch.arange(T, device="cuda"), torch.randint(0, V, (T,), generator=g, device="cuda")] -= 1
+    dy = (dy / T).to(d)
+    dx, dw = torch.autograd.grad(y, (x, w), dy)
+    q = llp.quantize_blocks
+    for got, a, b, K in ((y.detach(), q(x.detach()), q(w.detach(), rows=128), H),
+                         (dx, q(dy), q(w.detach(), rows=128, transpose=True), V),
+                         (dw.t(), q(x.detach(), transpose=True), q(dy, rows=128, transpose=True), T)):
+        ref, size = reference(*a, *b)
+        within(got.contiguous(), ref, size, K, step)
+    assert dx.shape == x.shape and dw.shape == w.shape and dx.dtype == d and dw.dtype == d
