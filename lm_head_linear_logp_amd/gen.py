@@ -1,7 +1,9 @@
 """Operators that decode and train with a head in 8-bit floating point (include/llp.h): block
 quantisation, products of such operands with their gradients, and one step of a beam search.
 Argument marshalling, as in ops.py: every tensor is checked here, every step runs in libllp.so on the
-tensors' own device and that device's current stream."""
+tensors' own device and that device's current stream. fp8_linear alone records a gradient: the other calls read and
+write tensors as they are, and a caller's tensor that one writes counts as changed in place, so that a
+backward pass which saved it before is refused."""
 from __future__ import annotations
 
 import ctypes as C
@@ -10,6 +12,7 @@ from typing import NamedTuple, Optional, Sequence
 
 import torch
 from torch.autograd.function import once_differentiable
+from torch.autograd.graph import increment_version as _changed
 
 from . import _capi as A
 from . import _need, _ptr, _status, _vocab
@@ -88,6 +91,8 @@ def quantize_blocks(x: torch.Tensor, *, rows: int = 1, transpose: bool = False,
                                   1 if transpose else 0, 0, q.data_ptr(), _stride(q, M, G * _BLOCK),
                                   scale.data_ptr(), lds)
     _call(dev, "llp_quantize_blocks", C.byref(req))
+    if out is not None:
+        _changed((q, scale))
     return q, scale
 
 
@@ -155,11 +160,14 @@ def linear_fp8(x: torch.Tensor, x_scale: torch.Tensor, weight: torch.Tensor,
             raise TypeError("bias must be a bf16 or fp32 tensor")
         r.bias, r.bias_dtype = _at(bias, "bias", bias.dtype, V, dev), _DTYPE[bias.dtype]
     _ready(dev)
-    if out is None:
+    given = out is not None
+    if not given:
         width = V + -V % (4 if out_dtype == _F32 else 8)
         out = torch.empty_strided((T, V), (width, 1), dtype=out_dtype, device=dev)
     r.out, r.out_dtype, r.out_stride = out.data_ptr(), _DTYPE[out_dtype], _stride(out, T, V)
     _call(dev, "llp_linear_fp8", C.byref(r))
+    if given:
+        _changed(out)
     return out
 
 
@@ -182,10 +190,13 @@ def dweight_fp8(dout_t: torch.Tensor, dout_scale: torch.Tensor, x_t: torch.Tenso
             raise TypeError("a dweight that is added to must be fp32")
     r.flags = A.LLP_FLAG_OVERWRITE_GRADS if overwrite else 0
     _ready(dev)
-    if dweight is None:
+    given = dweight is not None
+    if not given:
         dweight = torch.empty(V, H, dtype=out_dtype, device=dev)
     r.out, r.out_dtype, r.out_stride = dweight.data_ptr(), _DTYPE[out_dtype], _stride(dweight, V, H)
     _call(dev, "llp_dweight_fp8", C.byref(r))
+    if given:
+        _changed(dweight)
     return dweight
 
 
@@ -293,12 +304,15 @@ def beam_candidates(logits: torch.Tensor, num: int, *, temperature: float = 1.0,
     if out is not None:
         _check_parts(out, "out", R, num, dev)
     _ready(dev)
-    if out is None:
+    given = out is not None
+    if not given:
         out = dict(value=torch.empty(R, num, dtype=_F32, device=dev),
                    token=torch.empty(R, num, dtype=_I64, device=dev),
                    max=torch.empty(R, dtype=_F32, device=dev),
                    sum=torch.empty(R, dtype=_F64, device=dev))
     _call(dev, "llp_beam_candidates", C.byref(r), C.byref(_part_pointers(out)))
+    if given:
+        _changed(tuple(out[k] for k, _ in _PARTS))
     return out
 
 
@@ -353,12 +367,15 @@ def beam_select(parts: Sequence[dict], scores: torch.Tensor, num: Optional[int] 
             if not out[k].is_contiguous():
                 raise ValueError(f"out['{k}'] must be contiguous")
     _ready(dev)
-    if out is None:
+    given = out is not None
+    if not given:
         out = dict(token=torch.empty(B, num, dtype=_I64, device=dev),
                    parent=torch.empty(B, num, dtype=_I32, device=dev),
                    score=torch.empty(B, num, dtype=_F32, device=dev))
     o = A.llp_beam_out(out["token"].data_ptr(), out["parent"].data_ptr(), out["score"].data_ptr())
     _call(dev, "llp_beam_select", C.byref(r), C.byref(o))
+    if given:
+        _changed((out["token"], out["parent"], out["score"]))
     return out
 
 
@@ -482,6 +499,8 @@ def beam_reorder(states, parents: torch.Tensor, *, out=None, status: Optional[to
             (C.c_void_p * n)(*src_at), (C.c_void_p * n)(*dst_at), n, c.K, N, 0, B, c.outer, c.inner, c.sr,
             c.so, c.dr, c.do, parents.data_ptr(), _ptr(status))
         _call(dev, "llp_beam_reorder", C.byref(r))
+    if seen:
+        _changed(dst)
     return states if out is None else out
 
 
