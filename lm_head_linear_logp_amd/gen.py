@@ -448,8 +448,8 @@ def beam_reorder(states, parents: torch.Tensor, *, out=None, status: Optional[to
     """llp_beam_reorder: what is kept per beam follows the beams that were chosen. states: a tensor
     or a sequence of them, of any dtype, [B * K, ...] with the beams of a sequence in consecutive
     rows; parents int32 [B, N] (``beam_select``'s). In place (N = K) row b * N + j takes row
-    b * K + parents[b, j] as it was before the call; with `out` (the like of states, [B * N, ...],
-    apart from them) the rows go there. A parent of -1 leaves the row as it is; one past the beams
+    b * K + parents[b, j] as it was before the call; with `out` (the like of states, [B * N, ...], none
+    between a state's first byte and its last) the rows go there. A parent of -1 leaves the row as it is; one past the beams
     does too and sets PARENT_INVALID in `status`. A state may be a view: its dims behind the first are
     contiguous, or pieces at one stride, as a cache [rows, heads, room, dim] cut to its length is.
     Returns the tensors written."""
@@ -521,23 +521,28 @@ def _apart(seen, sources):
                 raise ValueError(f"out[{d[2]}] overlaps a state")
 
 
-def _interleaved(a, b):
-    """Whether two states of one layout, the second no lower in memory, lie between each other's pieces,
-    as the keys and values of a cache [rows, 2, ...] do."""
-    c = a[3]
-    if b[3] != c:
-        return False
-    shift = b[0] - a[0]
-    levels, extent = [], c.inner   # stride, steps, and the bytes of what lies within one step
+def _levels(c):
+    """A layout's strides, least first, each with the bytes of what lies within one step; and its extent."""
+    levels, extent = [], c.inner
     for s, n in sorted((s, n) for s, n in ((c.dr, c.rows), (c.do, c.outer)) if n > 1):
-        levels.append((s, n, extent))
+        levels.append((s, extent))
         extent += (n - 1) * s
+    return levels, extent
+
+
+def _interleaved(a, b):
+    """Whether two states, the second no lower in memory, lie between each other's rows or pieces, as the
+    keys and values of a cache [rows, 2, ...] do, or parts of one buffer's rows."""
+    shift = b[0] - a[0]
+    la, extent = _levels(a[3])
     if shift >= extent:
         return True
-    for s, n, within in reversed(levels):
+    lb, _ = _levels(b[3])
+    while la and lb and la[-1][0] == lb[-1][0]:   # a common stride, the larger ones first
+        (s, in_a), (_, in_b) = la.pop(), lb.pop()
         shift %= s
-        if shift + within > s:
+        if shift + in_b > s:
             return False
-        if shift >= within:
+        if shift >= in_a:
             return True
     return False
