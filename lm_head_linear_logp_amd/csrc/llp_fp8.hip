@@ -1068,11 +1068,13 @@ hipError_t launch_linear8(const Linear8Args& a, hipStream_t s) {
     if (a.out_bf16) return launch_linear8_bf16<true>(a, s);
     return launch_linear8_as<128, 128, 2, 2, 2, true, true, 2>(a, s);
   }
-  // Few rows, the weight's bytes bound them: where 128 columns a workgroup would leave compute units
-  // with one, and so with two steps in flight, 64 columns each (us in fp32, 128 and 64 columns: 1 row of 37984 36.7
-  // and 33.2, of 151936 108 and 112; 37 rows 43.5 and 38.5, of 151936 129 and 140). More steps in flight (4 to 6)
-  // or 256 columns are no faster.
-  const bool narrow = a.V < 65536;
+  // Few rows, the weight's bytes bound them: 64 or 128 columns a workgroup, whichever leaves the busiest of 256
+  // compute units fewer columns, 128 where they are alike, and from 65536 on (us of 4096 deep fp32, 64 and 128
+  // columns: 1 row of 16384 19.9 and 22.1, of 24000 24.8 and 23.0, of 33500 31.4 and 35.4, of 37984 32.8 and 36.5, of
+  // 48000 38.6 and 40.7, of 50000 43.8 and 40.6, of 70000 60.2 and 61.9, of 98304 76.4 and 70.7; 33 rows of 37984 38.2
+  // and 42.4, of 48000 41.7 and 45.0, of 50000 55.8 and 45.2, of 65536 64.4 and 52.6; alike in bf16 and 2048 deep). More
+  // steps in flight (4 to 6) or 256 columns are no faster.
+  const bool narrow = a.V < 65536 && (a.V + 16383) / 16384 % 2 != 0;
   if (a.out_bf16) {
     if (a.T <= 32) return narrow ? launch_linear8_as<64, 32, 2, 1, 3, false, false, 2>(a, s)
                                  : launch_linear8_as<128, 32, 4, 1, 3, false, false, 2>(a, s);

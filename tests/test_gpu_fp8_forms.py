@@ -159,6 +159,21 @@ def test_dweight_fp8_of_many_results(llp, T, V, K):
             assert torch.equal(z, start + llp.dweight_fp8(*plain[2:], *plain[:2]))
 
 
+# Where the few-row forms change the columns of a workgroup, and their neighbours.
+@pytest.mark.parametrize("V", [16383, 16384, 16385, 32768, 32769, 49152, 49153, 65535, 65536])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_linear_fp8_of_few_rows_at_every_width(llp, V, out):
+    K, d = 256, torch.bfloat16 if out == "bf16" else torch.float32
+    say(f"forms: few rows V={V} {out}")
+    plain, inside = operands(llp, 64, V, K, V)
+    ref, size = reference(*plain)
+    whole = llp.linear_fp8(*inside, out_dtype=d)
+    within(whole, ref, size, K, EPS if out == "f32" else 2.0 ** -8)
+    for n in (1, 31, 32, 33, 63):
+        part = llp.linear_fp8(inside[0][:n], inside[1][:n], *inside[2:], out_dtype=d)
+        assert bytes_equal(part.contiguous(), whole[:n].contiguous()), n
+
+
 @pytest.mark.parametrize("out", ["bf16", "f32"])
 def test_rows_have_the_same_bits_in_batches_of_every_form(llp, out):
     # With this many columns 1 to 32 rows, 33 to 64, and from 65 on several shapes of the wide tile.
