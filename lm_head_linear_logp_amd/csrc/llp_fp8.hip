@@ -432,9 +432,11 @@ hipError_t launch_quant8_both(const Quant8Args& a, const Quant8Args& t, hipStrea
 //
 // Precision. The e4m3 MFMAs (every form of them) add 8 products at a time cut towards zero at 2^-13
 // of the largest one's power of two: measured on values drawn as activations are, a sum of 64 is
-// 1.7e-5 of its norm off. That is a hundredth of bf16's rounding, so results that are written in
-// bf16 take it; results in fp32 (FULL) do not: their bytes become bf16 (exact) in front of the bf16
-// MFMA, whose sums keep fp32's bits, at half the matrix rate.
+// 1.7e-5 of its norm off. That is a hundredth of bf16's rounding of most results, so those written in bf16 take
+// it; but the cut goes by the products, not by their sum, and a result whose products nearly cancel keeps less
+// (300 rows of 37984, 4096 deep: 1.7 % of the results are not the nearest bf16 value, 0.3 % a step or more off; of
+// those below a hundredth of the rows' size, 0.8 % of them, a third). Results in fp32 (FULL) do not take it:
+// their bytes become bf16 (exact) in front of the bf16 MFMA, whose sums keep fp32's bits, at half the matrix rate.
 //
 // Either way every tile runs the same chain for each element, its groups in the same order, so an element
 // has the same bits whatever the tile and however many rows the call has.
@@ -483,9 +485,10 @@ __device__ __forceinline__ int swz16(int row) { return (row ^ ((row >> 3) & 1)) 
 // A workgroup's tile: TM weight rows x TN rows of x by WM x WN waves, NST stages in flight. A wave's
 // accumulators are MB x NB blocks of S x S: 16 in bf16 results, 32 in fp32 ones.
 // Groups of 128 are taken in turn from group (weight row / 1280) % groups on: workgroups that all read the
-// same columns of rows 4096 bytes apart crowd a few of the memory's channels (1 row of 37984 x 4096 fp8: 40.6
-// us from column 0 on, 33.0 so; of 151936: 121 and 111; 64 rows 133 and 123). 1280: whole tiles of every
-// form, so that a column's order of groups is the same in all of them.
+// same columns of rows 4096 bytes apart crowd a few of the memory's channels (1 row of 37984 x 4096: 37.0 us from
+// column 0 on, 33.0 so; of 151936 119 and 107; 64 rows 132 and 123; rows of 8192 bytes 65 and 60. Rows of 1024, 2048
+// and 5120 bytes: equal). The row is counted in the call's own weight. 1280: whole tiles of every form, so that a
+// column's order of groups is the same in all of them.
 constexpr int64_t TURN8 = 1280;
 __device__ __forceinline__ int first_group8(int64_t v0, int n) { return n > 0 ? (int)(v0 / TURN8 % n) : 0; }
 
@@ -1019,8 +1022,8 @@ static hipError_t launch_linear8_wide(Linear8Args a, hipStream_t s) {
 
 // The wide form's shape. A compute unit holds one workgroup, so a call takes as long as its rounds of 256
 // workgroups times what one takes: in units of a block's MFMA its MB NB, 10 for a step's other work and 2
-// where a wave's rows lie in two of the weight's blocks (fitted to every shape at 37 sizes; the shape that the
-// rule takes is 0.4 % slower than the best of them on average). us of a shard, 37984 x 4096, with the shape it
+// where a wave's rows lie in two of the weight's blocks (every shape measured at 40 sizes: the one that the rule
+// takes is 0.6 % slower than the best of them on average, 12 % at most, 180 rows of 18992 x 2048). us of a shard, 37984 x 4096, with the shape it
 // takes and with 8 x 4: 128 rows 37 and 59, 180 rows 42 and 60, 300 rows 56 and 102, 512 rows 91 and 108, 600
 // rows 104 and 114.
 template <bool GRAD>
