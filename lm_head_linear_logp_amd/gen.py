@@ -145,7 +145,9 @@ def linear_fp8(x: torch.Tensor, x_scale: torch.Tensor, weight: torch.Tensor,
                out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """llp_linear_fp8: x . weight^T + bias of operands as quantize_blocks gives them, x [T, K] with
     rows=1 and weight [V, K] with rows=128, summed in fp32 and rounded once to out_dtype (bf16 or
-    fp32). With the weight quantised transposed it is the input gradient. An allocated result has
+    fp32). Into bf16 the 8-bit matrix instructions add a group's products, with about 14 bits below the
+    largest: results whose products nearly cancel keep fewer than bf16's bits. With the weight quantised
+    transposed it is the input gradient. An allocated result has
     rows of a multiple of 16 bytes (a view [T, V] where V is not), as the calls that read logits
     take them."""
     r, dev, T, V = _product(x, x_scale, weight, weight_scale, ("x", "weight"))
@@ -176,7 +178,11 @@ def dweight_fp8(dout_t: torch.Tensor, dout_scale: torch.Tensor, x_t: torch.Tenso
                 overwrite: bool = False, out_dtype: torch.dtype = torch.float32) -> torch.Tensor:
     """llp_dweight_fp8: dweight (fp32 [V, H]) += dout^T . x with both operands quantised transposed,
     dout_t [V, T] in blocks (rows=128) and x_t [H, T] in groups (rows=1). overwrite=True writes
-    instead, and then dweight may be bf16. A missing dweight is allocated in out_dtype."""
+    instead, and then dweight may be bf16. A missing dweight is allocated in out_dtype.
+    A block's largest entry sets the scale of 128 columns and 128 tokens of dout, so that of a softmax's
+    gradient most small entries go to 0 beside the targets'. Where that matters
+    ``linear_fp8(*quantize_blocks(dout, transpose=True), *quantize_blocks(x, rows=128, transpose=True))``
+    is the same product with a scale for each column's 128 tokens of dout, and blocks along x."""
     r, dev, H, V = _product(x_t, x_scale, dout_t, dout_scale, ("x_t", "dout_t"))
     if dweight is None:
         overwrite = True
@@ -234,7 +240,7 @@ def fp8_linear(x: torch.Tensor, weight: torch.Tensor, *,
     """x . weight^T as an autograd node whose three products run in 8-bit floating point: x of any
     shape [..., K] and weight [V, K], bf16 or fp32, quantised here (x, and the upstream gradient, in
     groups of 128; the weight in blocks of 128 x 128; along the tokens, for the weight gradient, the
-    upstream gradient in blocks and x in groups). Gradients are those of the product at the
+    upstream gradient in blocks, see ``dweight_fp8`` for what that costs, and x in groups). Gradients are those of the product at the
     quantised operands, in x's and weight's own dtypes, summed in fp32."""
     _tensor(x, "x")
     dev = _rows(weight, "weight")
@@ -402,7 +408,8 @@ def _pieces(shape, *strides):
 
 
 class _Layout(NamedTuple):
-    """States' pieces: beams K of a sequence read, rows written, strides and lengths in bytes."""
+    """States' pieces: beams K of a sequence read, rows written, strides and lengths in bytes; `levels`:
+    the strides written, largest first, each with the bytes of what lies within one step."""
     K: int
     rows: int
     outer: int
@@ -413,6 +420,7 @@ class _Layout(NamedTuple):
     do: int
     extent: int
     src_extent: int
+    levels: tuple
 
 
 @functools.lru_cache(maxsize=1024)
@@ -435,13 +443,14 @@ def _reorder_layout(shape, stride, to_shape, to_stride, size, B, N, in_place):
     K = _num(shape[0] // B, "beams per sequence")
     dr = to_stride[0] * size if rows > 1 else 0
     sr = dr if in_place else stride[0] * size if shape[0] > 1 else 0
-    reach = inner
+    reach, levels = inner, ()
     for st, n in sorted((st, n) for st, n in ((dr, rows), (do, outer)) if n > 1):
         if st < reach:
             raise ValueError("has rows to be written that overlap")
+        levels = ((st, reach), *levels)
         reach += (n - 1) * st
-    return _Layout(K, rows, outer, inner, sr, so, dr, do, (rows - 1) * dr + (outer - 1) * do + inner,
-                   (shape[0] - 1) * sr + (outer - 1) * so + inner)
+    return _Layout(K, rows, outer, inner, sr, so, dr, do, reach, (shape[0] - 1) * sr + (outer - 1) * so + inner,
+                   levels)
 
 
 def beam_reorder(states, parents: torch.Tensor, *, out=None, status: Optional[torch.Tensor] = None):
@@ -521,25 +530,16 @@ def _apart(seen, sources):
                 raise ValueError(f"out[{d[2]}] overlaps a state")
 
 
-def _levels(c):
-    """A layout's strides, least first, each with the bytes of what lies within one step; and its extent."""
-    levels, extent = [], c.inner
-    for s, n in sorted((s, n) for s, n in ((c.dr, c.rows), (c.do, c.outer)) if n > 1):
-        levels.append((s, extent))
-        extent += (n - 1) * s
-    return levels, extent
-
-
 def _interleaved(a, b):
     """Whether two states, the second no lower in memory, lie between each other's rows or pieces, as the
     keys and values of a cache [rows, 2, ...] do, or parts of one buffer's rows."""
+    ca, cb = a[3], b[3]
     shift = b[0] - a[0]
-    la, extent = _levels(a[3])
-    if shift >= extent:
+    if shift >= ca.extent:
         return True
-    lb, _ = _levels(b[3])
-    while la and lb and la[-1][0] == lb[-1][0]:   # a common stride, the larger ones first
-        (s, in_a), (_, in_b) = la.pop(), lb.pop()
+    for (s, in_a), (sb, in_b) in zip(ca.levels, cb.levels):
+        if s != sb:
+            return False
         shift %= s
         if shift + in_b > s:
             return False
