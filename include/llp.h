@@ -568,10 +568,14 @@ typedef struct {
  *   rows, cols  0 .. 2^23 - 256; ceil(rows / 32) * ceil(cols / 128) < 2^23 (else
  *           LLP_ERR_UNSUPPORTED).
  * The groups are added in fp32 in ascending order from group (v / 1280) mod the number of groups on, then
- * from 0, so an element depends on its two rows and v alone, whatever the call's other rows. A
+ * from 0, so an element depends on its two rows and v alone, whatever the call's other rows. v is counted in
+ * the call: a weight row that is another column of another call, as in a shard and in the whole weight,
+ * gives a sum in another order, equal to rounding. A
  * group's 128 products are summed in fp32 where out is fp32; where it
  * is bf16 they are summed by the 8-bit matrix instructions, which cut 8 products at a time about 14
- * bits below the largest: a hundredth of the result's rounding to bf16.
+ * bits below the largest of them. That is a hundredth of the rounding to bf16 of a result as large as its products
+ * make it, and more than it where they nearly cancel (operands drawn as activations and weights are: 1.7 % of the
+ * results not the nearest bf16 value, 0.3 % a step or more off). fp32 results, rounded, have none of it.
  * llp_linear_fp8: out[t][v] = p + bias[v], [rows, cols] of out_dtype, row stride out_stride
  *   elements (>= cols), any alignment of its element type, rounded once. bias [cols] of bias_dtype
  *   or NULL. flags must be 0.
@@ -631,8 +635,9 @@ typedef struct {
  *   value   fp32 [num_rows, num], the logits x in descending order (-inf past the last candidate)
  *   token   int64 [num_rows, num] global ids (-1 past the last candidate)
  *   max     fp32 [num_rows], the largest logit (-inf for a row without one)
- *   sum     fp64 [num_rows], sum exp((x - max) fl32(1/temperature)) over the real columns; 0 for a
- *           row without a finite logit */
+ *   sum     fp64 [num_rows], sum exp((x - max) c), c = fl32(1/temperature), over the real columns; 0 for a
+ *           row without a finite logit. A term below 1 is within 2^-23 (1 + (max - x) c) of itself, and
+ *           terms are added in fp64. */
 typedef struct {
   float* value;
   int64_t* token;

@@ -290,8 +290,8 @@ __global__ __launch_bounds__(Q8_THREADS) void k_quant8(Quant8Args a) {
 }
 
 // Both that a weight's gradient step takes of one x: a by group, t in blocks and transposed. One read instead of
-// two (4096 x 37984 bf16: 108 and 103 us apart, 181
-// together; 4096 x 151936: 424 and 378, 590).
+// two (4096 x 37984 bf16: 108 and 103 us apart, 181 together, 622 MB at 3.4 TB/s; 4096 x 151936: 424 and 378, 590).
+// Every value is packed twice, and a's rows are written 128 bytes at a time: short of a copy's 5.1 TB/s.
 template <bool BF16, bool VEC>
 __global__ __launch_bounds__(Q8_THREADS) void k_quant8_both(Quant8Args a, Quant8Args t) {
   __shared__ uint32_t tops[4];
@@ -825,8 +825,9 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(EU
 // MFMAs. The barrier in front of those frees the step's stage, into which from there on a later step is
 // loaded, one load after an MFMA (nine in a row hold up the wave's MFMAs: 5 % slower).
 //
-// 4096 x 37984 x 4096: 561 us, 2.27e15/s; 4096 x 151936: 2.13 ms, 2.39e15/s; its gradients 490 (x) and 507 (weight);
-// the library's product of the same bytes with one scale a matrix 517, 1769 and 384 (x). Bound by LDS and matrix
+// 4096 x 37984 x 4096: 545 to 605 us over boxes and the clock that power leaves, 2.1 to 2.3e15/s; 4096 x 151936: 2.13
+// to 2.26 ms, 2.3 to 2.4e15/s; the shard's gradients 480 to 535 (x) and 507 to 632 (weight); the library's
+// product of the same bytes with one scale a matrix 517, 1769 and 384 (x). Bound by LDS and matrix
 // cores alike: a step's operands are 196 KB of reads and 64 KB of writes, 2030 cycles at 128 bytes each, and its MFMAs
 // 2048; eight waves of 128 x 64 are what the registers hold with sums that vector instructions scale.
 template <int MB_, int NB_>

@@ -489,7 +489,7 @@ struct ReorderArgs {
   const void* src[REORDER_STATES];
   void* dst[REORDER_STATES];
   int32_t states, K, N;              // K source beams, N slots per sequence
-  int32_t unit;                      // bytes per load: 16, 8, 4, 2 or 1
+  int32_t unit;                      // bytes per load: 16, 4 or 1
   int64_t seqs, outer, inner;
   int64_t sr, so, dr, dout;          // row and outer strides of src and dst, bytes
   const int32_t* parents;

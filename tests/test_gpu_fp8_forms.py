@@ -190,6 +190,26 @@ def test_rows_have_the_same_bits_in_batches_of_every_form(llp, out):
             assert bytes_equal(part.contiguous(), whole[at:at + n].contiguous()), (n, at)
 
 
+@pytest.mark.parametrize("T,H,V", [(130, 256, 1000), (512, 4096, 3001)])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_a_weight_gradient_with_a_scale_for_each_columns_tokens(llp, T, H, V, out):
+    # linear_fp8 with the roles of the operands turned: of a softmax's gradient it keeps what blocks lose.
+    d = torch.bfloat16 if out == "bf16" else torch.float32
+    say(f"forms: weight gradient by columns T={T} H={H} V={V} {out}")
+    g = torch.Generator(device="cuda").manual_seed(V)
+    dy = torch.softmax(2 * normal(g, T, V), 1)
+    dy[torch.arange(T, device="cuda"), torch.randint(0, V, (T,), generator=g, device="cuda")] -= 1
+    x = normal(g, T, H)
+    q = llp.quantize_blocks
+    a, b = q(dy, transpose=True), q(x, rows=128, transpose=True)
+    got = llp.linear_fp8(*a, *b, out_dtype=d)
+    assert got.shape == (V, H)
+    within(got, *reference(*a, *b), T, EPS if out == "f32" else 2.0 ** -8)
+    blocks = q(dy, rows=128, transpose=True)
+    zero = lambda y: int(((y[0][:, :T].float() == 0) & (dy.t() != 0)).sum())  # noqa: E731
+    assert zero(a) < zero(blocks)
+
+
 @pytest.mark.parametrize("T,H,V,dtype", [(300, 1100, 2500, "bf16"), (130, 2000, 1300, "f32"), (1000, 700, 3300, "bf16")])
 def test_fp8_linear_of_many_results(llp, T, H, V, dtype):
     # Forward, input and weight gradient each of more than 512 tiles (or of few rows), the upstream
