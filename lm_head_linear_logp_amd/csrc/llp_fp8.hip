@@ -825,7 +825,7 @@ __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(EU
 // MFMAs. The barrier in front of those frees the step's stage, into which from there on a later step is
 // loaded, one load after an MFMA (nine in a row hold up the wave's MFMAs: 5 % slower).
 //
-// 4096 x 37984 x 4096: 545 to 605 us over boxes and the clock that power leaves, 2.1 to 2.3e15/s; 4096 x 151936: 2.13
+// 4096 x 37984 x 4096: 545 to 640 us over boxes and the clock that power leaves, 2.0 to 2.3e15/s; 4096 x 151936: 2.13
 // to 2.26 ms, 2.3 to 2.4e15/s; the shard's gradients 480 to 535 (x) and 507 to 632 (weight); the library's
 // product of the same bytes with one scale a matrix 517, 1769 and 384 (x). Bound by LDS and matrix
 // cores alike: a step's operands are 196 KB of reads and 64 KB of writes, 2030 cycles at 128 bytes each, and its MFMAs

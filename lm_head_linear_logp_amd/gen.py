@@ -240,8 +240,9 @@ def fp8_linear(x: torch.Tensor, weight: torch.Tensor, *,
     """x . weight^T as an autograd node whose three products run in 8-bit floating point: x of any
     shape [..., K] and weight [V, K], bf16 or fp32, quantised here (x, and the upstream gradient, in
     groups of 128; the weight in blocks of 128 x 128; along the tokens, for the weight gradient, the
-    upstream gradient in blocks, see ``dweight_fp8`` for what that costs, and x in groups). Gradients are those of the product at the
-    quantised operands, in x's and weight's own dtypes, summed in fp32."""
+    upstream gradient in blocks, see ``dweight_fp8`` for what that costs, and x in groups). Gradients
+    are those of the product at the quantised operands, in x's and weight's own dtypes, summed as
+    ``linear_fp8`` does."""
     _tensor(x, "x")
     dev = _rows(weight, "weight")
     if x.dtype not in _DTYPE:
@@ -458,8 +459,8 @@ def beam_reorder(states, parents: torch.Tensor, *, out=None, status: Optional[to
     or a sequence of them, of any dtype, [B * K, ...] with the beams of a sequence in consecutive
     rows; parents int32 [B, N] (``beam_select``'s). In place (N = K) row b * N + j takes row
     b * K + parents[b, j] as it was before the call; with `out` (the like of states, [B * N, ...], none
-    between a state's first byte and its last) the rows go there. A parent of -1 leaves the row as it is; one past the beams
-    does too and sets PARENT_INVALID in `status`. A state may be a view: its dims behind the first are
+    between a state's first byte and its last) the rows go there. A parent of -1 leaves the row as it
+    is; one past the beams does too and sets PARENT_INVALID in `status`. A state may be a view: its dims behind the first are
     contiguous, or pieces at one stride, as a cache [rows, heads, room, dim] cut to its length is.
     Returns the tensors written."""
     single = isinstance(states, torch.Tensor)
